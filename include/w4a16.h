@@ -434,6 +434,119 @@ w4a16_status w4a8_mxfp4_grouped_gemm(const void *x, const int32_t *expert_offset
                                      int64_t E, int64_t R, int64_t K, int64_t N, int dt, void *workspace,
                                      size_t workspace_bytes, void *stream);
 
+/*
+ * ---- Fused linear operators -------------------------------------------------
+ * The int4 product with the rest of a linear layer in its epilogue, the gated
+ * feed-forward projection, and the gradients that training through frozen
+ * int4 weights needs (adapters, distillation: the input gradient multiplies
+ * by W^T straight from the same prepacked weights).
+ *
+ * Shared rules, on top of the conventions at the top of this file:
+ *  - w4a16_linear describes one weight matrix and is read during the call
+ *    only.  group_size is a multiple of 128 dividing K (weights from
+ *    w4a16_prepack, or w4a16_prepack_g with such a group size).
+ *  - act: one of w4a16_act, applied in fp32:
+ *      NONE v;  RELU max(v, 0) (derivative 0 at 0);  SILU v / (1 + exp(-v));
+ *      GELU v (1 + erf(v / sqrt 2)) / 2;
+ *      GELU_TANH v (1 + tanh(sqrt(2/pi) (v + 0.044715 v^3))) / 2.
+ *  - 16-bit tensors other than scale are 16-byte aligned, scale 2, dbias 4.
+ *    A row stride (ld...) counts elements, is a multiple of 8 and at least
+ *    the row length; 0 means rows without gaps.  Saved pre-activations and
+ *    their gradients (pre, h, dpre, dh) and dbias have no gaps.
+ *  - x must be finite for a finite result row (the bf16 decode kernel gives
+ *    NaN, not infinity, in the row of an infinite x).
+ *  - workspace: device, 16-byte aligned, at least the size the matching
+ *    query returns for the same (lin, M); may be NULL when that is 0.  Its
+ *    contents on entry are ignored.  Calls sharing one must be ordered on one
+ *    stream.  The queries return 0 for sizes the calls reject.
+ *  - Sums are fp32 in an order fixed by the sizes (no atomics): equal calls
+ *    give equal bits.
+ */
+typedef enum {
+    W4A16_ACT_NONE = 0,
+    W4A16_ACT_RELU = 1,
+    W4A16_ACT_SILU = 2,
+    W4A16_ACT_GELU = 3,
+    W4A16_ACT_GELU_TANH = 4
+} w4a16_act;
+
+typedef struct {
+    int64_t K, N;                /* W [K][N]                                           */
+    int64_t group_size;          /* rows per scale group                               */
+    const void *w_packed;        /* prepacked W                                        */
+    const void *scale;           /* [K/group_size][N], dtype of the activations        */
+    const void *zero;            /* uint4 [K/group_size][N/2], or NULL: signed weights */
+    const void *bias;            /* [N], dtype of the activations, or NULL             */
+} w4a16_linear;
+
+/*
+ * y = act(p) + residual, p = x . dequant(W) + bias.
+ *   x         [M][K], row stride ldx
+ *   residual  [M][N], row stride ldr, or NULL; may be y itself
+ *   pre       out, [M][N], p rounded to dt for the backward pass, or NULL
+ *   y         out, [M][N], row stride ldy
+ * Every output is rounded once from fp32.  M <= 64 runs a decode kernel whose
+ * waves split K, larger M a tile kernel; where the tiles would leave compute
+ * units idle K is cut into slices whose fp32 sums meet in the workspace.
+ */
+size_t w4a16_gemm_ep_workspace_bytes(const w4a16_linear *lin, int64_t M);
+
+w4a16_status w4a16_gemm_ep(const void *x, int64_t ldx, const w4a16_linear *lin, int act, const void *residual,
+                           int64_t ldr, void *pre, void *y, int64_t ldy, int64_t M, int dt, void *workspace,
+                           size_t workspace_bytes, void *stream);
+
+/*
+ * Backward pass of w4a16_gemm_ep through x and bias (W is frozen; the
+ * residual's gradient is dy itself):
+ *   dpre = dy * act'(pre), dbias[n] = sum_m dpre[m][n], dx = dpre . W^T + addend.
+ *   dy      [M][N], row stride lddy
+ *   pre     [M][N] as saved by the forward call; unused for W4A16_ACT_NONE
+ *   addend  [M][K], row stride ldadd, or NULL; may be dx itself (gradient
+ *           accumulation)
+ *   dpre    out, [M][N] rounded to dt; may be pre itself.  Required unless act
+ *           is W4A16_ACT_NONE, where dpre equals dy, nothing is written to it
+ *           and it may be NULL
+ *   dbias   out, [N] fp32 summed from the unrounded dpre, or NULL; zeros for M = 0
+ *   dx      out, [M][K], row stride lddx
+ * The product multiplies dpre and dequant(W), each rounded to dt (the
+ * matrix core takes 16-bit operands and the scales vary along the summed
+ * dimension), with fp32 sums and one rounding of dx.
+ */
+size_t w4a16_gemm_ep_backward_workspace_bytes(const w4a16_linear *lin, int64_t M);
+
+w4a16_status w4a16_gemm_ep_backward(const void *dy, int64_t lddy, const void *pre, const w4a16_linear *lin, int act,
+                                    const void *addend, int64_t ldadd, void *dpre, float *dbias, void *dx,
+                                    int64_t lddx, int64_t M, int dt, void *workspace, size_t workspace_bytes,
+                                    void *stream);
+
+/*
+ * Gated projection, both halves and their product in one kernel: with
+ * I = N / 2 (N % 128 == 0) and W holding the I gate columns, then the I up
+ * columns (the layout of the fused-experts W13),
+ *   h = x . dequant(W) + bias,  a[m][i] = act(h[m][i]) * h[m][I + i].
+ *   h   out, [M][2I] rounded to dt for the backward pass, or NULL
+ *   a   out, [M][I], row stride lda, rounded once from the fp32 sums
+ */
+size_t w4a16_glu_gemm_workspace_bytes(const w4a16_linear *lin, int64_t M);
+
+w4a16_status w4a16_glu_gemm(const void *x, int64_t ldx, const w4a16_linear *lin, int act, void *h, void *a,
+                            int64_t lda, int64_t M, int dt, void *workspace, size_t workspace_bytes, void *stream);
+
+/*
+ * Backward pass of w4a16_glu_gemm through x and bias:
+ *   dh[m][i] = da[m][i] h[m][I+i] act'(h[m][i]),  dh[m][I+i] = da[m][i] act(h[m][i]),
+ *   dbias[n] = sum_m dh[m][n],  dx = dh . W^T + addend.
+ *   da  [M][I], row stride ldda;  h  [M][2I] as saved by the forward call
+ *   dh  out, [M][2I] rounded to dt; may be h itself
+ *   addend, dbias, dx and the operand rounding as in w4a16_gemm_ep_backward
+ */
+size_t w4a16_glu_gemm_backward_workspace_bytes(const w4a16_linear *lin, int64_t M);
+
+w4a16_status w4a16_glu_gemm_backward(const void *da, int64_t ldda, const void *h, const w4a16_linear *lin, int act,
+                                     const void *addend, int64_t ldadd, void *dh, float *dbias, void *dx,
+                                     int64_t lddx, int64_t M, int dt, void *workspace, size_t workspace_bytes,
+                                     void *stream);
+
 #ifdef __cplusplus
 }
 #endif

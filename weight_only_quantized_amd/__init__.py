@@ -37,6 +37,15 @@ class WeightDesc(C.Structure):
                 ("scale", C.c_void_p), ("zero", C.c_void_p), ("channel_scale", C.c_void_p)]
 
 
+class Linear(C.Structure):
+    """w4a16_linear (include/w4a16.h): one weight matrix W [K][N] with its
+    scales, zero points and bias (device pointers).  Made by :func:`linear`."""
+    _fields_ = [("K", C.c_int64), ("N", C.c_int64), ("group_size", C.c_int64), ("w_packed", C.c_void_p),
+                ("scale", C.c_void_p), ("zero", C.c_void_p), ("bias", C.c_void_p)]
+
+
+W4A16_ACT_NONE, W4A16_ACT_RELU, W4A16_ACT_SILU, W4A16_ACT_GELU, W4A16_ACT_GELU_TANH = range(5)
+
 _lib = None
 _p = C.c_void_p
 _i64 = C.c_int64
@@ -71,6 +80,18 @@ _SIGS = {
     "w4a8_mxfp4_gemm": ([_p, _p, _p, _i64, _i64, _i64, C.c_int, _p, C.c_size_t, _p], C.c_int),
     "w4a8_mxfp4_grouped_workspace_bytes": ([_i64, _i64], C.c_size_t),
     "w4a8_mxfp4_grouped_gemm": ([_p, _p, _p, _p, _i64, _i64, _i64, _i64, C.c_int, _p, C.c_size_t, _p], C.c_int),
+    "w4a16_gemm_ep_workspace_bytes": ([C.POINTER(Linear), _i64], C.c_size_t),
+    "w4a16_gemm_ep": ([_p, _i64, C.POINTER(Linear), C.c_int, _p, _i64, _p, _p, _i64, _i64, C.c_int, _p, C.c_size_t,
+                       _p], C.c_int),
+    "w4a16_gemm_ep_backward_workspace_bytes": ([C.POINTER(Linear), _i64], C.c_size_t),
+    "w4a16_gemm_ep_backward": ([_p, _i64, _p, C.POINTER(Linear), C.c_int, _p, _i64, _p, _p, _p, _i64, _i64, C.c_int,
+                                _p, C.c_size_t, _p], C.c_int),
+    "w4a16_glu_gemm_workspace_bytes": ([C.POINTER(Linear), _i64], C.c_size_t),
+    "w4a16_glu_gemm": ([_p, _i64, C.POINTER(Linear), C.c_int, _p, _p, _i64, _i64, C.c_int, _p, C.c_size_t, _p],
+                       C.c_int),
+    "w4a16_glu_gemm_backward_workspace_bytes": ([C.POINTER(Linear), _i64], C.c_size_t),
+    "w4a16_glu_gemm_backward": ([_p, _i64, _p, C.POINTER(Linear), C.c_int, _p, _i64, _p, _p, _p, _i64, _i64, C.c_int,
+                                 _p, C.c_size_t, _p], C.c_int),
     "w4a16_test_unpack": ([_p, _p, _i64, _i64, _i64, C.c_int, _p], C.c_int),
     "w4a16_test_msd_intermediates": ([_p, _p, _i64, _i64, _i64, _i64, _p, _p, _p, _p, C.c_size_t, _p], C.c_int),
     "w4a16_test_msd_basic_workspace_bytes": ([_i64, _i64, _i64, _i64], C.c_size_t),
@@ -271,6 +292,58 @@ def w4a8_mxfp4_grouped_gemm(x, expert_offsets, w_packed, y, E, R, K, N, dt=W4A16
     _check(lib().w4a8_mxfp4_grouped_gemm(_ptr(x), _ptr(expert_offsets), _ptr(w_packed), _ptr(y), E, R, K, N,
                                          int(dt), _ptr(workspace), int(workspace_bytes), _stream(stream)),
            "w4a8_mxfp4_grouped_gemm")
+
+
+# ---- fused linear operators ----------------------------------------------------
+
+def linear(K, N, w_packed, scale, zero=None, bias=None, group_size=GROUP_SIZE) -> Linear:
+    """The description of one weight matrix that the fused linear operators
+    take; it keeps its tensors alive.  K, N, group_size: w4a16_linear."""
+    lin = Linear(K, N, group_size, _ptr(w_packed), _ptr(scale), _ptr(zero), _ptr(bias))
+    lin.tensors = (w_packed, scale, zero, bias)
+    return lin
+
+
+def w4a16_gemm_ep_workspace_bytes(lin, M) -> int:
+    return lib().w4a16_gemm_ep_workspace_bytes(lin, M)
+
+
+def w4a16_gemm_ep(x, lin, y, M, act=W4A16_ACT_NONE, residual=None, pre=None, dt=W4A16_BF16, ldx=0, ldr=0, ldy=0,
+                  workspace=None, workspace_bytes=0, stream=None):
+    _check(lib().w4a16_gemm_ep(_ptr(x), ldx, lin, int(act), _ptr(residual), ldr, _ptr(pre), _ptr(y), ldy, M, int(dt),
+                               _ptr(workspace), int(workspace_bytes), _stream(stream)), "w4a16_gemm_ep")
+
+
+def w4a16_gemm_ep_backward_workspace_bytes(lin, M) -> int:
+    return lib().w4a16_gemm_ep_backward_workspace_bytes(lin, M)
+
+
+def w4a16_gemm_ep_backward(dy, pre, lin, dx, M, act=W4A16_ACT_NONE, dpre=None, dbias=None, addend=None,
+                           dt=W4A16_BF16, lddy=0, ldadd=0, lddx=0, workspace=None, workspace_bytes=0, stream=None):
+    _check(lib().w4a16_gemm_ep_backward(_ptr(dy), lddy, _ptr(pre), lin, int(act), _ptr(addend), ldadd, _ptr(dpre),
+                                        _ptr(dbias), _ptr(dx), lddx, M, int(dt), _ptr(workspace),
+                                        int(workspace_bytes), _stream(stream)), "w4a16_gemm_ep_backward")
+
+
+def w4a16_glu_gemm_workspace_bytes(lin, M) -> int:
+    return lib().w4a16_glu_gemm_workspace_bytes(lin, M)
+
+
+def w4a16_glu_gemm(x, lin, a, M, act=W4A16_ACT_SILU, h=None, dt=W4A16_BF16, ldx=0, lda=0, workspace=None,
+                   workspace_bytes=0, stream=None):
+    _check(lib().w4a16_glu_gemm(_ptr(x), ldx, lin, int(act), _ptr(h), _ptr(a), lda, M, int(dt), _ptr(workspace),
+                                int(workspace_bytes), _stream(stream)), "w4a16_glu_gemm")
+
+
+def w4a16_glu_gemm_backward_workspace_bytes(lin, M) -> int:
+    return lib().w4a16_glu_gemm_backward_workspace_bytes(lin, M)
+
+
+def w4a16_glu_gemm_backward(da, h, lin, dx, M, act=W4A16_ACT_SILU, dh=None, dbias=None, addend=None, dt=W4A16_BF16,
+                            ldda=0, ldadd=0, lddx=0, workspace=None, workspace_bytes=0, stream=None):
+    _check(lib().w4a16_glu_gemm_backward(_ptr(da), ldda, _ptr(h), lin, int(act), _ptr(addend), ldadd, _ptr(dh),
+                                         _ptr(dbias), _ptr(dx), lddx, M, int(dt), _ptr(workspace),
+                                         int(workspace_bytes), _stream(stream)), "w4a16_glu_gemm_backward")
 
 
 # ---- test hooks (include/w4a16_test.h) ----------------------------------------

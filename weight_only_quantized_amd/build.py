@@ -17,7 +17,8 @@ CSRC = os.path.join(HERE, "csrc")
 BUILD = os.path.join(HERE, "_build")
 LIB = os.path.join(HERE, "libw4a16.so")
 
-HIP_SOURCES = ["prepack.hip", "gemm_small.hip", "gemm_tile.hip", "msd.hip", "moe.hip", "mxfp4.hip", "w8.hip", "fzero.hip"]
+HIP_SOURCES = ["prepack.hip", "gemm_small.hip", "gemm_tile.hip", "msd.hip", "moe.hip", "mxfp4.hip", "w8.hip", "fzero.hip",
+               "linear.hip", "linear_small.hip"]
 CPP_SOURCES = ["api.cpp"]
 ARCH = "gfx950"
 

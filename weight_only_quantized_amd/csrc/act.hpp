@@ -1,0 +1,141 @@
+// act.hpp — activations of the fused linear operators and what their kernels
+// share: the operand description, and the finishing step (bias, activation,
+// gated product, residual) applied to fp32 sums before the one rounding to
+// the activation dtype.
+#pragma once
+
+#include "common.hpp"
+#include "launch.hpp"
+
+namespace w4 {
+
+// e^x by the hardware's base-2 exponential.  The argument's rounding costs
+// |x| 2^-24 relative, far below the 16-bit rounding of every result.
+__device__ __forceinline__ float exp_fast(float x) { return __builtin_amdgcn_exp2f(x * 1.4426950408889634f); }
+
+// 1 / (1 + e^-x); e^-x = inf gives exactly 0.
+__device__ __forceinline__ float sigmoid_fast(float x) { return __builtin_amdgcn_rcpf(1.0f + exp_fast(-x)); }
+
+constexpr float kInvSqrt2 = 0.70710678118654752f;
+constexpr float kGeluC0 = 0.79788456080286536f;   // sqrt(2 / pi)
+constexpr float kGeluC1 = 0.044715f;
+
+// act(v).  GELU_TANH uses (1 + tanh(y)) / 2 = sigmoid(2 y).
+template <int V>
+__device__ __forceinline__ void act_fwd(float (&v)[V], int act) {
+    if (act == ACT_RELU) {
+#pragma unroll
+        for (int i = 0; i < V; ++i) v[i] = v[i] < 0.f ? 0.f : v[i];     // keeps NaN
+    } else if (act == ACT_SILU) {
+#pragma unroll
+        for (int i = 0; i < V; ++i) v[i] *= sigmoid_fast(v[i]);
+    } else if (act == ACT_GELU) {
+#pragma unroll
+        for (int i = 0; i < V; ++i) v[i] = 0.5f * v[i] * (1.0f + erff(v[i] * kInvSqrt2));
+    } else if (act == ACT_GELU_TANH) {
+#pragma unroll
+        for (int i = 0; i < V; ++i)
+            v[i] *= sigmoid_fast(2.0f * kGeluC0 * (v[i] + kGeluC1 * v[i] * v[i] * v[i]));
+    }
+}
+
+// f = act(v), d = act'(v) (0 at v = 0 for RELU).
+__device__ __forceinline__ void act_both(float v, int act, float &f, float &d) {
+    f = v;
+    d = 1.f;
+    if (act == ACT_RELU) {
+        f = v < 0.f ? 0.f : v;
+        d = v > 0.f ? 1.f : (v <= 0.f ? 0.f : v);                       // NaN stays NaN
+    } else if (act == ACT_SILU) {
+        const float s = sigmoid_fast(v);
+        f = v * s;
+        d = s * (1.0f + v * (1.0f - s));
+    } else if (act == ACT_GELU) {
+        const float cdf = 0.5f * (1.0f + erff(v * kInvSqrt2));
+        f = v * cdf;
+        d = cdf + v * exp_fast(-0.5f * v * v) * (0.5f * kInvSqrt2 * 1.12837916709551257f);
+    } else if (act == ACT_GELU_TANH) {
+        // |v| > 30: the sigmoid is exactly 0 or 1 long before, and the
+        // clamped polynomial cannot overflow (NaN passes both comparisons)
+        const float c = v > 30.f ? 30.f : (v < -30.f ? -30.f : v);
+        const float s = sigmoid_fast(2.0f * kGeluC0 * (c + kGeluC1 * c * c * c));
+        f = v * s;
+        d = s + c * s * (1.0f - s) * 2.0f * kGeluC0 * (1.0f + 3.0f * kGeluC1 * c * c);
+    }
+}
+
+// V consecutive 16-bit values to and from fp32.  V = 8 is one 16-byte access.
+template <int DT, int V>
+__device__ __forceinline__ void load_vec(const uint16_t *p, float (&v)[V]) {
+    if constexpr (V == 8) {
+        const u32x4_t w = ld128(p);
+#pragma unroll
+        for (int q = 0; q < 4; ++q) {
+            const uint32_t word = w[q];
+            v[2 * q] = h2f<DT>((uint16_t)(word & 0xFFFFu));
+            v[2 * q + 1] = h2f<DT>((uint16_t)(word >> 16));
+        }
+    } else {
+#pragma unroll
+        for (int i = 0; i < V; ++i) v[i] = h2f<DT>(p[i]);
+    }
+}
+template <int DT, int V>
+__device__ __forceinline__ void store_vec(uint16_t *p, const float (&v)[V]) {
+    if constexpr (V == 8) {
+        u32x4_t w;
+#pragma unroll
+        for (int q = 0; q < 4; ++q)
+            w[q] = (uint32_t)f2h<DT>(v[2 * q]) | (uint32_t)f2h<DT>(v[2 * q + 1]) << 16;
+        *reinterpret_cast<u32x4_t *>(p) = w;
+    } else {
+#pragma unroll
+        for (int i = 0; i < V; ++i) p[i] = f2h<DT>(v[i]);
+    }
+}
+
+// y = act(v + bias) + residual for V columns of one row; pre gets v + bias.
+template <int DT, int V>
+__device__ __forceinline__ void finish_ep(const LinArgs &p, float (&v)[V], int64_t row, int64_t col) {
+    if (p.bias) {
+        float b[V];
+        load_vec<DT, V>(p.bias + col, b);
+#pragma unroll
+        for (int i = 0; i < V; ++i) v[i] += b[i];
+    }
+    if (p.pre) store_vec<DT, V>(p.pre + row * p.cols + col, v);
+    act_fwd<V>(v, p.act);
+    if (p.res) {
+        float r[V];
+        load_vec<DT, V>(p.res + row * p.ldr + col, r);
+#pragma unroll
+        for (int i = 0; i < V; ++i) v[i] += r[i];
+    }
+    store_vec<DT, V>(p.y + row * p.ldy + col, v);
+}
+
+// a = act(g + bias_g) * (u + bias_u) for V of the I = cols / 2 columns of one
+// row; pre gets both biased sums (the gate half first).
+template <int DT, int V>
+__device__ __forceinline__ void finish_glu(const LinArgs &p, float (&g)[V], float (&u)[V], int64_t row, int64_t col) {
+    const int64_t I = p.cols / 2;
+    if (p.bias) {
+        float b[V];
+        load_vec<DT, V>(p.bias + col, b);
+#pragma unroll
+        for (int i = 0; i < V; ++i) g[i] += b[i];
+        load_vec<DT, V>(p.bias + I + col, b);
+#pragma unroll
+        for (int i = 0; i < V; ++i) u[i] += b[i];
+    }
+    if (p.pre) {
+        store_vec<DT, V>(p.pre + row * p.cols + col, g);
+        store_vec<DT, V>(p.pre + row * p.cols + I + col, u);
+    }
+    act_fwd<V>(g, p.act);
+#pragma unroll
+    for (int i = 0; i < V; ++i) g[i] *= u[i];
+    store_vec<DT, V>(p.y + row * p.ldy + col, g);
+}
+
+}  // namespace w4

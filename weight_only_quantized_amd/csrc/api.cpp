@@ -127,7 +127,7 @@ const char *w4a16_status_str(int status) {
         case W4A16_ERR_SHAPE: return "W4A16_ERR_SHAPE: sizes violate K>0, K%128==0, N>0, N%64==0, M>=0, E>=1";
         case W4A16_ERR_UNSUPPORTED: return "W4A16_ERR_UNSUPPORTED: group_size must be 32, 64 or a multiple of 128 (MSD and the MoE chain: 128; W8A16 and floating-point zero points: a multiple of 128), dtype F16 or BF16 (MSD: F16)";
         case W4A16_ERR_ALIGN: return "W4A16_ERR_ALIGN: x, w_packed, workspace need 16-byte, scale and y 2-byte alignment";
-        case W4A16_ERR_WORKSPACE: return "W4A16_ERR_WORKSPACE: MSD workspace is NULL or smaller than w4a16_msd_workspace_bytes()";
+        case W4A16_ERR_WORKSPACE: return "W4A16_ERR_WORKSPACE: workspace is NULL or smaller than the call's workspace query";
         case W4A16_ERR_DEVICE: return "W4A16_ERR_DEVICE: current device is not gfx950 or a launch failed";
         case W4A16_ERR_SCRATCH:
             return "W4A16_ERR_SCRATCH: the problem needs more workspace than the library's static scratch "
@@ -352,6 +352,175 @@ w4a16_status w4a16_fused_moe(const void *x, const int32_t *topk_ids, const float
     if (current_device_ok() != 1) return W4A16_ERR_DEVICE;
     return map_err(w4::launch_fused_moe(x, topk_ids, topk_w, w13_packed, s13, z13, w2_packed, s2, z2, out, T, topk,
                                         E, H, I, dt, workspace, (hipStream_t)stream));
+}
+
+// ---- Fused linear operators --------------------------------------------------
+
+}  // extern "C"
+
+namespace {
+
+w4a16_status check_linear(const w4a16_linear *lin, bool glu, int *gm) {
+    if (!lin) return W4A16_ERR_NULL;
+    w4a16_status st = check_kn_groups(lin->K, lin->N, lin->group_size, gm);
+    if (st != W4A16_OK) return st;
+    return glu && lin->N % 128 != 0 ? W4A16_ERR_SHAPE : W4A16_OK;
+}
+
+bool rows_ok(int64_t M) { return M >= 0 && M <= (int64_t(1) << 31) - 1; }
+
+// Row stride: 0 takes the row length.
+w4a16_status check_ld(int64_t *ld, int64_t width) {
+    if (*ld == 0) *ld = width;
+    if (*ld < width || *ld > (int64_t(1) << 31)) return W4A16_ERR_SHAPE;
+    return *ld % 8 == 0 ? W4A16_OK : W4A16_ERR_ALIGN;
+}
+
+w4a16_status linear_forward(bool glu, const void *x, int64_t ldx, const w4a16_linear *lin, int act,
+                            const void *residual, int64_t ldr, void *pre, void *y, int64_t ldy, int64_t M, int dt,
+                            void *workspace, size_t workspace_bytes, void *stream) {
+    if (!dt_ok(dt) || act < W4A16_ACT_NONE || act > W4A16_ACT_GELU_TANH) return W4A16_ERR_UNSUPPORTED;
+    int gm = 1;
+    w4a16_status st = check_linear(lin, glu, &gm);
+    if (st != W4A16_OK) return st;
+    if (!rows_ok(M)) return W4A16_ERR_SHAPE;
+    const int64_t width = glu ? lin->N / 2 : lin->N;
+    if ((st = check_ld(&ldx, lin->K)) != W4A16_OK || (st = check_ld(&ldy, width)) != W4A16_OK ||
+        (st = check_ld(&ldr, width)) != W4A16_OK)
+        return st;
+    if (M == 0) return W4A16_OK;
+    if (!x || !lin->w_packed || !lin->scale || !y) return W4A16_ERR_NULL;
+    const int mode = glu ? w4::LIN_GLU : w4::LIN_EP;
+    const size_t need = w4::lin_workspace_bytes(mode, M, lin->K, lin->N);
+    if (need > 0 && (!workspace || workspace_bytes < need)) return W4A16_ERR_WORKSPACE;
+    if (!aligned(x, 16) || !aligned(lin->w_packed, 16) || !aligned(lin->scale, 2) || !aligned(lin->bias, 16) ||
+        !aligned(residual, 16) || !aligned(pre, 16) || !aligned(y, 16) || !aligned(workspace, 16))
+        return W4A16_ERR_ALIGN;
+    if (current_device_ok() != 1) return W4A16_ERR_DEVICE;
+    w4::LinArgs p{};
+    p.a = (const uint16_t *)x;
+    p.lda = ldx;
+    p.wp = (const uint8_t *)lin->w_packed;
+    p.scale = (const uint16_t *)lin->scale;
+    p.zero = (const uint8_t *)lin->zero;
+    p.M = M;
+    p.K = lin->K;
+    p.N = p.cols = lin->N;
+    p.gm = gm;
+    p.act = act;
+    p.bias = (const uint16_t *)lin->bias;
+    p.res = (const uint16_t *)residual;
+    p.ldr = ldr;
+    p.pre = (uint16_t *)pre;
+    p.y = (uint16_t *)y;
+    p.ldy = ldy;
+    return map_err(w4::launch_lin(mode, p, dt, workspace, (hipStream_t)stream));
+}
+
+// Backward workspace: the column sums' partial rows, then the product's slices.
+size_t dact_bytes(int64_t M, int64_t N) { return (w4::lin_dact_workspace_bytes(M, N) + 255) / 256 * 256; }
+size_t backward_bytes(int64_t M, int64_t K, int64_t N) {
+    return dact_bytes(M, N) + w4::lin_workspace_bytes(w4::LIN_T, M, K, N);
+}
+
+w4a16_status linear_backward(bool glu, const void *dy, int64_t lddy, const void *h, const w4a16_linear *lin, int act,
+                             const void *addend, int64_t ldadd, void *d, float *dbias, void *dx, int64_t lddx,
+                             int64_t M, int dt, void *workspace, size_t workspace_bytes, void *stream) {
+    if (!dt_ok(dt) || act < W4A16_ACT_NONE || act > W4A16_ACT_GELU_TANH) return W4A16_ERR_UNSUPPORTED;
+    int gm = 1;
+    w4a16_status st = check_linear(lin, glu, &gm);
+    if (st != W4A16_OK) return st;
+    if (!rows_ok(M)) return W4A16_ERR_SHAPE;
+    const int64_t K = lin->K, N = lin->N;
+    if ((st = check_ld(&lddy, glu ? N / 2 : N)) != W4A16_OK || (st = check_ld(&lddx, K)) != W4A16_OK ||
+        (st = check_ld(&ldadd, K)) != W4A16_OK)
+        return st;
+    if (!aligned(dbias, 4)) return W4A16_ERR_ALIGN;
+    if (M == 0 && !dbias) return W4A16_OK;
+    const bool through = glu || act != W4A16_ACT_NONE;      // the product reads d, not dy
+    if (M > 0) {
+        if (!dy || !lin->w_packed || !lin->scale || !dx || (through && (!h || !d))) return W4A16_ERR_NULL;
+        const size_t need = backward_bytes(M, K, N);
+        if (!workspace || workspace_bytes < need) return W4A16_ERR_WORKSPACE;
+        if (!aligned(dy, 16) || !aligned(lin->w_packed, 16) || !aligned(lin->scale, 2) || !aligned(addend, 16) ||
+            (through && (!aligned(h, 16) || !aligned(d, 16))) || !aligned(dx, 16) || !aligned(workspace, 16))
+            return W4A16_ERR_ALIGN;
+    }
+    if (current_device_ok() != 1) return W4A16_ERR_DEVICE;
+    hipStream_t s = (hipStream_t)stream;
+    if (through || dbias) {
+        hipError_t err = w4::launch_lin_dact(glu, (const uint16_t *)dy, lddy, (const uint16_t *)h, (uint16_t *)d,
+                                             dbias, M, N, act, dt, workspace, s);
+        if (err != hipSuccess) return map_err(err);
+    }
+    if (M == 0) return W4A16_OK;
+    w4::LinArgs p{};
+    p.a = (const uint16_t *)(through ? d : dy);
+    p.lda = through ? N : lddy;
+    p.wp = (const uint8_t *)lin->w_packed;
+    p.scale = (const uint16_t *)lin->scale;
+    p.zero = (const uint8_t *)lin->zero;
+    p.M = M;
+    p.K = p.cols = K;
+    p.N = N;
+    p.gm = gm;
+    p.act = W4A16_ACT_NONE;
+    p.res = (const uint16_t *)addend;
+    p.ldr = ldadd;
+    p.y = (uint16_t *)dx;
+    p.ldy = lddx;
+    return map_err(w4::launch_lin(w4::LIN_T, p, dt, (uint8_t *)workspace + dact_bytes(M, N), s));
+}
+
+size_t linear_bytes(const w4a16_linear *lin, int64_t M, bool glu, bool backward) {
+    int gm = 1;
+    if (check_linear(lin, glu, &gm) != W4A16_OK || !rows_ok(M) || M == 0) return 0;
+    if (backward) return backward_bytes(M, lin->K, lin->N);
+    return w4::lin_workspace_bytes(glu ? w4::LIN_GLU : w4::LIN_EP, M, lin->K, lin->N);
+}
+
+}  // namespace
+
+extern "C" {
+
+size_t w4a16_gemm_ep_workspace_bytes(const w4a16_linear *lin, int64_t M) { return linear_bytes(lin, M, false, false); }
+
+w4a16_status w4a16_gemm_ep(const void *x, int64_t ldx, const w4a16_linear *lin, int act, const void *residual,
+                           int64_t ldr, void *pre, void *y, int64_t ldy, int64_t M, int dt, void *workspace,
+                           size_t workspace_bytes, void *stream) {
+    return linear_forward(false, x, ldx, lin, act, residual, ldr, pre, y, ldy, M, dt, workspace, workspace_bytes,
+                          stream);
+}
+
+size_t w4a16_gemm_ep_backward_workspace_bytes(const w4a16_linear *lin, int64_t M) {
+    return linear_bytes(lin, M, false, true);
+}
+
+w4a16_status w4a16_gemm_ep_backward(const void *dy, int64_t lddy, const void *pre, const w4a16_linear *lin, int act,
+                                    const void *addend, int64_t ldadd, void *dpre, float *dbias, void *dx,
+                                    int64_t lddx, int64_t M, int dt, void *workspace, size_t workspace_bytes,
+                                    void *stream) {
+    return linear_backward(false, dy, lddy, pre, lin, act, addend, ldadd, dpre, dbias, dx, lddx, M, dt, workspace,
+                           workspace_bytes, stream);
+}
+
+size_t w4a16_glu_gemm_workspace_bytes(const w4a16_linear *lin, int64_t M) { return linear_bytes(lin, M, true, false); }
+
+w4a16_status w4a16_glu_gemm(const void *x, int64_t ldx, const w4a16_linear *lin, int act, void *h, void *a,
+                            int64_t lda, int64_t M, int dt, void *workspace, size_t workspace_bytes, void *stream) {
+    return linear_forward(true, x, ldx, lin, act, nullptr, 0, h, a, lda, M, dt, workspace, workspace_bytes, stream);
+}
+
+size_t w4a16_glu_gemm_backward_workspace_bytes(const w4a16_linear *lin, int64_t M) {
+    return linear_bytes(lin, M, true, true);
+}
+
+w4a16_status w4a16_glu_gemm_backward(const void *da, int64_t ldda, const void *h, const w4a16_linear *lin, int act,
+                                     const void *addend, int64_t ldadd, void *dh, float *dbias, void *dx,
+                                     int64_t lddx, int64_t M, int dt, void *workspace, size_t workspace_bytes,
+                                     void *stream) {
+    return linear_backward(true, da, ldda, h, lin, act, addend, ldadd, dh, dbias, dx, lddx, M, dt, workspace,
+                           workspace_bytes, stream);
 }
 
 // ---- test hooks -------------------------------------------------------------

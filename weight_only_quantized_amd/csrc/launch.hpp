@@ -150,4 +150,43 @@ size_t fzero_workspace_bytes(int64_t M, int64_t K, int64_t N, int64_t gs);
 hipError_t launch_fzero_corr(const void *x, const void *scale, const void *zf, int64_t M, int64_t K, int64_t N,
                              int64_t gs, int bits, int dt, void *workspace, float **corr, hipStream_t stream);
 
+// Fused linear operators (epilogue products, gated products, their backward
+// passes).  One description serves every kernel of a call:
+//   forward     A = x [M][K], columns = N of W, y = finish(x . W)
+//   transposed  A = d [M][N], columns = K of W, y = d . W^T + res
+enum { ACT_NONE = 0, ACT_RELU = 1, ACT_SILU = 2, ACT_GELU = 3, ACT_GELU_TANH = 4 };
+enum { LIN_EP = 0, LIN_GLU = 1, LIN_T = 2 };
+struct LinArgs {
+    const uint16_t *a;          // A operand, row stride lda
+    int64_t lda;
+    const uint8_t *wp;          // prepacked W [K][N] (standard layout)
+    const uint16_t *scale;      // [K/(128 gm)][N]
+    const uint8_t *zero;        // [K/(128 gm)][N/2] or NULL
+    int64_t M, K, N;
+    int64_t cols;               // columns of the product: N, or K when transposed
+    int gm;                     // 128-row groups per scale group
+    int act;
+    const uint16_t *bias;       // [N] or NULL (forward)
+    const uint16_t *res;        // residual / addend, row stride ldr, or NULL
+    int64_t ldr;
+    uint16_t *pre;              // biased sums [M][N] or NULL (forward)
+    uint16_t *y;                // result, row stride ldy
+    int64_t ldy;
+    float *part;                // partial sums [slices][M][cols] (slices > 1)
+    int slices, stages;         // stages per slice
+    int mtiles, ntiles;
+};
+// Workspace of a product (partial sums of its slices), 0 if it runs in one.
+size_t lin_workspace_bytes(int mode, int64_t M, int64_t K, int64_t N);
+hipError_t launch_lin(int mode, LinArgs p, int dt, void *workspace, hipStream_t stream);
+// The decode-sized forward kernel (EP, GLU).
+bool lin_small_ok(int mode, int64_t M, int64_t K, int64_t N);
+hipError_t launch_lin_small(int mode, const LinArgs &p, int dt, hipStream_t stream);
+// d = gradient of the pre-activation h (glu: both halves), and its column
+// sums in fp32.  d is written unless act == NONE without a gate; colsum may be
+// NULL; part: lin_dact_workspace_bytes() of scratch (used with colsum only).
+size_t lin_dact_workspace_bytes(int64_t M, int64_t N);
+hipError_t launch_lin_dact(bool glu, const uint16_t *dy, int64_t lddy, const uint16_t *h, uint16_t *d, float *colsum,
+                           int64_t M, int64_t N, int act, int dt, void *part, hipStream_t stream);
+
 }  // namespace w4

@@ -443,15 +443,15 @@ w4a16_status w4a8_mxfp4_grouped_gemm(const void *x, const int32_t *expert_offset
  *
  * Shared rules, on top of the conventions at the top of this file:
  *  - w4a16_linear describes one weight matrix and is read during the call
- *    only.  group_size is a multiple of 128 dividing K (weights from
+ *    only.  K and N are at most 2^22, K * N at most 2^32.  group_size is a multiple of 128 dividing K (weights from
  *    w4a16_prepack, or w4a16_prepack_g with such a group size).
  *  - act: one of w4a16_act, applied in fp32:
  *      NONE v;  RELU max(v, 0) (derivative 0 at 0);  SILU v / (1 + exp(-v));
  *      GELU v (1 + erf(v / sqrt 2)) / 2;
  *      GELU_TANH v (1 + tanh(sqrt(2/pi) (v + 0.044715 v^3))) / 2.
  *  - 16-bit tensors other than scale are 16-byte aligned, scale 2, dbias 4.
- *    A row stride (ld...) counts elements, is a multiple of 8 and at least
- *    the row length; 0 means rows without gaps.  Saved pre-activations and
+ *    A row stride (ld...) counts elements, is a multiple of 8, at least the
+ *    row length and at most 2^22; 0 means rows without gaps.  Saved pre-activations and
  *    their gradients (pre, h, dpre, dh) and dbias have no gaps.
  *  - x must be finite for a finite result row (the bf16 decode kernel gives
  *    NaN, not infinity, in the row of an infinite x).

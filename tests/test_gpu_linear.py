@@ -383,7 +383,7 @@ def test_on_another_stream_and_in_a_graph():
 def test_offsets_past_32_bits():
     """Rows whose element offsets pass 2^31 and byte offsets 2^32: a wide
     stride, few rows."""
-    M, K, N, ld = 130, 128, 64, 1 << 25
+    M, K, N, ld = 1040, 128, 64, 1 << 22
     L = ref.layer(K, N, 128, F16, False, seed=3)
     D = Dev(L)
     big = torch.empty(M * ld, dtype=torch.float16, device=DEV)           # 8.7 GB

@@ -360,10 +360,15 @@ w4a16_status w4a16_fused_moe(const void *x, const int32_t *topk_ids, const float
 
 namespace {
 
+constexpr int64_t kLinMaxLd = int64_t(1) << 22;
+
 w4a16_status check_linear(const w4a16_linear *lin, bool glu, int *gm) {
     if (!lin) return W4A16_ERR_NULL;
     w4a16_status st = check_kn_groups(lin->K, lin->N, lin->group_size, gm);
     if (st != W4A16_OK) return st;
+    // the tile kernels address a weight matrix and 256 operand rows with 32-bit
+    // byte offsets
+    if (lin->K > kLinMaxLd || lin->N > kLinMaxLd || lin->K * lin->N > (int64_t(1) << 32)) return W4A16_ERR_SHAPE;
     return glu && lin->N % 128 != 0 ? W4A16_ERR_SHAPE : W4A16_OK;
 }
 
@@ -372,7 +377,7 @@ bool rows_ok(int64_t M) { return M >= 0 && M <= (int64_t(1) << 31) - 1; }
 // Row stride: 0 takes the row length.
 w4a16_status check_ld(int64_t *ld, int64_t width) {
     if (*ld == 0) *ld = width;
-    if (*ld < width || *ld > (int64_t(1) << 31)) return W4A16_ERR_SHAPE;
+    if (*ld < width || *ld > kLinMaxLd) return W4A16_ERR_SHAPE;
     return *ld % 8 == 0 ? W4A16_OK : W4A16_ERR_ALIGN;
 }
 

@@ -1,5 +1,7 @@
 // linear.hip — products of the fused linear operators on tiles of 256 columns:
 // forward (x . W with its epilogue, plain or gated) and transposed (d . W^T).
+#include <type_traits>
+
 #include "act.hpp"
 
 namespace w4 {
@@ -7,7 +9,7 @@ namespace w4 {
 constexpr int kXcd = 8;              // XCDs; workgroups go to them round-robin
 constexpr int kBK = 64;              // contraction elements per stage
 constexpr int kWideN = 256;          // columns per workgroup
-constexpr int kTRow = 576;           // LDS row stride (bytes) of the transposed W tile
+constexpr int kTRow = kWideN * 2;    // LDS row (bytes) of the transposed W tile
 
 typedef short v4s_t __attribute__((__vector_size__(8)));
 typedef v4s_t __attribute__((address_space(3))) *lds_v4s_ptr;
@@ -17,6 +19,32 @@ typedef v4s_t __attribute__((address_space(3))) *lds_v4s_ptr;
 // and lane i gets column i.
 __device__ __forceinline__ u32x2_t lds_tr16(const uint8_t *p) {
     return __builtin_bit_cast(u32x2_t, __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_v4s_ptr)(v4s_t *)(uint8_t *)p));
+}
+
+// LDS swizzles: 16-byte chunk c of row r sits at chunk c ^ key(r) of its row.
+// Writes move 128 bytes a cycle (8 lanes), 16-byte reads 256 (16 lanes).
+// Rows of 128 bytes (A, forward W; read and written down 16 and 8 rows at one
+// c): 8 consecutive rows get different chunks, and rows 8 apart, which share a
+// 128-byte half, too.
+__device__ __forceinline__ int key_row(int r) { return (r & 7) ^ ((r >> 3) & 1); }
+// Rows of 512 bytes (transposed W; written down 8 rows at one c, read as 4 rows
+// x 4 chunks): bits 2, 3 tell 4 rows apart for the reads, bits 0..2 tell 8 rows
+// apart for the writes.
+__device__ __forceinline__ int key_t(int n) { return (n & 3) << 2 | (n & 2) | ((n >> 2) & 1); }
+
+// Matrix-core step whose sources stay live past it (the destination must not
+// share their registers), without ordering it against memory operations.
+template <int DT>
+__device__ __forceinline__ f32x16_t mfma_step(const u32x4_t &a, const u32x4_t &b, const f32x16_t &c) {
+    f32x16_t r;
+    if constexpr (DT == DT_BF16)
+        r = __builtin_amdgcn_mfma_f32_32x32x16_bf16(__builtin_bit_cast(bf16x8_t, a), __builtin_bit_cast(bf16x8_t, b), c,
+                                                    0, 0, 0);
+    else
+        r = __builtin_amdgcn_mfma_f32_32x32x16_f16(__builtin_bit_cast(f16x8_t, a), __builtin_bit_cast(f16x8_t, b), c, 0,
+                                                   0, 0);
+    asm("" : "+v"(r) : "v"(a), "v"(b));
+    return r;
 }
 
 template <int DT, int MODE, int BM>
@@ -58,38 +86,34 @@ __global__ void __launch_bounds__(512, 2) lin_wide_kernel(const LinArgs p) {
     const int s0 = slice * p.stages, s1 = s0 + p.stages < nst ? s0 + p.stages : nst;
 
     // ---- A operand: BM rows of 64 elements per stage ------------------------------
-    const uint16_t *arow[XP];
-    int aoff[XP];
+    // (the rows of a thread are 64 apart: one LDS offset serves all)
+    const uint8_t *const abase = reinterpret_cast<const uint8_t *>(p.a + row0 * p.lda);
+    uint32_t aoff[XP];
+    const int ar_ = tid >> 3, ac_ = tid & 7;
 #pragma unroll
     for (int i = 0; i < XP; ++i) {
-        const int id16 = i * 512 + tid, r = id16 >> 3, c = id16 & 7;
-        const int64_t gr = row0 + r < p.M ? row0 + r : p.M - 1;
-        arow[i] = p.a + gr * p.lda + c * 8;
-        aoff[i] = r * (kBK * 2) + ((c ^ (r & 7)) << 4);
+        const int64_t r = row0 + i * 64 + ar_ < p.M ? i * 64 + ar_ : p.M - 1 - row0;
+        aoff[i] = (uint32_t)(r * p.lda + ac_ * 8) * 2u;
     }
+    uint8_t *const adst = lda_ + ar_ * (kBK * 2) + ((ac_ ^ key_row(ar_)) << 4);
     u32x4_t ar[XP];
-    auto load_a = [&](int s) {
-#pragma unroll
-        for (int i = 0; i < XP; ++i) ar[i] = ld128(arow[i] + (int64_t)s * kBK);
-    };
-    auto store_a = [&](int buf) {
-#pragma unroll
-        for (int i = 0; i < XP; ++i) *reinterpret_cast<u32x4_t *>(lda_ + buf * ABYTES + aoff[i]) = ar[i];
+    auto load_a = [&](int s, int i) { ar[i] = ld128(abase + (int64_t)s * (kBK * 2) + aoff[i]); };
+    auto store_a = [&](int buf, int i) {
+        *reinterpret_cast<u32x4_t *>(adst + buf * ABYTES + i * 64 * (kBK * 2)) = ar[i];
     };
 
     // ---- W operand: one 16-byte slot (32 rows of one column) per thread -----------
-    const int j = lane & 15;
-    const uint8_t *wptr;
-    const uint16_t *sptr;
+    const int j = lane & 15, c32 = T ? lane >> 4 : (lane >> 4) & 1;
     // without zero points the scales' own bytes are read and ignored: no branch
     // around a load
-    const uint8_t *zptr = p.zero ? p.zero : reinterpret_cast<const uint8_t *>(p.scale);
-    int64_t wstep;
-    int boff[4];
+    const uint8_t *const zbase = p.zero ? p.zero : reinterpret_cast<const uint8_t *>(p.scale);
+    uint32_t woff, soff;                              // bytes into W, columns into the scales
+    int64_t wstep;                                    // bytes of W per stage
+    uint32_t bdst;                                    // LDS byte of word 0; word t is at bdst ^ 16 t
     int wcol = 0;                                     // forward: column within the tile
-    int64_t ncol = 0;                                 // forward: column of W
+    int64_t srow_t = 0;                               // transposed: scale row of this wave's 128 outputs
     if constexpr (!T) {
-        const int cb = 2 * wave + (lane >> 5), c32 = (lane >> 4) & 1;
+        const int cb = 2 * wave + (lane >> 5);
         int64_t nb;
         if constexpr (MODE == LIN_GLU) {
             // 4 blocks per consuming wave: two gate, then the two up blocks of the same columns
@@ -102,93 +126,96 @@ __global__ void __launch_bounds__(512, 2) lin_wide_kernel(const LinArgs p) {
             if (nb >= p.cols / 16) nb = p.cols / 16 - 1;
         }
         wcol = cb * 16 + j;
-        ncol = nb * 16 + j;
-        wptr = p.wp + nb * G * kTileBytes + c32 * 256 + j * 16;
+        woff = (uint32_t)(nb * G * kTileBytes) + c32 * 256 + j * 16;
         wstep = 512;
-        sptr = p.scale + ncol;
-        zptr += ncol >> 1;
-#pragma unroll
-        for (int t = 0; t < 4; ++t) boff[t] = wcol * (kBK * 2) + (((4 * c32 + t) ^ (wcol & 7)) << 4);
+        soff = (uint32_t)(nb * 16 + j);
+        bdst = wcol * (kBK * 2) + (((4 * c32) ^ key_row(wcol)) << 4);
     } else {
-        const int nbi = wave & 3, gi = wave >> 2, c32 = lane >> 4;
+        const int nbi = wave & 3, gi = wave >> 2;
         int64_t g = nt * 2 + gi;
         if (g >= G) g = G - 1;
-        wptr = p.wp + (nbi * G + g) * kTileBytes + lane * 16;
+        woff = (uint32_t)((nbi * G + g) * kTileBytes) + lane * 16;
         wstep = 4 * G * kTileBytes;
-        sptr = p.scale + g / p.gm * p.N + nbi * 16 + j;
-        zptr += (g / p.gm * p.N + nbi * 16 + j) >> 1;
+        srow_t = g / p.gm * p.N;
         const int n = nbi * 16 + j;
-#pragma unroll
-        for (int t = 0; t < 4; ++t) boff[t] = n * kTRow + (((gi * 16 + c32 * 4 + t) ^ ((n >> 2) & 1)) << 4);
+        soff = n;
+        bdst = n * kTRow + (((gi * 16 + c32 * 4) ^ key_t(n)) << 4);
     }
-    u32x4_t wr;
-    uint16_t sr;
-    uint8_t zr;
-    auto load_w = [&](int s) {
-        wr = ld128(wptr + (int64_t)s * wstep);
-        const int64_t so = T ? (int64_t)s * kBK : (int64_t)(s >> 1) / p.gm * p.N;
-        sr = sptr[so];
-        zr = zptr[so >> 1];
+    u32x4_t wr[2];                                    // raw codes of the next two stages
+    uint16_t sr[2];
+    uint8_t zr[2];
+    auto load_w = [&](int d, int s) {
+        wr[d] = ld128(p.wp + (int64_t)s * wstep + woff);
+        const int64_t so = T ? srow_t + (int64_t)s * kBK : (int64_t)((s >> 1) / p.gm) * p.N;
+        sr[d] = p.scale[so + soff];
+        zr[d] = zbase[(so + soff) >> 1];
     };
-    float se = 0.f;                                   // forward: scale the sums are held in
-    auto store_w = [&](int buf) {
-        const float s = h2f<DT>(sr);
-        const uint32_t z = p.zero ? __builtin_amdgcn_ubfe((uint32_t)zr, (uint32_t)(j & 1) * 4u, 4) : 8u;
-        uint8_t *base = ldb_ + buf * BBYTES;
-        float f = 1.f;
+    // Forward: the sums are held in units of the running scale se; a new scale
+    // group multiplies them by se / s first and its codes enter the matrix core
+    // as exact integers.  smax: largest scale so far.  A scale below 2^-60 of it (or
+    // below the normal range, 0 among them) leaves the unit alone and its codes
+    // enter as 0: what it would add is below 2^-60 of what the larger scale's
+    // codes weigh, and the sums stay far from overflow.
+    float se = 0.f, smax = 0.f;
+    struct Deq { float s, zs; uint32_t z, sel; } dq;
+    auto deq_begin = [&](int d, int buf) {
+        const float s = h2f<DT>(sr[d]);
+        const uint32_t z = p.zero ? __builtin_amdgcn_ubfe((uint32_t)zr[d], (uint32_t)(j & 1) * 4u, 4) : 8u;
+        bool live = true;
         if constexpr (!T) {
-            float ratio;
             const float as_ = __builtin_fabsf(s);
-            if (as_ >= 0x1p-60f * __builtin_fabsf(se) && as_ >= 0x1p-100f) {
-                ratio = se * __builtin_amdgcn_rcpf(s);
-                se = s;
-            } else {
-                if (se == 0.f) se = 1.f;
-                ratio = 1.f;
-                f = s * __builtin_amdgcn_rcpf(se);
-            }
-            if (((lane >> 4) & 1) == 0) s_ratio[buf][wcol] = ratio;
+            live = !(as_ < 0x1p-60f * smax) && !(as_ < 0x1p-126f);      // NaN stays
+            const float ratio = live && s != se ? se * __builtin_amdgcn_rcpf(s) : 1.f;
+            se = live ? s : se;
+            smax = live ? __builtin_fmaxf(smax, as_) : smax;
+            s_ratio[buf][wcol] = ratio;               // both lanes of a column write the same value
         }
-        const bool rare = !T && __any(f != 1.f);
+        dq.s = s;
+        dq.z = z;
+        const float zf = (float)z;
+        dq.zs = T ? -zf * s : zf;
+        // bf16: byte selector of the upper halves, or of zeros; fp16: mask
+        dq.sel = DT == DT_BF16 ? (live ? 0x07060302u : 0x0C0C0C0Cu) : (live ? ~0u : 0u);
+    };
+    // Half-word i of the slot (word i / 2): codes of rows 0, 1, 4, 5 or 2, 3, 6, 7
+    // of its 8; the second half writes the 16 bytes to LDS.
+    u32x4_t dqo;
+    auto deq_half = [&](int d, int buf, int i) {
+        const int t = i >> 1, hf = i & 1;
+        const uint32_t w = wr[d][t];
         if constexpr (DT == DT_BF16) {
-            const float zf = (float)z, zs = -zf * s;
+            // bytes: rows 0, 4, 1, 5 (or 2, 6, 3, 7).  The empty asm keeps the masked
+            // word whole, so that each byte is one conversion.
+            uint32_t m = (hf ? w >> 4 : w) & 0x0F0F0F0Fu;
+            asm("" : "+v"(m));
+            float v[4];
+            v[0] = (float)(m & 0xFFu), v[2] = (float)((m >> 8) & 0xFFu);
+            v[1] = (float)((m >> 16) & 0xFFu), v[3] = (float)(m >> 24);
 #pragma unroll
-            for (int t = 0; t < 4; ++t) {
-                const uint32_t w = wr[t];
-                const uint32_t lo = w & 0x0F0F0F0Fu, hi = (w >> 4) & 0x0F0F0F0Fu;
-                // bytes of lo: rows 0, 4, 1, 5; of hi: rows 2, 6, 3, 7
-                float v[8];
-                v[0] = (float)(lo & 0xFFu), v[4] = (float)((lo >> 8) & 0xFFu);
-                v[1] = (float)((lo >> 16) & 0xFFu), v[5] = (float)(lo >> 24);
-                v[2] = (float)(hi & 0xFFu), v[6] = (float)((hi >> 8) & 0xFFu);
-                v[3] = (float)((hi >> 16) & 0xFFu), v[7] = (float)(hi >> 24);
-#pragma unroll
-                for (int i = 0; i < 8; ++i) v[i] = T ? __builtin_fmaf(v[i], s, zs) : v[i] - zf;
-                if (rare) {
-#pragma unroll
-                    for (int i = 0; i < 8; ++i) v[i] *= f;
+            for (int q = 0; q < 2; ++q) {
+                if constexpr (T) {
+                    const bf16x2_t b = {(__bf16)__builtin_fmaf(v[2 * q], dq.s, dq.zs),
+                                        (__bf16)__builtin_fmaf(v[2 * q + 1], dq.s, dq.zs)};
+                    dqo[hf + 2 * q] = __builtin_bit_cast(uint32_t, b);
+                } else {
+                    // integers up to 15: exact in the upper 16 bits
+                    dqo[hf + 2 * q] = __builtin_amdgcn_perm(__float_as_uint(v[2 * q + 1] - dq.zs),
+                                                            __float_as_uint(v[2 * q] - dq.zs), dq.sel);
                 }
-                u32x4_t o;
-#pragma unroll
-                for (int q = 0; q < 4; ++q) {
-                    const bf16x2_t b = {(__bf16)v[2 * q], (__bf16)v[2 * q + 1]};
-                    o[q] = __builtin_bit_cast(uint32_t, b);
-                }
-                *reinterpret_cast<u32x4_t *>(base + boff[t]) = o;
             }
-        } else {
-            const _Float16 m = (_Float16)(T ? s : f);
-            const f16x2_t m2 = {m, m};
+        } else if (hf) {
+            dqo = dequant_word<DT>(w, f16_negbias2(dq.z));
+            if constexpr (T) {
+                const _Float16 m = (_Float16)dq.s;
+                const f16x2_t m2 = {m, m};
 #pragma unroll
-            for (int t = 0; t < 4; ++t) {
-                u32x4_t o = dequant_word<DT>(wr[t], f16_negbias2(z));
-                if (T || rare) {
+                for (int q = 0; q < 4; ++q) dqo[q] = __builtin_bit_cast(uint32_t, as<f16x2_t>(dqo[q]) * m2);
+            } else {
 #pragma unroll
-                    for (int q = 0; q < 4; ++q) o[q] = __builtin_bit_cast(uint32_t, as<f16x2_t>(o[q]) * m2);
-                }
-                *reinterpret_cast<u32x4_t *>(base + boff[t]) = o;
+                for (int q = 0; q < 4; ++q) dqo[q] &= dq.sel;
             }
         }
+        if (hf) *reinterpret_cast<u32x4_t *>(ldb_ + buf * BBYTES + (bdst ^ (uint32_t)(t << 4))) = dqo;
     };
 
     // ---- main loop ---------------------------------------------------------------
@@ -200,80 +227,143 @@ __global__ void __launch_bounds__(512, 2) lin_wide_kernel(const LinArgs p) {
 #pragma unroll
             for (int r = 0; r < 16; ++r) acc[rt][ct][r] = 0.f;
 
-    const int abase = (wm * (BM / 2) + l31) * (kBK * 2);
+    const int rkey = key_row(l31);                    // (every row base is a multiple of 16)
+    const uint8_t *const afrag = lda_ + (wm * (BM / 2) + l31) * (kBK * 2);
     auto frag_a = [&](int buf, int rt, int t) {
-        return *reinterpret_cast<const u32x4_t *>(lda_ + buf * ABYTES + abase + rt * 32 * (kBK * 2) +
-                                                  (((2 * t + kg) ^ (lane & 7)) << 4));
+        return *reinterpret_cast<const u32x4_t *>(afrag + buf * ABYTES + rt * 32 * (kBK * 2) +
+                                                  (((2 * t + kg) ^ rkey) << 4));
     };
-    const int qq = lane >> 4, tr = (lane & 15) >> 2, tc = lane & 3;
+    const uint8_t *bfrag[T ? CT : 1][2];
+    if constexpr (T) {
+        const int qq = lane >> 4, tr = (lane & 15) >> 2, tc = lane & 3;
+#pragma unroll
+        for (int ct = 0; ct < CT; ++ct)
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+                const int n = 8 * (qq >> 1) + 4 * h + tr, ch = wn * 8 + ct * 4 + 2 * (qq & 1) + (tc >> 1);
+                bfrag[ct][h] = ldb_ + n * kTRow + ((ch ^ key_t(n)) << 4) + (tc & 1) * 8;
+            }
+    } else {
+        bfrag[0][0] = ldb_ + (wn * 64 + l31) * (kBK * 2);
+    }
     auto frag_b = [&](int buf, int ct, int t) -> u32x4_t {
         if constexpr (!T) {
-            const int col = wn * 64 + ct * 32 + l31;
-            return *reinterpret_cast<const u32x4_t *>(ldb_ + buf * BBYTES + col * (kBK * 2) +
-                                                      (((2 * t + kg) ^ (lane & 7)) << 4));
+            return *reinterpret_cast<const u32x4_t *>(bfrag[0][0] + buf * BBYTES + ct * 32 * (kBK * 2) +
+                                                      (((2 * t + kg) ^ rkey) << 4));
         } else {
-            const int n = 16 * t + 8 * (qq >> 1) + tr;
-            const int ch = wn * 8 + ct * 4 + 2 * (qq & 1) + (tc >> 1);
-            const uint8_t *b = ldb_ + buf * BBYTES + n * kTRow + (tc & 1) * 8;
-            const u32x2_t x0 = lds_tr16(b + (ch << 4)), x1 = lds_tr16(b + 4 * kTRow + ((ch ^ 1) << 4));
+            const int o = buf * BBYTES + 16 * t * kTRow;
+            const u32x2_t x0 = lds_tr16(bfrag[ct][0] + o), x1 = lds_tr16(bfrag[ct][1] + o);
             return u32x4_t{x0[0], x0[1], x1[0], x1[1]};
         }
     };
 
-    if (s0 < s1) {
-        load_a(s0);
-        load_w(s0);
-        store_a(0);
-        store_w(0);
-        const int sn = s0 + 1 < s1 ? s0 + 1 : s0;
-        load_a(sn);
-        load_w(sn);
-        __syncthreads();
-        for (int s = s0; s < s1; ++s) {
-            const int buf = (s - s0) & 1;
-            if constexpr (!T) {
-                if (s == s0 || s % (2 * p.gm) == 0) {
-                    float rr[CT];
+    // One stage: 4 steps of RT x CT products from buffer `buf`, while the next
+    // stage's operands (in registers) go to the other buffer and the loads of
+    // the one after are issued.  The one barrier stands before the last step's
+    // products: by then every wave has read all of this buffer and written all
+    // of the other, and the products still to be issued cover the barrier and
+    // the first operand reads of the next stage.  A step is cut into slices of
+    // one row tile (CT products), each with its share of the vector work, and
+    // the scheduler may not move work between slices: left alone it gathers the
+    // vector work in front of the products, where both waves of a SIMD then wait
+    // for the vector unit and later for the matrix core.
+    u32x4_t fa[RT], fb[2][CT];
+    float rr[CT];
+    auto scale_tiles = [&](int i0, int i1) {
 #pragma unroll
-                    for (int ct = 0; ct < CT; ++ct) rr[ct] = s_ratio[buf][wn * 64 + ct * 32 + l31];
+        for (int i = i0; i < i1; ++i)
 #pragma unroll
-                    for (int rt = 0; rt < RT; ++rt)
+            for (int r = 0; r < 16; ++r) acc[i / CT][i % CT][r] *= rr[i % CT];
+    };
+    auto stage = [&](auto bufc, int s) {
+        constexpr int buf = decltype(bufc)::value;
+        constexpr int HW = 4 / RT;                    // half-words per slice of steps 1 and 2
+        const int sl = s + 2 < s1 ? s + 2 : s1 - 1;
 #pragma unroll
-                        for (int ct = 0; ct < CT; ++ct)
+        for (int t = 0; t < 4; ++t) {
+            if (t == 3) __syncthreads();
+            const int nbuf = t < 3 ? buf : buf ^ 1, tn = (t + 1) & 3;
 #pragma unroll
-                            for (int r = 0; r < 16; ++r) acc[rt][ct][r] *= rr[ct];
+            for (int ct = 0; ct < CT; ++ct) fb[(t + 1) & 1][ct] = frag_b(nbuf, ct, tn);
+            if constexpr (!T && buf == 1) {
+                if (t == 3) {
+#pragma unroll
+                    for (int ct = 0; ct < CT; ++ct) rr[ct] = s_ratio[0][wn * 64 + ct * 32 + l31];
                 }
             }
 #pragma unroll
-            for (int t = 0; t < 4; ++t) {
-                u32x4_t a[RT], b[CT];
-#pragma unroll
-                for (int rt = 0; rt < RT; ++rt) a[rt] = frag_a(buf, rt, t);
-#pragma unroll
-                for (int ct = 0; ct < CT; ++ct) b[ct] = frag_b(buf, ct, t);
-#pragma unroll
-                for (int rt = 0; rt < RT; ++rt)
-#pragma unroll
-                    for (int ct = 0; ct < CT; ++ct) acc[rt][ct] = mfma32x32x16<DT>(a[rt], b[ct], acc[rt][ct]);
-                if (t == 1) {
-                    // the next stage's operands: their buffer was last read before
-                    // the previous barrier
-                    store_a(buf ^ 1);
-                    store_w(buf ^ 1);
-                    const int sl = s + 2 < s1 ? s + 2 : s1 - 1;
-                    load_a(sl);
-                    load_w(sl);
+            for (int rt = 0; rt < RT; ++rt) {
+                if constexpr (!T && buf == 0 && RT == 1) {
+                    if (t == 0) scale_tiles(0, 2);
                 }
+#pragma unroll
+                for (int ct = 0; ct < CT; ++ct) acc[rt][ct] = mfma_step<DT>(fa[rt], fb[t & 1][ct], acc[rt][ct]);
+                // forward: the sums change their unit between a group's last step and
+                // the next one's first, spread over the slices of both so that it
+                // stays behind the one's products and ahead of the other's
+                if constexpr (!T && RT == 4) {
+                    if (buf == 1 && t == 3 && rt == 1) scale_tiles(0, 1);
+                    if (buf == 1 && t == 3 && rt == 2) scale_tiles(1, 3);
+                    if (buf == 1 && t == 3 && rt == 3) scale_tiles(3, 4);
+                    if (buf == 0 && t == 0 && rt == 0) scale_tiles(4, 6);
+                    if (buf == 0 && t == 0 && rt == 1) scale_tiles(6, 8);
+                } else if constexpr (!T && RT == 2) {
+                    if (buf == 1 && t == 3 && rt == 1) scale_tiles(0, 2);
+                    if (buf == 0 && t == 0 && rt == 0) scale_tiles(2, 4);
+                }
+                fa[rt] = frag_a(nbuf, rt, tn);
+                if (t == 0) {
+                    if (rt == 0) {
+                        load_w(buf, sl);
+                        deq_begin(buf ^ 1, buf ^ 1);
+                    }
+                    store_a(buf ^ 1, rt);
+                    load_a(sl, rt);
+                } else if (t < 3) {
+#pragma unroll
+                    for (int i = 0; i < HW; ++i) deq_half(buf ^ 1, buf ^ 1, ((t - 1) * RT + rt) * HW + i);
+                }
+                __builtin_amdgcn_sched_barrier(0);
             }
-            __syncthreads();
         }
+    };
+
+    if (s0 < s1) {
+        // stage s reads buffer (s - s0) % 2, its codes come through register set
+        // (s - s0) % 2
+        const int sn = s0 + 1 < s1 ? s0 + 1 : s0;
+#pragma unroll
+        for (int i = 0; i < XP; ++i) load_a(s0, i);
+        load_w(0, s0);
+        load_w(1, sn);
+#pragma unroll
+        for (int i = 0; i < XP; ++i) store_a(0, i);
+        deq_begin(0, 0);
+#pragma unroll
+        for (int i = 0; i < 8; ++i) deq_half(0, 0, i);
+#pragma unroll
+        for (int i = 0; i < XP; ++i) load_a(sn, i);
+        __syncthreads();
+#pragma unroll
+        for (int rt = 0; rt < RT; ++rt) fa[rt] = frag_a(0, rt, 0);
+#pragma unroll
+        for (int ct = 0; ct < CT; ++ct) fb[0][ct] = frag_b(0, ct, 0);
+        rr[0] = rr[1] = 1.f;                          // (the sums are 0)
+        int s = s0;
+        for (; s + 1 < s1; s += 2) {
+            stage(std::integral_constant<int, 0>{}, s);
+            stage(std::integral_constant<int, 1>{}, s + 1);
+        }
+        // (forward slices hold whole 128-row groups)
+        if (T && s < s1) stage(std::integral_constant<int, 0>{}, s);
     }
+    __syncthreads();
 
     // ---- epilogue: wave tiles through LDS, rows of 8 columns per lane -----------------
     float scl[CT] = {1.f, 1.f};
     if constexpr (!T) {
         // scale that the sums are held in, per column
-        if (((lane >> 4) & 1) == 0) s_ratio[0][wcol] = se;
+        s_ratio[0][wcol] = se;
         __syncthreads();
 #pragma unroll
         for (int ct = 0; ct < CT; ++ct) scl[ct] = s_ratio[0][wn * 64 + ct * 32 + l31];
@@ -446,6 +536,7 @@ static WidePlan wide_plan(int mode, int64_t M, int64_t K, int64_t N) {
     int slices = 1;
     while ((int64_t)w.mtiles * w.ntiles * slices < 192 && nst / (2 * slices) >= 8) slices *= 2;
     w.stages = (nst + slices - 1) / slices;
+    w.stages += w.stages & 1;                          // whole 128-row groups (forward)
     w.slices = (nst + w.stages - 1) / w.stages;
     return w;
 }

@@ -173,15 +173,18 @@ struct LinArgs {
     uint16_t *y;                // result, row stride ldy
     int64_t ldy;
     float *part;                // partial sums [slices][M][cols] (slices > 1)
-    int slices, stages;         // stages per slice
+    int slices, stages;         // stages (decode kernel: 128-row groups) per slice
     int mtiles, ntiles;
 };
 // Workspace of a product (partial sums of its slices), 0 if it runs in one.
 size_t lin_workspace_bytes(int mode, int64_t M, int64_t K, int64_t N);
 hipError_t launch_lin(int mode, LinArgs p, int dt, void *workspace, hipStream_t stream);
 // The decode-sized forward kernel (EP, GLU).
-bool lin_small_ok(int mode, int64_t M, int64_t K, int64_t N);
-hipError_t launch_lin_small(int mode, const LinArgs &p, int dt, hipStream_t stream);
+bool lin_small_ok(int mode, int64_t M);
+size_t lin_small_workspace_bytes(int mode, int64_t M, int64_t K, int64_t N);
+hipError_t launch_lin_small(int mode, LinArgs p, int dt, void *workspace, hipStream_t stream);
+// Sum of the slices in p.part and the finishing step.
+hipError_t launch_lin_join(int mode, const LinArgs &p, int dt, hipStream_t stream);
 // d = gradient of the pre-activation h (glu: both halves), and its column
 // sums in fp32.  d is written unless act == NONE without a gate; colsum may be
 // NULL; part: lin_dact_workspace_bytes() of scratch (used with colsum only).

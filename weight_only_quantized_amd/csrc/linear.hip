@@ -8,8 +8,6 @@ namespace w4 {
 
 constexpr int kXcd = 8;              // XCDs; workgroups go to them round-robin
 constexpr int kBK = 64;              // contraction elements per stage
-constexpr int kWideN = 256;          // columns per workgroup
-constexpr int kTRow = kWideN * 2;    // LDS row (bytes) of the transposed W tile
 
 typedef short v4s_t __attribute__((__vector_size__(8)));
 typedef v4s_t __attribute__((address_space(3))) *lds_v4s_ptr;
@@ -27,7 +25,7 @@ __device__ __forceinline__ u32x2_t lds_tr16(const uint8_t *p) {
 // c): 8 consecutive rows get different chunks, and rows 8 apart, which share a
 // 128-byte half, too.
 __device__ __forceinline__ int key_row(int r) { return (r & 7) ^ ((r >> 3) & 1); }
-// Rows of 512 bytes (transposed W; written down 8 rows at one c, read as 4 rows
+// Rows of 256 or 512 bytes (transposed W; written down 8 rows at one c, read as 4 rows
 // x 4 chunks): bits 2, 3 tell 4 rows apart for the reads, bits 0..2 tell 8 rows
 // apart for the writes.
 __device__ __forceinline__ int key_t(int n) { return (n & 3) << 2 | (n & 2) | ((n >> 2) & 1); }
@@ -47,23 +45,26 @@ __device__ __forceinline__ f32x16_t mfma_step(const u32x4_t &a, const u32x4_t &b
     return r;
 }
 
-template <int DT, int MODE, int BM>
-__global__ void __launch_bounds__(512, 2) lin_wide_kernel(const LinArgs p) {
+template <int DT, int MODE, int BM, int BN>
+__global__ void __launch_bounds__(2 * BN, 2) lin_wide_kernel(const LinArgs p) {
     constexpr bool T = MODE == LIN_T;
-    constexpr int RT = BM / 64, CT = 2;              // 32 x 32 tiles per wave (2 x 4 waves)
-    constexpr int XP = BM / 64;                      // 16-byte A chunks per thread and stage
+    constexpr int NT = 2 * BN;                       // threads: 2 x BN / 64 waves of (BM / 2) x 64
+    constexpr int RT = BM / 64, CT = 2;              // 32 x 32 tiles per wave
+    constexpr int AROWS = NT / 8;                    // rows of A per staging pass
+    constexpr int XP = BM / AROWS;                   // 16-byte A chunks per thread and stage
     constexpr int ABYTES = BM * kBK * 2;
-    constexpr int BBYTES = T ? kBK * kTRow : kWideN * kBK * 2;
+    constexpr int BBYTES = BN * kBK * 2;
+    constexpr int kTRow = BN * 2;                    // LDS row (bytes) of the transposed W tile
     constexpr int OUTROW = 68;                       // floats per row of the output staging
     constexpr int LDSBYTES = 2 * (ABYTES + BBYTES);
-    static_assert(LDSBYTES >= 8 * 32 * OUTROW * 4, "output staging fits");
+    static_assert(LDSBYTES >= NT / 64 * 32 * OUTROW * 4, "output staging fits");
     __shared__ __attribute__((aligned(16))) uint8_t lds[LDSBYTES];
-    __shared__ float s_ratio[2][kWideN];             // per column: factor on the sums at a new scale group
+    __shared__ float s_ratio[2][BN];             // per column: factor on the sums at a new scale group
     uint8_t *const lda_ = lds, *const ldb_ = lds + 2 * ABYTES;
 
     const int tid = threadIdx.x, lane = tid & 63;
     const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
-    const int wm = wave >> 2, wn = wave & 3;
+    const int wm = wave / (BN / 64), wn = wave % (BN / 64);
     const int l31 = lane & 31, kg = lane >> 5;
 
     // ---- tile of this workgroup ------------------------------------------------
@@ -86,20 +87,25 @@ __global__ void __launch_bounds__(512, 2) lin_wide_kernel(const LinArgs p) {
     const int s0 = slice * p.stages, s1 = s0 + p.stages < nst ? s0 + p.stages : nst;
 
     // ---- A operand: BM rows of 64 elements per stage ------------------------------
-    // (the rows of a thread are 64 apart: one LDS offset serves all)
+    // (the rows of a thread are AROWS apart: one LDS offset serves all)
     const uint8_t *const abase = reinterpret_cast<const uint8_t *>(p.a + row0 * p.lda);
     uint32_t aoff[XP];
     const int ar_ = tid >> 3, ac_ = tid & 7;
 #pragma unroll
     for (int i = 0; i < XP; ++i) {
-        const int64_t r = row0 + i * 64 + ar_ < p.M ? i * 64 + ar_ : p.M - 1 - row0;
+        const int64_t r = row0 + i * AROWS + ar_ < p.M ? i * AROWS + ar_ : p.M - 1 - row0;
         aoff[i] = (uint32_t)(r * p.lda + ac_ * 8) * 2u;
     }
     uint8_t *const adst = lda_ + ar_ * (kBK * 2) + ((ac_ ^ key_row(ar_)) << 4);
-    u32x4_t ar[XP];
-    auto load_a = [&](int s, int i) { ar[i] = ld128(abase + (int64_t)s * (kBK * 2) + aoff[i]); };
-    auto store_a = [&](int buf, int i) {
-        *reinterpret_cast<u32x4_t *>(adst + buf * ABYTES + i * 64 * (kBK * 2)) = ar[i];
+    // Small tiles run a stage in less than a memory round trip: they hold two
+    // stages of A on the way (DEEP), the 256-row tile has registers for one.
+    constexpr bool DEEP = RT < 4;
+    u32x4_t ar[DEEP ? 2 : 1][XP];
+    auto load_a = [&](int d, int s, int i) {
+        ar[DEEP ? d : 0][i] = ld128(abase + (int64_t)s * (kBK * 2) + aoff[i]);
+    };
+    auto store_a = [&](int d, int buf, int i) {
+        *reinterpret_cast<u32x4_t *>(adst + buf * ABYTES + i * AROWS * (kBK * 2)) = ar[DEEP ? d : 0][i];
     };
 
     // ---- W operand: one 16-byte slot (32 rows of one column) per thread -----------
@@ -118,11 +124,11 @@ __global__ void __launch_bounds__(512, 2) lin_wide_kernel(const LinArgs p) {
         if constexpr (MODE == LIN_GLU) {
             // 4 blocks per consuming wave: two gate, then the two up blocks of the same columns
             const int64_t half = p.cols / 2;
-            int64_t c0 = nt * (kWideN / 2) + (cb >> 2) * 32 + (cb & 1) * 16;
+            int64_t c0 = nt * (BN / 2) + (cb >> 2) * 32 + (cb & 1) * 16;
             if (c0 >= half) c0 = half - 16;
             nb = ((cb & 2) ? half + c0 : c0) / 16;
         } else {
-            nb = nt * (kWideN / 16) + cb;
+            nb = nt * (BN / 16) + cb;
             if (nb >= p.cols / 16) nb = p.cols / 16 - 1;
         }
         wcol = cb * 16 + j;
@@ -132,7 +138,7 @@ __global__ void __launch_bounds__(512, 2) lin_wide_kernel(const LinArgs p) {
         bdst = wcol * (kBK * 2) + (((4 * c32) ^ key_row(wcol)) << 4);
     } else {
         const int nbi = wave & 3, gi = wave >> 2;
-        int64_t g = nt * 2 + gi;
+        int64_t g = nt * (BN / 128) + gi;
         if (g >= G) g = G - 1;
         woff = (uint32_t)((nbi * G + g) * kTileBytes) + lane * 16;
         wstep = 4 * G * kTileBytes;
@@ -267,7 +273,8 @@ __global__ void __launch_bounds__(512, 2) lin_wide_kernel(const LinArgs p) {
     // the scheduler may not move work between slices: left alone it gathers the
     // vector work in front of the products, where both waves of a SIMD then wait
     // for the vector unit and later for the matrix core.
-    u32x4_t fa[RT], fb[2][CT];
+    constexpr int FA = DEEP ? 2 : 1;                // operand sets of A: 128-row wave tiles re-read in place
+    u32x4_t fa[FA][RT], fb[2][CT];
     float rr[CT];
     auto scale_tiles = [&](int i0, int i1) {
 #pragma unroll
@@ -277,14 +284,20 @@ __global__ void __launch_bounds__(512, 2) lin_wide_kernel(const LinArgs p) {
     };
     auto stage = [&](auto bufc, int s) {
         constexpr int buf = decltype(bufc)::value;
-        constexpr int HW = 4 / RT;                    // half-words per slice of steps 1 and 2
-        const int sl = s + 2 < s1 ? s + 2 : s1 - 1;
+        const int sl = s + (DEEP ? 3 : 2) < s1 ? s + (DEEP ? 3 : 2) : s1 - 1;
 #pragma unroll
         for (int t = 0; t < 4; ++t) {
-            if (t == 3) __syncthreads();
+            if (t == 3) {
+                __syncthreads();
+                if (DEEP) load_w(buf ^ 1, sl);
+            }
             const int nbuf = t < 3 ? buf : buf ^ 1, tn = (t + 1) & 3;
 #pragma unroll
             for (int ct = 0; ct < CT; ++ct) fb[(t + 1) & 1][ct] = frag_b(nbuf, ct, tn);
+            if constexpr (FA == 2) {
+#pragma unroll
+                for (int rt = 0; rt < RT; ++rt) fa[(t + 1) & 1][rt] = frag_a(nbuf, rt, tn);
+            }
             if constexpr (!T && buf == 1) {
                 if (t == 3) {
 #pragma unroll
@@ -297,7 +310,8 @@ __global__ void __launch_bounds__(512, 2) lin_wide_kernel(const LinArgs p) {
                     if (t == 0) scale_tiles(0, 2);
                 }
 #pragma unroll
-                for (int ct = 0; ct < CT; ++ct) acc[rt][ct] = mfma_step<DT>(fa[rt], fb[t & 1][ct], acc[rt][ct]);
+                for (int ct = 0; ct < CT; ++ct)
+                    acc[rt][ct] = mfma_step<DT>(fa[t % FA][rt], fb[t & 1][ct], acc[rt][ct]);
                 // forward: the sums change their unit between a group's last step and
                 // the next one's first, spread over the slices of both so that it
                 // stays behind the one's products and ahead of the other's
@@ -311,17 +325,23 @@ __global__ void __launch_bounds__(512, 2) lin_wide_kernel(const LinArgs p) {
                     if (buf == 1 && t == 3 && rt == 1) scale_tiles(0, 2);
                     if (buf == 0 && t == 0 && rt == 0) scale_tiles(2, 4);
                 }
-                fa[rt] = frag_a(nbuf, rt, tn);
+                if (FA == 1) fa[0][rt] = frag_a(nbuf, rt, tn);
                 if (t == 0) {
                     if (rt == 0) {
-                        load_w(buf, sl);
+                        if (!DEEP) load_w(buf, sl);
                         deq_begin(buf ^ 1, buf ^ 1);
                     }
-                    store_a(buf ^ 1, rt);
-                    load_a(sl, rt);
-                } else if (t < 3) {
 #pragma unroll
-                    for (int i = 0; i < HW; ++i) deq_half(buf ^ 1, buf ^ 1, ((t - 1) * RT + rt) * HW + i);
+                    for (int i = rt * XP / RT; i < (rt + 1) * XP / RT; ++i) {
+                        store_a(buf ^ 1, buf ^ 1, i);
+                        load_a(buf ^ 1, sl, i);
+                    }
+                }
+                // the 8 half-words: over steps 1 and 2 (128-row wave tiles), or 0 to 2
+                const int q = FA == 1 ? (t - 1) * RT + rt : t * RT + rt, nq = FA == 1 ? 2 * RT : 3 * RT;
+                if (q >= 0 && t < 3) {
+#pragma unroll
+                    for (int i = 8 * q / nq; i < 8 * (q + 1) / nq; ++i) deq_half(buf ^ 1, buf ^ 1, i);
                 }
                 __builtin_amdgcn_sched_barrier(0);
             }
@@ -331,21 +351,26 @@ __global__ void __launch_bounds__(512, 2) lin_wide_kernel(const LinArgs p) {
     if (s0 < s1) {
         // stage s reads buffer (s - s0) % 2, its codes come through register set
         // (s - s0) % 2
-        const int sn = s0 + 1 < s1 ? s0 + 1 : s0;
+        const int sn = s0 + 1 < s1 ? s0 + 1 : s0, sn2 = s0 + 2 < s1 ? s0 + 2 : s1 - 1;
 #pragma unroll
-        for (int i = 0; i < XP; ++i) load_a(s0, i);
+        for (int i = 0; i < XP; ++i) load_a(0, s0, i);
         load_w(0, s0);
         load_w(1, sn);
+        if (DEEP) {
 #pragma unroll
-        for (int i = 0; i < XP; ++i) store_a(0, i);
+            for (int i = 0; i < XP; ++i) load_a(1, sn, i);
+        }
+#pragma unroll
+        for (int i = 0; i < XP; ++i) store_a(0, 0, i);
         deq_begin(0, 0);
 #pragma unroll
         for (int i = 0; i < 8; ++i) deq_half(0, 0, i);
+        if (DEEP) load_w(0, sn2);
 #pragma unroll
-        for (int i = 0; i < XP; ++i) load_a(sn, i);
+        for (int i = 0; i < XP; ++i) load_a(0, DEEP ? sn2 : sn, i);
         __syncthreads();
 #pragma unroll
-        for (int rt = 0; rt < RT; ++rt) fa[rt] = frag_a(0, rt, 0);
+        for (int rt = 0; rt < RT; ++rt) fa[0][rt] = frag_a(0, rt, 0);
 #pragma unroll
         for (int ct = 0; ct < CT; ++ct) fb[0][ct] = frag_b(0, ct, 0);
         rr[0] = rr[1] = 1.f;                          // (the sums are 0)
@@ -379,7 +404,7 @@ __global__ void __launch_bounds__(512, 2) lin_wide_kernel(const LinArgs p) {
         __syncthreads();
         const int64_t rbase = row0 + wm * (BM / 2) + rt * 32;
         if constexpr (MODE == LIN_GLU) {
-            const int64_t c0 = nt * (kWideN / 2) + wn * 32;
+            const int64_t c0 = nt * (BN / 2) + wn * 32;
             if (c0 < p.cols / 2) {
                 for (int i = 0; i < 2; ++i) {
                     const int r = i * 16 + (lane >> 2), c = (lane & 3) * 8;
@@ -399,7 +424,7 @@ __global__ void __launch_bounds__(512, 2) lin_wide_kernel(const LinArgs p) {
                 }
             }
         } else {
-            const int64_t c0 = nt * kWideN + wn * 64;
+            const int64_t c0 = nt * BN + wn * 64;
             if (c0 < p.cols) {
                 for (int i = 0; i < 4; ++i) {
                     const int r = i * 8 + (lane >> 3), c = (lane & 7) * 8;
@@ -514,72 +539,122 @@ lin_dact_kernel(const uint16_t *dy, int64_t lddy, const uint16_t *h, uint16_t *d
     }
 }
 
-__global__ void __launch_bounds__(256) lin_colsum_kernel(const float *part, float *colsum, int64_t N, int blocks) {
-    const int64_t c = (int64_t)blockIdx.x * 256 + threadIdx.x;
-    if (c >= N) return;
+// colsum[c] = sum over the row blocks' partial sums: 64 columns per workgroup,
+// each of its 16 waves takes a contiguous share of the blocks, and the waves'
+// sums meet in LDS in order.
+__global__ void __launch_bounds__(1024) lin_colsum_kernel(const float *part, float *colsum, int64_t N, int blocks) {
+    __shared__ float red[16][64];
+    const int tx = threadIdx.x & 63, ty = threadIdx.x >> 6;
+    const int64_t c = (int64_t)blockIdx.x * 64 + tx;       // N is a multiple of 64
+    const int per = (blocks + 15) / 16, b0 = ty * per, b1 = b0 + per < blocks ? b0 + per : blocks;
     float s = 0.f;
-    for (int b = 0; b < blocks; ++b) s += part[(int64_t)b * N + c];
-    colsum[c] = s;
+    for (int b = b0; b < b1; ++b) s += part[(int64_t)b * N + c];
+    red[ty][tx] = s;
+    __syncthreads();
+    if (ty == 0) {
+#pragma unroll
+        for (int y = 1; y < 16; ++y) s += red[y][tx];
+        colsum[c] = s;
+    }
 }
 
 // ---- plans and launches ---------------------------------------------------------
 
-struct WidePlan { int bm; int slices, stages, mtiles, ntiles; };
+struct WidePlan { int bm, bn; int slices, stages, mtiles, ntiles; };
 
+// Tile shape and slice count by estimated time.  A workgroup's stage takes
+// `alone` us on an otherwise empty compute unit and `shared` us of a full one
+// (`slots` of them are resident), plus `ends` us for its first loads and its
+// epilogue; slices write and read their fp32 sums at about 5 TB/s and cost
+// another launch.  The constants are fits to timings over M = 61..2048 on
+// matrices from 1024 x 2048 to 4096 x 28672 (each within about 10%): few tiles want
+// small ones and slices, many want the large one, whose dequantization serves
+// 256 rows (M = 512, 4096 x 28672 gated: 121 us against 155 with 128 x 128 tiles;
+// M = 256, 4096^2: 97 us unsliced with 256 x 256, 26 us with 64 x 128 and four slices).
 static WidePlan wide_plan(int mode, int64_t M, int64_t K, int64_t N) {
-    WidePlan w{};
+    struct Shape { int bm, bn, slots; double alone, shared, ends; };
+    static constexpr Shape kShapes[] = {{64, 128, 3, 0.59, 0.405, 1.0},
+                                        {128, 128, 2, 0.70, 0.59, 2.0},
+                                        {128, 256, 1, 1.08, 1.08, 4.0},
+                                        {256, 256, 1, 1.60, 1.60, 8.0}};
+    static constexpr int kSlices[] = {1, 2, 3, 4, 6, 8, 12, 16};
+    constexpr int64_t kCus = 256;
     const int64_t cols = mode == LIN_T ? K : N;
     const int nst = (int)((mode == LIN_T ? N : K) / kBK);
-    w.ntiles = (int)((cols + kWideN - 1) / kWideN);
-    w.bm = M <= 64 ? 64 : M <= 128 ? 128 : 256;
-    w.mtiles = (int)((M + w.bm - 1) / w.bm);
-    int slices = 1;
-    while ((int64_t)w.mtiles * w.ntiles * slices < 192 && nst / (2 * slices) >= 8) slices *= 2;
-    w.stages = (nst + slices - 1) / slices;
-    w.stages += w.stages & 1;                          // whole 128-row groups (forward)
-    w.slices = (nst + w.stages - 1) / w.stages;
-    return w;
+    WidePlan best{};
+    double best_us = 0;
+    for (const Shape &sh : kShapes)
+        for (int want : kSlices) {
+            WidePlan w{};
+            w.bm = sh.bm;
+            w.bn = sh.bn;
+            w.mtiles = (int)((M + w.bm - 1) / w.bm);
+            w.ntiles = (int)((cols + w.bn - 1) / w.bn);
+            w.stages = (nst + want - 1) / want;
+            w.stages += w.stages & 1;                  // whole 128-row groups (forward)
+            w.slices = (nst + w.stages - 1) / w.stages;
+            if (want > 1 && (w.slices != want || w.stages < 4)) continue;
+            const double n = (double)(((int64_t)w.mtiles * w.ntiles * w.slices + kCus - 1) / kCus);
+            const double one = w.stages * sh.alone + sh.ends, all = n * (w.stages * sh.shared + sh.ends);
+            double us = one > all ? one : all;
+            if (w.slices > 1) us += 3.0 + 8e-6 / 5.0 * w.slices * (double)M * (double)cols;
+            if (best.bm == 0 || us < best_us) {
+                best = w;
+                best_us = us;
+            }
+        }
+    return best;
 }
 
 size_t lin_workspace_bytes(int mode, int64_t M, int64_t K, int64_t N) {
-    if (M <= 0 || (mode != LIN_T && lin_small_ok(mode, M, K, N))) return 0;
+    if (M <= 0) return 0;
+    if (lin_small_ok(mode, M)) return lin_small_workspace_bytes(mode, M, K, N);
     const WidePlan w = wide_plan(mode, M, K, N);
     return w.slices > 1 ? (size_t)w.slices * (size_t)M * (size_t)(mode == LIN_T ? K : N) * sizeof(float) : 0;
 }
 
 template <int DT, int MODE>
-static hipError_t wide_launch(const LinArgs &p, int bm, hipStream_t stream) {
+static hipError_t wide_launch(const LinArgs &p, int bm, int bn, hipStream_t stream) {
     const int64_t total = (int64_t)p.mtiles * p.ntiles * p.slices;
     if (total > INT32_MAX) return hipErrorInvalidConfiguration;
-    const dim3 grid((unsigned)total), block(512);
-    if (bm == 64) hipLaunchKernelGGL((lin_wide_kernel<DT, MODE, 64>), grid, block, 0, stream, p);
-    else if (bm == 128) hipLaunchKernelGGL((lin_wide_kernel<DT, MODE, 128>), grid, block, 0, stream, p);
-    else hipLaunchKernelGGL((lin_wide_kernel<DT, MODE, 256>), grid, block, 0, stream, p);
-    hipError_t err = hipGetLastError();
-    if (err != hipSuccess || p.slices == 1) return err;
-    const int64_t work = p.M * ((MODE == LIN_GLU ? p.cols / 2 : p.cols) / 8);
-    const int64_t blocks = (work + 255) / 256;
-    hipLaunchKernelGGL((lin_join_kernel<DT, MODE == LIN_GLU>), dim3((unsigned)(blocks < 4096 ? blocks : 4096)), dim3(256), 0,
-                       stream, p);
+    const dim3 grid((unsigned)total), block(2 * bn);
+    if (bm == 64 && bn == 128) hipLaunchKernelGGL((lin_wide_kernel<DT, MODE, 64, 128>), grid, block, 0, stream, p);
+    else if (bm == 128 && bn == 128) hipLaunchKernelGGL((lin_wide_kernel<DT, MODE, 128, 128>), grid, block, 0, stream, p);
+    else if (bm == 128 && bn == 256) hipLaunchKernelGGL((lin_wide_kernel<DT, MODE, 128, 256>), grid, block, 0, stream, p);
+    else if (bm == 256 && bn == 256) hipLaunchKernelGGL((lin_wide_kernel<DT, MODE, 256, 256>), grid, block, 0, stream, p);
+    else return hipErrorInvalidValue;
     return hipGetLastError();
 }
 
+template <int DT, bool GLU>
+static hipError_t join_go(const LinArgs &p, hipStream_t stream) {
+    const int64_t work = p.M * ((GLU ? p.cols / 2 : p.cols) / 8), blocks = (work + 255) / 256;
+    hipLaunchKernelGGL((lin_join_kernel<DT, GLU>), dim3((unsigned)(blocks < 4096 ? blocks : 4096)), dim3(256), 0, stream, p);
+    return hipGetLastError();
+}
+
+hipError_t launch_lin_join(int mode, const LinArgs &p, int dt, hipStream_t stream) {
+    if (dt == DT_BF16) return mode == LIN_GLU ? join_go<DT_BF16, true>(p, stream) : join_go<DT_BF16, false>(p, stream);
+    return mode == LIN_GLU ? join_go<DT_F16, true>(p, stream) : join_go<DT_F16, false>(p, stream);
+}
+
+template <int DT>
+static hipError_t wide_dt(int mode, const LinArgs &p, const WidePlan &w, hipStream_t stream) {
+    if (mode == LIN_EP) return wide_launch<DT, LIN_EP>(p, w.bm, w.bn, stream);
+    if (mode == LIN_GLU) return wide_launch<DT, LIN_GLU>(p, w.bm, w.bn, stream);
+    return wide_launch<DT, LIN_T>(p, w.bm, w.bn, stream);
+}
+
 hipError_t launch_lin(int mode, LinArgs p, int dt, void *workspace, hipStream_t stream) {
-    if (mode != LIN_T && lin_small_ok(mode, p.M, p.K, p.N)) return launch_lin_small(mode, p, dt, stream);
+    if (lin_small_ok(mode, p.M)) return launch_lin_small(mode, p, dt, workspace, stream);
     const WidePlan w = wide_plan(mode, p.M, p.K, p.N);
     p.slices = w.slices;
     p.stages = w.stages;
     p.mtiles = w.mtiles;
     p.ntiles = w.ntiles;
     p.part = (float *)workspace;
-    if (dt == DT_BF16) {
-        if (mode == LIN_EP) return wide_launch<DT_BF16, LIN_EP>(p, w.bm, stream);
-        if (mode == LIN_GLU) return wide_launch<DT_BF16, LIN_GLU>(p, w.bm, stream);
-        return wide_launch<DT_BF16, LIN_T>(p, w.bm, stream);
-    }
-    if (mode == LIN_EP) return wide_launch<DT_F16, LIN_EP>(p, w.bm, stream);
-    if (mode == LIN_GLU) return wide_launch<DT_F16, LIN_GLU>(p, w.bm, stream);
-    return wide_launch<DT_F16, LIN_T>(p, w.bm, stream);
+    hipError_t err = dt == DT_BF16 ? wide_dt<DT_BF16>(mode, p, w, stream) : wide_dt<DT_F16>(mode, p, w, stream);
+    return err == hipSuccess && p.slices > 1 ? launch_lin_join(mode, p, dt, stream) : err;
 }
 
 // Row blocks of the column sums: enough workgroups to fill the machine, at
@@ -613,7 +688,7 @@ hipError_t launch_lin_dact(bool glu, const uint16_t *dy, int64_t lddy, const uin
         if (err != hipSuccess) return err;
     }
     if (!colsum) return hipSuccess;
-    hipLaunchKernelGGL(lin_colsum_kernel, dim3((unsigned)((N + 255) / 256)), dim3(256), 0, stream, (const float *)part,
+    hipLaunchKernelGGL(lin_colsum_kernel, dim3((unsigned)(N / 64)), dim3(1024), 0, stream, (const float *)part,
                        colsum, N, blocks);
     return hipGetLastError();
 }

@@ -9,20 +9,21 @@
 
 namespace w4 {
 
-constexpr int small_waves(int mt) { return mt == 1 ? 16 : 8; }
+constexpr int kSmallWaves = 8;       // most waves per workgroup
+constexpr int64_t kSmallMaxM = 32;   // rows of the decode kernel
 
 template <int DT, bool GLU, int NB, int MT>
-__global__ void __launch_bounds__(small_waves(MT) * 64) lin_small_kernel(const LinArgs p) {
+__global__ void __launch_bounds__(kSmallWaves * 64) lin_small_kernel(const LinArgs p) {
     static_assert(!GLU || NB % 2 == 0, "gate and up blocks in pairs");
     constexpr int D = 2;                              // groups in flight per wave
-    constexpr int WMAX = small_waves(MT);
-    const int G = (int)(p.K / kGroup);
     const int W = blockDim.x >> 6;
+    // this workgroup's groups: [g0, G)
+    const int g0 = (int)blockIdx.y * p.stages, Gall = (int)(p.K / kGroup);
+    const int G = g0 + p.stages < Gall ? g0 + p.stages : Gall;
     const int lane = threadIdx.x & 63;
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const int j = lane & 15, kc = lane >> 4;
     const int64_t half = p.cols / 2;
-    const int64_t m0 = (int64_t)blockIdx.y * 16 * MT;
     // first column of block b
     auto col_of = [&](int b) -> int64_t {
         if constexpr (GLU) {
@@ -36,12 +37,12 @@ __global__ void __launch_bounds__(small_waves(MT) * 64) lin_small_kernel(const L
     const uint16_t *xrow[MT];
 #pragma unroll
     for (int mt = 0; mt < MT; ++mt) {
-        const int64_t r = m0 + 16 * mt + j < p.M ? m0 + 16 * mt + j : p.M - 1;
+        const int64_t r = 16 * mt + j < p.M ? 16 * mt + j : p.M - 1;
         xrow[mt] = p.a + r * p.lda + 32 * kc;
     }
     const uint8_t *wb[NB];
 #pragma unroll
-    for (int b = 0; b < NB; ++b) wb[b] = p.wp + col_of(b) / 16 * G * kTileBytes + lane * 16;
+    for (int b = 0; b < NB; ++b) wb[b] = p.wp + col_of(b) / 16 * Gall * kTileBytes + lane * 16;
     // lane l fetches the scale and zero point of column l % (16 NB); without
     // zero points the scale's own bytes are read and ignored
     const int64_t scol = col_of((lane & (16 * NB - 1)) >> 4) + j;
@@ -111,8 +112,8 @@ __global__ void __launch_bounds__(small_waves(MT) * 64) lin_small_kernel(const L
     };
 
 #pragma unroll
-    for (int d = 0; d < D; ++d) load(d, wave + d * W);
-    for (int g = wave; g < G; g += D * W) {
+    for (int d = 0; d < D; ++d) load(d, g0 + wave + d * W);
+    for (int g = g0 + wave; g < G; g += D * W) {
 #pragma unroll
         for (int d = 0; d < D; ++d) {
             if (g + d * W < G) compute(d);
@@ -121,7 +122,7 @@ __global__ void __launch_bounds__(small_waves(MT) * 64) lin_small_kernel(const L
     }
 
     // ---- sums of the waves, in wave order, then the finishing step ----------------
-    __shared__ float red[WMAX][NB][16 * MT][17];
+    __shared__ float red[kSmallWaves][NB][16 * MT][17];
 #pragma unroll
     for (int b = 0; b < NB; ++b)
 #pragma unroll
@@ -132,53 +133,93 @@ __global__ void __launch_bounds__(small_waves(MT) * 64) lin_small_kernel(const L
     constexpr int OB = GLU ? NB / 2 : NB;
     for (int i = threadIdx.x; i < OB * 256 * MT; i += blockDim.x) {
         const int b = i / (256 * MT), r = (i >> 4) % (16 * MT), c = i & 15;
-        const int64_t row = m0 + r;
+        const int64_t row = r;
         if (row >= p.M) continue;
         float v[1] = {0.f}, u[1] = {0.f};
         for (int w = 0; w < W; ++w) {
             v[0] += red[w][b][r][c];
             if constexpr (GLU) u[0] += red[w][b + NB / 2][r][c];
         }
+        if (p.slices > 1) {
+            float *o = p.part + ((int64_t)blockIdx.y * p.M + row) * p.cols + col_of(b) + c;
+            o[0] = v[0];
+            if constexpr (GLU) o[half] = u[0];
+            continue;
+        }
         if constexpr (GLU) finish_glu<DT, 1>(p, v, u, row, col_of(b) + c);
         else finish_ep<DT, 1>(p, v, row, col_of(b) + c);
     }
 }
 
-bool lin_small_ok(int mode, int64_t M, int64_t K, int64_t N) {
-    (void)K;
-    (void)N;
-    return mode != LIN_T && M <= 64;
+// Column blocks per workgroup, waves, 16-row tiles and K slices of a call.
+struct SmallPlan { int nb, waves, mt, slices, groups; };
+
+// Widest workgroups that still give about one per compute unit.  Every
+// workgroup reads all of x (16 mt rows), N K 2 mt / nb bytes in all through L2 at
+// about 10 TB/s: beyond four rows it pays to take four column blocks and cut K
+// into slices instead once that saves more than the join's 4 us (40 MB).
+// Measured, M = 16: K 14336 x N 4096 17.9 -> 13.3 us, while 8192^2 would go from 12.2
+// to 13.2 and 4096^2 from 6.9 to 8.1.  Four waves per workgroup once there are more
+// workgroups than compute units and x is not a single tile's few rows (K 4096
+// x N 28672, M = 32: 26.9 -> 23.9 us), else eight (M = 1: 13.2 against 13.7 us).
+static SmallPlan small_plan(int mode, int64_t M, int64_t K, int64_t N) {
+    SmallPlan s{};
+    const int G = (int)(K / kGroup);
+    s.mt = M <= 16 ? 1 : 2;
+    s.nb = N / 64 >= 224 ? 4 : N / 32 >= 224 || mode == LIN_GLU ? 2 : 1;
+    int64_t slices = 1;
+    if (M > 4 && s.nb < 4 && 2 * s.mt * N * K / s.nb - 2 * s.mt * N * K / 4 > 40000000) {
+        s.nb = 4;
+        slices = 256 / (N / 64) < 1 ? 1 : 256 / (N / 64);
+        if (slices > 8) slices = 8;
+    }
+    s.groups = (int)((G + slices - 1) / slices);
+    s.slices = (G + s.groups - 1) / s.groups;
+    s.waves = M <= 4 || N / (16 * s.nb) * s.slices <= 256 ? kSmallWaves : 4;
+    if (s.waves > s.groups) s.waves = s.groups;
+    return s;
 }
 
-template <int DT, bool GLU, int NB>
-static hipError_t small_go(const LinArgs &p, hipStream_t stream) {
-    const int mt = p.M <= 16 ? 1 : p.M <= 32 ? 2 : 4;
-    const int64_t G = p.K / kGroup;
-    const int waves = (int)(G < 8 ? G : 8);
-    const dim3 grid((unsigned)(p.cols / (16 * NB)), (unsigned)((p.M + 16 * mt - 1) / (16 * mt))), block(waves * 64);
-    if (mt == 1) {
-        hipLaunchKernelGGL((lin_small_kernel<DT, GLU, NB, 1>), grid, block, 0, stream, p);
-    } else if (mt == 2) {
-        hipLaunchKernelGGL((lin_small_kernel<DT, GLU, NB, 2>), grid, block, 0, stream, p);
-    } else {
-        if constexpr (NB <= 2) hipLaunchKernelGGL((lin_small_kernel<DT, GLU, NB, 4>), grid, block, 0, stream, p);
-        else return hipErrorInvalidValue;
-    }
+bool lin_small_ok(int mode, int64_t M) { return mode != LIN_T && M <= kSmallMaxM; }
+
+size_t lin_small_workspace_bytes(int mode, int64_t M, int64_t K, int64_t N) {
+    const SmallPlan s = small_plan(mode, M, K, N);
+    return s.slices > 1 ? (size_t)s.slices * (size_t)M * (size_t)N * sizeof(float) : 0;
+}
+
+template <int DT, bool GLU, int NB, int MT>
+static hipError_t small_go(const LinArgs &p, const SmallPlan &s, hipStream_t stream) {
+    const dim3 grid((unsigned)(p.cols / (16 * NB)), (unsigned)s.slices);
+    hipLaunchKernelGGL((lin_small_kernel<DT, GLU, NB, MT>), grid, dim3((unsigned)s.waves * 64), 0, stream, p);
     return hipGetLastError();
 }
 
-template <int DT>
-static hipError_t small_dt(int mode, const LinArgs &p, hipStream_t stream) {
-    // fewer column blocks per workgroup where NB = 4 would leave compute units
-    // without one
-    const bool narrow = p.cols / 64 < 256 || p.M > 32;      // four 16-row tiles: NB = 4 does not fit in registers
-    if (mode == LIN_GLU) return narrow ? small_go<DT, true, 2>(p, stream) : small_go<DT, true, 4>(p, stream);
-    if (narrow) return p.cols / 32 < 256 ? small_go<DT, false, 1>(p, stream) : small_go<DT, false, 2>(p, stream);
-    return small_go<DT, false, 4>(p, stream);
+template <int DT, bool GLU, int NB>
+static hipError_t small_mt(const LinArgs &p, const SmallPlan &s, hipStream_t stream) {
+    if (s.mt == 1) return small_go<DT, GLU, NB, 1>(p, s, stream);
+    return small_go<DT, GLU, NB, 2>(p, s, stream);
 }
 
-hipError_t launch_lin_small(int mode, const LinArgs &p, int dt, hipStream_t stream) {
-    return dt == DT_BF16 ? small_dt<DT_BF16>(mode, p, stream) : small_dt<DT_F16>(mode, p, stream);
+template <int DT>
+static hipError_t small_dt(int mode, const LinArgs &p, const SmallPlan &s, hipStream_t stream) {
+    if (mode == LIN_GLU) {
+        if (s.nb == 2) return small_mt<DT, true, 2>(p, s, stream);
+        if (s.nb == 4) return small_mt<DT, true, 4>(p, s, stream);
+    } else {
+        if (s.nb == 1) return small_mt<DT, false, 1>(p, s, stream);
+        if (s.nb == 2) return small_mt<DT, false, 2>(p, s, stream);
+        if (s.nb == 4) return small_mt<DT, false, 4>(p, s, stream);
+    }
+    return hipErrorInvalidValue;
+}
+
+hipError_t launch_lin_small(int mode, LinArgs p, int dt, void *workspace, hipStream_t stream) {
+    const SmallPlan s = small_plan(mode, p.M, p.K, p.N);
+    p.slices = s.slices;
+    p.stages = s.groups;
+    p.part = (float *)workspace;
+    hipError_t err = dt == DT_BF16 ? small_dt<DT_BF16>(mode, p, s, stream) : small_dt<DT_F16>(mode, p, s, stream);
+    return err == hipSuccess && p.slices > 1 ? launch_lin_join(mode, p, dt, stream) : err;
 }
 
 }  // namespace w4

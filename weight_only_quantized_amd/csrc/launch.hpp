@@ -165,6 +165,7 @@ struct LinArgs {
     int64_t M, K, N;
     int64_t cols;               // columns of the product: N, or K when transposed
     int gm;                     // 128-row groups per scale group
+    uint64_t gm_inv;            // ceil(2^32 / gm): n / gm = n gm_inv >> 32 for the n < 2^15 groups (set by launch_lin)
     int act;
     const uint16_t *bias;       // [N] or NULL (forward)
     const uint16_t *res;        // residual / addend, row stride ldr, or NULL

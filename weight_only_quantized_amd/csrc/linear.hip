@@ -59,7 +59,7 @@ __global__ void __launch_bounds__(2 * BN, 2) lin_wide_kernel(const LinArgs p) {
     constexpr int LDSBYTES = 2 * (ABYTES + BBYTES);
     static_assert(LDSBYTES >= NT / 64 * 32 * OUTROW * 4, "output staging fits");
     __shared__ __attribute__((aligned(16))) uint8_t lds[LDSBYTES];
-    __shared__ float s_ratio[2][BN];             // per column: factor on the sums at a new scale group
+    __shared__ float s_ratio[T ? 1 : BN];            // per column: factor on the sums at a new scale group
     uint8_t *const lda_ = lds, *const ldb_ = lds + 2 * ABYTES;
 
     const int tid = threadIdx.x, lane = tid & 63;
@@ -68,19 +68,19 @@ __global__ void __launch_bounds__(2 * BN, 2) lin_wide_kernel(const LinArgs p) {
     const int l31 = lane & 31, kg = lane >> 5;
 
     // ---- tile of this workgroup ------------------------------------------------
-    const int64_t total = (int64_t)p.mtiles * p.ntiles * p.slices;
-    const int64_t id = blockIdx.x, xcd = id % kXcd;
-    const int64_t q8 = total / kXcd, r8 = total % kXcd;
-    const int64_t idx = xcd * q8 + (xcd < r8 ? xcd : r8) + id / kXcd;
-    const int64_t tiles = (int64_t)p.mtiles * p.ntiles;
+    // XCD x takes a contiguous share of the list (slices, then groups of four row
+    // tiles by column tile by row tile): the workgroups of one L2 share operands.
+    const uint32_t total = gridDim.x, id = blockIdx.x, xcd = id % kXcd;
+    const uint32_t r8 = total % kXcd, idx = xcd * (total / kXcd) + (xcd < r8 ? xcd : r8) + id / kXcd;
+    const uint32_t tiles = (uint32_t)p.mtiles * (uint32_t)p.ntiles;
+    constexpr uint32_t GM = 4;
     const int slice = (int)(idx / tiles);
-    const int64_t tile = idx % tiles;
-    constexpr int GM = 4;
-    const int64_t grp = tile / (GM * p.ntiles), m_first = grp * GM;
-    const int64_t gmt = p.mtiles - m_first < GM ? p.mtiles - m_first : GM;
-    const int64_t rem = tile - m_first * p.ntiles;
-    const int64_t row0 = (m_first + rem % gmt) * BM;
+    const uint32_t tile = idx - slice * tiles;
+    const uint32_t m_first = tile / (GM * p.ntiles) * GM;
+    const uint32_t gmt = p.mtiles - m_first < GM ? p.mtiles - m_first : GM;
+    const uint32_t rem = tile - m_first * p.ntiles;
     const int64_t nt = rem / gmt;
+    const int64_t row0 = (int64_t)(m_first + rem % gmt) * BM;
 
     const int64_t G = p.K / kGroup;
     const int nst = (int)((T ? p.N : p.K) / kBK);
@@ -148,13 +148,29 @@ __global__ void __launch_bounds__(2 * BN, 2) lin_wide_kernel(const LinArgs p) {
         bdst = n * kTRow + (((gi * 16 + c32 * 4) ^ key_t(n)) << 4);
     }
     u32x4_t wr[2];                                    // raw codes of the next two stages
-    uint16_t sr[2];
-    uint8_t zr[2];
-    auto load_w = [&](int d, int s) {
-        wr[d] = ld128(p.wp + (int64_t)s * wstep + woff);
-        const int64_t so = T ? srow_t + (int64_t)s * kBK : (int64_t)((s >> 1) / p.gm) * p.N;
-        sr[d] = p.scale[so + soff];
-        zr[d] = zbase[(so + soff) >> 1];
+    auto load_w = [&](int d, int s) { wr[d] = ld128(p.wp + (int64_t)s * wstep + woff); };
+    // Scales and zero points travel well ahead of the codes (a 2-byte load waits
+    // as long as a 16-byte one).  Forward: those of the next 128-row group, two
+    // stages ahead.  Transposed, where every stage has other columns: the four
+    // lanes of a column fetch four stages at once, four stages ahead, and hand
+    // them over with a lane permute.
+    uint32_t scur = 0;                                // transposed: scale | zero << 16 of 4 stages
+    uint16_t snext;
+    uint8_t znext;
+    auto load_s = [&](int s) {
+        int64_t so;
+        if constexpr (T) {
+            const int sl = s + c32 < s1 ? s + c32 : s1 - 1;
+            so = srow_t + (int64_t)sl * kBK + soff;
+        } else {
+            const int sl = s < s1 ? s : s1 - 1;
+            so = (int64_t)(((uint64_t)(sl >> 1) * p.gm_inv) >> 32) * p.N + soff;
+        }
+        snext = p.scale[so];
+        znext = zbase[so >> 1];
+    };
+    auto zero_of = [&](uint32_t zb) {
+        return p.zero ? __builtin_amdgcn_ubfe(zb, (uint32_t)(j & 1) * 4u, 4) : 8u;
     };
     // Forward: the sums are held in units of the running scale se; a new scale
     // group multiplies them by se / s first and its codes enter the matrix core
@@ -164,17 +180,28 @@ __global__ void __launch_bounds__(2 * BN, 2) lin_wide_kernel(const LinArgs p) {
     // codes weigh, and the sums stay far from overflow.
     float se = 0.f, smax = 0.f;
     struct Deq { float s, zs; uint32_t z, sel; } dq;
-    auto deq_begin = [&](int d, int buf) {
-        const float s = h2f<DT>(sr[d]);
-        const uint32_t z = p.zero ? __builtin_amdgcn_ubfe((uint32_t)zr[d], (uint32_t)(j & 1) * 4u, 4) : 8u;
+    // stage st is about to be dequantized: its column's scale and zero point
+    // (forward: once per 128-row group, from the loaded values)
+    auto deq_begin = [&](int st) {
+        uint32_t sb, z;
+        if constexpr (T) {
+            const uint32_t v = (uint32_t)__builtin_amdgcn_ds_bpermute((((st - s0) & 3) * 16 + j) << 2, (int)scur);
+            sb = v & 0xFFFFu;
+            z = v >> 16;
+        } else {
+            sb = snext;
+            z = zero_of(znext);
+        }
+        const float s = h2f<DT>((uint16_t)sb);
         bool live = true;
         if constexpr (!T) {
             const float as_ = __builtin_fabsf(s);
-            live = !(as_ < 0x1p-60f * smax) && !(as_ < 0x1p-126f);      // NaN stays
-            const float ratio = live && s != se ? se * __builtin_amdgcn_rcpf(s) : 1.f;
+            live = !((as_ < 0x1p-60f * smax) | (as_ < 0x1p-126f));      // NaN stays
+            float ratio = se * __builtin_amdgcn_rcpf(s);
+            ratio = live & (s != se) ? ratio : 1.f;
             se = live ? s : se;
-            smax = live ? __builtin_fmaxf(smax, as_) : smax;
-            s_ratio[buf][wcol] = ratio;               // both lanes of a column write the same value
+            smax = live & (as_ > smax) ? as_ : smax;
+            s_ratio[wcol] = ratio;                    // both lanes of a column write the same value
         }
         dq.s = s;
         dq.z = z;
@@ -301,7 +328,7 @@ __global__ void __launch_bounds__(2 * BN, 2) lin_wide_kernel(const LinArgs p) {
             if constexpr (!T && buf == 1) {
                 if (t == 3) {
 #pragma unroll
-                    for (int ct = 0; ct < CT; ++ct) rr[ct] = s_ratio[0][wn * 64 + ct * 32 + l31];
+                    for (int ct = 0; ct < CT; ++ct) rr[ct] = s_ratio[wn * 64 + ct * 32 + l31];
                 }
             }
 #pragma unroll
@@ -329,7 +356,16 @@ __global__ void __launch_bounds__(2 * BN, 2) lin_wide_kernel(const LinArgs p) {
                 if (t == 0) {
                     if (rt == 0) {
                         if (!DEEP) load_w(buf, sl);
-                        deq_begin(buf ^ 1, buf ^ 1);
+                        if constexpr (T) {
+                            if (buf == 1 && ((s + 1 - s0) & 3) == 0) {
+                                scur = snext | zero_of(znext) << 16;
+                                load_s(s + 5);
+                            }
+                            deq_begin(s + 1);
+                        } else if (buf == 1) {
+                            deq_begin(s + 1);
+                            load_s(s + 3);
+                        }
                     }
 #pragma unroll
                     for (int i = rt * XP / RT; i < (rt + 1) * XP / RT; ++i) {
@@ -354,6 +390,7 @@ __global__ void __launch_bounds__(2 * BN, 2) lin_wide_kernel(const LinArgs p) {
         const int sn = s0 + 1 < s1 ? s0 + 1 : s0, sn2 = s0 + 2 < s1 ? s0 + 2 : s1 - 1;
 #pragma unroll
         for (int i = 0; i < XP; ++i) load_a(0, s0, i);
+        load_s(s0);
         load_w(0, s0);
         load_w(1, sn);
         if (DEEP) {
@@ -362,7 +399,14 @@ __global__ void __launch_bounds__(2 * BN, 2) lin_wide_kernel(const LinArgs p) {
         }
 #pragma unroll
         for (int i = 0; i < XP; ++i) store_a(0, 0, i);
-        deq_begin(0, 0);
+        if (T) {
+            scur = snext | zero_of(znext) << 16;
+            load_s(s0 + 4);
+            deq_begin(s0);
+        } else {
+            deq_begin(s0);
+            load_s(s0 + 2);
+        }
 #pragma unroll
         for (int i = 0; i < 8; ++i) deq_half(0, 0, i);
         if (DEEP) load_w(0, sn2);
@@ -388,10 +432,10 @@ __global__ void __launch_bounds__(2 * BN, 2) lin_wide_kernel(const LinArgs p) {
     float scl[CT] = {1.f, 1.f};
     if constexpr (!T) {
         // scale that the sums are held in, per column
-        s_ratio[0][wcol] = se;
+        s_ratio[wcol] = se;
         __syncthreads();
 #pragma unroll
-        for (int ct = 0; ct < CT; ++ct) scl[ct] = s_ratio[0][wn * 64 + ct * 32 + l31];
+        for (int ct = 0; ct < CT; ++ct) scl[ct] = s_ratio[wn * 64 + ct * 32 + l31];
     }
     float *const ot = reinterpret_cast<float *>(lds) + wave * 32 * OUTROW;
 #pragma unroll
@@ -653,14 +697,15 @@ hipError_t launch_lin(int mode, LinArgs p, int dt, void *workspace, hipStream_t 
     p.mtiles = w.mtiles;
     p.ntiles = w.ntiles;
     p.part = (float *)workspace;
+    p.gm_inv = ((uint64_t(1) << 32) + p.gm - 1) / p.gm;
     hipError_t err = dt == DT_BF16 ? wide_dt<DT_BF16>(mode, p, w, stream) : wide_dt<DT_F16>(mode, p, w, stream);
     return err == hipSuccess && p.slices > 1 ? launch_lin_join(mode, p, dt, stream) : err;
 }
 
-// Row blocks of the column sums: enough workgroups to fill the machine, at
-// least four rows per thread, at most 64 partial rows.
+// Row blocks of the activation gradient, one partial row of column sums each:
+// one row per thread (four per block) up to 64 blocks.
 static int dact_blocks(int64_t M) {
-    const int64_t b = (M + 15) / 16;
+    const int64_t b = (M + 3) / 4;
     return (int)(b < 1 ? 1 : b > 64 ? 64 : b);
 }
 

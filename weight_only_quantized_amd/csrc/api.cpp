@@ -453,12 +453,12 @@ w4a16_status linear_backward(bool glu, const void *dy, int64_t lddy, const void 
     }
     if (current_device_ok() != 1) return W4A16_ERR_DEVICE;
     hipStream_t s = (hipStream_t)stream;
+    if (M == 0) return map_err(w4::launch_lin_zero_colsum(dbias, N, s));
     if (through || dbias) {
-        hipError_t err = w4::launch_lin_dact(glu, (const uint16_t *)dy, lddy, (const uint16_t *)h, (uint16_t *)d,
-                                             dbias, M, N, act, dt, workspace, s);
+        hipError_t err = w4::launch_lin_dact(glu, (const uint16_t *)dy, lddy, (const uint16_t *)h, (uint16_t *)d, M, N,
+                                             act, dt, dbias ? (float *)workspace : nullptr, s);
         if (err != hipSuccess) return map_err(err);
     }
-    if (M == 0) return W4A16_OK;
     w4::LinArgs p{};
     p.a = (const uint16_t *)(through ? d : dy);
     p.lda = through ? N : lddy;
@@ -474,6 +474,9 @@ w4a16_status linear_backward(bool glu, const void *dy, int64_t lddy, const void 
     p.ldr = ldadd;
     p.y = (uint16_t *)dx;
     p.ldy = lddx;
+    p.cpart = (const float *)workspace;
+    p.colsum = dbias;
+    p.cblocks = w4::lin_dact_blocks(M);
     return map_err(w4::launch_lin(w4::LIN_T, p, dt, (uint8_t *)workspace + dact_bytes(M, N), s));
 }
 

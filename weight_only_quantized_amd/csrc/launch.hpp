@@ -176,6 +176,9 @@ struct LinArgs {
     float *part;                // partial sums [slices][M][cols] (slices > 1)
     int slices, stages;         // stages (decode kernel: 128-row groups) per slice
     int mtiles, ntiles;
+    const float *cpart;         // transposed: partial column sums [cblocks][N] of d
+    float *colsum;              // and where their sums go, or NULL
+    int cblocks;
 };
 // Workspace of a product (partial sums of its slices), 0 if it runs in one.
 size_t lin_workspace_bytes(int mode, int64_t M, int64_t K, int64_t N);
@@ -186,11 +189,14 @@ size_t lin_small_workspace_bytes(int mode, int64_t M, int64_t K, int64_t N);
 hipError_t launch_lin_small(int mode, LinArgs p, int dt, void *workspace, hipStream_t stream);
 // Sum of the slices in p.part and the finishing step.
 hipError_t launch_lin_join(int mode, const LinArgs &p, int dt, hipStream_t stream);
-// d = gradient of the pre-activation h (glu: both halves), and its column
-// sums in fp32.  d is written unless act == NONE without a gate; colsum may be
-// NULL; part: lin_dact_workspace_bytes() of scratch (used with colsum only).
+// d = gradient of the pre-activation h (glu: both halves); d is written unless
+// act == NONE without a gate.  part (or NULL): one row of partial column sums
+// of d per row block, lin_dact_workspace_bytes() in all; the transposed product
+// adds them up (cpart, cblocks, colsum).
+int lin_dact_blocks(int64_t M);
 size_t lin_dact_workspace_bytes(int64_t M, int64_t N);
-hipError_t launch_lin_dact(bool glu, const uint16_t *dy, int64_t lddy, const uint16_t *h, uint16_t *d, float *colsum,
-                           int64_t M, int64_t N, int act, int dt, void *part, hipStream_t stream);
+hipError_t launch_lin_dact(bool glu, const uint16_t *dy, int64_t lddy, const uint16_t *h, uint16_t *d, int64_t M,
+                           int64_t N, int act, int dt, float *part, hipStream_t stream);
+hipError_t launch_lin_zero_colsum(float *colsum, int64_t N, hipStream_t stream);
 
 }  // namespace w4

@@ -30,6 +30,13 @@ __device__ __forceinline__ int key_row(int r) { return (r & 7) ^ ((r >> 3) & 1);
 // apart for the writes.
 __device__ __forceinline__ int key_t(int n) { return (n & 3) << 2 | (n & 2) | ((n >> 2) & 1); }
 
+// Orders LDS accesses of one wave for the compiler (the hardware keeps a wave's
+// LDS operations in order): lanes exchange values through wave-private LDS.
+__device__ __forceinline__ void wave_lds_sync() {
+    __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+    __builtin_amdgcn_wave_barrier();
+}
+
 // Matrix-core step whose sources stay live past it (the destination must not
 // share their registers), without ordering it against memory operations.
 template <int DT>
@@ -43,6 +50,31 @@ __device__ __forceinline__ f32x16_t mfma_step(const u32x4_t &a, const u32x4_t &b
                                                    0, 0);
     asm("" : "+v"(r) : "v"(a), "v"(b));
     return r;
+}
+
+// colsum[c] = sum over the row blocks' partial sums of 64 columns: each of the
+// NW waves takes a contiguous share of the blocks, and the waves' sums meet in
+// LDS in order.
+template <int NW>
+__device__ __forceinline__ void colsum_body(const float *part, float *colsum, int64_t N, int blocks, int64_t c0,
+                                            float *red) {
+    const int tx = threadIdx.x & 63, ty = threadIdx.x >> 6;
+    const int64_t c = c0 + tx;                         // N is a multiple of 64
+    const int per = (blocks + NW - 1) / NW, b0 = ty * per, b1 = b0 + per < blocks ? b0 + per : blocks;
+    float s = 0.f;
+    for (int b = b0; b < b1; ++b) s += part[(int64_t)b * N + c];
+    red[ty * 64 + tx] = s;
+    __syncthreads();
+    if (ty == 0) {
+#pragma unroll
+        for (int y = 1; y < NW; ++y) s += red[y * 64 + tx];
+        colsum[c] = s;
+    }
+}
+
+__global__ void __launch_bounds__(512) lin_colsum_kernel(const float *part, float *colsum, int64_t N, int blocks) {
+    __shared__ float red[8 * 64];
+    colsum_body<8>(part, colsum, N, blocks, (int64_t)blockIdx.x * 64, red);
 }
 
 template <int DT, int MODE, int BM, int BN>
@@ -70,9 +102,18 @@ __global__ void __launch_bounds__(2 * BN, 2) lin_wide_kernel(const LinArgs p) {
     // ---- tile of this workgroup ------------------------------------------------
     // XCD x takes a contiguous share of the list (slices, then groups of four row
     // tiles by column tile by row tile): the workgroups of one L2 share operands.
-    const uint32_t total = gridDim.x, id = blockIdx.x, xcd = id % kXcd;
+    const uint32_t tiles = (uint32_t)p.mtiles * (uint32_t)p.ntiles, total = tiles * (uint32_t)p.slices;
+    const uint32_t id = blockIdx.x, xcd = id % kXcd;
+    if constexpr (T) {
+        // workgroups past the product's: the bias gradient, 64 columns each (one
+        // launch less than a kernel of its own)
+        if (id >= total) {
+            colsum_body<NT / 64>(p.cpart, p.colsum, p.N, p.cblocks, (int64_t)(id - total) * 64,
+                                 reinterpret_cast<float *>(lds));
+            return;
+        }
+    }
     const uint32_t r8 = total % kXcd, idx = xcd * (total / kXcd) + (xcd < r8 ? xcd : r8) + id / kXcd;
-    const uint32_t tiles = (uint32_t)p.mtiles * (uint32_t)p.ntiles;
     constexpr uint32_t GM = 4;
     const int slice = (int)(idx / tiles);
     const uint32_t tile = idx - slice * tiles;
@@ -198,9 +239,9 @@ __global__ void __launch_bounds__(2 * BN, 2) lin_wide_kernel(const LinArgs p) {
             const float as_ = __builtin_fabsf(s);
             live = !((as_ < 0x1p-60f * smax) | (as_ < 0x1p-126f));      // NaN stays
             float ratio = se * __builtin_amdgcn_rcpf(s);
-            ratio = live & (s != se) ? ratio : 1.f;
+            ratio = (live & (s != se)) ? ratio : 1.f;
             se = live ? s : se;
-            smax = live & (as_ > smax) ? as_ : smax;
+            smax = (live & (as_ > smax)) ? as_ : smax;
             s_ratio[wcol] = ratio;                    // both lanes of a column write the same value
         }
         dq.s = s;
@@ -445,7 +486,7 @@ __global__ void __launch_bounds__(2 * BN, 2) lin_wide_kernel(const LinArgs p) {
 #pragma unroll
             for (int r = 0; r < 16; ++r)
                 ot[(8 * (r >> 2) + 4 * kg + (r & 3)) * OUTROW + ct * 32 + l31] = acc[rt][ct][r] * scl[ct];
-        __syncthreads();
+        wave_lds_sync();
         const int64_t rbase = row0 + wm * (BM / 2) + rt * 32;
         if constexpr (MODE == LIN_GLU) {
             const int64_t c0 = nt * (BN / 2) + wn * 32;
@@ -488,7 +529,7 @@ __global__ void __launch_bounds__(2 * BN, 2) lin_wide_kernel(const LinArgs p) {
                 }
             }
         }
-        __syncthreads();
+        wave_lds_sync();
     }
 }
 
@@ -519,7 +560,7 @@ __global__ void __launch_bounds__(256) lin_join_kernel(const LinArgs p) {
 // workgroup takes 512 columns (glu: of each half) and every gridDim.y-th block
 // of four rows; a thread owns 8 columns of one row in each block and sums its
 // rows in ascending order.  The four rows' sums meet in LDS, the workgroups'
-// sums in lin_colsum_kernel: every sum has a fixed order.
+// sums in the product's extra workgroups: every sum has a fixed order.
 template <int DT, bool GLU>
 __global__ void __launch_bounds__(256)
 lin_dact_kernel(const uint16_t *dy, int64_t lddy, const uint16_t *h, uint16_t *d, float *part, int64_t M, int64_t N,
@@ -583,25 +624,6 @@ lin_dact_kernel(const uint16_t *dy, int64_t lddy, const uint16_t *h, uint16_t *d
     }
 }
 
-// colsum[c] = sum over the row blocks' partial sums: 64 columns per workgroup,
-// each of its 16 waves takes a contiguous share of the blocks, and the waves'
-// sums meet in LDS in order.
-__global__ void __launch_bounds__(1024) lin_colsum_kernel(const float *part, float *colsum, int64_t N, int blocks) {
-    __shared__ float red[16][64];
-    const int tx = threadIdx.x & 63, ty = threadIdx.x >> 6;
-    const int64_t c = (int64_t)blockIdx.x * 64 + tx;       // N is a multiple of 64
-    const int per = (blocks + 15) / 16, b0 = ty * per, b1 = b0 + per < blocks ? b0 + per : blocks;
-    float s = 0.f;
-    for (int b = b0; b < b1; ++b) s += part[(int64_t)b * N + c];
-    red[ty][tx] = s;
-    __syncthreads();
-    if (ty == 0) {
-#pragma unroll
-        for (int y = 1; y < 16; ++y) s += red[y][tx];
-        colsum[c] = s;
-    }
-}
-
 // ---- plans and launches ---------------------------------------------------------
 
 struct WidePlan { int bm, bn; int slices, stages, mtiles, ntiles; };
@@ -660,8 +682,9 @@ size_t lin_workspace_bytes(int mode, int64_t M, int64_t K, int64_t N) {
 template <int DT, int MODE>
 static hipError_t wide_launch(const LinArgs &p, int bm, int bn, hipStream_t stream) {
     const int64_t total = (int64_t)p.mtiles * p.ntiles * p.slices;
-    if (total > INT32_MAX) return hipErrorInvalidConfiguration;
-    const dim3 grid((unsigned)total), block(2 * bn);
+    const int64_t extra = MODE == LIN_T && p.colsum ? p.N / 64 : 0;
+    if (total + extra > INT32_MAX) return hipErrorInvalidConfiguration;
+    const dim3 grid((unsigned)(total + extra)), block(2 * bn);
     if (bm == 64 && bn == 128) hipLaunchKernelGGL((lin_wide_kernel<DT, MODE, 64, 128>), grid, block, 0, stream, p);
     else if (bm == 128 && bn == 128) hipLaunchKernelGGL((lin_wide_kernel<DT, MODE, 128, 128>), grid, block, 0, stream, p);
     else if (bm == 128 && bn == 256) hipLaunchKernelGGL((lin_wide_kernel<DT, MODE, 128, 256>), grid, block, 0, stream, p);
@@ -704,37 +727,32 @@ hipError_t launch_lin(int mode, LinArgs p, int dt, void *workspace, hipStream_t 
 
 // Row blocks of the activation gradient, one partial row of column sums each:
 // one row per thread (four per block) up to 64 blocks.
-static int dact_blocks(int64_t M) {
+int lin_dact_blocks(int64_t M) {
     const int64_t b = (M + 3) / 4;
     return (int)(b < 1 ? 1 : b > 64 ? 64 : b);
 }
 
-size_t lin_dact_workspace_bytes(int64_t M, int64_t N) { return (size_t)dact_blocks(M) * (size_t)N * sizeof(float); }
+size_t lin_dact_workspace_bytes(int64_t M, int64_t N) { return (size_t)lin_dact_blocks(M) * (size_t)N * sizeof(float); }
 
-hipError_t launch_lin_dact(bool glu, const uint16_t *dy, int64_t lddy, const uint16_t *h, uint16_t *d, float *colsum,
-                           int64_t M, int64_t N, int act, int dt, void *part, hipStream_t stream) {
+hipError_t launch_lin_dact(bool glu, const uint16_t *dy, int64_t lddy, const uint16_t *h, uint16_t *d, int64_t M,
+                           int64_t N, int act, int dt, float *part, hipStream_t stream) {
     const int64_t W = glu ? N / 2 : N;
-    int blocks = 0;
-    if (M > 0) {
-        blocks = dact_blocks(M);
-        const dim3 grid((unsigned)((W + 511) / 512), (unsigned)blocks);
-        float *ps = colsum ? (float *)part : nullptr;
+    const dim3 grid((unsigned)((W + 511) / 512), (unsigned)lin_dact_blocks(M));
 #define W4_DACT(DTV, GLUV)                                                                                       \
-    hipLaunchKernelGGL((lin_dact_kernel<DTV, GLUV>), grid, dim3(256), 0, stream, dy, lddy, h, d, ps, M, N, act)
-        if (dt == DT_BF16) {
-            if (glu) W4_DACT(DT_BF16, true);
-            else W4_DACT(DT_BF16, false);
-        } else {
-            if (glu) W4_DACT(DT_F16, true);
-            else W4_DACT(DT_F16, false);
-        }
-#undef W4_DACT
-        hipError_t err = hipGetLastError();
-        if (err != hipSuccess) return err;
+    hipLaunchKernelGGL((lin_dact_kernel<DTV, GLUV>), grid, dim3(256), 0, stream, dy, lddy, h, d, part, M, N, act)
+    if (dt == DT_BF16) {
+        if (glu) W4_DACT(DT_BF16, true);
+        else W4_DACT(DT_BF16, false);
+    } else {
+        if (glu) W4_DACT(DT_F16, true);
+        else W4_DACT(DT_F16, false);
     }
-    if (!colsum) return hipSuccess;
-    hipLaunchKernelGGL(lin_colsum_kernel, dim3((unsigned)(N / 64)), dim3(1024), 0, stream, (const float *)part,
-                       colsum, N, blocks);
+#undef W4_DACT
+    return hipGetLastError();
+}
+
+hipError_t launch_lin_zero_colsum(float *colsum, int64_t N, hipStream_t stream) {
+    hipLaunchKernelGGL(lin_colsum_kernel, dim3((unsigned)(N / 64)), dim3(512), 0, stream, nullptr, colsum, N, 0);
     return hipGetLastError();
 }
 

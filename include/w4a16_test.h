@@ -102,6 +102,12 @@ int w4a16_test_mx_tile_config(int idx);
 /* Name of the kernel variant the dispatcher picks for a dense call. */
 const char *w4a16_test_variant_name(int64_t M, int64_t K, int64_t N, int dt, int has_zero);
 
+/* Fused linear operators: force a tile shape (index below the returned count;
+ * such calls also take the tile kernel at decode sizes) and a slice count
+ * (where the sizes allow it); shape -1 and slices 0 choose by size.  Workspace
+ * queries follow.  Returns the number of shapes. */
+int w4a16_test_linear_plan(int shape, int slices);
+
 #ifdef __cplusplus
 }
 #endif

@@ -219,6 +219,65 @@ def test_gradients_match_differences(glu, a):
         assert abs(num - got) <= sd + kink, (seed, num, got, sd)
 
 
+@pytest.fixture
+def plan():
+    """Forces a tile shape and slice count; back to the choice by size after the test."""
+    yield w4.w4a16_test_linear_plan
+    w4.w4a16_test_linear_plan(-1, 0)
+
+
+SHAPES = 4
+
+
+@pytest.mark.parametrize("slices", [1, 3])
+@pytest.mark.parametrize("shape", range(SHAPES))
+@pytest.mark.parametrize("dt", [F16, BF16])
+def test_every_tile_shape(plan, shape, slices, dt):
+    """Each tile shape, whole and in slices, on rows and columns that end inside
+    it: one row, a few, more than one tile; an odd number of 64-column stages in
+    the transposed product; scale groups of one and several 128-row groups."""
+    assert plan(-1, 0) == SHAPES
+    for M, K, N, group, zero in ((1, 768, 128, 128, True), (70, 768, 448, 384, False), (300, 1152, 640, 128, True)):
+        L = ref.layer(K, N, group, dt, zero, seed=M)
+        D = Dev(L)
+        plan(shape, slices)
+        x, r = ref.normal(M, K, 1.0, dt, 1), ref.normal(M, N, 1.0, dt, 2)
+        y, p = run_ep(D, x, GELU, r, save=True)
+        yr, pr = ref.ep(x, L, GELU, r)
+        ref.close(p, pr, ref.tol_ep(pr, pr, dt), "pre")
+        ref.close(y, yr, ref.tol_ep(yr, pr, dt), "ep")
+        h = ref.normal(M, N, 1.5, dt, 3)
+        dx, d, db = run_bwd(D, False, r, h, SILU)
+        rx, rd, rb = ref.ep_backward(r, h, L, SILU)
+        ref.close(dx, rx, ref.tol_dx(rx, rd, L, dt), "dx")
+        ref.close(db, rb, 2.0 ** -20 * (rd.abs().sum(0) + rd.abs().amax()), "dbias")
+        if N % 128 == 0:
+            y, h = run_glu(D, x, SILU, save=True)
+            yr, hr = ref.glu(x, L, SILU)
+            ref.close(y, yr, ref.tol_glu(yr, hr, dt), "glu")
+            ref.close(h, hr, ref.tol_ep(hr, hr, dt), "h")
+
+
+@pytest.mark.parametrize("shape", range(SHAPES))
+def test_every_tile_shape_holds_its_scales(plan, shape):
+    """The unit change of the tile kernel's sums (zero, tiny and huge scales) in
+    every shape, in whole calls and slices that start inside a scale group."""
+    K, N, M = 1024, 256, 150
+    for group, slices in ((128, 1), (512, 4)):
+        L = ref.layer(K, N, group, BF16, True, bias=False, seed=8)
+        s = L.scale.clone()
+        s[0, :16], s[-1, 8:32] = 0, 0
+        s[0, 32:48], s[-1, 40:56] = 2.0 ** 20, 2.0 ** -100
+        s[:, 64:96] *= torch.tensor([-1.0, 1.0]).repeat(16).to(s.dtype)
+        L.scale = s
+        plan(shape, slices)
+        x = ref.normal(M, K, 1.0, BF16, 1)
+        y, _ = run_ep(Dev(L), x, NONE)
+        yr, _ = ref.ep(x, L, NONE)
+        size = (x.double().square() @ L.weights().square()).sqrt()
+        ref.close(y, yr, ref.ULP[BF16] * 1.01 * yr.abs() + 8 * ref.SUM * size + 2.0 ** -134, "scales")
+
+
 def test_in_place_residual_and_gradients():
     """y may be the residual, dpre the saved pre, dx the addend."""
     for M in (9, 200):

@@ -586,6 +586,11 @@ const char *w4a16_test_variant_name(int64_t M, int64_t K, int64_t N, int dt, int
     return pick_variant(M, K) == 1 ? "gemm_small_kernel" : "gemm_tile_kernel";
 }
 
+int w4a16_test_linear_plan(int shape, int slices) {
+    w4::set_lin_plan(shape, slices);
+    return w4::lin_shape_count();
+}
+
 int w4a16_test_small_config(int idx) {
     w4::set_small_config(idx);
     return w4::small_config_count();

@@ -183,6 +183,9 @@ struct LinArgs {
 // Workspace of a product (partial sums of its slices), 0 if it runs in one.
 size_t lin_workspace_bytes(int mode, int64_t M, int64_t K, int64_t N);
 hipError_t launch_lin(int mode, LinArgs p, int dt, void *workspace, hipStream_t stream);
+// Test hook: force a tile shape (-1: by size) and a slice count (0: by size).
+int lin_shape_count();
+void set_lin_plan(int shape, int slices);
 // The decode-sized forward kernel (EP, GLU).
 bool lin_small_ok(int mode, int64_t M);
 size_t lin_small_workspace_bytes(int mode, int64_t M, int64_t K, int64_t N);

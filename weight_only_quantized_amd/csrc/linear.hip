@@ -1,5 +1,6 @@
 // linear.hip — products of the fused linear operators on tiles of 256 columns:
 // forward (x . W with its epilogue, plain or gated) and transposed (d . W^T).
+#include <atomic>
 #include <type_traits>
 
 #include "act.hpp"
@@ -629,28 +630,42 @@ lin_dact_kernel(const uint16_t *dy, int64_t lddy, const uint16_t *h, uint16_t *d
 struct WidePlan { int bm, bn; int slices, stages, mtiles, ntiles; };
 
 // Tile shape and slice count by estimated time.  A workgroup's stage takes
-// `alone` us on an otherwise empty compute unit and `shared` us of a full one
-// (`slots` of them are resident), plus `ends` us for its first loads and its
-// epilogue; slices write and read their fp32 sums at about 5 TB/s and cost
-// another launch.  The constants are fits to timings over M = 61..2048 on
-// matrices from 1024 x 2048 to 4096 x 28672 (each within about 10%): few tiles want
-// small ones and slices, many want the large one, whose dequantization serves
-// 256 rows (M = 512, 4096 x 28672 gated: 121 us against 155 with 128 x 128 tiles;
-// M = 256, 4096^2: 97 us unsliced with 256 x 256, 26 us with 64 x 128 and four slices).
+// `alone` us while compute units are idle and `shared` us of a busy one (three
+// 64 x 128 or two 128 x 128 workgroups share a compute unit, and the clock drops
+// under full matrix load), plus `ends` us for its first loads and its epilogue;
+// slices write and read their fp32 sums at about 5 TB/s and cost another launch.
+// The constants are fits to timings over 20 sizes (M = 20..4096, matrices from
+// 1024 x 1024 to 4096 x 28672, both directions); the choice is within 5% of the
+// best of all shapes and slice counts on them.  Few tiles want small ones and
+// slices, many the large one, whose dequantization serves 256 rows: M = 256,
+// 4096^2 24 us with 128 x 128 and four slices, 91 us with 256 x 256 unsliced;
+// M = 512, 4096 x 28672 118 us with 256 x 256, 178 us with 64 x 128.
+struct Shape { int bm, bn; double alone, shared, ends; };
+static constexpr Shape kShapes[] = {{64, 128, 0.50, 0.405, 1.0},
+                                    {128, 128, 0.64, 0.58, 2.0},
+                                    {128, 256, 0.88, 1.08, 4.0},
+                                    {256, 256, 1.38, 1.65, 8.0}};
+static std::atomic<int> g_lin_shape{-1}, g_lin_slices{0};     // test hook: -1 and 0 choose
+
+int lin_shape_count() { return (int)(sizeof(kShapes) / sizeof(kShapes[0])); }
+void set_lin_plan(int shape, int slices) {
+    g_lin_shape.store(shape, std::memory_order_relaxed);
+    g_lin_slices.store(slices, std::memory_order_relaxed);
+}
+
 static WidePlan wide_plan(int mode, int64_t M, int64_t K, int64_t N) {
-    struct Shape { int bm, bn, slots; double alone, shared, ends; };
-    static constexpr Shape kShapes[] = {{64, 128, 3, 0.59, 0.405, 1.0},
-                                        {128, 128, 2, 0.70, 0.59, 2.0},
-                                        {128, 256, 1, 1.08, 1.08, 4.0},
-                                        {256, 256, 1, 1.60, 1.60, 8.0}};
     static constexpr int kSlices[] = {1, 2, 3, 4, 6, 8, 12, 16};
     constexpr int64_t kCus = 256;
+    const int shape = g_lin_shape.load(std::memory_order_relaxed);
+    const int forced = g_lin_slices.load(std::memory_order_relaxed);
     const int64_t cols = mode == LIN_T ? K : N;
     const int nst = (int)((mode == LIN_T ? N : K) / kBK);
     WidePlan best{};
     double best_us = 0;
     for (const Shape &sh : kShapes)
         for (int want : kSlices) {
+            if (shape >= 0 && shape < lin_shape_count() && &sh != &kShapes[shape]) continue;
+            if (forced > 0 && want != 1 && want != forced) continue;
             WidePlan w{};
             w.bm = sh.bm;
             w.bn = sh.bn;
@@ -659,12 +674,13 @@ static WidePlan wide_plan(int mode, int64_t M, int64_t K, int64_t N) {
             w.stages = (nst + want - 1) / want;
             w.stages += w.stages & 1;                  // whole 128-row groups (forward)
             w.slices = (nst + w.stages - 1) / w.stages;
-            if (want > 1 && (w.slices != want || w.stages < 4)) continue;
-            const double n = (double)(((int64_t)w.mtiles * w.ntiles * w.slices + kCus - 1) / kCus);
-            const double one = w.stages * sh.alone + sh.ends, all = n * (w.stages * sh.shared + sh.ends);
+            if (want > 1 && (w.slices != want || (w.stages < 4 && want != forced))) continue;
+            const int64_t wgs = (int64_t)w.mtiles * w.ntiles * w.slices;
+            const double load = wgs <= kCus ? (double)wgs / kCus : (double)((wgs + kCus - 1) / kCus);
+            const double one = w.stages * sh.alone + sh.ends, all = load * (w.stages * sh.shared + sh.ends);
             double us = one > all ? one : all;
             if (w.slices > 1) us += 3.0 + 8e-6 / 5.0 * w.slices * (double)M * (double)cols;
-            if (best.bm == 0 || us < best_us) {
+            if (best.bm == 0 || us < best_us || want == forced) {
                 best = w;
                 best_us = us;
             }
@@ -672,9 +688,14 @@ static WidePlan wide_plan(int mode, int64_t M, int64_t K, int64_t N) {
     return best;
 }
 
+// A forced tile shape also takes the rows that the decode kernel would.
+static bool use_small(int mode, int64_t M) {
+    return lin_small_ok(mode, M) && g_lin_shape.load(std::memory_order_relaxed) < 0;
+}
+
 size_t lin_workspace_bytes(int mode, int64_t M, int64_t K, int64_t N) {
     if (M <= 0) return 0;
-    if (lin_small_ok(mode, M)) return lin_small_workspace_bytes(mode, M, K, N);
+    if (use_small(mode, M)) return lin_small_workspace_bytes(mode, M, K, N);
     const WidePlan w = wide_plan(mode, M, K, N);
     return w.slices > 1 ? (size_t)w.slices * (size_t)M * (size_t)(mode == LIN_T ? K : N) * sizeof(float) : 0;
 }
@@ -713,7 +734,7 @@ static hipError_t wide_dt(int mode, const LinArgs &p, const WidePlan &w, hipStre
 }
 
 hipError_t launch_lin(int mode, LinArgs p, int dt, void *workspace, hipStream_t stream) {
-    if (lin_small_ok(mode, p.M)) return launch_lin_small(mode, p, dt, workspace, stream);
+    if (use_small(mode, p.M)) return launch_lin_small(mode, p, dt, workspace, stream);
     const WidePlan w = wide_plan(mode, p.M, p.K, p.N);
     p.slices = w.slices;
     p.stages = w.stages;

@@ -36,7 +36,8 @@
  *    prepacked by w4a16_prepack_g with that group size; exactly 128 for the
  *    MSD path (whose page fixes the group at 128 rows) and the MoE chain.  M == 0 (or an expert without rows) is a
  *    no-op that returns W4A16_OK.
- *  - Alignment: x, w_packed, workspace 16 bytes; scale, y 2 bytes.
+ *  - Alignment: x, w_packed, workspace 16 bytes; scale, y 2 bytes (the fused
+ *    linear operators state their own).
  *  - Errors: every argument is checked on the host before anything is
  *    enqueued; on error nothing is launched and y is untouched.  A launch
  *    failure reported by the runtime maps to W4A16_ERR_DEVICE, as does a
@@ -485,9 +486,11 @@ typedef struct {
  *   residual  [M][N], row stride ldr, or NULL; may be y itself
  *   pre       out, [M][N], p rounded to dt for the backward pass, or NULL
  *   y         out, [M][N], row stride ldy
- * Every output is rounded once from fp32.  M <= 64 runs a decode kernel whose
+ * Every output is rounded once from fp32.  M <= 32 runs a decode kernel whose
  * waves split K, larger M a tile kernel; where the tiles would leave compute
- * units idle K is cut into slices whose fp32 sums meet in the workspace.
+ * units idle K is cut into slices whose fp32 sums meet in the workspace.  (The
+ * tile kernel takes a scale below 2^-60 of a larger one before it in its column,
+ * or below 2^-126, as zero.)
  */
 size_t w4a16_gemm_ep_workspace_bytes(const w4a16_linear *lin, int64_t M);
 

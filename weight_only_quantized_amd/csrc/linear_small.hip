@@ -1,10 +1,26 @@
-// linear_small.hip — decode-sized products of the fused linear operators:
-// y = act(x . W + bias) + residual and a = act(g) * u for a few rows.
+// linear_small.hip — decode kernel of the fused linear operators: up to 32 rows
+// of y = act(x . W + bias) + residual or a = act(g) * u.
 //
 // A workgroup owns NB 16-column blocks (GLU: NB / 2 gate blocks and the up
-// blocks of the same columns) and all of K; its waves take the 128-row groups
-// in turn (wave w: groups w, w + W, ...), so that at any moment they read
-// consecutive kilobytes of each column block.
+// blocks of the same columns) and all of K or a slice of it; its waves take the
+// 128-row groups in turn (wave w: groups w, w + W, ...), so that at any moment
+// they read consecutive kilobytes of each column block.  Two groups are on the
+// way per wave: NB 16-byte slots of W per lane, x straight in operand order,
+// one scale and one zero point per lane (lane l those of column l % (16 NB),
+// handed to the lane that needs them by a lane permute).  The waves' sums meet in
+// LDS in wave order and every output is finished and rounded once.
+//
+// Codes enter the matrix core (16 x 16 x 32 steps, rows padded to 16 MT) as
+// exact integers: fp16 as u - z, bf16 as 128 + u, the pattern that one byte
+// permute makes; four more steps with ones give the row sums of x, and
+// (128 + z) times them is subtracted in fp32.  The group's scale multiplies the
+// fp32 sum.  An infinite x therefore gives NaN in its row.
+//
+// Bound: the weight stream at the start (latency) and through the launch.
+// Measured (bf16, zero points): gated 4096 x 28672, one row 12.8 us (61 MB, 4.8
+// TB/s, the rate of a large copy), 16 rows 14.7 us; 14336 x 4096, one row 8.1 us
+// (3.8 TB/s).  More groups on the way and bounded buffer loads measured slower
+// (8.7 -> 9.9 us and more for 14336 x 4096).
 #include "act.hpp"
 
 namespace w4 {

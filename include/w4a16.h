@@ -455,7 +455,8 @@ w4a16_status w4a8_mxfp4_grouped_gemm(const void *x, const int32_t *expert_offset
  *    row length and at most 2^22; 0 means rows without gaps.  Saved pre-activations and
  *    their gradients (pre, h, dpre, dh) and dbias have no gaps.
  *  - x must be finite for a finite result row (the bf16 decode kernel gives
- *    NaN, not infinity, in the row of an infinite x).
+ *    NaN, not infinity, in the row of an infinite x); other rows are not
+ *    affected.
  *  - workspace: device, 16-byte aligned, at least the size the matching
  *    query returns for the same (lin, M); may be NULL when that is 0.  Its
  *    contents on entry are ignored.  Calls sharing one must be ordered on one

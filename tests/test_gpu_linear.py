@@ -161,6 +161,11 @@ BACKWARD = [
     (129, 256, 1152, 128, F16, True, SILU, False, False),
     (258, 1152, 256, 384, BF16, False, GELU, True, True),
     (515, 512, 1088, 512, F16, False, NONE, True, False),
+    # few rows: one block of columns, odd blocks, N cut into slices
+    (2, 128, 64, 128, F16, True, GELU, False, True),
+    (17, 384, 320, 384, BF16, False, NONE, True, True),
+    (32, 128, 4224, 128, BF16, True, SILU, True, False),
+    (31, 256, 6528, 256, F16, False, RELU, False, True),
 ]
 
 

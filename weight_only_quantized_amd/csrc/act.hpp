@@ -1,7 +1,6 @@
 // act.hpp — activations of the fused linear operators and what their kernels
-// share: the operand description, and the finishing step (bias, activation,
-// gated product, residual) applied to fp32 sums before the one rounding to
-// the activation dtype.
+// share: the finishing step (bias, activation, gated product, residual) applied
+// to fp32 sums before the one rounding to the activation dtype, and LDS helpers.
 #pragma once
 
 #include "common.hpp"
@@ -151,6 +150,41 @@ __device__ __forceinline__ void finish_glu(const LinArgs &p, float (&g)[V], floa
 #pragma unroll
     for (int i = 0; i < V; ++i) g[i] *= u[i];
     store_vec<DT, V>(p.y + row * p.ldy + col, g);
+}
+
+typedef short v4s_t __attribute__((__vector_size__(8)));
+typedef v4s_t __attribute__((address_space(3))) *lds_v4s_ptr;
+
+// Four 16-bit elements of one column from four LDS rows: the 16 lanes of a
+// group read 4 rows x 16 columns (lane 4 r + c addresses row r, columns 4 c ..)
+// and lane i gets column i.
+__device__ __forceinline__ u32x2_t lds_tr16(const uint8_t *p) {
+    return __builtin_bit_cast(u32x2_t, __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_v4s_ptr)(v4s_t *)(uint8_t *)p));
+}
+
+// Orders LDS accesses of one wave for the compiler (the hardware keeps a wave's
+// LDS operations in order): lanes exchange values through wave-private LDS.
+__device__ __forceinline__ void wave_lds_sync() {
+    __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+    __builtin_amdgcn_wave_barrier();
+}
+
+// colsum[c] = sum over the row blocks' partial sums of 64 columns: each wave of
+// the workgroup takes a contiguous share of the blocks, and the waves' sums meet
+// in LDS (64 floats per wave) in order.
+__device__ __forceinline__ void colsum_body(const float *part, float *colsum, int64_t N, int blocks, int64_t c0,
+                                            float *red) {
+    const int tx = threadIdx.x & 63, ty = threadIdx.x >> 6, nw = blockDim.x >> 6;
+    const int64_t c = c0 + tx;                         // N is a multiple of 64
+    const int per = (blocks + nw - 1) / nw, b0 = ty * per, b1 = b0 + per < blocks ? b0 + per : blocks;
+    float s = 0.f;
+    for (int b = b0; b < b1; ++b) s += part[(int64_t)b * N + c];
+    red[ty * 64 + tx] = s;
+    __syncthreads();
+    if (ty == 0) {
+        for (int y = 1; y < nw; ++y) s += red[y * 64 + tx];
+        colsum[c] = s;
+    }
 }
 
 }  // namespace w4

@@ -156,6 +156,7 @@ hipError_t launch_fzero_corr(const void *x, const void *scale, const void *zf, i
 //   transposed  A = d [M][N], columns = K of W, y = d . W^T + res
 enum { ACT_NONE = 0, ACT_RELU = 1, ACT_SILU = 2, ACT_GELU = 3, ACT_GELU_TANH = 4 };
 enum { LIN_EP = 0, LIN_GLU = 1, LIN_T = 2 };
+inline bool lin_transposed(int mode) { return mode == LIN_T; }
 struct LinArgs {
     const uint16_t *a;          // A operand, row stride lda
     int64_t lda;
@@ -186,8 +187,8 @@ hipError_t launch_lin(int mode, LinArgs p, int dt, void *workspace, hipStream_t 
 // Test hook: force a tile shape (-1: by size) and a slice count (0: by size).
 int lin_shape_count();
 void set_lin_plan(int shape, int slices);
-// The decode-sized forward kernel (EP, GLU).
-bool lin_small_ok(int mode, int64_t M);
+// The decode-sized kernels.
+bool lin_small_ok(int mode, int64_t M, int64_t K, int64_t N);
 size_t lin_small_workspace_bytes(int mode, int64_t M, int64_t K, int64_t N);
 hipError_t launch_lin_small(int mode, LinArgs p, int dt, void *workspace, hipStream_t stream);
 // Sum of the slices in p.part and the finishing step.

@@ -49,16 +49,6 @@ namespace w4 {
 constexpr int kXcd = 8;              // XCDs; workgroups go to them round-robin
 constexpr int kBK = 64;              // contraction elements per stage
 
-typedef short v4s_t __attribute__((__vector_size__(8)));
-typedef v4s_t __attribute__((address_space(3))) *lds_v4s_ptr;
-
-// Four 16-bit elements of one column from four LDS rows: the 16 lanes of a
-// group read 4 rows x 16 columns (lane 4 r + c addresses row r, columns 4 c ..)
-// and lane i gets column i.
-__device__ __forceinline__ u32x2_t lds_tr16(const uint8_t *p) {
-    return __builtin_bit_cast(u32x2_t, __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_v4s_ptr)(v4s_t *)(uint8_t *)p));
-}
-
 // LDS swizzles: 16-byte chunk c of row r sits at chunk c ^ key(r) of its row.
 // Writes move 128 bytes a cycle (8 lanes), 16-byte reads 256 (16 lanes).
 // Rows of 128 bytes (A, forward W; read and written down 16 and 8 rows at one
@@ -69,13 +59,6 @@ __device__ __forceinline__ int key_row(int r) { return (r & 7) ^ ((r >> 3) & 1);
 // x 4 chunks): bits 2, 3 tell 4 rows apart for the reads, bits 0..2 tell 8 rows
 // apart for the writes.
 __device__ __forceinline__ int key_t(int n) { return (n & 3) << 2 | (n & 2) | ((n >> 2) & 1); }
-
-// Orders LDS accesses of one wave for the compiler (the hardware keeps a wave's
-// LDS operations in order): lanes exchange values through wave-private LDS.
-__device__ __forceinline__ void wave_lds_sync() {
-    __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
-    __builtin_amdgcn_wave_barrier();
-}
 
 // Matrix-core step whose sources stay live past it (the destination must not
 // share their registers), without ordering it against memory operations.
@@ -92,29 +75,9 @@ __device__ __forceinline__ f32x16_t mfma_step(const u32x4_t &a, const u32x4_t &b
     return r;
 }
 
-// colsum[c] = sum over the row blocks' partial sums of 64 columns: each of the
-// NW waves takes a contiguous share of the blocks, and the waves' sums meet in
-// LDS in order.
-template <int NW>
-__device__ __forceinline__ void colsum_body(const float *part, float *colsum, int64_t N, int blocks, int64_t c0,
-                                            float *red) {
-    const int tx = threadIdx.x & 63, ty = threadIdx.x >> 6;
-    const int64_t c = c0 + tx;                         // N is a multiple of 64
-    const int per = (blocks + NW - 1) / NW, b0 = ty * per, b1 = b0 + per < blocks ? b0 + per : blocks;
-    float s = 0.f;
-    for (int b = b0; b < b1; ++b) s += part[(int64_t)b * N + c];
-    red[ty * 64 + tx] = s;
-    __syncthreads();
-    if (ty == 0) {
-#pragma unroll
-        for (int y = 1; y < NW; ++y) s += red[y * 64 + tx];
-        colsum[c] = s;
-    }
-}
-
 __global__ void __launch_bounds__(512) lin_colsum_kernel(const float *part, float *colsum, int64_t N, int blocks) {
     __shared__ float red[8 * 64];
-    colsum_body<8>(part, colsum, N, blocks, (int64_t)blockIdx.x * 64, red);
+    colsum_body(part, colsum, N, blocks, (int64_t)blockIdx.x * 64, red);
 }
 
 template <int DT, int MODE, int BM, int BN>
@@ -148,8 +111,7 @@ __global__ void __launch_bounds__(2 * BN, 2) lin_wide_kernel(const LinArgs p) {
         // workgroups past the product's: the bias gradient, 64 columns each (one
         // launch less than a kernel of its own)
         if (id >= total) {
-            colsum_body<NT / 64>(p.cpart, p.colsum, p.N, p.cblocks, (int64_t)(id - total) * 64,
-                                 reinterpret_cast<float *>(lds));
+            colsum_body(p.cpart, p.colsum, p.N, p.cblocks, (int64_t)(id - total) * 64, reinterpret_cast<float *>(lds));
             return;
         }
     }
@@ -734,13 +696,13 @@ static WidePlan wide_plan(int mode, int64_t M, int64_t K, int64_t N) {
 }
 
 // A forced tile shape also takes the rows that the decode kernel would.
-static bool use_small(int mode, int64_t M) {
-    return lin_small_ok(mode, M) && g_lin_shape.load(std::memory_order_relaxed) < 0;
+static bool use_small(int mode, int64_t M, int64_t K, int64_t N) {
+    return lin_small_ok(mode, M, K, N) && g_lin_shape.load(std::memory_order_relaxed) < 0;
 }
 
 size_t lin_workspace_bytes(int mode, int64_t M, int64_t K, int64_t N) {
     if (M <= 0) return 0;
-    if (use_small(mode, M)) return lin_small_workspace_bytes(mode, M, K, N);
+    if (use_small(mode, M, K, N)) return lin_small_workspace_bytes(mode, M, K, N);
     const WidePlan w = wide_plan(mode, M, K, N);
     return w.slices > 1 ? (size_t)w.slices * (size_t)M * (size_t)(mode == LIN_T ? K : N) * sizeof(float) : 0;
 }
@@ -779,7 +741,7 @@ static hipError_t wide_dt(int mode, const LinArgs &p, const WidePlan &w, hipStre
 }
 
 hipError_t launch_lin(int mode, LinArgs p, int dt, void *workspace, hipStream_t stream) {
-    if (use_small(mode, p.M)) return launch_lin_small(mode, p, dt, workspace, stream);
+    if (use_small(mode, p.M, p.K, p.N)) return launch_lin_small(mode, p, dt, workspace, stream);
     const WidePlan w = wide_plan(mode, p.M, p.K, p.N);
     p.slices = w.slices;
     p.stages = w.stages;

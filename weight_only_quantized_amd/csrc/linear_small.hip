@@ -1,7 +1,7 @@
-// linear_small.hip — decode kernel of the fused linear operators: up to 32 rows
-// of y = act(x . W + bias) + residual or a = act(g) * u.
+// linear_small.hip — decode kernels of the fused linear operators: up to 32 rows
+// of y = act(x . W + bias) + residual or a = act(g) * u, and of d . W^T.
 //
-// A workgroup owns NB 16-column blocks (GLU: NB / 2 gate blocks and the up
+// Forward (lin_small_kernel): a workgroup owns NB 16-column blocks (GLU: NB / 2 gate blocks and the up
 // blocks of the same columns) and all of K or a slice of it; its waves take the
 // 128-row groups in turn (wave w: groups w, w + W, ...), so that at any moment
 // they read consecutive kilobytes of each column block.  Two groups are on the
@@ -28,6 +28,12 @@ namespace w4 {
 constexpr int kSmallWaves = 8;       // most waves per workgroup
 constexpr int64_t kSmallMaxM = 32;   // rows of the decode kernel
 
+// A byte offset past the end of every buffer (at most 2^31 bytes).
+constexpr uint32_t kPast = 0xFFFFFF00u;
+__device__ __forceinline__ u32x4_t buffer_ld128(__amdgpu_buffer_rsrc_t buf, uint32_t off) {
+    return __builtin_bit_cast(u32x4_t, __builtin_amdgcn_raw_buffer_load_b128(buf, (int)off, 0, 0));
+}
+
 template <int DT, bool GLU, int NB, int MT>
 __global__ void __launch_bounds__(kSmallWaves * 64) lin_small_kernel(const LinArgs p) {
     static_assert(!GLU || NB % 2 == 0, "gate and up blocks in pairs");
@@ -49,13 +55,18 @@ __global__ void __launch_bounds__(kSmallWaves * 64) lin_small_kernel(const LinAr
         return (int64_t)blockIdx.x * (16 * NB) + b * 16;
     };
 
-    // rows past M read row M - 1; their results are not stored
-    const uint16_t *xrow[MT];
+    // Rows past M and groups past the end: with one row tile they read row M - 1
+    // and the last group again (few lines, in L2); with two, where that would be
+    // many lines, they are requested past the end of x's buffer, which gives zeros
+    // without a memory access (M = 32: 1024^2 7.4 -> 5.5 us, 4096^2 12.6 -> 11.6;
+    // one row 8.7 -> 10.1 us for 14336 x 4096 if x and W did so).
+    const __amdgpu_buffer_rsrc_t xbuf = __builtin_amdgcn_make_buffer_rsrc(
+        const_cast<uint16_t *>(p.a), (short)0, (int)(((p.M - 1) * p.lda + p.K) * 2), 0x00020000);
+    uint32_t xoff[MT];
 #pragma unroll
-    for (int mt = 0; mt < MT; ++mt) {
-        const int64_t r = 16 * mt + j < p.M ? 16 * mt + j : p.M - 1;
-        xrow[mt] = p.a + r * p.lda + 32 * kc;
-    }
+    for (int mt = 0; mt < MT; ++mt)
+        xoff[mt] = 16 * mt + j < p.M ? (uint32_t)((16 * mt + j) * p.lda + 32 * kc) * 2u : kPast;
+    const uint16_t *const xrow = p.a + (j < p.M ? j : p.M - 1) * p.lda + 32 * kc;
     const uint8_t *wb[NB];
 #pragma unroll
     for (int b = 0; b < NB; ++b) wb[b] = p.wp + col_of(b) / 16 * Gall * kTileBytes + lane * 16;
@@ -73,10 +84,17 @@ __global__ void __launch_bounds__(kSmallWaves * 64) lin_small_kernel(const LinAr
         const int64_t so = (int64_t)(gc / p.gm) * p.N + scol;
         sr[d] = p.scale[so];
         zr[d] = zp[so >> 1];
+        if constexpr (MT == 1) {
 #pragma unroll
-        for (int mt = 0; mt < MT; ++mt)
+            for (int t = 0; t < 4; ++t) xa[d][0][t] = ld128(xrow + (int64_t)gc * kGroup + 8 * t);
+        } else {
 #pragma unroll
-            for (int t = 0; t < 4; ++t) xa[d][mt][t] = ld128(xrow[mt] + (int64_t)gc * kGroup + 8 * t);
+            for (int mt = 0; mt < MT; ++mt) {
+                const uint32_t xo = g < G && xoff[mt] != kPast ? xoff[mt] + g * (kGroup * 2) : kPast;
+#pragma unroll
+                for (int t = 0; t < 4; ++t) xa[d][mt][t] = buffer_ld128(xbuf, xo + 16 * t);
+            }
+        }
     };
 
     float yacc[NB][MT][4];
@@ -167,6 +185,153 @@ __global__ void __launch_bounds__(kSmallWaves * 64) lin_small_kernel(const LinAr
     }
 }
 
+// Transposed product for a few rows: y [M][K] = d . W^T (+ addend), M <= 32.
+//
+// A workgroup owns 32 output columns (one 32-row chunk of a 128-row group) and all
+// of N or a slice of it; its waves take blocks of 64 columns of W in turn.  Per
+// block a lane dequantizes 32 codes of one column to (u - z) s in the activation
+// dtype, the wave writes them as rows [n][32 k] of its own 4 KB of LDS and reads
+// them back transposed as the matrix-core operand (32 x 32 x 16 steps, rows of d
+// padded to 32); no barrier until the waves' sums meet in LDS in wave order.
+// 16-byte chunk c of row n sits at chunk c ^ (n / 2 % 4): writes of 8 rows at one
+// chunk and reads of 4 whole rows both touch different banks.
+//
+// Every workgroup reads all of d: K / 32 times M N 2 bytes, which bounds it for
+// many rows of large matrices; the weights' stream and the launch otherwise.
+// Measured (bf16): one row of 1024^2 5.8 us, of 4096^2 8.5 us, of 4096 x 28672 30 us;
+// 32 rows 7.2, 13.8 us.  The tile kernel with its slices takes 7.9, 11.9, 34 and
+// 8.7, 13.1 us; from M K N = 6e8 on it is the faster one.
+constexpr int kSmallTWaves = 16;
+
+template <int DT>
+__global__ void __launch_bounds__(kSmallTWaves * 64) lin_small_t_kernel(const LinArgs p) {
+    constexpr int D = 3;                              // blocks of 64 columns in flight per wave
+    const int W = blockDim.x >> 6;
+    const int lane = threadIdx.x & 63;
+    const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    const int j = lane & 15, qq = lane >> 4;
+    // 4 KB per wave for the operand; the sums use the same memory at the end
+    __shared__ __attribute__((aligned(16))) uint8_t lds[kSmallTWaves * 32 * 33 * 4];
+    static_assert(32 * 33 * 4 >= 4096, "operand fits in a wave's share");
+    if (blockIdx.x >= p.K / 32) {
+        // workgroups past the product's: the bias gradient, 64 columns each
+        if (blockIdx.y == 0)
+            colsum_body(p.cpart, p.colsum, p.N, p.cblocks, (int64_t)(blockIdx.x - p.K / 32) * 64,
+                        reinterpret_cast<float *>(lds));
+        return;
+    }
+    const int64_t G = p.K / kGroup, g = blockIdx.x >> 2;
+    const int c = blockIdx.x & 3;
+    // this workgroup's blocks: [b0, b1)
+    const int b0 = (int)blockIdx.y * p.stages, nblk = (int)(p.N / 64);
+    const int b1 = b0 + p.stages < nblk ? b0 + p.stages : nblk;
+
+    // Rows of d past M and blocks past the end are requested past the end of its
+    // buffer: zeros, without a memory access or a branch around the load (M = 32,
+    // 1024^2: 11.9 us with clamped loads, 7.2 so)
+    const __amdgpu_buffer_rsrc_t abuf = __builtin_amdgcn_make_buffer_rsrc(
+        const_cast<uint16_t *>(p.a), (short)0, (int)(((p.M - 1) * p.lda + p.N) * 2), 0x00020000);
+    const uint32_t aoff = (lane & 31) < p.M ? (uint32_t)((lane & 31) * p.lda + 8 * (lane >> 5)) * 2u : kPast;
+    const uint8_t *const wbase = p.wp + (qq * G + g) * kTileBytes + c * 256 + j * 16;
+    const int64_t srow = g / p.gm * p.N + qq * 16 + j;
+    const uint8_t *const zbase = p.zero ? p.zero : reinterpret_cast<const uint8_t *>(p.scale);
+
+    u32x4_t wr[D], ar[D][4];
+    uint32_t sr[D], zr[D];
+    auto load = [&](int d, int b) {
+        const bool in = b < b1;
+        const int64_t bc = in ? b : b1 - 1;
+        wr[d] = ld128(wbase + bc * (4 * G * kTileBytes));
+        const int64_t so = srow + bc * 64;
+        sr[d] = p.scale[so];
+        zr[d] = zbase[so >> 1];
+        const uint32_t ao = in && aoff != kPast ? aoff + b * 128 : kPast;
+#pragma unroll
+        for (int t = 0; t < 4; ++t) ar[d][t] = buffer_ld128(abuf, ao + 32 * t);
+    };
+
+    uint8_t *const mine = lds + wave * (32 * 33 * 4);
+    const int n = 16 * qq + j;                        // this lane's column of the block
+    uint8_t *const dst = mine + n * 64;
+    const int wkey = (n >> 1) & 3;
+    // transposing reads: rows 8 (lane / 32) + 4 h + lane % 16 / 4 of step t
+    const int tr = (lane & 15) >> 2, tc = lane & 3, ch = 2 * (qq & 1) + (tc >> 1);
+    const uint8_t *src[2];
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+        const int row = 8 * (qq >> 1) + 4 * h + tr;
+        src[h] = mine + row * 64 + ((ch ^ ((row >> 1) & 3)) << 4) + (tc & 1) * 8;
+    }
+
+    f32x16_t acc;
+#pragma unroll
+    for (int i = 0; i < 16; ++i) acc[i] = 0.f;
+    auto compute = [&](int d) {
+        const uint32_t z = p.zero ? __builtin_amdgcn_ubfe(zr[d], (uint32_t)(j & 1) * 4u, 4) : 8u;
+        const float s = h2f<DT>((uint16_t)sr[d]), zs = -(float)z * s;
+#pragma unroll
+        for (int t = 0; t < 4; ++t) {
+            u32x4_t o;
+            if constexpr (DT == DT_BF16) {
+                const uint32_t w = wr[d][t];
+                uint32_t lo = w & 0x0F0F0F0Fu, hi = (w >> 4) & 0x0F0F0F0Fu;
+                asm("" : "+v"(lo), "+v"(hi));         // one conversion per byte
+                float v[8];
+                v[0] = (float)(lo & 0xFFu), v[4] = (float)((lo >> 8) & 0xFFu);
+                v[1] = (float)((lo >> 16) & 0xFFu), v[5] = (float)(lo >> 24);
+                v[2] = (float)(hi & 0xFFu), v[6] = (float)((hi >> 8) & 0xFFu);
+                v[3] = (float)((hi >> 16) & 0xFFu), v[7] = (float)(hi >> 24);
+#pragma unroll
+                for (int i = 0; i < 8; ++i) v[i] = __builtin_fmaf(v[i], s, zs);
+#pragma unroll
+                for (int q = 0; q < 4; ++q) {
+                    const bf16x2_t b = {(__bf16)v[2 * q], (__bf16)v[2 * q + 1]};
+                    o[q] = __builtin_bit_cast(uint32_t, b);
+                }
+            } else {
+                o = dequant_word<DT>(wr[d][t], f16_negbias2(z));
+                const _Float16 m = (_Float16)s;
+                const f16x2_t m2 = {m, m};
+#pragma unroll
+                for (int i = 0; i < 4; ++i) o[i] = __builtin_bit_cast(uint32_t, as<f16x2_t>(o[i]) * m2);
+            }
+            *reinterpret_cast<u32x4_t *>(dst + ((t ^ wkey) << 4)) = o;
+        }
+        wave_lds_sync();
+#pragma unroll
+        for (int t = 0; t < 4; ++t) {
+            const u32x2_t x0 = lds_tr16(src[0] + t * 16 * 64), x1 = lds_tr16(src[1] + t * 16 * 64);
+            acc = mfma32x32x16<DT>(ar[d][t], u32x4_t{x0[0], x0[1], x1[0], x1[1]}, acc);
+        }
+        wave_lds_sync();
+    };
+
+#pragma unroll
+    for (int d = 0; d < D; ++d) load(d, b0 + wave + d * W);
+    for (int b = b0 + wave; b < b1; b += D * W) {
+#pragma unroll
+        for (int d = 0; d < D; ++d) {
+            if (b + d * W < b1) compute(d);
+            load(d, b + (d + D) * W);
+        }
+    }
+
+    // ---- sums of the waves, in wave order, then the finishing step ----------------
+    float *const red = reinterpret_cast<float *>(mine);
+#pragma unroll
+    for (int i = 0; i < 16; ++i) red[(8 * (i >> 2) + 4 * (lane >> 5) + (i & 3)) * 33 + (lane & 31)] = acc[i];
+    __syncthreads();
+    for (int i = threadIdx.x; i < 1024; i += blockDim.x) {
+        const int rr = i >> 5, cc = i & 31;
+        if (rr >= p.M) break;
+        float v[1] = {0.f};
+        for (int w = 0; w < W; ++w) v[0] += reinterpret_cast<const float *>(lds)[w * (32 * 33) + rr * 33 + cc];
+        const int64_t col = (int64_t)blockIdx.x * 32 + cc;
+        if (p.slices > 1) p.part[((int64_t)blockIdx.y * p.M + rr) * p.cols + col] = v[0];
+        else finish_ep<DT, 1>(p, v, rr, col);
+    }
+}
+
 // Column blocks per workgroup, waves, 16-row tiles and K slices of a call.
 struct SmallPlan { int nb, waves, mt, slices, groups; };
 
@@ -180,6 +345,19 @@ struct SmallPlan { int nb, waves, mt, slices, groups; };
 // x N 28672, M = 32: 26.9 -> 23.9 us), else eight (M = 1: 13.2 against 13.7 us).
 static SmallPlan small_plan(int mode, int64_t M, int64_t K, int64_t N) {
     SmallPlan s{};
+    if (lin_transposed(mode)) {
+        // slices of at least 32 blocks where K gives fewer than 128 workgroups
+        // (256 x 14336: 9.5 us in eight)
+        const int nblk = (int)(N / 64);
+        int64_t slices = 128 / (K / 32);
+        if (slices > nblk / 32) slices = nblk / 32;
+        if (slices > 8) slices = 8;
+        if (slices < 1) slices = 1;
+        s.groups = (int)((nblk + slices - 1) / slices);
+        s.slices = (nblk + s.groups - 1) / s.groups;
+        s.waves = s.groups < kSmallTWaves ? s.groups : kSmallTWaves;
+        return s;
+    }
     const int G = (int)(K / kGroup);
     s.mt = M <= 16 ? 1 : 2;
     s.nb = N / 64 >= 224 ? 4 : N / 32 >= 224 || mode == LIN_GLU ? 2 : 1;
@@ -196,11 +374,14 @@ static SmallPlan small_plan(int mode, int64_t M, int64_t K, int64_t N) {
     return s;
 }
 
-bool lin_small_ok(int mode, int64_t M) { return mode != LIN_T && M <= kSmallMaxM; }
+// The decode kernels' range (transposed: see there).
+bool lin_small_ok(int mode, int64_t M, int64_t K, int64_t N) {
+    return M <= kSmallMaxM && (!lin_transposed(mode) || M * K * N <= 600000000);
+}
 
 size_t lin_small_workspace_bytes(int mode, int64_t M, int64_t K, int64_t N) {
     const SmallPlan s = small_plan(mode, M, K, N);
-    return s.slices > 1 ? (size_t)s.slices * (size_t)M * (size_t)N * sizeof(float) : 0;
+    return s.slices > 1 ? (size_t)s.slices * (size_t)M * (size_t)(lin_transposed(mode) ? K : N) * sizeof(float) : 0;
 }
 
 template <int DT, bool GLU, int NB, int MT>
@@ -218,6 +399,11 @@ static hipError_t small_mt(const LinArgs &p, const SmallPlan &s, hipStream_t str
 
 template <int DT>
 static hipError_t small_dt(int mode, const LinArgs &p, const SmallPlan &s, hipStream_t stream) {
+    if (lin_transposed(mode)) {
+        const dim3 grid((unsigned)(p.cols / 32 + (p.colsum ? p.N / 64 : 0)), (unsigned)s.slices);
+        hipLaunchKernelGGL(lin_small_t_kernel<DT>, grid, dim3((unsigned)s.waves * 64), 0, stream, p);
+        return hipGetLastError();
+    }
     if (mode == LIN_GLU) {
         if (s.nb == 2) return small_mt<DT, true, 2>(p, s, stream);
         if (s.nb == 4) return small_mt<DT, true, 4>(p, s, stream);

@@ -634,7 +634,7 @@ lin_dact_kernel(const uint16_t *dy, int64_t lddy, const uint16_t *h, uint16_t *d
 
 // ---- plans and launches ---------------------------------------------------------
 
-struct WidePlan { int bm, bn; int slices, stages, mtiles, ntiles; };
+struct WidePlan { int bm, bn; int slices, stages, mtiles, ntiles; double us; };
 
 // Tile shape and slice count by estimated time.  A workgroup's stage takes
 // `alone` us while compute units are idle and `shared` us of a busy one (three
@@ -668,7 +668,6 @@ static WidePlan wide_plan(int mode, int64_t M, int64_t K, int64_t N) {
     const int64_t cols = mode == LIN_T ? K : N;
     const int nst = (int)((mode == LIN_T ? N : K) / kBK);
     WidePlan best{};
-    double best_us = 0;
     for (const Shape &sh : kShapes)
         for (int want : kSlices) {
             if (shape >= 0 && shape < lin_shape_count() && &sh != &kShapes[shape]) continue;
@@ -687,17 +686,20 @@ static WidePlan wide_plan(int mode, int64_t M, int64_t K, int64_t N) {
             const double one = w.stages * sh.alone + sh.ends, all = load * (w.stages * sh.shared + sh.ends);
             double us = one > all ? one : all;
             if (w.slices > 1) us += 3.0 + 8e-6 / 5.0 * w.slices * (double)M * (double)cols;
-            if (best.bm == 0 || us < best_us || want == forced) {
+            if (best.bm == 0 || us < best.us || want == forced) {
                 best = w;
-                best_us = us;
+                best.us = us;
             }
         }
     return best;
 }
 
-// A forced tile shape also takes the rows that the decode kernel would.
+// A forced tile shape also takes the rows that the decode kernels would.
 static bool use_small(int mode, int64_t M, int64_t K, int64_t N) {
-    return lin_small_ok(mode, M, K, N) && g_lin_shape.load(std::memory_order_relaxed) < 0;
+    if (g_lin_shape.load(std::memory_order_relaxed) >= 0) return false;
+    if (lin_small_ok(mode, M, K, N)) return true;
+    // (a launch and its first loads take the tile kernel 2.8 us besides its stages)
+    return M > 32 && lin_small_us(mode, M, K, N) < wide_plan(mode, M, K, N).us + 2.8;
 }
 
 size_t lin_workspace_bytes(int mode, int64_t M, int64_t K, int64_t N) {

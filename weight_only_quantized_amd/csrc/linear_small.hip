@@ -8,7 +8,8 @@
 // way per wave: NB 16-byte slots of W per lane, x straight in operand order,
 // one scale and one zero point per lane (lane l those of column l % (16 NB),
 // handed to the lane that needs them by a lane permute).  The waves' sums meet in
-// LDS in wave order and every output is finished and rounded once.
+// LDS in wave order and every output is finished and rounded once.  More than 16
+// MT rows of a small matrix lie as further row groups on the grid.
 //
 // Codes enter the matrix core (16 x 16 x 32 steps, rows padded to 16 MT) as
 // exact integers: fp16 as u - z, bf16 as 128 + u, the pattern that one byte
@@ -26,7 +27,8 @@
 namespace w4 {
 
 constexpr int kSmallWaves = 8;       // most waves per workgroup
-constexpr int64_t kSmallMaxM = 32;   // rows of the decode kernel
+constexpr int64_t kSmallMaxM = 32;   // rows up to which the decode kernels always run
+constexpr int64_t kSmallGroupsM = 512;
 
 // A byte offset past the end of every buffer (at most 2^31 bytes).
 constexpr uint32_t kPast = 0xFFFFFF00u;
@@ -46,6 +48,8 @@ __global__ void __launch_bounds__(kSmallWaves * 64) lin_small_kernel(const LinAr
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const int j = lane & 15, kc = lane >> 4;
     const int64_t half = p.cols / 2;
+    const int64_t m0 = (int64_t)blockIdx.z * (16 * MT), rows = p.M - m0;       // this workgroup's rows
+    const uint16_t *const a = p.a + m0 * p.lda;
     // first column of block b
     auto col_of = [&](int b) -> int64_t {
         if constexpr (GLU) {
@@ -61,12 +65,12 @@ __global__ void __launch_bounds__(kSmallWaves * 64) lin_small_kernel(const LinAr
     // without a memory access (M = 32: 1024^2 7.4 -> 5.5 us, 4096^2 12.6 -> 11.6;
     // one row 8.7 -> 10.1 us for 14336 x 4096 if x and W did so).
     const __amdgpu_buffer_rsrc_t xbuf = __builtin_amdgcn_make_buffer_rsrc(
-        const_cast<uint16_t *>(p.a), (short)0, (int)(((p.M - 1) * p.lda + p.K) * 2), 0x00020000);
+        const_cast<uint16_t *>(a), (short)0, (int)((((rows < 16 * MT ? rows : 16 * MT) - 1) * p.lda + p.K) * 2), 0x00020000);
     uint32_t xoff[MT];
 #pragma unroll
     for (int mt = 0; mt < MT; ++mt)
-        xoff[mt] = 16 * mt + j < p.M ? (uint32_t)((16 * mt + j) * p.lda + 32 * kc) * 2u : kPast;
-    const uint16_t *const xrow = p.a + (j < p.M ? j : p.M - 1) * p.lda + 32 * kc;
+        xoff[mt] = 16 * mt + j < rows ? (uint32_t)((16 * mt + j) * p.lda + 32 * kc) * 2u : kPast;
+    const uint16_t *const xrow = a + (j < rows ? j : rows - 1) * p.lda + 32 * kc;
     const uint8_t *wb[NB];
 #pragma unroll
     for (int b = 0; b < NB; ++b) wb[b] = p.wp + col_of(b) / 16 * Gall * kTileBytes + lane * 16;
@@ -167,8 +171,8 @@ __global__ void __launch_bounds__(kSmallWaves * 64) lin_small_kernel(const LinAr
     constexpr int OB = GLU ? NB / 2 : NB;
     for (int i = threadIdx.x; i < OB * 256 * MT; i += blockDim.x) {
         const int b = i / (256 * MT), r = (i >> 4) % (16 * MT), c = i & 15;
-        const int64_t row = r;
-        if (row >= p.M) continue;
+        if (r >= rows) continue;
+        const int64_t row = m0 + r;
         float v[1] = {0.f}, u[1] = {0.f};
         for (int w = 0; w < W; ++w) {
             v[0] += red[w][b][r][c];
@@ -185,7 +189,8 @@ __global__ void __launch_bounds__(kSmallWaves * 64) lin_small_kernel(const LinAr
     }
 }
 
-// Transposed product for a few rows: y [M][K] = d . W^T (+ addend), M <= 32.
+// Transposed product for a few rows: y [M][K] = d . W^T (+ addend), 32 rows per
+// workgroup.
 //
 // A workgroup owns 32 output columns (one 32-row chunk of a 128-row group) and all
 // of N or a slice of it; its waves take blocks of 64 columns of W in turn.  Per
@@ -215,13 +220,14 @@ __global__ void __launch_bounds__(kSmallTWaves * 64) lin_small_t_kernel(const Li
     static_assert(32 * 33 * 4 >= 4096, "operand fits in a wave's share");
     if (blockIdx.x >= p.K / 32) {
         // workgroups past the product's: the bias gradient, 64 columns each
-        if (blockIdx.y == 0)
+        if (blockIdx.y == 0 && blockIdx.z == 0)
             colsum_body(p.cpart, p.colsum, p.N, p.cblocks, (int64_t)(blockIdx.x - p.K / 32) * 64,
                         reinterpret_cast<float *>(lds));
         return;
     }
     const int64_t G = p.K / kGroup, g = blockIdx.x >> 2;
     const int c = blockIdx.x & 3;
+    const int64_t m0 = (int64_t)blockIdx.z * 32, rows = p.M - m0 < 32 ? p.M - m0 : 32;   // this workgroup's rows
     // this workgroup's blocks: [b0, b1)
     const int b0 = (int)blockIdx.y * p.stages, nblk = (int)(p.N / 64);
     const int b1 = b0 + p.stages < nblk ? b0 + p.stages : nblk;
@@ -230,8 +236,8 @@ __global__ void __launch_bounds__(kSmallTWaves * 64) lin_small_t_kernel(const Li
     // buffer: zeros, without a memory access or a branch around the load (M = 32,
     // 1024^2: 11.9 us with clamped loads, 7.2 so)
     const __amdgpu_buffer_rsrc_t abuf = __builtin_amdgcn_make_buffer_rsrc(
-        const_cast<uint16_t *>(p.a), (short)0, (int)(((p.M - 1) * p.lda + p.N) * 2), 0x00020000);
-    const uint32_t aoff = (lane & 31) < p.M ? (uint32_t)((lane & 31) * p.lda + 8 * (lane >> 5)) * 2u : kPast;
+        const_cast<uint16_t *>(p.a + m0 * p.lda), (short)0, (int)(((rows - 1) * p.lda + p.N) * 2), 0x00020000);
+    const uint32_t aoff = (lane & 31) < rows ? (uint32_t)((lane & 31) * p.lda + 8 * (lane >> 5)) * 2u : kPast;
     const uint8_t *const wbase = p.wp + (qq * G + g) * kTileBytes + c * 256 + j * 16;
     const int64_t srow = g / p.gm * p.N + qq * 16 + j;
     const uint8_t *const zbase = p.zero ? p.zero : reinterpret_cast<const uint8_t *>(p.scale);
@@ -323,12 +329,12 @@ __global__ void __launch_bounds__(kSmallTWaves * 64) lin_small_t_kernel(const Li
     __syncthreads();
     for (int i = threadIdx.x; i < 1024; i += blockDim.x) {
         const int rr = i >> 5, cc = i & 31;
-        if (rr >= p.M) break;
+        if (rr >= rows) break;
         float v[1] = {0.f};
         for (int w = 0; w < W; ++w) v[0] += reinterpret_cast<const float *>(lds)[w * (32 * 33) + rr * 33 + cc];
         const int64_t col = (int64_t)blockIdx.x * 32 + cc;
-        if (p.slices > 1) p.part[((int64_t)blockIdx.y * p.M + rr) * p.cols + col] = v[0];
-        else finish_ep<DT, 1>(p, v, rr, col);
+        if (p.slices > 1) p.part[((int64_t)blockIdx.y * p.M + m0 + rr) * p.cols + col] = v[0];
+        else finish_ep<DT, 1>(p, v, m0 + rr, col);
     }
 }
 
@@ -374,9 +380,29 @@ static SmallPlan small_plan(int mode, int64_t M, int64_t K, int64_t N) {
     return s;
 }
 
-// The decode kernels' range (transposed: see there).
+// Where the decode kernels always run (transposed: see there).  Beyond, up to
+// kSmallGroupsM rows in 32-row groups on the grid, they compete with the tile
+// kernel by estimated time: small matrices leave most of the machine idle there.
 bool lin_small_ok(int mode, int64_t M, int64_t K, int64_t N) {
     return M <= kSmallMaxM && (!lin_transposed(mode) || M * K * N <= 600000000);
+}
+
+// Estimated us of a call with several 32-row groups (whole K or N, no slices; a
+// large value where it may not run), launch included: rounds of 256 workgroups,
+// each as long as its share of the contraction.  Fits to M = 33..400 on matrices
+// from 256^2 to 4096^2 (1024^2, M = 100: 5.7 against 9.4 us on tiles, transposed 7.5
+// against 9.4; 1408 x 2816 gated, M = 64: 6.8 against 15.0).
+double lin_small_us(int mode, int64_t M, int64_t K, int64_t N) {
+    const SmallPlan s = small_plan(mode, M, K, N);
+    if (M > kSmallGroupsM || (s.slices > 1 && !lin_transposed(mode))) return 1e9;
+    const int64_t groups = (M + 31) / 32;
+    if (lin_transposed(mode)) {
+        const double rounds = (double)((K / 32 * groups * s.slices + 255) / 256);
+        return 3.6 + rounds * (rounds > 1 ? 1.3 : 1.0) * (1.0 + 2.3 / 1024 * (double)N / s.slices) +
+               (s.slices > 1 ? 3.0 : 0.0);
+    }
+    const double rounds = (double)((N / (16 * s.nb) * groups + 255) / 256);
+    return 3.2 + (s.nb == 1 ? 2.4 : 3.1) / 1024 * (double)K * rounds;
 }
 
 size_t lin_small_workspace_bytes(int mode, int64_t M, int64_t K, int64_t N) {
@@ -386,7 +412,7 @@ size_t lin_small_workspace_bytes(int mode, int64_t M, int64_t K, int64_t N) {
 
 template <int DT, bool GLU, int NB, int MT>
 static hipError_t small_go(const LinArgs &p, const SmallPlan &s, hipStream_t stream) {
-    const dim3 grid((unsigned)(p.cols / (16 * NB)), (unsigned)s.slices);
+    const dim3 grid((unsigned)(p.cols / (16 * NB)), (unsigned)s.slices, (unsigned)((p.M + 16 * MT - 1) / (16 * MT)));
     hipLaunchKernelGGL((lin_small_kernel<DT, GLU, NB, MT>), grid, dim3((unsigned)s.waves * 64), 0, stream, p);
     return hipGetLastError();
 }
@@ -400,7 +426,7 @@ static hipError_t small_mt(const LinArgs &p, const SmallPlan &s, hipStream_t str
 template <int DT>
 static hipError_t small_dt(int mode, const LinArgs &p, const SmallPlan &s, hipStream_t stream) {
     if (lin_transposed(mode)) {
-        const dim3 grid((unsigned)(p.cols / 32 + (p.colsum ? p.N / 64 : 0)), (unsigned)s.slices);
+        const dim3 grid((unsigned)(p.cols / 32 + (p.colsum ? p.N / 64 : 0)), (unsigned)s.slices, (unsigned)((p.M + 31) / 32));
         hipLaunchKernelGGL(lin_small_t_kernel<DT>, grid, dim3((unsigned)s.waves * 64), 0, stream, p);
         return hipGetLastError();
     }

@@ -8,6 +8,17 @@
 
 namespace w4 {
 
+// Two of the four codes (one per byte, 0..15) of m in fp32: bytes 0, 1 or 2, 3.  As an
+// 8-bit float (4 exponent bits, 3 of mantissa) a byte u < 16 is u 2^-9 exactly, so
+// one conversion with the factor 2^9 gives two codes (a byte conversion each:
+// 2% more time of every bf16 tile product, 819 against 804 us for gated 4096 x 4096
+// x 28672).
+typedef float f32x2_t __attribute__((ext_vector_type(2)));
+template <int HALF>
+__device__ __forceinline__ f32x2_t codes_f32(uint32_t m) {
+    return __builtin_amdgcn_cvt_scalef32_pk_f32_fp8(m, 512.0f, HALF != 0);
+}
+
 // e^x by the hardware's base-2 exponential.  The argument's rounding costs
 // |x| 2^-24 relative, far below the 16-bit rounding of every result.
 __device__ __forceinline__ float exp_fast(float x) { return __builtin_amdgcn_exp2f(x * 1.4426950408889634f); }

@@ -260,13 +260,11 @@ __global__ void __launch_bounds__(2 * BN, 2) lin_wide_kernel(const LinArgs p) {
         const int t = i >> 1, hf = i & 1;
         const uint32_t w = wr[d][t];
         if constexpr (DT == DT_BF16) {
-            // bytes: rows 0, 4, 1, 5 (or 2, 6, 3, 7).  The empty asm keeps the masked
-            // word whole, so that each byte is one conversion.
-            uint32_t m = (hf ? w >> 4 : w) & 0x0F0F0F0Fu;
-            asm("" : "+v"(m));
-            float v[4];
-            v[0] = (float)(m & 0xFFu), v[2] = (float)((m >> 8) & 0xFFu);
-            v[1] = (float)((m >> 16) & 0xFFu), v[3] = (float)(m >> 24);
+            // bytes: rows 0, 4, 1, 5 (or 2, 6, 3, 7)
+            const uint32_t m = (hf ? w >> 4 : w) & 0x0F0F0F0Fu;
+            const f32x2_t c04 = codes_f32<0>(m);
+            const f32x2_t c15 = codes_f32<1>(m);
+            const float v[4] = {c04[0], c15[0], c04[1], c15[1]};
 #pragma unroll
             for (int q = 0; q < 2; ++q) {
                 if constexpr (T) {

@@ -280,13 +280,9 @@ __global__ void __launch_bounds__(kSmallTWaves * 64) lin_small_t_kernel(const Li
             u32x4_t o;
             if constexpr (DT == DT_BF16) {
                 const uint32_t w = wr[d][t];
-                uint32_t lo = w & 0x0F0F0F0Fu, hi = (w >> 4) & 0x0F0F0F0Fu;
-                asm("" : "+v"(lo), "+v"(hi));         // one conversion per byte
-                float v[8];
-                v[0] = (float)(lo & 0xFFu), v[4] = (float)((lo >> 8) & 0xFFu);
-                v[1] = (float)((lo >> 16) & 0xFFu), v[5] = (float)(lo >> 24);
-                v[2] = (float)(hi & 0xFFu), v[6] = (float)((hi >> 8) & 0xFFu);
-                v[3] = (float)((hi >> 16) & 0xFFu), v[7] = (float)(hi >> 24);
+                const uint32_t lo = w & 0x0F0F0F0Fu, hi = (w >> 4) & 0x0F0F0F0Fu;
+                const f32x2_t c04 = codes_f32<0>(lo), c15 = codes_f32<1>(lo), c26 = codes_f32<0>(hi), c37 = codes_f32<1>(hi);
+                float v[8] = {c04[0], c15[0], c26[0], c37[0], c04[1], c15[1], c26[1], c37[1]};
 #pragma unroll
                 for (int i = 0; i < 8; ++i) v[i] = __builtin_fmaf(v[i], s, zs);
 #pragma unroll
@@ -351,6 +347,7 @@ struct SmallPlan { int nb, waves, mt, slices, groups; };
 // x N 28672, M = 32: 26.9 -> 23.9 us), else eight (M = 1: 13.2 against 13.7 us).
 static SmallPlan small_plan(int mode, int64_t M, int64_t K, int64_t N) {
     SmallPlan s{};
+    const int finish = M > 16 ? 8 : M > 8 ? 4 : 1;
     if (lin_transposed(mode)) {
         // slices of at least 32 blocks where K gives fewer than 128 workgroups
         // (256 x 14336: 9.5 us in eight)
@@ -361,7 +358,7 @@ static SmallPlan small_plan(int mode, int64_t M, int64_t K, int64_t N) {
         if (slices < 1) slices = 1;
         s.groups = (int)((nblk + slices - 1) / slices);
         s.slices = (nblk + s.groups - 1) / s.groups;
-        s.waves = s.groups < kSmallTWaves ? s.groups : kSmallTWaves;
+        s.waves = s.groups < finish ? finish : s.groups < kSmallTWaves ? s.groups : kSmallTWaves;
         return s;
     }
     const int G = (int)(K / kGroup);
@@ -376,7 +373,7 @@ static SmallPlan small_plan(int mode, int64_t M, int64_t K, int64_t N) {
     s.groups = (int)((G + slices - 1) / slices);
     s.slices = (G + s.groups - 1) / s.groups;
     s.waves = M <= 4 || N / (16 * s.nb) * s.slices <= 256 ? kSmallWaves : 4;
-    if (s.waves > s.groups) s.waves = s.groups;
+    if (s.waves > s.groups) s.waves = s.groups < finish ? finish : s.groups;
     return s;
 }
 

@@ -264,6 +264,26 @@ def test_every_tile_shape(plan, shape, slices, dt):
 
 
 @pytest.mark.parametrize("shape", range(SHAPES))
+@pytest.mark.parametrize("M,n", [(3, 1), (65, 2), (33, 3), (130, 5), (40, 7)])
+def test_short_and_uneven_contractions(plan, shape, M, n):
+    """Contractions of one to seven 128-row groups forward and of one to seven
+    64-column stages transposed: the second wave group of a 128-column tile gets
+    a smaller share or none."""
+    K, N = 128 * n, 64 * n
+    L = ref.layer(K, N, 128, BF16, True, seed=n)
+    D = Dev(L)
+    plan(shape, 1)
+    x, r = ref.normal(M, K, 1.0, BF16, 1), ref.normal(M, N, 1.0, BF16, 2)
+    y, _ = run_ep(D, x, SILU, r, save=True)
+    yr, pr = ref.ep(x, L, SILU, r)
+    ref.close(y, yr, ref.tol_ep(yr, pr, BF16), "ep")
+    h = ref.normal(M, N, 1.5, BF16, 3)
+    dx, _, _ = run_bwd(D, False, r, h, SILU)
+    rx, rd, _ = ref.ep_backward(r, h, L, SILU)
+    ref.close(dx, rx, ref.tol_dx(rx, rd, L, BF16), "dx")
+
+
+@pytest.mark.parametrize("shape", range(SHAPES))
 def test_every_tile_shape_holds_its_scales(plan, shape):
     """The unit change of the tile kernel's sums (zero, tiny and huge scales) in
     every shape, in whole calls and slices that start inside a scale group."""

@@ -3,9 +3,14 @@
 // the transposed product d . W^T of their backward passes; the activation
 // gradient d with its column sums; the sum of sliced products.
 //
-// Tile kernel (lin_wide_kernel): a workgroup of 2 x BN / 64 waves owns a BM x BN
-// tile and runs over the contraction in stages of 64 elements; a wave owns
-// (BM / 2) x 64 of it in 32 x 32 x 16 matrix-core steps.  Both operands of a stage
+// Forward tiles of 64 or 128 rows by 128 columns: lin_mid_kernel, below.
+//
+// Tile kernel (lin_wide_kernel): a workgroup owns a BM x BN tile; 2 x BN / 64 waves
+// run over the contraction in stages of 64 elements, each with (BM / 2) x 64 of
+// the tile in 32 x 32 x 16 matrix-core steps.  Tiles of 128 columns (transposed) have
+// two such groups of waves, each with half of the contraction and LDS of its
+// own: two waves per SIMD, one's vector work beside the other's products (64 x 128,
+// M = 128, 4096^2 unsliced 34 -> 26 us).  Both operands of a stage
 // lie in LDS, double buffered.  W is dequantized once per workgroup on its way
 // there (32 codes of one column per thread and stage), so one conversion serves
 // BM rows: with 256 rows 3 vector instructions per matrix-core step, where a
@@ -31,13 +36,13 @@
 // contraction elements 8 (l / 32) .. + 7; result register r of lane l is row
 // 8 (r / 4) + 4 (l / 32) + r % 4, column l % 32.
 //
-// Bound: the matrix core, at the clock that it leaves under full load.  Measured
-// (bf16, graph replay): gated 4096 x 4096 x 28672 with h saved 812 us (1.18
+// Bound: large products by the matrix core, at the clock that it leaves under full load.  Measured
+// (bf16, graph replay): gated 4096 x 4096 x 28672 with h saved 804 us (1.20
 // PFLOP/s; a library product of unquantized bf16 operands of that size takes
 // 731 us here), transposed 4096 x 28672 x 4096 750 us (1.28 PFLOP/s; library 681 us),
-// 4096^3 126 us forward and 120 us transposed (library 126 us).  The matrix core
-// is busy 57% (forward) and 66% (transposed) of 1.8-1.9 GHz cycles; LDS accesses
-// without bank conflicts take 35% of them.  Wave priorities, 128 x 128 wave tiles and
+// 4096^3 125 us forward and 120 us transposed (library 126 us).  The matrix core
+// is busy 60% (forward) and 67% (transposed) of 1.7 GHz cycles; LDS accesses,
+// 1% of them bank conflicts, take 40%.  Wave priorities, 128 x 128 wave tiles and
 // other placements of the vector work measured even or slower.
 #include <atomic>
 #include <type_traits>
@@ -48,6 +53,8 @@ namespace w4 {
 
 constexpr int kXcd = 8;              // XCDs; workgroups go to them round-robin
 constexpr int kBK = 64;              // contraction elements per stage
+// Wave groups of a BM x BN workgroup, each with a share of the contraction.
+constexpr int wide_groups(int bm, int bn) { return bm <= 128 && bn <= 128 ? 2 : 1; }
 
 // LDS swizzles: 16-byte chunk c of row r sits at chunk c ^ key(r) of its row.
 // Writes move 128 bytes a cycle (8 lanes), 16-byte reads 256 (16 lanes).
@@ -80,10 +87,66 @@ __global__ void __launch_bounds__(512) lin_colsum_kernel(const float *part, floa
     colsum_body(part, colsum, N, blocks, (int64_t)blockIdx.x * 64, red);
 }
 
+// Forward products: the sums of a column are held in units of its running scale.
+// A new scale group multiplies them by unit / s first and its codes enter the
+// matrix core as exact integers.  A scale below 2^-60 of the largest so far (or
+// below the normal range, 0 among them) leaves the unit alone and its codes enter
+// as 0: what it would add is below 2^-60 of what the larger scale's codes weigh,
+// and the sums stay far from overflow.
+template <int DT>
+struct ScaleUnit {
+    float unit = 0.f, largest = 0.f, ratio = 1.f;
+    float zf;
+    uint32_t z, sel;
+    __device__ __forceinline__ void next(float s, uint32_t zero) {
+        const float as_ = __builtin_fabsf(s);
+        const bool live = !((as_ < 0x1p-60f * largest) | (as_ < 0x1p-126f));      // NaN stays
+        const float q = unit * __builtin_amdgcn_rcpf(s);
+        ratio = (live & (s != unit)) ? q : 1.f;
+        unit = live ? s : unit;
+        largest = (live & (as_ > largest)) ? as_ : largest;
+        z = zero;
+        zf = (float)zero;
+        // bf16: byte selector of the upper halves, or of zeros; fp16: mask
+        sel = DT == DT_BF16 ? (live ? 0x07060302u : 0x0C0C0C0Cu) : (live ? ~0u : 0u);
+    }
+    // The 8 codes of a word as u - z, rows in order, in two halves: words HF and
+    // HF + 2 of the operand (fp16: all of it with the second).
+    template <int HF>
+    __device__ __forceinline__ void dequant(uint32_t w, u32x4_t &o) const {
+        if constexpr (DT == DT_BF16) {
+            const uint32_t m = (HF ? w >> 4 : w) & 0x0F0F0F0Fu;            // bytes: rows 0, 4, 1, 5 or 2, 6, 3, 7
+            const f32x2_t a = codes_f32<0>(m), b = codes_f32<1>(m);
+            o[HF] = __builtin_amdgcn_perm(__float_as_uint(b[0] - zf), __float_as_uint(a[0] - zf), sel);
+            o[HF + 2] = __builtin_amdgcn_perm(__float_as_uint(b[1] - zf), __float_as_uint(a[1] - zf), sel);
+        } else if constexpr (HF == 1) {
+            o = dequant_word<DT>(w, f16_negbias2(z));
+#pragma unroll
+            for (int q = 0; q < 4; ++q) o[q] &= sel;
+        }
+    }
+};
+
+struct TilePos { int slice; int64_t nt, mt; };
+// XCD x takes a contiguous share of the list (slices, then groups of four row
+// tiles by column tile by row tile): the workgroups of one L2 share operands.
+__device__ __forceinline__ TilePos tile_pos(const LinArgs &p, uint32_t total) {
+    constexpr uint32_t GM = 4;
+    const uint32_t tiles = (uint32_t)p.mtiles * (uint32_t)p.ntiles;
+    const uint32_t id = blockIdx.x, xcd = id % kXcd;
+    const uint32_t r8 = total % kXcd, idx = xcd * (total / kXcd) + (xcd < r8 ? xcd : r8) + id / kXcd;
+    const uint32_t slice = idx / tiles, tile = idx - slice * tiles;
+    const uint32_t m_first = tile / (GM * p.ntiles) * GM;
+    const uint32_t gmt = p.mtiles - m_first < GM ? p.mtiles - m_first : GM;
+    const uint32_t rem = tile - m_first * p.ntiles;
+    return {(int)slice, (int64_t)(rem / gmt), (int64_t)(m_first + rem % gmt)};
+}
+
 template <int DT, int MODE, int BM, int BN>
-__global__ void __launch_bounds__(2 * BN, 2) lin_wide_kernel(const LinArgs p) {
+__global__ void __launch_bounds__(wide_groups(BM, BN) * 2 * BN, 2) lin_wide_kernel(const LinArgs p) {
     constexpr bool T = MODE == LIN_T;
-    constexpr int NT = 2 * BN;                       // threads: 2 x BN / 64 waves of (BM / 2) x 64
+    constexpr int NT = 2 * BN;                       // threads of a wave group: 2 x BN / 64 waves of (BM / 2) x 64
+    constexpr int KS = wide_groups(BM, BN);
     constexpr int RT = BM / 64, CT = 2;              // 32 x 32 tiles per wave
     constexpr int AROWS = NT / 8;                    // rows of A per staging pass
     constexpr int XP = BM / AROWS;                   // 16-byte A chunks per thread and stage
@@ -93,41 +156,39 @@ __global__ void __launch_bounds__(2 * BN, 2) lin_wide_kernel(const LinArgs p) {
     constexpr int OUTROW = 68;                       // floats per row of the output staging
     constexpr int LDSBYTES = 2 * (ABYTES + BBYTES);
     static_assert(LDSBYTES >= NT / 64 * 32 * OUTROW * 4, "output staging fits");
-    __shared__ __attribute__((aligned(16))) uint8_t lds[LDSBYTES];
-    __shared__ float s_ratio[T ? 1 : BN];            // per column: factor on the sums at a new scale group
-    uint8_t *const lda_ = lds, *const ldb_ = lds + 2 * ABYTES;
+    __shared__ __attribute__((aligned(16))) uint8_t lds[KS * LDSBYTES];
+    __shared__ float s_ratios[T ? 1 : KS * BN];      // per column: factor on the sums at a new scale group
 
-    const int tid = threadIdx.x, lane = tid & 63;
-    const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+    const int tid = threadIdx.x % NT, lane = tid & 63;
+    const int wave_all = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    const int grp = wave_all / (NT / 64), wave = wave_all % (NT / 64);     // wave group, wave in it
+    uint8_t *const lda_ = lds + grp * LDSBYTES, *const ldb_ = lda_ + 2 * ABYTES;
+    float *const s_ratio = s_ratios + (T ? 0 : grp * BN);
     const int wm = wave / (BN / 64), wn = wave % (BN / 64);
     const int l31 = lane & 31, kg = lane >> 5;
 
     // ---- tile of this workgroup ------------------------------------------------
-    // XCD x takes a contiguous share of the list (slices, then groups of four row
-    // tiles by column tile by row tile): the workgroups of one L2 share operands.
-    const uint32_t tiles = (uint32_t)p.mtiles * (uint32_t)p.ntiles, total = tiles * (uint32_t)p.slices;
-    const uint32_t id = blockIdx.x, xcd = id % kXcd;
+    const uint32_t total = (uint32_t)p.mtiles * (uint32_t)p.ntiles * (uint32_t)p.slices;
     if constexpr (T) {
         // workgroups past the product's: the bias gradient, 64 columns each (one
         // launch less than a kernel of its own)
-        if (id >= total) {
-            colsum_body(p.cpart, p.colsum, p.N, p.cblocks, (int64_t)(id - total) * 64, reinterpret_cast<float *>(lds));
+        if (blockIdx.x >= total) {
+            colsum_body(p.cpart, p.colsum, p.N, p.cblocks, (int64_t)(blockIdx.x - total) * 64,
+                        reinterpret_cast<float *>(lds));
             return;
         }
     }
-    const uint32_t r8 = total % kXcd, idx = xcd * (total / kXcd) + (xcd < r8 ? xcd : r8) + id / kXcd;
-    constexpr uint32_t GM = 4;
-    const int slice = (int)(idx / tiles);
-    const uint32_t tile = idx - slice * tiles;
-    const uint32_t m_first = tile / (GM * p.ntiles) * GM;
-    const uint32_t gmt = p.mtiles - m_first < GM ? p.mtiles - m_first : GM;
-    const uint32_t rem = tile - m_first * p.ntiles;
-    const int64_t nt = rem / gmt;
-    const int64_t row0 = (int64_t)(m_first + rem % gmt) * BM;
+    const TilePos tp = tile_pos(p, total);
+    const int slice = tp.slice;
+    const int64_t nt = tp.nt, row0 = tp.mt * BM;
 
     const int64_t G = p.K / kGroup;
     const int nst = (int)((T ? p.N : p.K) / kBK);
-    const int s0 = slice * p.stages, s1 = s0 + p.stages < nst ? s0 + p.stages : nst;
+    // this slice's stages [b0, b1); wave group g takes `share` of them from b0 + g share
+    // on (an even number: whole 128-row groups), fewer or none at the end
+    const int b0 = slice * p.stages, b1 = b0 + p.stages < nst ? b0 + p.stages : nst;
+    const int share = KS == 1 ? b1 - b0 : ((b1 - b0 + KS - 1) / KS + 1) & ~1;
+    const int s0 = b0 + grp * share < b1 ? b0 + grp * share : b1, s1 = s0 + share < b1 ? s0 + share : b1;
 
     // ---- A operand: BM rows of 64 elements per stage ------------------------------
     // (the rows of a thread are AROWS apart: one LDS offset serves all)
@@ -215,12 +276,8 @@ __global__ void __launch_bounds__(2 * BN, 2) lin_wide_kernel(const LinArgs p) {
     auto zero_of = [&](uint32_t zb) {
         return p.zero ? __builtin_amdgcn_ubfe(zb, (uint32_t)(j & 1) * 4u, 4) : 8u;
     };
-    // Forward: the sums are held in units of the running scale se; a new scale
-    // group multiplies them by se / s first and its codes enter the matrix core
-    // as exact integers.  smax: largest scale so far.  A scale below 2^-60 of it (or
-    // below the normal range, 0 among them) leaves the unit alone and its codes
-    // enter as 0: what it would add is below 2^-60 of what the larger scale's
-    // codes weigh, and the sums stay far from overflow.
+    // Forward: ScaleUnit's scheme (unit se, largest scale smax), the factors handed
+    // to the waves that hold a column's sums through LDS.
     float se = 0.f, smax = 0.f;
     struct Deq { float s, zs; uint32_t z, sel; } dq;
     // stage st is about to be dequantized: its column's scale and zero point
@@ -374,9 +431,6 @@ __global__ void __launch_bounds__(2 * BN, 2) lin_wide_kernel(const LinArgs p) {
             }
 #pragma unroll
             for (int rt = 0; rt < RT; ++rt) {
-                if constexpr (!T && buf == 0 && RT == 1) {
-                    if (t == 0) scale_tiles(0, 2);
-                }
 #pragma unroll
                 for (int ct = 0; ct < CT; ++ct)
                     acc[rt][ct] = mfma_step<DT>(fa[t % FA][rt], fb[t & 1][ct], acc[rt][ct]);
@@ -467,6 +521,12 @@ __global__ void __launch_bounds__(2 * BN, 2) lin_wide_kernel(const LinArgs p) {
         // (forward slices hold whole 128-row groups)
         if (T && s < s1) stage(std::integral_constant<int, 0>{}, s);
     }
+    if constexpr (KS > 1) {
+        // the first group met one barrier before its stages and one in each; the
+        // others wait at the ones that they have not come to
+        const int most = share < b1 - b0 ? share : b1 - b0;
+        for (int i = s0 < s1 ? s1 - s0 + 1 : 0; i < most + 1; ++i) __syncthreads();
+    }
     __syncthreads();
 
     // ---- epilogue: wave tiles through LDS, rows of 8 columns per lane -----------------
@@ -478,7 +538,19 @@ __global__ void __launch_bounds__(2 * BN, 2) lin_wide_kernel(const LinArgs p) {
 #pragma unroll
         for (int ct = 0; ct < CT; ++ct) scl[ct] = s_ratio[wn * 64 + ct * 32 + l31];
     }
-    float *const ot = reinterpret_cast<float *>(lds) + wave * 32 * OUTROW;
+    float *const ot = reinterpret_cast<float *>(lds) + wave_all * 32 * OUTROW;
+    // the same wave tile of all wave groups, added in their order
+    const float *const os = reinterpret_cast<const float *>(lds) + wave * 32 * OUTROW;
+    auto sum_of = [&](int i) {
+        float v = os[i];
+#pragma unroll
+        for (int g = 1; g < KS; ++g) v += os[g * (NT / 64) * 32 * OUTROW + i];
+        return v;
+    };
+    auto tile_sync = [&] {
+        if constexpr (KS > 1) __syncthreads();
+        else wave_lds_sync();
+    };
 #pragma unroll
     for (int rt = 0; rt < RT; ++rt) {
 #pragma unroll
@@ -486,18 +558,18 @@ __global__ void __launch_bounds__(2 * BN, 2) lin_wide_kernel(const LinArgs p) {
 #pragma unroll
             for (int r = 0; r < 16; ++r)
                 ot[(8 * (r >> 2) + 4 * kg + (r & 3)) * OUTROW + ct * 32 + l31] = acc[rt][ct][r] * scl[ct];
-        wave_lds_sync();
+        tile_sync();
         const int64_t rbase = row0 + wm * (BM / 2) + rt * 32;
         if constexpr (MODE == LIN_GLU) {
             const int64_t c0 = nt * (BN / 2) + wn * 32;
             if (c0 < p.cols / 2) {
-                for (int i = 0; i < 2; ++i) {
+                for (int i = grp; i < 2; i += KS) {
                     const int r = i * 16 + (lane >> 2), c = (lane & 3) * 8;
                     const int64_t row = rbase + r;
                     if (row < p.M) {
                         float g[8], u[8];
 #pragma unroll
-                        for (int e = 0; e < 8; ++e) g[e] = ot[r * OUTROW + c + e], u[e] = ot[r * OUTROW + 32 + c + e];
+                        for (int e = 0; e < 8; ++e) g[e] = sum_of(r * OUTROW + c + e), u[e] = sum_of(r * OUTROW + 32 + c + e);
                         if (p.slices > 1) {
                             float *o = p.part + ((int64_t)slice * p.M + row) * p.cols + c0 + c;
 #pragma unroll
@@ -511,13 +583,13 @@ __global__ void __launch_bounds__(2 * BN, 2) lin_wide_kernel(const LinArgs p) {
         } else {
             const int64_t c0 = nt * BN + wn * 64;
             if (c0 < p.cols) {
-                for (int i = 0; i < 4; ++i) {
+                for (int i = grp; i < 4; i += KS) {
                     const int r = i * 8 + (lane >> 3), c = (lane & 7) * 8;
                     const int64_t row = rbase + r;
                     if (row < p.M) {
                         float v[8];
 #pragma unroll
-                        for (int e = 0; e < 8; ++e) v[e] = ot[r * OUTROW + c + e];
+                        for (int e = 0; e < 8; ++e) v[e] = sum_of(r * OUTROW + c + e);
                         if (p.slices > 1) {
                             float *o = p.part + ((int64_t)slice * p.M + row) * p.cols + c0 + c;
 #pragma unroll
@@ -529,7 +601,238 @@ __global__ void __launch_bounds__(2 * BN, 2) lin_wide_kernel(const LinArgs p) {
                 }
             }
         }
-        wave_lds_sync();
+        tile_sync();
+    }
+}
+
+// Forward products of few row tiles (BM = 64 or 128 rows, 128 columns).
+//
+// Two wave groups of four waves share the contraction (stages of 64 elements); a
+// wave owns all BM rows of 32 columns.  No other wave of its group needs those
+// columns, so W never enters LDS: a lane's 16-byte slot holds 32 rows of its
+// column, word t of it (8 rows) is dequantized straight into the operand of
+// step t (contraction elements 32 (lane / 32) + 8 t .. + 7), and the column's scale
+// stays in the lane whose sums it divides.  Only x goes through LDS: 40 KB of
+// accesses per stage and group at BM = 64, where a W tile in LDS would make it 72.
+//
+// Bound: vector and matrix instructions of two waves per SIMD (BM = 64: 0.55 us for
+// a stage of both groups, 840 vector and 512 matrix cycles), and the join where the
+// rows are so few that K is sliced.  More waves would not fit the registers (4 per
+// SIMD: 26 spilled, 22 -> 32 us).  Measured (bf16, graph replay), before with W in
+// LDS and one wave group: M = 128, 4096 x 14336 gated 42.5 -> 24.5 us; M = 512, 4096^2
+// 35.2 -> 25.6; M = 77, 14336 x 4096 in 8 slices 33.0 -> 27.1; M = 333, 2048 x 2816
+// gated fp16 18.9 -> 14.4.
+template <int DT, bool GLU, int BM>
+__global__ void __launch_bounds__(512, 2) lin_mid_kernel(const LinArgs p) {
+    constexpr int RT = BM / 32, XP = BM / 32, KS = 2;
+    constexpr int ABYTES = BM * kBK * 2, OUTROW = 36;
+    constexpr int OUTBYTES = 8 * 32 * OUTROW * 4;
+    constexpr int LDSBYTES = KS * 2 * ABYTES > OUTBYTES ? KS * 2 * ABYTES : OUTBYTES;
+    __shared__ __attribute__((aligned(16))) uint8_t lds[LDSBYTES];
+
+    const int tid = threadIdx.x & 255, lane = tid & 63;
+    const int wave_all = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    const int grp = wave_all >> 2, wn = wave_all & 3;
+    const int l31 = lane & 31, kg = lane >> 5, j = lane & 15;
+    const TilePos tp = tile_pos(p, (uint32_t)p.mtiles * (uint32_t)p.ntiles * (uint32_t)p.slices);
+    const int64_t nt = tp.nt, row0 = tp.mt * BM, half = p.cols / 2, G = p.K / kGroup;
+
+    // this slice's stages [b0, b1), this wave group's [s0, s1): whole 128-row groups,
+    // the second group's share is the smaller one (or none)
+    const int nst = (int)(p.K / kBK);
+    const int b0 = tp.slice * p.stages, b1 = b0 + p.stages < nst ? b0 + p.stages : nst;
+    const int share = ((b1 - b0 + 1) / 2 + 1) & ~1;
+    const int s0 = b0 + grp * share < b1 ? b0 + grp * share : b1, s1 = s0 + share < b1 ? s0 + share : b1;
+
+    // ---- x: BM rows of 64 elements per stage, two stages on the way ------------------
+    uint8_t *const la = lds + grp * 2 * ABYTES;
+    const uint8_t *const abase = reinterpret_cast<const uint8_t *>(p.a + row0 * p.lda);
+    const int ar_ = tid >> 3, ac_ = tid & 7;
+    uint32_t aoff[XP];
+#pragma unroll
+    for (int i = 0; i < XP; ++i) {
+        const int64_t r = row0 + i * 32 + ar_ < p.M ? i * 32 + ar_ : p.M - 1 - row0;
+        aoff[i] = (uint32_t)(r * p.lda + ac_ * 8) * 2u;
+    }
+    uint8_t *const adst = la + ar_ * (kBK * 2) + ((ac_ ^ key_row(ar_)) << 4);
+    u32x4_t ar[2][XP];
+    auto load_a = [&](int d, int s, int i) { ar[d][i] = ld128(abase + (int64_t)s * (kBK * 2) + aoff[i]); };
+    auto store_a = [&](int d, int i) {
+        *reinterpret_cast<u32x4_t *>(adst + d * ABYTES + i * 32 * (kBK * 2)) = ar[d][i];
+    };
+    const uint8_t *const afrag = la + l31 * (kBK * 2);
+    const int rkey = key_row(l31);
+    auto frag_a = [&](int buf, int rt, int t) {
+        return *reinterpret_cast<const u32x4_t *>(afrag + buf * ABYTES + rt * 32 * (kBK * 2) +
+                                                  (((4 * kg + t) ^ rkey) << 4));
+    };
+
+    // ---- W: this lane's column, four stages on the way -------------------------------
+    int64_t nb;
+    if constexpr (GLU) {
+        nb = (nt * 64 + wn * 16 + (l31 >= 16 ? half : 0)) / 16;    // 16 gate and the same 16 up columns
+    } else {
+        nb = nt * 8 + wn * 2 + (l31 >> 4);
+        if (nb >= p.cols / 16) nb = p.cols / 16 - 1;
+    }
+    const uint32_t woff = (uint32_t)(nb * G * kTileBytes) + kg * 256 + j * 16;
+    const uint32_t soff = (uint32_t)(nb * 16 + j);
+    const uint8_t *const zbase = p.zero ? p.zero : reinterpret_cast<const uint8_t *>(p.scale);
+    u32x4_t wr[4], bq[4];
+    auto load_w = [&](int d, int s) {
+        const int sl = s < s1 ? s : s1 - 1;
+        wr[d] = ld128(p.wp + (int64_t)sl * 512 + woff);
+    };
+    uint16_t snext;
+    uint8_t znext;
+    auto load_s = [&](int s) {
+        const int sl = s < s1 ? s : s1 - 1;
+        const int64_t so = (int64_t)(((uint64_t)(sl >> 1) * p.gm_inv) >> 32) * p.N + soff;
+        snext = p.scale[so];
+        znext = zbase[so >> 1];
+    };
+    ScaleUnit<DT> su;
+    auto next_group = [&] {
+        su.next(h2f<DT>(snext), p.zero ? __builtin_amdgcn_ubfe(znext, (uint32_t)(j & 1) * 4u, 4) : 8u);
+    };
+
+    f32x16_t acc[RT];
+#pragma unroll
+    for (int rt = 0; rt < RT; ++rt)
+#pragma unroll
+        for (int r = 0; r < 16; ++r) acc[rt][r] = 0.f;
+    auto scale_tile = [&](int rt) {
+#pragma unroll
+        for (int r = 0; r < 16; ++r) acc[rt][r] *= su.ratio;
+    };
+
+    // One stage, D = (s - s0) % 4.  Step t's products run beside the dequantization of
+    // the operand that step t - 1 has just used up (for the next stage; step 3's in
+    // the next stage's step 0).  The one barrier stands before the last step's
+    // products, as in the kernel above.
+    u32x4_t fa[2][RT];
+    auto stage = [&](auto dc, int s) {
+        constexpr int D = decltype(dc)::value, buf = D & 1;
+        const int sa = s + 3 < s1 ? s + 3 : s1 - 1;
+#pragma unroll
+        for (int t = 0; t < 4; ++t) {
+            if (t == 3) __syncthreads();
+#pragma unroll
+            for (int rt = 0; rt < RT; ++rt) fa[(t + 1) & 1][rt] = frag_a(t < 3 ? buf : buf ^ 1, rt, (t + 1) & 3);
+#pragma unroll
+            for (int rt = 0; rt < RT; ++rt) {
+                // the sums take the new group's unit before its first products
+                if (buf == 0 && t == 0) scale_tile(rt);
+                acc[rt] = mfma_step<DT>(fa[t & 1][rt], bq[t], acc[rt]);
+                if (t == 0) {
+#pragma unroll
+                    for (int i = rt * XP / RT; i < (rt + 1) * XP / RT; ++i) {
+                        store_a(buf ^ 1, i);
+                        load_a(buf ^ 1, sa, i);
+                    }
+                }
+                const int q = (t + 3) & 3;
+                const uint32_t w = wr[t == 0 ? D : (D + 1) & 3][q];
+                if (rt == RT / 2 - 1) su.template dequant<0>(w, bq[q]);
+                if (rt == RT - 1) su.template dequant<1>(w, bq[q]);
+                if (t == 0 && rt == RT - 1) {
+                    load_w(D, s + 4);
+                    // the next stage's group, and the scales of the one after it
+                    if (buf == 1) {
+                        next_group();
+                        load_s(s + 3);
+                    }
+                }
+                __builtin_amdgcn_sched_barrier(0);
+            }
+        }
+    };
+    if (s0 < s1) {
+        const int sn = s0 + 1 < s1 ? s0 + 1 : s1 - 1, sn2 = s0 + 2 < s1 ? s0 + 2 : s1 - 1;
+#pragma unroll
+        for (int i = 0; i < XP; ++i) load_a(0, s0, i);
+        load_s(s0);
+#pragma unroll
+        for (int d = 0; d < 4; ++d) load_w(d, s0 + d);
+#pragma unroll
+        for (int i = 0; i < XP; ++i) load_a(1, sn, i);
+#pragma unroll
+        for (int i = 0; i < XP; ++i) store_a(0, i);
+        next_group();
+        load_s(s0 + 2);
+#pragma unroll
+        for (int t = 0; t < 3; ++t) {
+            su.template dequant<0>(wr[0][t], bq[t]);
+            su.template dequant<1>(wr[0][t], bq[t]);
+        }
+#pragma unroll
+        for (int i = 0; i < XP; ++i) load_a(0, sn2, i);
+        __syncthreads();
+#pragma unroll
+        for (int rt = 0; rt < RT; ++rt) fa[0][rt] = frag_a(0, rt, 0);
+        int s = s0;
+        for (; s + 2 < s1; s += 4) {
+            stage(std::integral_constant<int, 0>{}, s);
+            stage(std::integral_constant<int, 1>{}, s + 1);
+            stage(std::integral_constant<int, 2>{}, s + 2);
+            stage(std::integral_constant<int, 3>{}, s + 3);
+        }
+        if (s < s1) {
+            stage(std::integral_constant<int, 0>{}, s);
+            stage(std::integral_constant<int, 1>{}, s + 1);
+        }
+    }
+    // The first group met one barrier before its stages and one in each; the second
+    // waits at the ones that it has not come to.
+    for (int i = s0 < s1 ? s1 - s0 + 1 : 0; i < (share < b1 - b0 ? share : b1 - b0) + 1; ++i) __syncthreads();
+
+    // ---- epilogue: wave tiles through LDS, rows of 8 columns per lane; wave group g
+    // finishes the row tiles rt = g (mod 2) -----------------------------------------------
+    float *const ot = reinterpret_cast<float *>(lds) + wave_all * 32 * OUTROW;
+    const float *const os = reinterpret_cast<const float *>(lds) + wn * 32 * OUTROW;
+    auto sum_of = [&](int i) { return os[i] + os[4 * 32 * OUTROW + i]; };
+#pragma unroll
+    for (int rt = 0; rt < RT; ++rt) {
+        __syncthreads();
+#pragma unroll
+        for (int r = 0; r < 16; ++r) ot[(8 * (r >> 2) + 4 * kg + (r & 3)) * OUTROW + l31] = acc[rt][r] * su.unit;
+        __syncthreads();
+        if ((rt & 1) != grp) continue;
+        const int64_t rbase = row0 + rt * 32;
+        if constexpr (GLU) {
+            const int r = lane >> 1, c = (lane & 1) * 8;
+            const int64_t row = rbase + r, col = nt * 64 + wn * 16 + c;
+            if (row < p.M) {
+                float g[8], u[8];
+#pragma unroll
+                for (int e = 0; e < 8; ++e) g[e] = sum_of(r * OUTROW + c + e), u[e] = sum_of(r * OUTROW + 16 + c + e);
+                if (p.slices > 1) {
+                    float *o = p.part + ((int64_t)tp.slice * p.M + row) * p.cols + col;
+#pragma unroll
+                    for (int e = 0; e < 8; ++e) o[e] = g[e], o[half + e] = u[e];
+                } else {
+                    finish_glu<DT, 8>(p, g, u, row, col);
+                }
+            }
+        } else {
+            const int64_t col = nt * 128 + wn * 32 + (lane & 3) * 8;
+#pragma unroll
+            for (int i = 0; i < 2; ++i) {
+                const int r = i * 16 + (lane >> 2), c = (lane & 3) * 8;
+                const int64_t row = rbase + r;
+                if (row >= p.M || col >= p.cols) continue;
+                float v[8];
+#pragma unroll
+                for (int e = 0; e < 8; ++e) v[e] = sum_of(r * OUTROW + c + e);
+                if (p.slices > 1) {
+                    float *o = p.part + ((int64_t)tp.slice * p.M + row) * p.cols + col;
+#pragma unroll
+                    for (int e = 0; e < 8; ++e) o[e] = v[e];
+                } else {
+                    finish_ep<DT, 8>(p, v, row, col);
+                }
+            }
+        }
     }
 }
 
@@ -634,25 +937,30 @@ lin_dact_kernel(const uint16_t *dy, int64_t lddy, const uint16_t *h, uint16_t *d
 
 struct WidePlan { int bm, bn; int slices, stages, mtiles, ntiles; double us; };
 
-// Tile shape and slice count by estimated time.  A workgroup's stage takes
-// `alone` us while compute units are idle and `shared` us of a busy one (three
-// 64 x 128 or two 128 x 128 workgroups share a compute unit, and the clock drops
-// under full matrix load), plus `ends` us for its first loads and its epilogue;
-// slices write and read their fp32 sums at about 5 TB/s and cost another launch.
-// The constants are fits to timings over 20 sizes (M = 20..4096, matrices from
-// 1024 x 1024 to 4096 x 28672, both directions); the choice is within 5% of the
-// best of all shapes and slice counts on them.  Few tiles want small ones and
-// slices, many the large one, whose dequantization serves 256 rows: M = 256,
-// 4096^2 24 us with 128 x 128 and four slices, 91 us with 256 x 256 unsliced;
-// M = 512, 4096 x 28672 118 us with 256 x 256, 178 us with 64 x 128.
+// Tile shape and slice count by estimated time.  A workgroup's step (a stage, with
+// two wave groups one of each) takes `alone` us while compute units are idle and
+// `shared` us where all are busy (the clock drops and L2 is shared), plus `ends` us
+// for its first loads and its epilogue; slices write and read their fp32 sums at
+// about 5 TB/s and cost another launch.  The constants are fits to timings over
+// 20 sizes (M = 64..4096, matrices from 1024 x 1024 to 4096 x 28672, both directions);
+// on 40 random ones the choice was within 6% of the best of all shapes and slice
+// counts on 38 and within 8% on another.  Few tiles want small ones and slices, many
+// the large one, whose dequantization serves 256 rows: M = 128, 4096^2 16 us with
+// 64 x 128 and four slices, 56 with 128 x 256 unsliced; M = 512, 4096 x 14336 70 us with
+// 128 x 256, 95 with 64 x 128.
 struct Shape { int bm, bn; double alone, shared, ends; };
-static constexpr Shape kShapes[] = {{64, 128, 0.50, 0.405, 1.0},
-                                    {128, 128, 0.64, 0.58, 2.0},
-                                    {128, 256, 0.88, 1.08, 4.0},
-                                    {256, 256, 1.38, 1.65, 8.0}};
+static constexpr Shape kForward[] = {{64, 128, 0.55, 0.68, 2.0},
+                                     {128, 128, 0.79, 1.09, 3.5},
+                                     {128, 256, 0.88, 1.08, 4.0},
+                                     {256, 256, 1.36, 1.62, 8.0}};
+static constexpr Shape kTransposed[] = {{64, 128, 0.71, 0.85, 1.5},
+                                        {128, 128, 0.89, 1.14, 3.0},
+                                        {128, 256, 0.88, 1.08, 4.0},
+                                        {256, 256, 1.38, 1.65, 8.0}};
+constexpr int kShapeCount = (int)(sizeof(kForward) / sizeof(kForward[0]));
 static std::atomic<int> g_lin_shape{-1}, g_lin_slices{0};     // test hook: -1 and 0 choose
 
-int lin_shape_count() { return (int)(sizeof(kShapes) / sizeof(kShapes[0])); }
+int lin_shape_count() { return kShapeCount; }
 void set_lin_plan(int shape, int slices) {
     g_lin_shape.store(shape, std::memory_order_relaxed);
     g_lin_slices.store(slices, std::memory_order_relaxed);
@@ -666,9 +974,11 @@ static WidePlan wide_plan(int mode, int64_t M, int64_t K, int64_t N) {
     const int64_t cols = mode == LIN_T ? K : N;
     const int nst = (int)((mode == LIN_T ? N : K) / kBK);
     WidePlan best{};
-    for (const Shape &sh : kShapes)
+    const Shape *const shapes = mode == LIN_T ? kTransposed : kForward;
+    for (int si = 0; si < kShapeCount; ++si)
         for (int want : kSlices) {
-            if (shape >= 0 && shape < lin_shape_count() && &sh != &kShapes[shape]) continue;
+            const Shape &sh = shapes[si];
+            if (shape >= 0 && shape < kShapeCount && si != shape) continue;
             if (forced > 0 && want != 1 && want != forced) continue;
             WidePlan w{};
             w.bm = sh.bm;
@@ -681,7 +991,9 @@ static WidePlan wide_plan(int mode, int64_t M, int64_t K, int64_t N) {
             if (want > 1 && (w.slices != want || (w.stages < 4 && want != forced))) continue;
             const int64_t wgs = (int64_t)w.mtiles * w.ntiles * w.slices;
             const double load = wgs <= kCus ? (double)wgs / kCus : (double)((wgs + kCus - 1) / kCus);
-            const double one = w.stages * sh.alone + sh.ends, all = load * (w.stages * sh.shared + sh.ends);
+            const int groups = wide_groups(w.bm, w.bn);         // a wave group's share: as in the kernel
+            const int steps = groups == 1 ? w.stages : ((w.stages + groups - 1) / groups + 1) & ~1;
+            const double one = steps * sh.alone + sh.ends, all = load * (steps * sh.shared + sh.ends);
             double us = one > all ? one : all;
             if (w.slices > 1) us += 3.0 + 8e-6 / 5.0 * w.slices * (double)M * (double)cols;
             if (best.bm == 0 || us < best.us || want == forced) {
@@ -712,10 +1024,19 @@ static hipError_t wide_launch(const LinArgs &p, int bm, int bn, hipStream_t stre
     const int64_t total = (int64_t)p.mtiles * p.ntiles * p.slices;
     const int64_t extra = MODE == LIN_T && p.colsum ? p.N / 64 : 0;
     if (total + extra > INT32_MAX) return hipErrorInvalidConfiguration;
-    const dim3 grid((unsigned)(total + extra)), block(2 * bn);
-    if (bm == 64 && bn == 128) hipLaunchKernelGGL((lin_wide_kernel<DT, MODE, 64, 128>), grid, block, 0, stream, p);
-    else if (bm == 128 && bn == 128) hipLaunchKernelGGL((lin_wide_kernel<DT, MODE, 128, 128>), grid, block, 0, stream, p);
-    else if (bm == 128 && bn == 256) hipLaunchKernelGGL((lin_wide_kernel<DT, MODE, 128, 256>), grid, block, 0, stream, p);
+    const dim3 grid((unsigned)(total + extra)), block((unsigned)(wide_groups(bm, bn) * 2 * bn));
+    if constexpr (MODE != LIN_T) {
+        if (bn == 128) {
+            if (bm == 64) hipLaunchKernelGGL((lin_mid_kernel<DT, MODE == LIN_GLU, 64>), grid, block, 0, stream, p);
+            else hipLaunchKernelGGL((lin_mid_kernel<DT, MODE == LIN_GLU, 128>), grid, block, 0, stream, p);
+            return hipGetLastError();
+        }
+    } else if (bn == 128) {
+        if (bm == 64) hipLaunchKernelGGL((lin_wide_kernel<DT, MODE, 64, 128>), grid, block, 0, stream, p);
+        else hipLaunchKernelGGL((lin_wide_kernel<DT, MODE, 128, 128>), grid, block, 0, stream, p);
+        return hipGetLastError();
+    }
+    if (bm == 128 && bn == 256) hipLaunchKernelGGL((lin_wide_kernel<DT, MODE, 128, 256>), grid, block, 0, stream, p);
     else if (bm == 256 && bn == 256) hipLaunchKernelGGL((lin_wide_kernel<DT, MODE, 256, 256>), grid, block, 0, stream, p);
     else return hipErrorInvalidValue;
     return hipGetLastError();

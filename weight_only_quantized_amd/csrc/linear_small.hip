@@ -347,6 +347,8 @@ struct SmallPlan { int nb, waves, mt, slices, groups; };
 // x N 28672, M = 32: 26.9 -> 23.9 us), else eight (M = 1: 13.2 against 13.7 us).
 static SmallPlan small_plan(int mode, int64_t M, int64_t K, int64_t N) {
     SmallPlan s{};
+    // waves that finish the outputs, also where fewer have a share of the contraction
+    // (100 rows of 128 x 1024 4.6 -> 3.2 us; one row 2.6 us, 2.7 with four)
     const int finish = M > 16 ? 8 : M > 8 ? 4 : 1;
     if (lin_transposed(mode)) {
         // slices of at least 32 blocks where K gives fewer than 128 workgroups
@@ -386,7 +388,7 @@ bool lin_small_ok(int mode, int64_t M, int64_t K, int64_t N) {
 
 // Estimated us of a call with several 32-row groups (whole K or N, no slices; a
 // large value where it may not run), launch included: rounds of 256 workgroups,
-// each as long as its share of the contraction.  Fits to M = 33..400 on matrices
+// each as long as its share of the contraction and 0.9 us for its ends.  Fits to M = 33..400 on matrices
 // from 256^2 to 4096^2 (1024^2, M = 100: 5.7 against 9.4 us on tiles, transposed 7.5
 // against 9.4; 1408 x 2816 gated, M = 64: 6.8 against 15.0).
 double lin_small_us(int mode, int64_t M, int64_t K, int64_t N) {
@@ -399,7 +401,7 @@ double lin_small_us(int mode, int64_t M, int64_t K, int64_t N) {
                (s.slices > 1 ? 3.0 : 0.0);
     }
     const double rounds = (double)((N / (16 * s.nb) * groups + 255) / 256);
-    return 3.2 + (s.nb == 1 ? 2.4 : 3.1) / 1024 * (double)K * rounds;
+    return 3.2 + (s.nb == 1 ? 2.4 : 3.1) / 1024 * (double)K * rounds + 0.9 * (rounds - 1);
 }
 
 size_t lin_small_workspace_bytes(int mode, int64_t M, int64_t K, int64_t N) {

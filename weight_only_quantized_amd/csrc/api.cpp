@@ -396,8 +396,8 @@ w4a16_status linear_forward(bool glu, const void *x, int64_t ldx, const w4a16_li
     if (M == 0) return W4A16_OK;
     if (!x || !lin->w_packed || !lin->scale || !y) return W4A16_ERR_NULL;
     const int mode = glu ? w4::LIN_GLU : w4::LIN_EP;
-    const size_t need = w4::lin_workspace_bytes(mode, M, lin->K, lin->N);
-    if (need > 0 && (!workspace || workspace_bytes < need)) return W4A16_ERR_WORKSPACE;
+    const w4::LinPlan plan = w4::lin_plan(mode, M, lin->K, lin->N);
+    if (plan.workspace_bytes > 0 && (!workspace || workspace_bytes < plan.workspace_bytes)) return W4A16_ERR_WORKSPACE;
     if (!aligned(x, 16) || !aligned(lin->w_packed, 16) || !aligned(lin->scale, 2) || !aligned(lin->bias, 16) ||
         !aligned(residual, 16) || !aligned(pre, 16) || !aligned(y, 16) || !aligned(workspace, 16))
         return W4A16_ERR_ALIGN;
@@ -419,14 +419,11 @@ w4a16_status linear_forward(bool glu, const void *x, int64_t ldx, const w4a16_li
     p.pre = (uint16_t *)pre;
     p.y = (uint16_t *)y;
     p.ldy = ldy;
-    return map_err(w4::launch_lin(mode, p, dt, workspace, (hipStream_t)stream));
+    return map_err(w4::launch_lin(mode, p, plan, dt, workspace, (hipStream_t)stream));
 }
 
 // Backward workspace: the column sums' partial rows, then the product's slices.
 size_t dact_bytes(int64_t M, int64_t N) { return (w4::lin_dact_workspace_bytes(M, N) + 255) / 256 * 256; }
-size_t backward_bytes(int64_t M, int64_t K, int64_t N) {
-    return dact_bytes(M, N) + w4::lin_workspace_bytes(w4::LIN_T, M, K, N);
-}
 
 w4a16_status linear_backward(bool glu, const void *dy, int64_t lddy, const void *h, const w4a16_linear *lin, int act,
                              const void *addend, int64_t ldadd, void *d, float *dbias, void *dx, int64_t lddx,
@@ -442,11 +439,12 @@ w4a16_status linear_backward(bool glu, const void *dy, int64_t lddy, const void 
         return st;
     if (!aligned(dbias, 4)) return W4A16_ERR_ALIGN;
     if (M == 0 && !dbias) return W4A16_OK;
+    w4::LinPlan plan{};
     const bool through = glu || act != W4A16_ACT_NONE;      // the product reads d, not dy
     if (M > 0) {
         if (!dy || !lin->w_packed || !lin->scale || !dx || (through && (!h || !d))) return W4A16_ERR_NULL;
-        const size_t need = backward_bytes(M, K, N);
-        if (!workspace || workspace_bytes < need) return W4A16_ERR_WORKSPACE;
+        plan = w4::lin_plan(w4::LIN_T, M, K, N);
+        if (!workspace || workspace_bytes < dact_bytes(M, N) + plan.workspace_bytes) return W4A16_ERR_WORKSPACE;
         if (!aligned(dy, 16) || !aligned(lin->w_packed, 16) || !aligned(lin->scale, 2) || !aligned(addend, 16) ||
             (through && (!aligned(h, 16) || !aligned(d, 16))) || !aligned(dx, 16) || !aligned(workspace, 16))
             return W4A16_ERR_ALIGN;
@@ -477,14 +475,14 @@ w4a16_status linear_backward(bool glu, const void *dy, int64_t lddy, const void 
     p.cpart = (const float *)workspace;
     p.colsum = dbias;
     p.cblocks = w4::lin_dact_blocks(M);
-    return map_err(w4::launch_lin(w4::LIN_T, p, dt, (uint8_t *)workspace + dact_bytes(M, N), s));
+    return map_err(w4::launch_lin(w4::LIN_T, p, plan, dt, (uint8_t *)workspace + dact_bytes(M, N), s));
 }
 
 size_t linear_bytes(const w4a16_linear *lin, int64_t M, bool glu, bool backward) {
     int gm = 1;
     if (check_linear(lin, glu, &gm) != W4A16_OK || !rows_ok(M) || M == 0) return 0;
-    if (backward) return backward_bytes(M, lin->K, lin->N);
-    return w4::lin_workspace_bytes(glu ? w4::LIN_GLU : w4::LIN_EP, M, lin->K, lin->N);
+    if (backward) return dact_bytes(M, lin->N) + w4::lin_plan(w4::LIN_T, M, lin->K, lin->N).workspace_bytes;
+    return w4::lin_plan(glu ? w4::LIN_GLU : w4::LIN_EP, M, lin->K, lin->N).workspace_bytes;
 }
 
 }  // namespace

@@ -181,9 +181,15 @@ struct LinArgs {
     float *colsum;              // and where their sums go, or NULL
     int cblocks;
 };
-// Workspace of a product (partial sums of its slices), 0 if it runs in one.
-size_t lin_workspace_bytes(int mode, int64_t M, int64_t K, int64_t N);
-hipError_t launch_lin(int mode, LinArgs p, int dt, void *workspace, hipStream_t stream);
+// How a product runs, and its workspace (partial sums of its slices, 0 if it runs
+// in one).  Made once per call (a second time cost 0.15 us).
+struct LinPlan {
+    bool small;                 // the decode-sized kernels, else tiles of bm x bn
+    int bm, bn, slices, stages, mtiles, ntiles;
+    size_t workspace_bytes;
+};
+LinPlan lin_plan(int mode, int64_t M, int64_t K, int64_t N);      // M > 0
+hipError_t launch_lin(int mode, LinArgs p, const LinPlan &plan, int dt, void *workspace, hipStream_t stream);
 // Test hook: force a tile shape (-1: by size) and a slice count (0: by size).
 int lin_shape_count();
 void set_lin_plan(int shape, int slices);

@@ -1004,19 +1004,26 @@ static WidePlan wide_plan(int mode, int64_t M, int64_t K, int64_t N) {
     return best;
 }
 
-// A forced tile shape also takes the rows that the decode kernels would.
-static bool use_small(int mode, int64_t M, int64_t K, int64_t N) {
-    if (g_lin_shape.load(std::memory_order_relaxed) >= 0) return false;
-    if (lin_small_ok(mode, M, K, N)) return true;
-    // (a launch and its first loads take the tile kernel 2.8 us besides its stages)
-    return M > 32 && lin_small_us(mode, M, K, N) < wide_plan(mode, M, K, N).us + 2.8;
-}
-
-size_t lin_workspace_bytes(int mode, int64_t M, int64_t K, int64_t N) {
-    if (M <= 0) return 0;
-    if (use_small(mode, M, K, N)) return lin_small_workspace_bytes(mode, M, K, N);
-    const WidePlan w = wide_plan(mode, M, K, N);
-    return w.slices > 1 ? (size_t)w.slices * (size_t)M * (size_t)(mode == LIN_T ? K : N) * sizeof(float) : 0;
+LinPlan lin_plan(int mode, int64_t M, int64_t K, int64_t N) {
+    LinPlan plan{};
+    // a forced tile shape also takes the rows that the decode kernels would
+    const bool free = g_lin_shape.load(std::memory_order_relaxed) < 0;
+    plan.small = free && lin_small_ok(mode, M, K, N);
+    if (!plan.small) {
+        const WidePlan w = wide_plan(mode, M, K, N);
+        // (a launch and its first loads take the tile kernels 2.8 us besides their stages)
+        plan.small = free && M > 32 && lin_small_us(mode, M, K, N) < w.us + 2.8;
+        plan.bm = w.bm;
+        plan.bn = w.bn;
+        plan.slices = w.slices;
+        plan.stages = w.stages;
+        plan.mtiles = w.mtiles;
+        plan.ntiles = w.ntiles;
+        if (w.slices > 1)
+            plan.workspace_bytes = (size_t)w.slices * (size_t)M * (size_t)(mode == LIN_T ? K : N) * sizeof(float);
+    }
+    if (plan.small) plan.workspace_bytes = lin_small_workspace_bytes(mode, M, K, N);
+    return plan;
 }
 
 template <int DT, int MODE>
@@ -1055,22 +1062,21 @@ hipError_t launch_lin_join(int mode, const LinArgs &p, int dt, hipStream_t strea
 }
 
 template <int DT>
-static hipError_t wide_dt(int mode, const LinArgs &p, const WidePlan &w, hipStream_t stream) {
-    if (mode == LIN_EP) return wide_launch<DT, LIN_EP>(p, w.bm, w.bn, stream);
-    if (mode == LIN_GLU) return wide_launch<DT, LIN_GLU>(p, w.bm, w.bn, stream);
-    return wide_launch<DT, LIN_T>(p, w.bm, w.bn, stream);
+static hipError_t wide_dt(int mode, const LinArgs &p, const LinPlan &plan, hipStream_t stream) {
+    if (mode == LIN_EP) return wide_launch<DT, LIN_EP>(p, plan.bm, plan.bn, stream);
+    if (mode == LIN_GLU) return wide_launch<DT, LIN_GLU>(p, plan.bm, plan.bn, stream);
+    return wide_launch<DT, LIN_T>(p, plan.bm, plan.bn, stream);
 }
 
-hipError_t launch_lin(int mode, LinArgs p, int dt, void *workspace, hipStream_t stream) {
-    if (use_small(mode, p.M, p.K, p.N)) return launch_lin_small(mode, p, dt, workspace, stream);
-    const WidePlan w = wide_plan(mode, p.M, p.K, p.N);
-    p.slices = w.slices;
-    p.stages = w.stages;
-    p.mtiles = w.mtiles;
-    p.ntiles = w.ntiles;
+hipError_t launch_lin(int mode, LinArgs p, const LinPlan &plan, int dt, void *workspace, hipStream_t stream) {
+    if (plan.small) return launch_lin_small(mode, p, dt, workspace, stream);
+    p.slices = plan.slices;
+    p.stages = plan.stages;
+    p.mtiles = plan.mtiles;
+    p.ntiles = plan.ntiles;
     p.part = (float *)workspace;
     p.gm_inv = ((uint64_t(1) << 32) + p.gm - 1) / p.gm;
-    hipError_t err = dt == DT_BF16 ? wide_dt<DT_BF16>(mode, p, w, stream) : wide_dt<DT_F16>(mode, p, w, stream);
+    hipError_t err = dt == DT_BF16 ? wide_dt<DT_BF16>(mode, p, plan, stream) : wide_dt<DT_F16>(mode, p, plan, stream);
     return err == hipSuccess && p.slices > 1 ? launch_lin_join(mode, p, dt, stream) : err;
 }
 

@@ -203,9 +203,9 @@ __global__ void __launch_bounds__(kSmallWaves * 64) lin_small_kernel(const LinAr
 //
 // Every workgroup reads all of d: K / 32 times M N 2 bytes, which bounds it for
 // many rows of large matrices; the weights' stream and the launch otherwise.
-// Measured (bf16): one row of 1024^2 5.8 us, of 4096^2 8.5 us, of 4096 x 28672 30 us;
-// 32 rows 7.2, 13.8 us.  The tile kernel with its slices takes 7.9, 11.9, 34 and
-// 8.7, 13.1 us; from M K N = 6e8 on it is the faster one.
+// Measured (bf16, graph replay): one row of 1024^2 6.6 us, of 4096^2 9.3 us, of
+// 4096 x 28672 29 us; 32 rows 7.8, 14.6 us.  The tile kernel with its best slices takes
+// 8.4, 11.9, 30 and 9.2, 13.4 us; from M K N = 6e8 on it is the faster one.
 constexpr int kSmallTWaves = 16;
 
 template <int DT>
@@ -388,9 +388,9 @@ bool lin_small_ok(int mode, int64_t M, int64_t K, int64_t N) {
 
 // Estimated us of a call with several 32-row groups (whole K or N, no slices; a
 // large value where it may not run), launch included: rounds of 256 workgroups,
-// each as long as its share of the contraction and 0.9 us for its ends.  Fits to M = 33..400 on matrices
-// from 256^2 to 4096^2 (1024^2, M = 100: 5.7 against 9.4 us on tiles, transposed 7.5
-// against 9.4; 1408 x 2816 gated, M = 64: 6.8 against 15.0).
+// each as long as its share of the contraction and 0.9 us for its ends.  Fits to
+// M = 33..400 on matrices from 256^2 to 4096^2 (1024^2, M = 100: 6.2 against 9.0 us on
+// tiles, transposed 8.2 against 10.0; 1408 x 2816 gated, M = 64: 7.6 against 10.7).
 double lin_small_us(int mode, int64_t M, int64_t K, int64_t N) {
     const SmallPlan s = small_plan(mode, M, K, N);
     if (M > kSmallGroupsM || (s.slices > 1 && !lin_transposed(mode))) return 1e9;

@@ -484,3 +484,56 @@ def test_offsets_past_32_bits():
     w4.w4a16_gemm_ep_backward(y, None, D.lin, dx, M, NONE, dt=F16, lddy=ld, lddx=ld, workspace=ws, workspace_bytes=nb)
     rx, rd, _ = ref.ep_backward(y.cpu(), None, L, NONE)
     ref.close(dx, rx, ref.tol_dx(rx, rd, L, F16), "wide stride dx")
+
+
+def on_device(L):
+    """The layer with its tensors on the GPU: the 64-bit reference of a large one."""
+    return ref.Layer(L.K, L.N, L.group, L.dt, *(t if t is None else t.to(DEV) for t in (L.q, L.scale, L.zero, L.bias)))
+
+
+# decode kernel: column blocks per workgroup (1 by default, 2 and 4 for wide
+# matrices), and K in slices (few rows of 13 to 80 million weights and more)
+@pytest.mark.parametrize("glu,M,K,N,group,dt,slices", [
+    (False, 3, 256, 7168, 128, BF16, 1), (False, 20, 384, 7168, 384, F16, 1),
+    (False, 1, 256, 14336, 128, F16, 1), (False, 16, 384, 14336, 128, BF16, 1), (False, 32, 128, 14336, 128, BF16, 1),
+    (True, 1, 256, 14336, 128, BF16, 1), (True, 16, 384, 14336, 384, F16, 1), (True, 32, 256, 14336, 128, BF16, 1),
+    (False, 5, 14336, 4096, 128, BF16, 4), (False, 17, 14336, 4096, 512, F16, 4), (False, 32, 14336, 4096, 256, BF16, 4),
+    (False, 16, 53376, 512, 128, F16, 8), (False, 19, 26752, 512, 128, BF16, 8),
+    (True, 5, 40960, 2048, 128, F16, 8), (True, 16, 40960, 2048, 256, BF16, 8), (True, 17, 20608, 2048, 128, BF16, 8),
+])
+def test_decode_blocks_and_slices(glu, M, K, N, group, dt, slices):
+    L = ref.layer(K, N, group, dt, True, seed=M)
+    D, dev = Dev(L), on_device(L)
+    query = w4.w4a16_glu_gemm_workspace_bytes if glu else w4.w4a16_gemm_ep_workspace_bytes
+    assert query(D.lin, M) == (slices * M * N * 4 if slices > 1 else 0)
+    # sums of about the size that K = 256 gives: the activation is then not saturated
+    x, r = ref.normal(M, K, 16.0 / K ** 0.5, dt, 1), ref.normal(M, N, 1.0, dt, 2)
+    if glu:
+        y, h = run_glu(D, x, SILU, save=True)
+        yr, hr = (t.cpu() for t in ref.glu(x.to(DEV), dev, SILU))
+        ref.close(y, yr, ref.tol_glu(yr, hr, dt), "glu")
+    else:
+        y, h = run_ep(D, x, GELU, r, save=True)
+        yr, hr = (t.cpu() for t in ref.ep(x.to(DEV), dev, GELU, r.to(DEV)))
+        ref.close(y, yr, ref.tol_ep(yr, hr, dt), "ep")
+    ref.close(h, hr, ref.tol_ep(hr, hr, dt), "pre")
+
+
+@pytest.mark.parametrize("glu", [False, True])
+@pytest.mark.parametrize("M,dt", [(64, BF16), (75, F16)])
+def test_transposed_decode_slices_of_several_row_groups(glu, M, dt):
+    """Rows past 32 with N in slices: seven of them, which no tile plan has; the
+    bias gradient is formed once."""
+    K, N = 128, 14336
+    L = ref.layer(K, N, 128, dt, True, seed=5)
+    D = Dev(L)
+    query = w4.w4a16_glu_gemm_backward_workspace_bytes if glu else w4.w4a16_gemm_ep_backward_workspace_bytes
+    rows = 4 * N * ((M + 3) // 4)                    # partial column sums, one row per block of four
+    assert query(D.lin, M) == rows + 7 * M * K * 4
+    dy = ref.normal(M, N // 2 if glu else N, 0.5, dt, 1)
+    h, r = ref.normal(M, N, 1.5, dt, 2), ref.normal(M, K, 0.5, dt, 3)
+    dx, d, db = run_bwd(D, glu, dy, h, SILU, r)
+    rx, rd, rb = (ref.glu_backward if glu else ref.ep_backward)(dy, h, L, SILU, r)
+    ref.close(d, rd, ref.tol_d(rd, dt), "d")
+    ref.close(dx, rx, ref.tol_dx(rx, rd, L, dt), "dx")
+    ref.close(db, rb, 2.0 ** -20 * (rd.abs().sum(0) + rd.abs().amax()), "dbias")

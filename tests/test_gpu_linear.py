@@ -537,3 +537,29 @@ def test_transposed_decode_slices_of_several_row_groups(glu, M, dt):
     ref.close(d, rd, ref.tol_d(rd, dt), "d")
     ref.close(dx, rx, ref.tol_dx(rx, rd, L, dt), "dx")
     ref.close(db, rb, 2.0 ** -20 * (rd.abs().sum(0) + rd.abs().amax()), "dbias")
+
+
+def large_x(D, M, size):
+    """A product of x of the given size and scales near 2^-38 against 64 bits: y, x W
+    and what a sum in fp32 is off by."""
+    x = ref.normal(M, D.L.K, size, BF16, 1)
+    y, _ = run_ep(D, x, NONE)
+    yr, _ = ref.ep(x, D.L, NONE)
+    terms = (x.double().square() @ D.L.weights().square()).sqrt()
+    ref.close(y, yr, ref.ULP[BF16] * 1.01 * yr.abs() + 8 * ref.SUM * terms, f"x of size {size}")
+
+
+def scaled_layer(K, N, factor, seed=8):
+    L = ref.layer(K, N, 128, BF16, True, bias=False, seed=seed)
+    L.scale = (L.scale.float() * factor).bfloat16()
+    return L
+
+
+@pytest.mark.parametrize("size", [2.0 ** 117, 2.0 ** 125])
+@pytest.mark.parametrize("M", [2, 20])
+def test_large_finite_x_on_few_rows(M, size):
+    """Finite x up to the type's largest values (normal numbers of size 2^125 reach
+    2^127) times small scales, and as small ones times large scales: what the terms
+    of the sum allow is finite and keeps its bits."""
+    large_x(Dev(scaled_layer(256, 128, 2.0 ** -30)), M, size)
+    large_x(Dev(scaled_layer(256, 128, 2.0 ** 30)), M, 2.0 ** -118)

@@ -11,11 +11,14 @@
 // LDS in wave order and every output is finished and rounded once.  More than 16
 // MT rows of a small matrix lie as further row groups on the grid.
 //
-// Codes enter the matrix core (16 x 16 x 32 steps, rows padded to 16 MT) as
-// exact integers: fp16 as u - z, bf16 as 128 + u, the pattern that one byte
-// permute makes; four more steps with ones give the row sums of x, and
-// (128 + z) times them is subtracted in fp32.  The group's scale multiplies the
-// fp32 sum.  An infinite x therefore gives NaN in its row.
+// Codes enter the matrix core (16 x 16 x 32 steps, rows padded to 16 MT) exactly:
+// fp16 as u - z, bf16 as (128 + u) 2^-16, a pattern that one byte permute makes; four
+// more steps with 2^-16 give the row sums of x, and (128 + z) times them is
+// subtracted in fp32.  That small, both sums stay finite for any finite x (with 128 + u
+// itself they passed fp32's range from x = 2e34 on, and their difference was NaN).
+// The group's scale multiplies the difference; 2^8 of the factor comes back with
+// it and 2^8 with the result, so that neither a scale below 2^120 nor a normal result
+// leaves the range.  An infinite x gives NaN in its row.
 //
 // Bound: the weight stream at the start (latency) and through the launch.
 // Measured (bf16, zero points): gated 4096 x 28672, one row 12.8 us (61 MB, 4.8
@@ -36,10 +39,22 @@ __device__ __forceinline__ u32x4_t buffer_ld128(__amdgpu_buffer_rsrc_t buf, uint
     return __builtin_bit_cast(u32x4_t, __builtin_amdgcn_raw_buffer_load_b128(buf, (int)off, 0, 0));
 }
 
+// The 8 codes of a prepacked word as the kernel's operand: u - z, or (128 + u) 2^-16 (see
+// dequant_word, whose bf16 pattern this is under another exponent byte).
+template <int DT>
+__device__ __forceinline__ u32x4_t small_operand(uint32_t w, uint32_t z) {
+    if constexpr (DT == DT_F16) return dequant_word<DT>(w, f16_negbias2(z));
+    constexpr uint32_t expb = 0x3B3B3B3Bu;
+    const uint32_t lo = w & 0x0F0F0F0Fu, hi = (w >> 4) & 0x0F0F0F0Fu;
+    return u32x4_t{__builtin_amdgcn_perm(expb, lo, 0x04020400u), __builtin_amdgcn_perm(expb, hi, 0x04020400u),
+                   __builtin_amdgcn_perm(expb, lo, 0x04030401u), __builtin_amdgcn_perm(expb, hi, 0x04030401u)};
+}
+
 template <int DT, bool GLU, int NB, int MT>
 __global__ void __launch_bounds__(kSmallWaves * 64) lin_small_kernel(const LinArgs p) {
     static_assert(!GLU || NB % 2 == 0, "gate and up blocks in pairs");
     constexpr int D = 2;                              // groups in flight per wave
+    constexpr float back = DT == DT_BF16 ? 256.f : 1.f;       // half of the operand's 2^-16
     const int W = blockDim.x >> 6;
     // this workgroup's groups: [g0, G)
     const int g0 = (int)blockIdx.y * p.stages, Gall = (int)(p.K / kGroup);
@@ -112,15 +127,15 @@ __global__ void __launch_bounds__(kSmallWaves * 64) lin_small_kernel(const LinAr
     auto compute = [&](int d) {
         const uint32_t z = p.zero ? __builtin_amdgcn_ubfe(zr[d], (uint32_t)(j & 1) * 4u, 4) : 8u;
         const uint32_t sz = sr[d] | z << 16;
-        // bf16: the operand is 128 + v; S = row sums of x take (128 + z) S out
+        // bf16: S = 2^-16 of the row sums of x take (128 + z) S out
         f32x4_t S[MT];
         if constexpr (DT == DT_BF16) {
-            const u32x4_t ones = {0x3F803F80u, 0x3F803F80u, 0x3F803F80u, 0x3F803F80u};
+            const u32x4_t part = {0x37803780u, 0x37803780u, 0x37803780u, 0x37803780u};
 #pragma unroll
             for (int mt = 0; mt < MT; ++mt) {
                 S[mt] = f32x4_t{0.f, 0.f, 0.f, 0.f};
 #pragma unroll
-                for (int t = 0; t < 4; ++t) S[mt] = mfma16x16x32<DT>(xa[d][mt][t], ones, S[mt]);
+                for (int t = 0; t < 4; ++t) S[mt] = mfma16x16x32<DT>(xa[d][mt][t], part, S[mt]);
             }
         }
 #pragma unroll
@@ -132,11 +147,11 @@ __global__ void __launch_bounds__(kSmallWaves * 64) lin_small_kernel(const LinAr
             for (int mt = 0; mt < MT; ++mt) acc[mt] = f32x4_t{0.f, 0.f, 0.f, 0.f};
 #pragma unroll
             for (int t = 0; t < 4; ++t) {
-                const u32x4_t wq = dequant_word<DT>(wr[d][b][t], f16_negbias2(zb));
+                const u32x4_t wq = small_operand<DT>(wr[d][b][t], zb);
 #pragma unroll
                 for (int mt = 0; mt < MT; ++mt) acc[mt] = mfma16x16x32<DT>(xa[d][mt][t], wq, acc[mt]);
             }
-            const float s = h2f<DT>((uint16_t)(v & 0xFFFFu));
+            const float s = h2f<DT>((uint16_t)(v & 0xFFFFu)) * back;
             const float nbias = -(128.f + (float)zb);
 #pragma unroll
             for (int mt = 0; mt < MT; ++mt)
@@ -178,6 +193,8 @@ __global__ void __launch_bounds__(kSmallWaves * 64) lin_small_kernel(const LinAr
             v[0] += red[w][b][r][c];
             if constexpr (GLU) u[0] += red[w][b + NB / 2][r][c];
         }
+        v[0] *= back;
+        u[0] *= back;
         if (p.slices > 1) {
             float *o = p.part + ((int64_t)blockIdx.y * p.M + row) * p.cols + col_of(b) + c;
             o[0] = v[0];

@@ -489,9 +489,7 @@ typedef struct {
  *   y         out, [M][N], row stride ldy
  * Every output is rounded once from fp32.  M <= 32 runs a decode kernel whose
  * waves split K (so do more rows of a small matrix), larger M a tile kernel; where the tiles would leave compute
- * units idle K is cut into slices whose fp32 sums meet in the workspace.  (The
- * tile kernel takes a scale below 2^-60 of a larger one before it in its column,
- * or below 2^-126, as zero.)
+ * units idle K is cut into slices whose fp32 sums meet in the workspace.
  */
 size_t w4a16_gemm_ep_workspace_bytes(const w4a16_linear *lin, int64_t M);
 

@@ -563,3 +563,35 @@ def test_large_finite_x_on_few_rows(M, size):
     of the sum allow is finite and keeps its bits."""
     large_x(Dev(scaled_layer(256, 128, 2.0 ** -30)), M, size)
     large_x(Dev(scaled_layer(256, 128, 2.0 ** 30)), M, 2.0 ** -118)
+
+
+@pytest.mark.parametrize("size", [2.0 ** 117, 2.0 ** 125])
+@pytest.mark.parametrize("shape", range(SHAPES))
+def test_large_finite_x_in_every_tile_shape(plan, shape, size):
+    plan(shape, 1)
+    D = Dev(scaled_layer(256, 128, 2.0 ** -30))
+    large_x(D, 150, size)
+    # a falling scale may not carry the sums past the type's range
+    D.L.scale[0] *= 2.0 ** 10
+    D.L.scale[1] *= 2.0 ** -40
+    large_x(Dev(D.L), 150, 2.0 ** 100)
+
+
+@pytest.mark.parametrize("shape", [-1, *range(SHAPES)])
+def test_scales_far_apart_and_x_zero_between_them(plan, shape):
+    """Groups of scales that lie 2^100 and more apart, subnormal ones among them, and
+    x zero in the groups of the larger: the rest is the whole result."""
+    K, N, M = 512, 128, 20 if shape < 0 else 150
+    L = ref.layer(K, N, 128, BF16, True, bias=False, seed=8)
+    s = L.scale
+    s[0, :32], s[1:3, :32], s[3, :32] = 2.0 ** 10, 2.0 ** -70, 2.0 ** 20
+    s[0, 32:64], s[1, 32:64], s[2, 32:64], s[3, 32:64] = 2.0 ** -3, 2.0 ** -66, 2.0 ** -110, 2.0 ** 30
+    s[1:3, 64:96] = 3 * 2.0 ** -132
+    s[1, 96:112], s[2, 96:112] = 3 * 2.0 ** -131, 0
+    plan(shape, int(shape >= 0))
+    x = ref.normal(M, K, 2.0 ** 24, BF16, 1)
+    x[:, :128], x[:, 384:] = 0, 0
+    y, _ = run_ep(Dev(L), x, NONE)
+    yr, _ = ref.ep(x, L, NONE)
+    terms = (x.double().square() @ L.weights().square()).sqrt()
+    ref.close(y, yr, ref.ULP[BF16] * 1.01 * yr.abs() + 8 * ref.SUM * terms, "far apart")

@@ -17,12 +17,12 @@
 // wave that dequantizes its own columns for 64 rows needs 7.
 //
 // Forward (contraction over K): codes enter the matrix core as exact integers
-// u - z and the scale acts on fp32 sums.  The sums are kept in units of the
-// current group's scale: entering group g they are multiplied by s[g-1] / s[g]
-// in place (Horner's scheme for sum_g s_g P_g), and by the last scale at the
-// end.  So no second set of accumulators is needed, and nothing but the result
-// is rounded to 16 bits.  A group multiplies every sum once: 2 vector
-// instructions per matrix-core step.
+// u - z (bf16: times the scale's power of two) and the scale acts on fp32 sums.  The
+// sums are kept in units of the current group's scale (bf16: of its significand):
+// entering group g they are multiplied by s[g-1] / s[g] in place (Horner's scheme
+// for sum_g s_g P_g), and by the last scale at the end.  So no second set of
+// accumulators is needed, and nothing but the result is rounded to 16 bits.  A
+// group multiplies every sum once: 2 vector instructions per matrix-core step.
 //
 // Transposed (contraction over N): column n of W contributes to all outputs of
 // its group with one scale s[g][n], which varies along the contraction; it must
@@ -89,34 +89,50 @@ __global__ void __launch_bounds__(512) lin_colsum_kernel(const float *part, floa
 
 // Forward products: the sums of a column are held in units of its running scale.
 // A new scale group multiplies them by unit / s first and its codes enter the
-// matrix core as exact integers.  A scale below 2^-60 of the largest so far (or
-// below the normal range, 0 among them) leaves the unit alone and its codes enter
-// as 0: what it would add is below 2^-60 of what the larger scale's codes weigh,
-// and the sums stay far from overflow.
+// matrix core as exact integers.
+//
+// bf16: of a scale m 2^e only m (1 <= |m| < 2) is the unit; 2^e goes into the codes, which
+// stay exact.  So the sums have the size of the result: they pass fp32's range, and
+// terms vanish, where those of x (u - z) s in fp32 would (with the whole scale as
+// the unit, a group beside one 2^60 larger had to count as zero, and sums grew by the
+// ratio of two scales).  Subnormal scales and those past 2^110 leave a part of 2^e in
+// the unit.  fp16: scales lie within 2^40 of each other and sums of x (u - z) below 2^42,
+// so the unit is the scale.  A scale of 0 leaves the unit alone and its codes
+// enter as 0.
 template <int DT>
 struct ScaleUnit {
-    float unit = 0.f, largest = 0.f, ratio = 1.f;
-    float zf;
+    float unit = 0.f, ratio = 1.f;
+    float f = 512.f, zf, m;           // bf16: factor of the codes' conversion, zero point times 2^e; the group's own unit
     uint32_t z, sel;
+    // A new group: what its codes need.
     __device__ __forceinline__ void next(float s, uint32_t zero) {
-        const float as_ = __builtin_fabsf(s);
-        const bool live = !((as_ < 0x1p-60f * largest) | (as_ < 0x1p-126f));      // NaN stays
-        const float q = unit * __builtin_amdgcn_rcpf(s);
-        ratio = (live & (s != unit)) ? q : 1.f;
-        unit = live ? s : unit;
-        largest = (live & (as_ > largest)) ? as_ : largest;
         z = zero;
-        zf = (float)zero;
+        m = s;
+        if constexpr (DT == DT_BF16) {
+            uint32_t e = __float_as_uint(s) & 0x7F800000u;
+            e = e < (1u << 23) ? 1u << 23 : e > (237u << 23) ? 237u << 23 : e;
+            f = __uint_as_float(e + (9u << 23));
+            zf = codes_f32<0>(zero, f)[0];
+            m = s * __uint_as_float((254u << 23) - e);                            // NaN and infinity stay
+        }
         // bf16: byte selector of the upper halves, or of zeros; fp16: mask
-        sel = DT == DT_BF16 ? (live ? 0x07060302u : 0x0C0C0C0Cu) : (live ? ~0u : 0u);
+        sel = DT == DT_BF16 ? (s != 0.f ? 0x07060302u : 0x0C0C0C0Cu) : (s != 0.f ? ~0u : 0u);
     }
-    // The 8 codes of a word as u - z, rows in order, in two halves: words HF and
-    // HF + 2 of the operand (fp16: all of it with the second).
+    // Its unit and the factor on the sums before it (lin_mid_kernel: later than the codes'
+    // part, 333 rows gated 15.2 -> 15.0 us).
+    __device__ __forceinline__ void change() {
+        const bool live = m != 0.f;                                               // NaN among them
+        const float q = unit * __builtin_amdgcn_rcpf(m);
+        ratio = (live & (m != unit)) ? q : 1.f;
+        unit = live ? m : unit;
+    }
+    // The 8 codes of a word as u - z (bf16: times 2^e), rows in order, in two halves: words HF
+    // and HF + 2 of the operand (fp16: all of it with the second).
     template <int HF>
     __device__ __forceinline__ void dequant(uint32_t w, u32x4_t &o) const {
         if constexpr (DT == DT_BF16) {
             const uint32_t m = (HF ? w >> 4 : w) & 0x0F0F0F0Fu;            // bytes: rows 0, 4, 1, 5 or 2, 6, 3, 7
-            const f32x2_t a = codes_f32<0>(m), b = codes_f32<1>(m);
+            const f32x2_t a = codes_f32<0>(m, f), b = codes_f32<1>(m, f);
             o[HF] = __builtin_amdgcn_perm(__float_as_uint(b[0] - zf), __float_as_uint(a[0] - zf), sel);
             o[HF + 2] = __builtin_amdgcn_perm(__float_as_uint(b[1] - zf), __float_as_uint(a[1] - zf), sel);
         } else if constexpr (HF == 1) {
@@ -276,39 +292,24 @@ __global__ void __launch_bounds__(wide_groups(BM, BN) * 2 * BN, 2) lin_wide_kern
     auto zero_of = [&](uint32_t zb) {
         return p.zero ? __builtin_amdgcn_ubfe(zb, (uint32_t)(j & 1) * 4u, 4) : 8u;
     };
-    // Forward: ScaleUnit's scheme (unit se, largest scale smax), the factors handed
-    // to the waves that hold a column's sums through LDS.
-    float se = 0.f, smax = 0.f;
-    struct Deq { float s, zs; uint32_t z, sel; } dq;
+    // Forward: the factors on the sums reach the waves that hold a column's sums
+    // through LDS.  Transposed: W = u s - z s.
+    ScaleUnit<DT> su;
+    float ds, dzs;
+    uint32_t dz;
     // stage st is about to be dequantized: its column's scale and zero point
     // (forward: once per 128-row group, from the loaded values)
     auto deq_begin = [&](int st) {
-        uint32_t sb, z;
         if constexpr (T) {
             const uint32_t v = (uint32_t)__builtin_amdgcn_ds_bpermute((((st - s0) & 3) * 16 + j) << 2, (int)scur);
-            sb = v & 0xFFFFu;
-            z = v >> 16;
+            ds = h2f<DT>((uint16_t)(v & 0xFFFFu));
+            dz = v >> 16;
+            dzs = -(float)dz * ds;
         } else {
-            sb = snext;
-            z = zero_of(znext);
+            su.next(h2f<DT>(snext), zero_of(znext));
+            su.change();
+            s_ratio[wcol] = su.ratio;                 // both lanes of a column write the same value
         }
-        const float s = h2f<DT>((uint16_t)sb);
-        bool live = true;
-        if constexpr (!T) {
-            const float as_ = __builtin_fabsf(s);
-            live = !((as_ < 0x1p-60f * smax) | (as_ < 0x1p-126f));      // NaN stays
-            float ratio = se * __builtin_amdgcn_rcpf(s);
-            ratio = (live & (s != se)) ? ratio : 1.f;
-            se = live ? s : se;
-            smax = (live & (as_ > smax)) ? as_ : smax;
-            s_ratio[wcol] = ratio;                    // both lanes of a column write the same value
-        }
-        dq.s = s;
-        dq.z = z;
-        const float zf = (float)z;
-        dq.zs = T ? -zf * s : zf;
-        // bf16: byte selector of the upper halves, or of zeros; fp16: mask
-        dq.sel = DT == DT_BF16 ? (live ? 0x07060302u : 0x0C0C0C0Cu) : (live ? ~0u : 0u);
     };
     // Half-word i of the slot (word i / 2): codes of rows 0, 1, 4, 5 or 2, 3, 6, 7
     // of its 8; the second half writes the 16 bytes to LDS.
@@ -316,35 +317,24 @@ __global__ void __launch_bounds__(wide_groups(BM, BN) * 2 * BN, 2) lin_wide_kern
     auto deq_half = [&](int d, int buf, int i) {
         const int t = i >> 1, hf = i & 1;
         const uint32_t w = wr[d][t];
-        if constexpr (DT == DT_BF16) {
+        if constexpr (!T) {
+            if (hf) su.template dequant<1>(w, dqo);
+            else su.template dequant<0>(w, dqo);
+        } else if constexpr (DT == DT_BF16) {
             // bytes: rows 0, 4, 1, 5 (or 2, 6, 3, 7)
             const uint32_t m = (hf ? w >> 4 : w) & 0x0F0F0F0Fu;
-            const f32x2_t c04 = codes_f32<0>(m);
-            const f32x2_t c15 = codes_f32<1>(m);
-            const float v[4] = {c04[0], c15[0], c04[1], c15[1]};
+            const f32x2_t c04 = codes_f32<0>(m), c15 = codes_f32<1>(m);
 #pragma unroll
             for (int q = 0; q < 2; ++q) {
-                if constexpr (T) {
-                    const bf16x2_t b = {(__bf16)__builtin_fmaf(v[2 * q], dq.s, dq.zs),
-                                        (__bf16)__builtin_fmaf(v[2 * q + 1], dq.s, dq.zs)};
-                    dqo[hf + 2 * q] = __builtin_bit_cast(uint32_t, b);
-                } else {
-                    // integers up to 15: exact in the upper 16 bits
-                    dqo[hf + 2 * q] = __builtin_amdgcn_perm(__float_as_uint(v[2 * q + 1] - dq.zs),
-                                                            __float_as_uint(v[2 * q] - dq.zs), dq.sel);
-                }
+                const bf16x2_t b = {(__bf16)__builtin_fmaf(c04[q], ds, dzs), (__bf16)__builtin_fmaf(c15[q], ds, dzs)};
+                dqo[hf + 2 * q] = __builtin_bit_cast(uint32_t, b);
             }
         } else if (hf) {
-            dqo = dequant_word<DT>(w, f16_negbias2(dq.z));
-            if constexpr (T) {
-                const _Float16 m = (_Float16)dq.s;
-                const f16x2_t m2 = {m, m};
+            dqo = dequant_word<DT>(w, f16_negbias2(dz));
+            const _Float16 m = (_Float16)ds;
+            const f16x2_t m2 = {m, m};
 #pragma unroll
-                for (int q = 0; q < 4; ++q) dqo[q] = __builtin_bit_cast(uint32_t, as<f16x2_t>(dqo[q]) * m2);
-            } else {
-#pragma unroll
-                for (int q = 0; q < 4; ++q) dqo[q] &= dq.sel;
-            }
+            for (int q = 0; q < 4; ++q) dqo[q] = __builtin_bit_cast(uint32_t, as<f16x2_t>(dqo[q]) * m2);
         }
         if (hf) *reinterpret_cast<u32x4_t *>(ldb_ + buf * BBYTES + (bdst ^ (uint32_t)(t << 4))) = dqo;
     };
@@ -533,7 +523,7 @@ __global__ void __launch_bounds__(wide_groups(BM, BN) * 2 * BN, 2) lin_wide_kern
     float scl[CT] = {1.f, 1.f};
     if constexpr (!T) {
         // scale that the sums are held in, per column
-        s_ratio[wcol] = se;
+        s_ratio[wcol] = su.unit;
         __syncthreads();
 #pragma unroll
         for (int ct = 0; ct < CT; ++ct) scl[ct] = s_ratio[wn * 64 + ct * 32 + l31];
@@ -743,6 +733,7 @@ __global__ void __launch_bounds__(512, 2) lin_mid_kernel(const LinArgs p) {
                         load_s(s + 3);
                     }
                 }
+                if (t == 2 && rt == 0 && buf == 1) su.change();
                 __builtin_amdgcn_sched_barrier(0);
             }
         }
@@ -759,6 +750,7 @@ __global__ void __launch_bounds__(512, 2) lin_mid_kernel(const LinArgs p) {
 #pragma unroll
         for (int i = 0; i < XP; ++i) store_a(0, i);
         next_group();
+        su.change();
         load_s(s0 + 2);
 #pragma unroll
         for (int t = 0; t < 3; ++t) {

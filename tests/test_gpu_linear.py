@@ -595,3 +595,30 @@ def test_scales_far_apart_and_x_zero_between_them(plan, shape):
     yr, _ = ref.ep(x, L, NONE)
     terms = (x.double().square() @ L.weights().square()).sqrt()
     ref.close(y, yr, ref.ULP[BF16] * 1.01 * yr.abs() + 8 * ref.SUM * terms, "far apart")
+
+
+@pytest.mark.parametrize("dt", [F16, BF16])
+@pytest.mark.parametrize("M", [3, 300])
+def test_gelu_keeps_its_lower_tail(M, dt):
+    """GELU and its derivative at pre-activations from -12 to -2 that are exact (x = 0, the
+    bias is all there is): relative to the result's own size.  The exponent's
+    rounding (v^2 / 2 = 72 at most, a few 2^-24 of it) stays below 2^-14; fp16 has
+    its subnormal spacing on top."""
+    v = -2 - 10 * torch.arange(256) / 255
+    L = ref.layer(128, 512, 128, dt, seed=1)
+    L.bias = torch.cat((v, torch.full((256,), 512.0))).to(ref.TD[dt])
+    v = L.bias[:256].double()
+    cdf, pdf = torch.exp(torch.special.log_ndtr(v)), torch.exp(-v * v / 2) / math.sqrt(2 * math.pi)
+    D, tiny = Dev(L), 2.0 ** -25 * 1.01 if dt == F16 else 0.0
+
+    def near(got, want, what):
+        want = want.expand(M, 256)
+        ref.close(got, want, (ref.ULP[dt] * 1.01 + 2.0 ** -14) * want.abs() + tiny, what)
+
+    x = torch.zeros((M, 128), dtype=ref.TD[dt])
+    near(run_ep(D, x, GELU)[0][:, :256], v * cdf, "gelu")
+    near(run_glu(D, x, GELU)[0], v * cdf * 512, "gelu times 512")
+    dy = torch.ones((M, 512), dtype=ref.TD[dt])
+    h = L.bias.expand(M, 512).contiguous()
+    near(run_bwd(D, False, dy, h, GELU)[1][:, :256], cdf + v * pdf, "gelu'")
+    near(run_bwd(D, True, dy[:, :256].contiguous(), h, GELU)[1][:, 256:], v * cdf, "gelu, up half")

@@ -194,8 +194,8 @@ hipError_t launch_lin(int mode, LinArgs p, const LinPlan &plan, int dt, void *wo
 int lin_shape_count();
 void set_lin_plan(int shape, int slices);
 // The decode-sized kernels.
-bool lin_small_ok(int mode, int64_t M, int64_t K, int64_t N);
-double lin_small_us(int mode, int64_t M, int64_t K, int64_t N);      // estimate past that range
+bool lin_small_ok(int mode, int64_t M);                              // always run
+double lin_small_us(int mode, int64_t M, int64_t K, int64_t N);      // estimate where they may not
 size_t lin_small_workspace_bytes(int mode, int64_t M, int64_t K, int64_t N);
 hipError_t launch_lin_small(int mode, LinArgs p, int dt, void *workspace, hipStream_t stream);
 // Sum of the slices in p.part and the finishing step.

@@ -1000,11 +1000,13 @@ LinPlan lin_plan(int mode, int64_t M, int64_t K, int64_t N) {
     LinPlan plan{};
     // a forced tile shape also takes the rows that the decode kernels would
     const bool free = g_lin_shape.load(std::memory_order_relaxed) < 0;
-    plan.small = free && lin_small_ok(mode, M, K, N);
+    plan.small = free && lin_small_ok(mode, M);
     if (!plan.small) {
         const WidePlan w = wide_plan(mode, M, K, N);
-        // (a launch and its first loads take the tile kernels 2.8 us besides their stages)
-        plan.small = free && M > 32 && lin_small_us(mode, M, K, N) < w.us + 2.8;
+        // (a launch and its first loads take the tile kernels 2.8 us besides their stages;
+        // 32 rows in more than eight slices 2 us more: each has few stages and more to join)
+        const double tiles = w.us + 2.8 + (M <= 32 && w.slices > 8 ? 2.5 : 0.0);
+        plan.small = free && lin_small_us(mode, M, K, N) < tiles;
         plan.bm = w.bm;
         plan.bn = w.bn;
         plan.slices = w.slices;

@@ -30,7 +30,10 @@
 namespace w4 {
 
 constexpr int kSmallWaves = 8;       // most waves per workgroup
-constexpr int64_t kSmallMaxM = 32;   // rows up to which the decode kernels always run
+// Rows up to which the forward decode kernel always runs: within 3% of the tile kernel or
+// faster on nine matrices (32 rows: 4096^2 11.3 against 11.8 us, 1024^2 5.5 against 7.7, gated 4096 x
+// 28672 23.8 against 23.1).
+constexpr int64_t kSmallMaxM = 32;
 constexpr int64_t kSmallGroupsM = 512;
 
 // A byte offset past the end of every buffer (at most 2^31 bytes).
@@ -220,9 +223,9 @@ __global__ void __launch_bounds__(kSmallWaves * 64) lin_small_kernel(const LinAr
 //
 // Every workgroup reads all of d: K / 32 times M N 2 bytes, which bounds it for
 // many rows of large matrices; the weights' stream and the launch otherwise.
-// Measured (bf16, graph replay): one row of 1024^2 6.6 us, of 4096^2 9.3 us, of
-// 4096 x 28672 29 us; 32 rows 7.8, 14.6 us.  The tile kernel with its best slices takes
-// 8.4, 11.9, 30 and 9.2, 13.4 us; from M K N = 6e8 on it is the faster one.
+// Measured (bf16, graph replay; the tile kernel with its best slices behind it): one row of
+// 1024^2 5.9 (7.9) us, of 4096^2 8.5 (11.2), of 14336 x 1024 10.8 (9.4), of 4096 x 28672 28.5
+// (28.7); 32 rows 7.2 (8.6), 13.7 (12.5), 14.0 (10.1), 60 (30).
 constexpr int kSmallTWaves = 16;
 
 template <int DT>
@@ -396,24 +399,33 @@ static SmallPlan small_plan(int mode, int64_t M, int64_t K, int64_t N) {
     return s;
 }
 
-// Where the decode kernels always run (transposed: see there).  Beyond, up to
-// kSmallGroupsM rows in 32-row groups on the grid, they compete with the tile
+// Where the decode kernels always run.  Beyond (forward up to kSmallGroupsM rows in
+// row groups on the grid, transposed from one row on) they compete with the tile
 // kernel by estimated time: small matrices leave most of the machine idle there.
-bool lin_small_ok(int mode, int64_t M, int64_t K, int64_t N) {
-    return M <= kSmallMaxM && (!lin_transposed(mode) || M * K * N <= 600000000);
-}
+bool lin_small_ok(int mode, int64_t M) { return M <= kSmallMaxM && !lin_transposed(mode); }
 
-// Estimated us of a call with several 32-row groups (whole K or N, no slices; a
-// large value where it may not run), launch included: rounds of 256 workgroups,
+// Estimated us of a transposed call or one with several 32-row groups (forward: whole K,
+// no slices; a large value where it may not run), launch included: rounds of 256 workgroups,
 // each as long as its share of the contraction and 0.9 us for its ends.  Fits to
 // M = 33..400 on matrices from 256^2 to 4096^2 (1024^2, M = 100: 6.2 against 9.0 us on
 // tiles, transposed 8.2 against 10.0; 1408 x 2816 gated, M = 64: 7.6 against 10.7).
+// Transposed, up to 32 rows: what a block costs grows with the rows of d, and a second
+// round starts cold.  On 24 random matrices and six row counts up to 32 each the choice was
+// within 5% of the better kernel in 141 of 144 (14, 18 and 21% off for nine rows of large ones).
 double lin_small_us(int mode, int64_t M, int64_t K, int64_t N) {
     const SmallPlan s = small_plan(mode, M, K, N);
     if (M > kSmallGroupsM || (s.slices > 1 && !lin_transposed(mode))) return 1e9;
     const int64_t groups = (M + 31) / 32;
     if (lin_transposed(mode)) {
-        const double rounds = (double)((K / 32 * groups * s.slices + 255) / 256);
+        const int64_t wgs = K / 32 * groups * s.slices;
+        if (M <= kSmallMaxM) {
+            // (two workgroups of up to eight waves share a compute unit)
+            const int64_t once = s.waves > 8 ? 256 : 512;
+            const double rounds = (double)((wgs + once - 1) / once);
+            return 2.6 + (rounds > 1 ? 1.3 * rounds : 1.0) * (2.0 + (0.9 + 1.1 / 32 * (double)M) / 1024 * (double)N / s.slices) +
+                   (s.slices > 1 ? 3.0 : 0.0);
+        }
+        const double rounds = (double)((wgs + 255) / 256);
         return 3.6 + rounds * (rounds > 1 ? 1.3 : 1.0) * (1.0 + 2.3 / 1024 * (double)N / s.slices) +
                (s.slices > 1 ? 3.0 : 0.0);
     }

@@ -60,9 +60,9 @@ typedef enum {
     W4A16_OK = 0,
     W4A16_ERR_NULL = 1,         /* a required pointer is NULL               */
     W4A16_ERR_SHAPE = 2,        /* a size violates the shape rules          */
-    W4A16_ERR_UNSUPPORTED = 3,  /* group_size or dtype not supported        */
-    W4A16_ERR_ALIGN = 4,        /* a pointer is not aligned as required     */
-    W4A16_ERR_WORKSPACE = 5,    /* MSD workspace missing or too small       */
+    W4A16_ERR_UNSUPPORTED = 3,  /* group_size, dtype or act not supported   */
+    W4A16_ERR_ALIGN = 4,        /* a pointer or row stride is not aligned   */
+    W4A16_ERR_WORKSPACE = 5,    /* workspace missing or too small           */
     W4A16_ERR_DEVICE = 6,       /* not a gfx950 device, or a launch failed  */
     W4A16_ERR_SCRATCH = 7       /* needs more than the static scratch holds */
 } w4a16_status;

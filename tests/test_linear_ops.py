@@ -136,3 +136,19 @@ def test_few_rows_backward_takes_the_faster_kernel():
         rows = 4 * N * ((M + 3) // 4)                # partial column sums, one row per block of four
         need = w4.w4a16_gemm_ep_backward_workspace_bytes(lin(K=K, N=N), M)
         assert need == rows + slices * M * K * 4, (M, K, N)
+
+
+@pytest.mark.parametrize("refused,words", [
+    (lambda: fwd(False, lin(group_size=64)), ("fused linear operators", "multiple of 128")),
+    (lambda: fwd(False, lin(), act=9), ("w4a16_act",)),
+    (lambda: fwd(False, lin(), ldx=248), ("row strides", "2^22")),
+    (lambda: fwd(True, lin(N=192)), ("gated N%128",)),
+    (lambda: fwd(False, lin(K=1 << 23)), ("up to 2^22",)),
+    (lambda: fwd(False, lin(group_size=384)), ("group_size dividing K",)),
+    (lambda: fwd(False, lin(), ldx=260), ("multiple of 8",)),
+    (lambda: fwd(False, lin(), y=F + 2), ("fused linear operators: 16 bytes",)),
+    (lambda: bwd(False, lin(), db=F + 2), ("dbias, 4",)),
+])
+def test_a_refusal_names_its_rule(refused, words):
+    text = w4.w4a16_status_str(refused())
+    assert all(w in text for w in words), text

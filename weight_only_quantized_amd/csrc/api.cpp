@@ -124,9 +124,9 @@ const char *w4a16_status_str(int status) {
     switch (status) {
         case W4A16_OK: return "W4A16_OK";
         case W4A16_ERR_NULL: return "W4A16_ERR_NULL: a required pointer is NULL";
-        case W4A16_ERR_SHAPE: return "W4A16_ERR_SHAPE: sizes violate K>0, K%128==0, N>0, N%64==0, M>=0, E>=1";
-        case W4A16_ERR_UNSUPPORTED: return "W4A16_ERR_UNSUPPORTED: group_size must be 32, 64 or a multiple of 128 (MSD and the MoE chain: 128; W8A16 and floating-point zero points: a multiple of 128), dtype F16 or BF16 (MSD: F16)";
-        case W4A16_ERR_ALIGN: return "W4A16_ERR_ALIGN: x, w_packed, workspace need 16-byte, scale and y 2-byte alignment";
+        case W4A16_ERR_SHAPE: return "W4A16_ERR_SHAPE: sizes violate K>0, K%128==0, N>0, N%64==0, M>=0, E>=1, group_size dividing K (fused linear operators: also gated N%128==0, K and N up to 2^22, K*N up to 2^32, row strides from the row length to 2^22)";
+        case W4A16_ERR_UNSUPPORTED: return "W4A16_ERR_UNSUPPORTED: group_size must be 32, 64 or a multiple of 128 (MSD and the MoE chain: 128; W8A16, floating-point zero points and the fused linear operators: a multiple of 128), dtype F16 or BF16 (MSD: F16), act a w4a16_act";
+        case W4A16_ERR_ALIGN: return "W4A16_ERR_ALIGN: x, w_packed, workspace need 16-byte, scale and y 2-byte alignment (fused linear operators: 16 bytes for all but scale, 2, and dbias, 4; row strides a multiple of 8 elements)";
         case W4A16_ERR_WORKSPACE: return "W4A16_ERR_WORKSPACE: workspace is NULL or smaller than the call's workspace query";
         case W4A16_ERR_DEVICE: return "W4A16_ERR_DEVICE: current device is not gfx950 or a launch failed";
         case W4A16_ERR_SCRATCH:

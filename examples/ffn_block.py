@@ -42,19 +42,18 @@ def dequantized(plain):
 
 
 class FeedForward:
-    """The block's weights and one workspace for all of its calls."""
+    """The block's weights and one workspace for all of its calls of up to max_tokens rows."""
 
     def __init__(self, hidden, width, max_tokens, seed=0, device="cuda"):
         gen = torch.Generator(device=device).manual_seed(seed)
         self.hidden, self.width, self.device = hidden, width, device
         self.w13, self.plain13 = quantized(hidden, 2 * width, gen)
         self.w2, self.plain2 = quantized(width, hidden, gen)
-        # (not monotonic in the row count: small counts may be cut into slices)
-        counts = {1 << i for i in range(max_tokens.bit_length())} | {max_tokens}
-        self.ws_bytes = max(q(lin, m) for m in counts for lin, qs in (
+        # (a size is not monotonic in the row count, since fewer rows may be cut into more
+        # slices: the largest of all counts up to max_tokens)
+        self.ws_bytes = max(q(lin, m) for m in range(1, max_tokens + 1) for lin, qs in (
             (self.w13, (w4.w4a16_glu_gemm_workspace_bytes, w4.w4a16_glu_gemm_backward_workspace_bytes)),
             (self.w2, (w4.w4a16_gemm_ep_workspace_bytes, w4.w4a16_gemm_ep_backward_workspace_bytes))) for q in qs)
-        self.counts = counts
         self.ws = torch.empty(max(self.ws_bytes, 16), device=device, dtype=torch.uint8)
 
     def new(self, rows, cols):
@@ -63,7 +62,6 @@ class FeedForward:
     def forward(self, x, save=False):
         """y, and what backward needs when `save` is set."""
         M = x.shape[0]
-        assert M in self.counts
         h = self.new(M, 2 * self.width) if save else None
         a, y = self.new(M, self.width), self.new(M, self.hidden)
         ws = dict(workspace=self.ws, workspace_bytes=self.ws_bytes)

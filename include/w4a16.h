@@ -460,7 +460,10 @@ w4a16_status w4a8_mxfp4_grouped_gemm(const void *x, const int32_t *expert_offset
  *  - workspace: device, 16-byte aligned, at least the size the matching
  *    query returns for the same (lin, M); may be NULL when that is 0.  Its
  *    contents on entry are ignored.  Calls sharing one must be ordered on one
- *    stream.  The queries return 0 for sizes the calls reject.
+ *    stream.  The queries return 0 for sizes the calls reject.  They are not
+ *    monotonic in M (fewer rows may be cut into more slices): one workspace
+ *    for varying row counts is as large as the largest of their queries, which
+ *    take a microsecond each.
  *  - Sums are fp32 in an order fixed by the sizes (no atomics): equal calls
  *    give equal bits.
  */

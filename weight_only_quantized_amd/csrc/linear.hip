@@ -10,8 +10,7 @@
 // the tile in 32 x 32 x 16 matrix-core steps.  Tiles of 128 columns (transposed) have
 // two such groups of waves, each with half of the contraction and LDS of its
 // own: two waves per SIMD, one's vector work beside the other's products (64 x 128,
-// M = 128, 4096^2 unsliced 34 -> 26 us).  Both operands of a stage
-// lie in LDS, double buffered.  W is dequantized once per workgroup on its way
+// M = 128, 4096^2 unsliced 33.9 -> 26.7 us).  Both operands of a stage lie in LDS, double buffered.  W is dequantized once per workgroup on its way
 // there (32 codes of one column per thread and stage), so one conversion serves
 // BM rows: with 256 rows 3 vector instructions per matrix-core step, where a
 // wave that dequantizes its own columns for 64 rows needs 7.
@@ -173,13 +172,13 @@ __global__ void __launch_bounds__(wide_groups(BM, BN) * 2 * BN, 2) lin_wide_kern
     constexpr int LDSBYTES = 2 * (ABYTES + BBYTES);
     static_assert(LDSBYTES >= NT / 64 * 32 * OUTROW * 4, "output staging fits");
     __shared__ __attribute__((aligned(16))) uint8_t lds[KS * LDSBYTES];
-    __shared__ float s_ratios[T ? 1 : KS * BN];      // per column: factor on the sums at a new scale group
+    static_assert(T || KS == 1, "forward tiles of 128 columns: lin_mid_kernel");
+    __shared__ float s_ratio[T ? 1 : BN];            // per column: factor on the sums at a new scale group
 
     const int tid = threadIdx.x % NT, lane = tid & 63;
     const int wave_all = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const int grp = wave_all / (NT / 64), wave = wave_all % (NT / 64);     // wave group, wave in it
     uint8_t *const lda_ = lds + grp * LDSBYTES, *const ldb_ = lda_ + 2 * ABYTES;
-    float *const s_ratio = s_ratios + (T ? 0 : grp * BN);
     const int wm = wave / (BN / 64), wn = wave % (BN / 64);
     const int l31 = lane & 31, kg = lane >> 5;
 
@@ -553,13 +552,13 @@ __global__ void __launch_bounds__(wide_groups(BM, BN) * 2 * BN, 2) lin_wide_kern
         if constexpr (MODE == LIN_GLU) {
             const int64_t c0 = nt * (BN / 2) + wn * 32;
             if (c0 < p.cols / 2) {
-                for (int i = grp; i < 2; i += KS) {
+                for (int i = 0; i < 2; ++i) {
                     const int r = i * 16 + (lane >> 2), c = (lane & 3) * 8;
                     const int64_t row = rbase + r;
                     if (row < p.M) {
                         float g[8], u[8];
 #pragma unroll
-                        for (int e = 0; e < 8; ++e) g[e] = sum_of(r * OUTROW + c + e), u[e] = sum_of(r * OUTROW + 32 + c + e);
+                        for (int e = 0; e < 8; ++e) g[e] = os[r * OUTROW + c + e], u[e] = os[r * OUTROW + 32 + c + e];
                         if (p.slices > 1) {
                             float *o = p.part + ((int64_t)slice * p.M + row) * p.cols + c0 + c;
 #pragma unroll

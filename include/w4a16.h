@@ -515,7 +515,8 @@ w4a16_status w4a16_gemm_ep(const void *x, int64_t ldx, const w4a16_linear *lin, 
  *   dx      out, [M][K], row stride lddx
  * The product multiplies dpre and dequant(W), each rounded to dt (the
  * matrix core takes 16-bit operands and the scales vary along the summed
- * dimension), with fp32 sums and one rounding of dx.
+ * dimension; fp16: |(q - z) s| past 65504 becomes infinite there), with fp32
+ * sums and one rounding of dx.
  */
 size_t w4a16_gemm_ep_backward_workspace_bytes(const w4a16_linear *lin, int64_t M);
 

@@ -26,7 +26,11 @@
 // Transposed (contraction over N): column n of W contributes to all outputs of
 // its group with one scale s[g][n], which varies along the contraction; it must
 // sit on an operand.  W is therefore rounded to the activation dtype as
-// (u - z) s, like d itself; both are the 16-bit operands any matrix core needs.
+// (u - z) s, and d enters as it is stored; both are the 16-bit operands the matrix
+// core needs.  That costs accuracy: against 64 bits dx is 1.3 times as far off as one rounding
+// of the result, 1.6 times where d was rounded too (plain fp32: once).  A second
+// product with the remainder of W would bring those to 1 and 1.4, and
+// its matrix instructions alone take gated 4096 x 4096 x 28672 from 875 to 1390 us.
 // The codes of one lane belong to one column n and 32 rows k, while the operand
 // wants 8 columns n of one k: the tile is written as [n][k] rows and read with
 // the transposing LDS read.
@@ -36,10 +40,10 @@
 // 8 (r / 4) + 4 (l / 32) + r % 4, column l % 32.
 //
 // Bound: large products by the matrix core, at the clock that it leaves under full load.  Measured
-// (bf16, graph replay): gated 4096 x 4096 x 28672 with h saved 804 us (1.20
-// PFLOP/s; a library product of unquantized bf16 operands of that size takes
+// (bf16, graph replay): gated 4096 x 4096 x 28672 with h saved 804 to 821 us on
+// different cards (1.2 PFLOP/s; a library product of unquantized bf16 operands of that size takes
 // 731 us here), transposed 4096 x 28672 x 4096 750 us (1.28 PFLOP/s; library 681 us),
-// 4096^3 125 us forward and 120 us transposed (library 126 us).  The matrix core
+// 4096^3 124 to 135 us forward and 120 us transposed (library 126 us).  The matrix core
 // is busy 60% (forward) and 67% (transposed) of 1.7 GHz cycles; LDS accesses,
 // 1% of them bank conflicts, take 40%.  Wave priorities, 128 x 128 wave tiles and
 // other placements of the vector work measured even or slower.
@@ -607,7 +611,7 @@ __global__ void __launch_bounds__(wide_groups(BM, BN) * 2 * BN, 2) lin_wide_kern
 // Bound: vector and matrix instructions of two waves per SIMD (BM = 64: 0.55 us for
 // a stage of both groups, 840 vector and 512 matrix cycles), and the join where the
 // rows are so few that K is sliced.  More waves would not fit the registers (4 per
-// SIMD: 26 spilled, 22 -> 32 us).  Measured (bf16, graph replay), before with W in
+// SIMD, with spills: 22 -> 32 us).  Measured (bf16, graph replay), before with W in
 // LDS and one wave group: M = 128, 4096 x 14336 gated 42.5 -> 24.5 us; M = 512, 4096^2
 // 35.2 -> 25.6; M = 77, 14336 x 4096 in 8 slices 33.0 -> 27.1; M = 333, 2048 x 2816
 // gated fp16 18.9 -> 14.4.
@@ -856,7 +860,9 @@ __global__ void __launch_bounds__(256) lin_join_kernel(const LinArgs p) {
 // Bound by memory: dy and h are read and d is written once (gated, 4096 x 28672:
 // 587 MB in 98 us, 6.0 TB/s; the column sums come with it).
 //
-// d (and with it the column sums) from dy and the saved pre-activation.  A
+// d (and with it the column sums, of the unrounded values) from dy and the saved
+// pre-activation.  The product reads d back as it is stored, in 16 bits: forming it again
+// from dy and h per column tile cost 1.3 us a stage.  A
 // workgroup takes 512 columns (glu: of each half) and every gridDim.y-th block
 // of four rows; a thread owns 8 columns of one row in each block and sums its
 // rows in ascending order.  The four rows' sums meet in LDS, the workgroups'

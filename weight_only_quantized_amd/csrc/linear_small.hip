@@ -22,8 +22,8 @@
 //
 // Bound: the weight stream at the start (latency) and through the launch.
 // Measured (bf16, zero points): gated 4096 x 28672, one row 12.8 us (61 MB, 4.8
-// TB/s, the rate of a large copy), 16 rows 14.7 us; 14336 x 4096, one row 8.1 us
-// (3.8 TB/s).  More groups on the way and bounded buffer loads measured slower
+// TB/s, the rate of a large copy), 16 rows 14.7 us; 14336 x 4096, one row 8.3 us
+// (3.7 TB/s).  More groups on the way and bounded buffer loads measured slower
 // (8.7 -> 9.9 us and more for 14336 x 4096).
 #include "act.hpp"
 

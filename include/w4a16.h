@@ -67,7 +67,11 @@ typedef enum {
     W4A16_ERR_SCRATCH = 7       /* needs more than the static scratch holds */
 } w4a16_status;
 
-typedef enum { W4A16_F16 = 0, W4A16_BF16 = 1 } w4a16_dtype;
+typedef enum {
+    W4A16_F16 = 0,
+    W4A16_BF16 = 1,
+    W4A16_F32 = 2               /* logits of the MoE router only            */
+} w4a16_dtype;
 
 /* Human-readable name of a status code (static string, never NULL). */
 const char *w4a16_status_str(int status);
@@ -552,6 +556,118 @@ w4a16_status w4a16_glu_gemm_backward(const void *da, int64_t ldda, const void *h
                                      const void *addend, int64_t ldadd, void *dh, float *dbias, void *dx,
                                      int64_t lddx, int64_t M, int dt, void *workspace, size_t workspace_bytes,
                                      void *stream);
+
+/*
+ * ---- W8A8: products of 8-bit integers ----------------------------------------
+ * Activations quantized per row (token), int8 weights with one fp32 scale per
+ * column:
+ *   s_m = fl32(max_k |x[m][k]| / 127),
+ *   q[m][k] = x[m][k] / s_m rounded to nearest even (the exact quotient) and
+ *             limited to [-127, 127]; 0 where s_m = 0,
+ *   y[m][n] = s_m sw[n] sum_k q[m][k] W[k][n] + bias[n], rounded to dt.
+ * The sum is exact in 32 bits; scales, bias and the one rounding follow in fp32
+ * (a product of scales outside fp32's range does no harm where y is inside it).  A
+ * row that holds a NaN or an infinity has s_m = NaN and codes 0: its results are
+ * NaN, those of other rows are not affected.
+ * Weights: prepacked by w8a16_prepack with is_signed = 1 (the same packed copy
+ * serves w8a16_gemm), [-128, 127].
+ *  - K % 128 == 0, K < 2^17 (the sums stay below 2^31), N % 64 == 0, M >= 0,
+ *    M and N below 2^31 and 2^22.
+ *  - x, qx, w_packed, y, workspace 16-byte aligned, bias 2, fp32 and int32 arrays 4.
+ *    Row strides ldx, ldy count elements: a multiple of 8, at least the row length,
+ *    at most 2^22; 0 means rows without gaps.
+ *  - Results do not depend on the kernel that a size picks: equal rows give equal
+ *    bits in every batch.
+ */
+
+/* Codes qx [M][K] (int8) and scales sx [M] of x [M][K] (dtype dt).  row_count, if
+ * not NULL, is a DEVICE int32 with the number of rows to process (at most M);
+ * rows behind it are left as they were. */
+w4a16_status w8a8_quantize(const void *x, int64_t ldx, const int32_t *row_count, void *qx, float *sx, int64_t M,
+                           int64_t K, int dt, void *stream);
+
+/* y [M][N] (dtype dt) from codes and scales.  Codes may be any int8 (-128 too).
+ * bias [N] in dt or NULL. */
+w4a16_status w8a8_gemm_prequant(const void *qx, const float *sx, const void *w_packed, const float *sw,
+                                const void *bias, void *y, int64_t ldy, int64_t M, int64_t K, int64_t N, int dt,
+                                void *stream);
+
+/* Scratch of w8a8_gemm: the codes and scales of M rows.  0 for sizes that the call rejects. */
+size_t w8a8_workspace_bytes(int64_t M, int64_t K);
+
+/* y [M][N] from x [M][K] (dtype dt): w8a8_quantize into the workspace, then the
+ * product.  Contents of the workspace on entry are ignored, on return unspecified;
+ * calls sharing it must be ordered on one stream. */
+w4a16_status w8a8_gemm(const void *x, int64_t ldx, const void *w_packed, const float *sw, const void *bias, void *y,
+                       int64_t ldy, int64_t M, int64_t K, int64_t N, int dt, void *workspace, size_t workspace_bytes,
+                       void *stream);
+
+/* Scratch of w8a8_grouped_gemm, for R rows whether or not they are gathered. */
+size_t w8a8_grouped_workspace_bytes(int64_t R, int64_t K);
+
+/*
+ * Grouped (MoE) form: rows expert_offsets[e] .. expert_offsets[e+1]-1 of y are
+ * products with expert e's weights.
+ *   sorted_ids  NULL: row r multiplies row r of x [R][K].  Else the int32 array that
+ *               w4a16_moe_align writes for R = T * topk entries: row r multiplies row
+ *               sorted_ids[r] / topk of x [T][K], and every token is quantized once
+ *   topk        entries per token, R % topk == 0; ignored without sorted_ids
+ *   expert_offsets  DEVICE int32[E+1], non-decreasing, offsets[0] = 0, offsets[E] <= R
+ *               (read on the device only); rows behind offsets[E] are left as they were
+ *   w_packed    the E experts' prepacked weights; sw [E][N]; y [R][N], no gaps
+ * 1 <= E <= 2^20.  Workspace as for w8a8_gemm.
+ */
+w4a16_status w8a8_grouped_gemm(const void *x, const int32_t *sorted_ids, int64_t topk, const int32_t *expert_offsets,
+                               const void *w_packed, const float *sw, void *y, int64_t E, int64_t R, int64_t K,
+                               int64_t N, int dt, void *workspace, size_t workspace_bytes, void *stream);
+
+/*
+ * ---- MoE router -----------------------------------------------------------------
+ * Makes the topk_ids and topk_w of the chain above from the router's logits, with
+ * the balance loss of a training step, and the gradient of both.
+ *   p_t = softmax(logits_t) over all E experts, in fp32
+ *   topk_ids[t]  the topk largest logits in falling order, the lowest index first
+ *                among equals
+ *   topk_w[t][k] p at topk_ids[t][k]; with renormalize divided by the sum of the
+ *                token's topk_w
+ *   counts       [E + 1]: entries of every expert, then the number of tokens Tv
+ *   loss         E sum_e (counts[e] / C) (1 / Tv) sum_t p_te, C the sum of the E counts;
+ *                1 when all is even.  0 without tokens
+ * A token whose token_mask byte is 0 (padding) has ids -1 and weights 0 and enters
+ * neither counts nor loss; so does a token whose logits are all -inf.  An expert
+ * at -inf is never chosen: entries that find no expert are -1 with weight 0.  A
+ * token with a NaN or +inf logit has ids -1 and weights NaN, counts as a token and
+ * makes the loss NaN.  (Ids of -1 are not routed by the chain.)
+ *  - logits [T][E], row stride ld (elements, at least E, at most 2^22; 0: no gaps), dtype
+ *    W4A16_F16, W4A16_BF16 or W4A16_F32, aligned to its size.  1 <= E <= 1024,
+ *    1 <= topk <= E, T * topk < 2^31.
+ *  - token_mask: [T] bytes or NULL.  counts may be NULL, loss too; loss needs counts.
+ *  - workspace (4-byte aligned): at least w4a16_moe_route_workspace_bytes(T, E); may be NULL
+ *    without counts or where that is 0.  Contents on entry are ignored; calls
+ *    sharing it must be ordered on one stream.
+ *  - No atomics on floating-point values: equal calls give equal bits.
+ */
+size_t w4a16_moe_route_workspace_bytes(int64_t T, int64_t E);
+
+w4a16_status w4a16_moe_route(const void *logits, int64_t ld, const uint8_t *token_mask, int64_t T, int64_t E,
+                             int64_t topk, int renormalize, int32_t *topk_ids, float *topk_w, int32_t *counts,
+                             float *loss, int dt, void *workspace, size_t workspace_bytes, void *stream);
+
+/*
+ * dlogits [T][E] (dtype dt, row stride lddl; every element is written) of
+ *   sum_tk dtopk_w[t][k] topk_w[t][k] + (*dloss) loss
+ * with the choice of experts and the counts held fixed.  logits, token_mask, topk_ids,
+ * topk_w, counts as in the forward call and as it left them.
+ *   dtopk_w  [T][topk] or NULL (no gradient through the weights; topk_ids and topk_w may
+ *            then be NULL)
+ *   dloss    DEVICE fp32 scalar or NULL (counts may then be NULL)
+ * Tokens without a distribution get zeros, those with a NaN or +inf logit NaN.
+ * dlogits must not overlap an input.
+ */
+w4a16_status w4a16_moe_route_backward(const void *logits, int64_t ld, const uint8_t *token_mask,
+                                      const int32_t *topk_ids, const float *topk_w, const int32_t *counts,
+                                      const float *dtopk_w, const float *dloss, int64_t T, int64_t E, int64_t topk,
+                                      int renormalize, void *dlogits, int64_t lddl, int dt, void *stream);
 
 #ifdef __cplusplus
 }

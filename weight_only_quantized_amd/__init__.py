@@ -17,6 +17,7 @@ LIB_PATH = os.path.join(_HERE, "libw4a16.so")
 
 W4A16_F16 = 0
 W4A16_BF16 = 1
+W4A16_F32 = 2          # logits of the MoE router only
 GROUP_SIZE = 128
 
 W4A16_OK = 0
@@ -92,6 +93,16 @@ _SIGS = {
     "w4a16_glu_gemm_backward_workspace_bytes": ([C.POINTER(Linear), _i64], C.c_size_t),
     "w4a16_glu_gemm_backward": ([_p, _i64, _p, C.POINTER(Linear), C.c_int, _p, _i64, _p, _p, _p, _i64, _i64, C.c_int,
                                  _p, C.c_size_t, _p], C.c_int),
+    "w8a8_quantize": ([_p, _i64, _p, _p, _p, _i64, _i64, C.c_int, _p], C.c_int),
+    "w8a8_gemm_prequant": ([_p, _p, _p, _p, _p, _p, _i64, _i64, _i64, _i64, C.c_int, _p], C.c_int),
+    "w8a8_workspace_bytes": ([_i64, _i64], C.c_size_t),
+    "w8a8_gemm": ([_p, _i64, _p, _p, _p, _p, _i64, _i64, _i64, _i64, C.c_int, _p, C.c_size_t, _p], C.c_int),
+    "w8a8_grouped_workspace_bytes": ([_i64, _i64], C.c_size_t),
+    "w8a8_grouped_gemm": ([_p, _p, _i64, _p, _p, _p, _p, _i64, _i64, _i64, _i64, C.c_int, _p, C.c_size_t, _p], C.c_int),
+    "w4a16_moe_route_workspace_bytes": ([_i64, _i64], C.c_size_t),
+    "w4a16_moe_route": ([_p, _i64, _p, _i64, _i64, _i64, C.c_int, _p, _p, _p, _p, C.c_int, _p, C.c_size_t, _p], C.c_int),
+    "w4a16_moe_route_backward": ([_p, _i64, _p, _p, _p, _p, _p, _p, _i64, _i64, _i64, C.c_int, _p, _i64, C.c_int, _p],
+                                 C.c_int),
     "w4a16_test_unpack": ([_p, _p, _i64, _i64, _i64, C.c_int, _p], C.c_int),
     "w4a16_test_msd_intermediates": ([_p, _p, _i64, _i64, _i64, _i64, _p, _p, _p, _p, C.c_size_t, _p], C.c_int),
     "w4a16_test_msd_basic_workspace_bytes": ([_i64, _i64, _i64, _i64], C.c_size_t),
@@ -350,6 +361,59 @@ def w4a16_glu_gemm_backward(da, h, lin, dx, M, act=W4A16_ACT_SILU, dh=None, dbia
     _check(lib().w4a16_glu_gemm_backward(_ptr(da), ldda, _ptr(h), lin, int(act), _ptr(addend), ldadd, _ptr(dh),
                                          _ptr(dbias), _ptr(dx), lddx, M, int(dt), _ptr(workspace),
                                          int(workspace_bytes), _stream(stream)), "w4a16_glu_gemm_backward")
+
+
+# ---- W8A8: products of 8-bit integers --------------------------------------------
+
+def w8a8_quantize(x, qx, sx, M, K, dt=W4A16_BF16, row_count=None, ldx=0, stream=None):
+    _check(lib().w8a8_quantize(_ptr(x), ldx, _ptr(row_count), _ptr(qx), _ptr(sx), M, K, int(dt), _stream(stream)),
+           "w8a8_quantize")
+
+
+def w8a8_gemm_prequant(qx, sx, w_packed, sw, y, M, K, N, bias=None, dt=W4A16_BF16, ldy=0, stream=None):
+    _check(lib().w8a8_gemm_prequant(_ptr(qx), _ptr(sx), _ptr(w_packed), _ptr(sw), _ptr(bias), _ptr(y), ldy, M, K, N,
+                                    int(dt), _stream(stream)), "w8a8_gemm_prequant")
+
+
+def w8a8_workspace_bytes(M: int, K: int) -> int:
+    return lib().w8a8_workspace_bytes(M, K)
+
+
+def w8a8_gemm(x, w_packed, sw, y, M, K, N, bias=None, dt=W4A16_BF16, ldx=0, ldy=0, workspace=None,
+              workspace_bytes=0, stream=None):
+    _check(lib().w8a8_gemm(_ptr(x), ldx, _ptr(w_packed), _ptr(sw), _ptr(bias), _ptr(y), ldy, M, K, N, int(dt),
+                           _ptr(workspace), int(workspace_bytes), _stream(stream)), "w8a8_gemm")
+
+
+def w8a8_grouped_workspace_bytes(R: int, K: int) -> int:
+    return lib().w8a8_grouped_workspace_bytes(R, K)
+
+
+def w8a8_grouped_gemm(x, expert_offsets, w_packed, sw, y, E, R, K, N, sorted_ids=None, topk=1, dt=W4A16_BF16,
+                      workspace=None, workspace_bytes=0, stream=None):
+    _check(lib().w8a8_grouped_gemm(_ptr(x), _ptr(sorted_ids), topk, _ptr(expert_offsets), _ptr(w_packed), _ptr(sw),
+                                   _ptr(y), E, R, K, N, int(dt), _ptr(workspace), int(workspace_bytes),
+                                   _stream(stream)), "w8a8_grouped_gemm")
+
+
+# ---- MoE router --------------------------------------------------------------------
+
+def w4a16_moe_route_workspace_bytes(T: int, E: int) -> int:
+    return lib().w4a16_moe_route_workspace_bytes(T, E)
+
+
+def w4a16_moe_route(logits, T, E, topk, topk_ids, topk_w, counts=None, loss=None, token_mask=None, renormalize=True,
+                    dt=W4A16_F32, ld=0, workspace=None, workspace_bytes=0, stream=None):
+    _check(lib().w4a16_moe_route(_ptr(logits), ld, _ptr(token_mask), T, E, topk, int(renormalize), _ptr(topk_ids),
+                                 _ptr(topk_w), _ptr(counts), _ptr(loss), int(dt), _ptr(workspace),
+                                 int(workspace_bytes), _stream(stream)), "w4a16_moe_route")
+
+
+def w4a16_moe_route_backward(logits, topk_ids, topk_w, dlogits, T, E, topk, counts=None, dtopk_w=None, dloss=None,
+                             token_mask=None, renormalize=True, dt=W4A16_F32, ld=0, lddl=0, stream=None):
+    _check(lib().w4a16_moe_route_backward(_ptr(logits), ld, _ptr(token_mask), _ptr(topk_ids), _ptr(topk_w),
+                                          _ptr(counts), _ptr(dtopk_w), _ptr(dloss), T, E, topk, int(renormalize),
+                                          _ptr(dlogits), lddl, int(dt), _stream(stream)), "w4a16_moe_route_backward")
 
 
 # ---- test hooks (include/w4a16_test.h) ----------------------------------------

@@ -18,7 +18,7 @@ BUILD = os.path.join(HERE, "_build")
 LIB = os.path.join(HERE, "libw4a16.so")
 
 HIP_SOURCES = ["prepack.hip", "gemm_small.hip", "gemm_tile.hip", "msd.hip", "moe.hip", "mxfp4.hip", "w8.hip", "fzero.hip",
-               "linear.hip", "linear_small.hip"]
+               "linear.hip", "linear_small.hip", "w8a8.hip", "route.hip"]
 CPP_SOURCES = ["api.cpp"]
 ARCH = "gfx950"
 

@@ -124,9 +124,9 @@ const char *w4a16_status_str(int status) {
     switch (status) {
         case W4A16_OK: return "W4A16_OK";
         case W4A16_ERR_NULL: return "W4A16_ERR_NULL: a required pointer is NULL";
-        case W4A16_ERR_SHAPE: return "W4A16_ERR_SHAPE: sizes violate K>0, K%128==0, N>0, N%64==0, M>=0, E>=1, group_size dividing K (fused linear operators: also gated N%128==0, K and N up to 2^22, K*N up to 2^32, row strides from the row length to 2^22)";
-        case W4A16_ERR_UNSUPPORTED: return "W4A16_ERR_UNSUPPORTED: group_size must be 32, 64 or a multiple of 128 (MSD and the MoE chain: 128; W8A16, floating-point zero points and the fused linear operators: a multiple of 128), dtype F16 or BF16 (MSD: F16), act a w4a16_act";
-        case W4A16_ERR_ALIGN: return "W4A16_ERR_ALIGN: x, w_packed, workspace need 16-byte, scale and y 2-byte alignment (fused linear operators: 16 bytes for all but scale, 2, and dbias, 4; row strides a multiple of 8 elements)";
+        case W4A16_ERR_SHAPE: return "W4A16_ERR_SHAPE: sizes violate K>0, K%128==0, N>0, N%64==0, M>=0, E>=1, group_size dividing K (fused linear operators: also gated N%128==0, K and N up to 2^22, K*N up to 2^32, row strides from the row length to 2^22; W8A8: K below 2^17, N up to 2^22, R a multiple of topk; router: topk up to E)";
+        case W4A16_ERR_UNSUPPORTED: return "W4A16_ERR_UNSUPPORTED: group_size must be 32, 64 or a multiple of 128 (MSD and the MoE chain: 128; W8A16, floating-point zero points and the fused linear operators: a multiple of 128), dtype F16 or BF16 (MSD: F16; router: F32 too), act a w4a16_act, at most 1024 experts in the MoE chain and router";
+        case W4A16_ERR_ALIGN: return "W4A16_ERR_ALIGN: x, w_packed, workspace need 16-byte, scale and y 2-byte alignment (fused linear operators: 16 bytes for all but scale, 2, and dbias, 4; row strides a multiple of 8 elements; W8A8: y 16 bytes, bias 2; fp32 and int32 arrays 4)";
         case W4A16_ERR_WORKSPACE: return "W4A16_ERR_WORKSPACE: workspace is NULL or smaller than the call's workspace query";
         case W4A16_ERR_DEVICE: return "W4A16_ERR_DEVICE: current device is not gfx950 or a launch failed";
         case W4A16_ERR_SCRATCH:
@@ -527,6 +527,213 @@ w4a16_status w4a16_glu_gemm_backward(const void *da, int64_t ldda, const void *h
                                      void *stream) {
     return linear_backward(true, da, ldda, h, lin, act, addend, ldadd, dh, dbias, dx, lddx, M, dt, workspace,
                            workspace_bytes, stream);
+}
+
+// ---- W8A8 and the MoE router --------------------------------------------------
+
+}  // extern "C"
+
+namespace {
+
+constexpr int64_t kW8A8MaxK = int64_t(1) << 17;   // (127 or 128) * 128 * K stays below 2^31
+
+w4a16_status check_w8a8(int64_t M, int64_t K, int64_t N) {
+    if (K <= 0 || K % 128 != 0 || K >= kW8A8MaxK) return W4A16_ERR_SHAPE;
+    if (N <= 0 || N % 64 != 0 || N > kLinMaxLd) return W4A16_ERR_SHAPE;
+    return rows_ok(M) ? W4A16_OK : W4A16_ERR_SHAPE;
+}
+
+// Workspace: the codes, then the scales.
+size_t w8a8_sx_offset(int64_t M, int64_t K) { return ((size_t)M * (size_t)K + 255) & ~(size_t)255; }
+
+size_t w8a8_bytes(int64_t M, int64_t K) {
+    if (check_w8a8(M, K, 64) != W4A16_OK || M == 0) return 0;
+    return w8a8_sx_offset(M, K) + 4 * (size_t)M;
+}
+
+w4a16_status check_router(int64_t T, int64_t E, int64_t topk, int dt) {
+    if (!dt_ok(dt) && dt != W4A16_F32) return W4A16_ERR_UNSUPPORTED;
+    w4a16_status st = check_route(T, topk, E);
+    if (st != W4A16_OK) return st;
+    return topk <= E ? W4A16_OK : W4A16_ERR_SHAPE;
+}
+
+w4a16_status check_logit_ld(int64_t *ld, int64_t E) {
+    if (*ld == 0) *ld = E;
+    return *ld < E || *ld > kLinMaxLd ? W4A16_ERR_SHAPE : W4A16_OK;
+}
+
+}  // namespace
+
+extern "C" {
+
+w4a16_status w8a8_quantize(const void *x, int64_t ldx, const int32_t *row_count, void *qx, float *sx, int64_t M,
+                           int64_t K, int dt, void *stream) {
+    if (!dt_ok(dt)) return W4A16_ERR_UNSUPPORTED;
+    w4a16_status st = check_w8a8(M, K, 64);
+    if (st != W4A16_OK || (st = check_ld(&ldx, K)) != W4A16_OK) return st;
+    if (M == 0) return W4A16_OK;
+    if (!x || !qx || !sx) return W4A16_ERR_NULL;
+    if (!aligned(x, 16) || !aligned(qx, 16) || !aligned(sx, 4) || !aligned(row_count, 4)) return W4A16_ERR_ALIGN;
+    if (current_device_ok() != 1) return W4A16_ERR_DEVICE;
+    return map_err(w4::launch_w8a8_quantize(x, ldx, row_count, qx, sx, M, K, dt, (hipStream_t)stream));
+}
+
+w4a16_status w8a8_gemm_prequant(const void *qx, const float *sx, const void *w_packed, const float *sw,
+                                const void *bias, void *y, int64_t ldy, int64_t M, int64_t K, int64_t N, int dt,
+                                void *stream) {
+    if (!dt_ok(dt)) return W4A16_ERR_UNSUPPORTED;
+    w4a16_status st = check_w8a8(M, K, N);
+    if (st != W4A16_OK || (st = check_ld(&ldy, N)) != W4A16_OK) return st;
+    if (M == 0) return W4A16_OK;
+    if (!qx || !sx || !w_packed || !sw || !y) return W4A16_ERR_NULL;
+    if (!aligned(qx, 16) || !aligned(w_packed, 16) || !aligned(y, 16) || !aligned(sx, 4) || !aligned(sw, 4) ||
+        !aligned(bias, 2))
+        return W4A16_ERR_ALIGN;
+    if (current_device_ok() != 1) return W4A16_ERR_DEVICE;
+    w4::W8A8Args p{};
+    p.qx = (const uint8_t *)qx;
+    p.sx = sx;
+    p.X = p.M = M;
+    p.wp = (const uint8_t *)w_packed;
+    p.sw = sw;
+    p.bias = (const uint16_t *)bias;
+    p.y = (uint16_t *)y;
+    p.ldy = ldy;
+    p.K = K;
+    p.N = N;
+    p.E = 1;
+    return map_err(w4::launch_w8a8(p, dt, (hipStream_t)stream));
+}
+
+size_t w8a8_workspace_bytes(int64_t M, int64_t K) { return w8a8_bytes(M, K); }
+
+w4a16_status w8a8_gemm(const void *x, int64_t ldx, const void *w_packed, const float *sw, const void *bias, void *y,
+                       int64_t ldy, int64_t M, int64_t K, int64_t N, int dt, void *workspace, size_t workspace_bytes,
+                       void *stream) {
+    if (!dt_ok(dt)) return W4A16_ERR_UNSUPPORTED;
+    w4a16_status st = check_w8a8(M, K, N);
+    if (st != W4A16_OK || (st = check_ld(&ldx, K)) != W4A16_OK || (st = check_ld(&ldy, N)) != W4A16_OK) return st;
+    if (M == 0) return W4A16_OK;
+    if (!x || !w_packed || !sw || !y) return W4A16_ERR_NULL;
+    if (!workspace || workspace_bytes < w8a8_bytes(M, K)) return W4A16_ERR_WORKSPACE;
+    if (!aligned(x, 16) || !aligned(workspace, 16) || !aligned(w_packed, 16) || !aligned(y, 16) || !aligned(sw, 4) ||
+        !aligned(bias, 2))
+        return W4A16_ERR_ALIGN;
+    uint8_t *qx = (uint8_t *)workspace;
+    float *sx = (float *)(qx + w8a8_sx_offset(M, K));
+    st = w8a8_quantize(x, ldx, nullptr, qx, sx, M, K, dt, stream);
+    if (st != W4A16_OK) return st;
+    return w8a8_gemm_prequant(qx, sx, w_packed, sw, bias, y, ldy, M, K, N, dt, stream);
+}
+
+size_t w8a8_grouped_workspace_bytes(int64_t R, int64_t K) { return w8a8_bytes(R, K); }
+
+w4a16_status w8a8_grouped_gemm(const void *x, const int32_t *sorted_ids, int64_t topk, const int32_t *expert_offsets,
+                               const void *w_packed, const float *sw, void *y, int64_t E, int64_t R, int64_t K,
+                               int64_t N, int dt, void *workspace, size_t workspace_bytes, void *stream) {
+    if (!dt_ok(dt)) return W4A16_ERR_UNSUPPORTED;
+    w4a16_status st = check_w8a8(R, K, N);
+    if (st != W4A16_OK) return st;
+    if (E < 1 || E > (int64_t(1) << 20)) return W4A16_ERR_SHAPE;
+    if (sorted_ids && (topk < 1 || topk > INT32_MAX || R % topk != 0)) return W4A16_ERR_SHAPE;
+    if (R == 0) return W4A16_OK;
+    if (!x || !expert_offsets || !w_packed || !sw || !y) return W4A16_ERR_NULL;
+    if (!workspace || workspace_bytes < w8a8_bytes(R, K)) return W4A16_ERR_WORKSPACE;
+    if (!aligned(x, 16) || !aligned(workspace, 16) || !aligned(w_packed, 16) || !aligned(y, 16) || !aligned(sw, 4) ||
+        !aligned(expert_offsets, 4) || !aligned(sorted_ids, 4))
+        return W4A16_ERR_ALIGN;
+    if (current_device_ok() != 1) return W4A16_ERR_DEVICE;
+    const int64_t X = sorted_ids ? R / topk : R;
+    uint8_t *qx = (uint8_t *)workspace;
+    float *sx = (float *)(qx + w8a8_sx_offset(R, K));
+    // without a gather only the rows in front of offsets[E] exist
+    st = map_err(w4::launch_w8a8_quantize(x, K, sorted_ids ? nullptr : expert_offsets + E, qx, sx, X, K, dt,
+                                          (hipStream_t)stream));
+    if (st != W4A16_OK) return st;
+    w4::W8A8Args p{};
+    p.qx = qx;
+    p.sx = sx;
+    p.X = X;
+    p.offsets = expert_offsets;
+    p.sorted = sorted_ids;
+    p.topk = sorted_ids ? (int)topk : 1;
+    p.wp = (const uint8_t *)w_packed;
+    p.sw = sw;
+    p.y = (uint16_t *)y;
+    p.ldy = N;
+    p.M = R;
+    p.K = K;
+    p.N = N;
+    p.E = (int)E;
+    return map_err(w4::launch_w8a8(p, dt, (hipStream_t)stream));
+}
+
+size_t w4a16_moe_route_workspace_bytes(int64_t T, int64_t E) {
+    return check_route(T, 1, E) == W4A16_OK && T > 0 ? w4::route_workspace_bytes(T, E) : 0;
+}
+
+w4a16_status w4a16_moe_route(const void *logits, int64_t ld, const uint8_t *token_mask, int64_t T, int64_t E,
+                             int64_t topk, int renormalize, int32_t *topk_ids, float *topk_w, int32_t *counts,
+                             float *loss, int dt, void *workspace, size_t workspace_bytes, void *stream) {
+    w4a16_status st = check_router(T, E, topk, dt);
+    if (st != W4A16_OK || (st = check_logit_ld(&ld, E)) != W4A16_OK) return st;
+    if (loss && !counts) return W4A16_ERR_NULL;
+    if (T == 0 && !counts) return W4A16_OK;
+    if (T > 0 && (!logits || !topk_ids || !topk_w)) return W4A16_ERR_NULL;
+    if (counts && T > 0) {
+        const size_t need = w4::route_workspace_bytes(T, E);
+        if (need > 0 && (!workspace || workspace_bytes < need)) return W4A16_ERR_WORKSPACE;
+    }
+    if (!aligned(logits, dt == W4A16_F32 ? 4 : 2) || !aligned(topk_ids, 4) || !aligned(topk_w, 4) ||
+        !aligned(counts, 4) || !aligned(loss, 4) || (counts && !aligned(workspace, 4)))
+        return W4A16_ERR_ALIGN;
+    if (current_device_ok() != 1) return W4A16_ERR_DEVICE;
+    w4::RouteArgs p{};
+    p.logits = logits;
+    p.ld = ld;
+    p.mask = token_mask;
+    p.T = T;
+    p.E = (int)E;
+    p.topk = (int)topk;
+    p.renorm = renormalize != 0;
+    p.ids = topk_ids;
+    p.w = topk_w;
+    p.counts = counts;
+    p.loss = loss;
+    return map_err(w4::launch_route(p, dt, workspace, (hipStream_t)stream));
+}
+
+w4a16_status w4a16_moe_route_backward(const void *logits, int64_t ld, const uint8_t *token_mask,
+                                      const int32_t *topk_ids, const float *topk_w, const int32_t *counts,
+                                      const float *dtopk_w, const float *dloss, int64_t T, int64_t E, int64_t topk,
+                                      int renormalize, void *dlogits, int64_t lddl, int dt, void *stream) {
+    w4a16_status st = check_router(T, E, topk, dt);
+    if (st != W4A16_OK || (st = check_logit_ld(&ld, E)) != W4A16_OK || (st = check_logit_ld(&lddl, E)) != W4A16_OK)
+        return st;
+    if (T == 0) return W4A16_OK;
+    if (!logits || !dlogits || (dtopk_w && (!topk_ids || !topk_w)) || (dloss && !counts)) return W4A16_ERR_NULL;
+    const uintptr_t a = dt == W4A16_F32 ? 4 : 2;
+    if (!aligned(logits, a) || !aligned(dlogits, a) || !aligned(topk_ids, 4) || !aligned(topk_w, 4) ||
+        !aligned(counts, 4) || !aligned(dtopk_w, 4) || !aligned(dloss, 4))
+        return W4A16_ERR_ALIGN;
+    if (current_device_ok() != 1) return W4A16_ERR_DEVICE;
+    w4::RouteArgs p{};
+    p.logits = logits;
+    p.ld = ld;
+    p.mask = token_mask;
+    p.T = T;
+    p.E = (int)E;
+    p.topk = (int)topk;
+    p.renorm = renormalize != 0;
+    p.ids = const_cast<int32_t *>(topk_ids);
+    p.w = const_cast<float *>(topk_w);
+    p.counts = const_cast<int32_t *>(counts);
+    p.dw = dtopk_w;
+    p.dloss = dloss;
+    p.dlogits = dlogits;
+    p.ldd = lddl;
+    return map_err(w4::launch_route_backward(p, dt, (hipStream_t)stream));
 }
 
 // ---- test hooks -------------------------------------------------------------

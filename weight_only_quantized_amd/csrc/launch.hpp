@@ -210,4 +210,45 @@ hipError_t launch_lin_dact(bool glu, const uint16_t *dy, int64_t lddy, const uin
                            int64_t N, int act, int dt, float *part, hipStream_t stream);
 hipError_t launch_lin_zero_colsum(float *colsum, int64_t N, hipStream_t stream);
 
+// W8A8: activations quantized per row, products of 8-bit integers.
+hipError_t launch_w8a8_quantize(const void *x, int64_t ldx, const int32_t *row_count, void *qx, float *sx, int64_t M,
+                                int64_t K, int dt, hipStream_t stream);
+struct W8A8Args {
+    const uint8_t *qx;          // codes [X][K] and scales [X] of the activations
+    const float *sx;
+    int64_t X;
+    const int32_t *offsets;     // grouped: rows of the experts, else NULL
+    const int32_t *sorted;      // grouped: row r reads x row sorted[r] / topk, or NULL: x row r
+    int topk;
+    const uint8_t *wp;          // prepacked weights [E][K][N] (8-bit tiles)
+    const float *sw;            // [E][N]
+    const uint16_t *bias;       // [N] or NULL (dense)
+    uint16_t *y;                // [M][N], row stride ldy
+    int64_t ldy;
+    int64_t M, K, N;
+    int E;
+};
+hipError_t launch_w8a8(const W8A8Args &p, int dt, hipStream_t stream);
+
+// MoE router: logits dtypes 0 fp16, 1 bf16, 2 fp32.
+size_t route_workspace_bytes(int64_t T, int64_t E);
+struct RouteArgs {
+    const void *logits;         // [T][E], row stride ld
+    int64_t ld;
+    const uint8_t *mask;        // [T] or NULL
+    int64_t T;
+    int E, topk;
+    bool renorm;
+    int32_t *ids;               // [T][topk] (backward: input)
+    float *w;                   // [T][topk] (backward: input)
+    int32_t *counts;            // [E + 1] or NULL (backward: input)
+    float *loss;                // or NULL
+    const float *dw;            // backward: [T][topk] or NULL
+    const float *dloss;         // backward: scalar or NULL
+    void *dlogits;              // backward: [T][E], row stride ldd
+    int64_t ldd;
+};
+hipError_t launch_route(const RouteArgs &p, int dt, void *workspace, hipStream_t stream);
+hipError_t launch_route_backward(const RouteArgs &p, int dt, hipStream_t stream);
+
 }  // namespace w4

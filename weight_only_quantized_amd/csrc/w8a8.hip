@@ -1,0 +1,296 @@
+// w8a8.hip — products of 8-bit integers: activations quantized per row (token),
+// int8 weights with one scale per column, dense and grouped (experts).
+//
+//   s_m = fl32(max_k |x[m][k]| / 127),  q[m][k] = rne(x[m][k] / s_m) in [-127, 127]
+//   y[m][n] = round(s_m sw[n] sum_k q[m][k] W[k][n] + bias[n])
+//
+// The integer sum is exact (|q W| <= 2^14 and K < 2^17: below 2^31), so every
+// kernel and every split of K gives the same bits.
+//
+// Weights: the 2048-byte tiles of w8.hip (16 columns x 128 rows, stored as
+// q + 128; slot 16 c + j holds rows 32 c .. + 31 of column j).  Matrix-core
+// mapping (v_mfma_i32_16x16x64_i8): W is the first operand and x the second,
+// so lane l feeds weight column l % 16 and x row l % 16, both with rows
+// 128 g + 32 (l / 16) + 16 h .. + 15 of step h; result register r of lane l is
+// column 4 (l / 16) + r of x row l % 16: four neighbouring outputs per lane.
+#include "common.hpp"
+#include "launch.hpp"
+
+namespace w4 {
+
+constexpr int kW8Tile = 2048;
+typedef uint32_t u32x2s_t __attribute__((__vector_size__(2 * sizeof(uint32_t))));
+
+// ---------------------------------------------------------------------------
+// Quantization of rows
+// ---------------------------------------------------------------------------
+
+// Scale of a row from its largest magnitude: NaN if the row holds a NaN or an
+// infinity (amax is then either, see row_amax).
+__device__ __forceinline__ float row_scale(float amax) {
+    return amax < INFINITY ? amax / 127.0f : __builtin_nanf("");
+}
+
+// rne(x / s), exactly, for x of a 16-bit type, |x| <= 127 s (1 + 2^-23):
+// t = x (1 / s) is within 2^-15 of the quotient, so rint(t) is off by at most
+// one, and only where the quotient lies next to a border k + 1/2.  The
+// remainder x - q s is exact in fp32 (x and s / 2 are multiples of one unit that
+// |x - q s| <= s exceeds at most 2^24 times), so comparing it with s / 2 decides;
+// ties go to the even code.  Rows of tiny values are scaled by 2^64
+// (both x and s, exactly), which keeps s, 1 / s and s / 2 normal numbers.
+struct RowQuant {
+    float up, s, inv, half;       // multiplier of x, scaled s, its reciprocal, s / 2
+    __device__ __forceinline__ explicit RowQuant(float scale) {
+        up = scale < 0x1p-60f ? 0x1p64f : 1.0f;
+        s = scale * up;
+        const bool none = !(s > 0.0f);           // zero or NaN: every code is 0
+        inv = none ? 0.0f : 1.0f / s;
+        half = none ? INFINITY : 0.5f * s;
+        if (none) { s = 0.0f; up = 0.0f; }
+    }
+    __device__ __forceinline__ int code(float x) const {
+        const float v = x * up;
+        float q = __builtin_rintf(v * inv);
+        const float r = __builtin_fmaf(-q, s, v);
+        const bool odd = ((int)q & 1) != 0;
+        if (r > half || (r == half && odd)) q += 1.0f;
+        if (r < -half || (r == -half && odd)) q -= 1.0f;
+        const int c = (int)q;
+        return c > 127 ? 127 : c < -127 ? -127 : c;
+    }
+};
+
+// max |x| where a NaN anywhere gives NaN: magnitudes compare as integers, NaN
+// patterns above infinity's.
+template <int DT>
+__device__ __forceinline__ uint32_t mag_bits(uint32_t h) { return h & 0x7FFFu; }
+template <int DT>
+__device__ __forceinline__ float mag_value(uint32_t m) { return h2f<DT>((uint16_t)m); }
+
+template <int DT>
+__global__ void __launch_bounds__(256)
+w8a8_quantize_kernel(const uint16_t *__restrict__ x, int64_t ldx, const int32_t *__restrict__ row_count,
+                     uint8_t *__restrict__ qx, float *__restrict__ sx, int64_t K) {
+    const int64_t m = blockIdx.x;
+    if (row_count && m >= *row_count) return;
+    const uint16_t *row = x + m * ldx;
+    uint32_t top = 0;
+    for (int64_t k = (int64_t)threadIdx.x * 8; k < K; k += 256 * 8) {
+        const u32x4_t v = ld128(row + k);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            const uint32_t w = v[i];
+            const uint32_t a = mag_bits<DT>(w), b = mag_bits<DT>(w >> 16);
+            top = a > top ? a : top;
+            top = b > top ? b : top;
+        }
+    }
+    __shared__ uint32_t tops[4];
+#pragma unroll
+    for (int off = 32; off > 0; off >>= 1) {
+        const uint32_t o = __shfl_xor(top, off);
+        top = o > top ? o : top;
+    }
+    if (lane_id() == 0) tops[threadIdx.x >> 6] = top;
+    __syncthreads();
+#pragma unroll
+    for (int w = 0; w < 4; ++w) top = tops[w] > top ? tops[w] : top;
+    const float scale = row_scale(mag_value<DT>(top));
+    const RowQuant rq(scale);
+    for (int64_t k = (int64_t)threadIdx.x * 8; k < K; k += 256 * 8) {
+        const u32x4_t v = ld128(row + k);
+        uint32_t out[2] = {0, 0};
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+            const uint32_t w = v[i >> 1];
+            // codes of a row without a scale stay 0 (0 * inf would be NaN)
+            const int c = scale > 0.0f ? rq.code(h2f<DT>((uint16_t)(w >> (16 * (i & 1))))) : 0;
+            out[i >> 2] |= ((uint32_t)c & 0xFFu) << (8 * (i & 3));
+        }
+        *reinterpret_cast<u32x2s_t *>(qx + m * K + k) = u32x2s_t{out[0], out[1]};
+    }
+    if (threadIdx.x == 0) sx[m] = scale;
+}
+
+// ---------------------------------------------------------------------------
+// Shared pieces of the products
+// ---------------------------------------------------------------------------
+
+// A scale as significand and exponent: s_m sw_n may leave fp32's range where
+// their product with the sum does not.
+struct Split {
+    float m;
+    int e;
+    __device__ __forceinline__ explicit Split(float s)
+        : m(__builtin_amdgcn_frexp_mantf(s)), e(__builtin_amdgcn_frexp_expf(s)) {}
+};
+
+__device__ __forceinline__ float finish(int acc, const Split &row, const Split &col, float bias) {
+    return __builtin_ldexpf((float)acc * (row.m * col.m), row.e + col.e) + bias;
+}
+
+// Row tile `tile` of BM rows, the tiles numbered over all experts: its expert
+// and rows; false past the last tile.  Every wave finds it by itself (64 experts
+// per scan); rows never leave [0, R) whatever the offsets hold.
+__device__ __forceinline__ bool expert_tile(const int32_t *__restrict__ offsets, int E, int64_t R, int BM,
+                                            int64_t tile, int &e, int64_t &row0, int64_t &row_end) {
+    const int lane = lane_id();
+    int64_t before = 0;
+    for (int base = 0; base < E; base += 64) {
+        const int ee = base + lane;
+        int o0 = ee < E ? offsets[ee] : 0, o1 = ee < E ? offsets[ee + 1] : 0;
+        o0 = o0 < 0 ? 0 : o0;
+        o1 = o1 > R ? (int)R : o1;
+        const int rows = o1 - o0;
+        const int tl = rows > 0 ? (rows + BM - 1) / BM : 0;
+        const int incl = wave_incl_scan(tl);
+        const int64_t at = tile - before;
+        const uint64_t hit = __ballot(at >= incl - tl && at < incl);
+        if (hit) {
+            const int src = __builtin_ctzll(hit);
+            e = base + src;
+            const int in = (int)at - __builtin_amdgcn_readlane(incl - tl, src);
+            row0 = __builtin_amdgcn_readlane(o0, src) + (int64_t)in * BM;
+            row_end = __builtin_amdgcn_readlane(o1, src);
+            return true;
+        }
+        before += __builtin_amdgcn_readlane(incl, 63);
+    }
+    return false;
+}
+
+// ---------------------------------------------------------------------------
+// Split-K kernel: a workgroup owns 16 MT rows x 16 NB columns, its waves split
+// the 128-row groups of K and meet in LDS.
+// ---------------------------------------------------------------------------
+template <int DT, int MT, int NB, bool GROUPED, int WMAX>
+__global__ void __launch_bounds__(WMAX * 64)
+w8a8_split_kernel(const uint8_t *__restrict__ qx, const float *__restrict__ sx, const int32_t *__restrict__ offsets,
+                  const int32_t *__restrict__ sorted, int topk, const uint8_t *__restrict__ wp,
+                  const float *__restrict__ sw, const uint16_t *__restrict__ bias, uint16_t *__restrict__ y,
+                  int64_t ldy, int64_t M, int64_t X, int64_t K, int64_t N, int E, int ncb) {
+    extern __shared__ __attribute__((aligned(16))) uint8_t lds_raw[];
+    i32x4_t *red = reinterpret_cast<i32x4_t *>(lds_raw);      // [wave][MT * NB][64]
+    const int G = (int)(K / kGroup), W = blockDim.x >> 6;
+    const int lane = lane_id();
+    const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    const int j = lane & 15, c = lane >> 4;
+    const int64_t n0 = (int64_t)(blockIdx.x % (unsigned)ncb) * (16 * NB);
+    const int64_t tile = blockIdx.x / (unsigned)ncb;
+    int e = 0;
+    int64_t row0 = tile * (16 * MT), row_end = M;
+    if constexpr (GROUPED) {
+        if (!expert_tile(offsets, E, M, 16 * MT, tile, e, row0, row_end)) return;
+    }
+    // x row of a tile's row; rows past the end take the last one and are not stored
+    auto src_row = [&](int64_t r) -> int64_t {
+        if (r >= row_end) r = row_end - 1;
+        if constexpr (GROUPED) {
+            if (sorted) {
+                const int64_t t = (int64_t)((uint32_t)sorted[r] / (uint32_t)topk);
+                return t < X ? t : X - 1;
+            }
+        }
+        return r;
+    };
+    const uint8_t *xp[MT];
+#pragma unroll
+    for (int t = 0; t < MT; ++t) xp[t] = qx + src_row(row0 + 16 * t + j) * K + 32 * c;
+    const uint8_t *wb = wp + ((int64_t)e * (N / 16) + n0 / 16) * G * kW8Tile + lane * 32;
+
+    i32x4_t acc[NB][MT];
+#pragma unroll
+    for (int b = 0; b < NB; ++b)
+#pragma unroll
+        for (int t = 0; t < MT; ++t) acc[b][t] = i32x4_t{0, 0, 0, 0};
+
+    const int g0 = (int)((int64_t)G * wave / W), g1 = (int)((int64_t)G * (wave + 1) / W);
+    u32x4_t wf[NB][2], xf[MT][2];
+    for (int g = g0; g < g1; ++g) {
+#pragma unroll
+        for (int b = 0; b < NB; ++b)
+#pragma unroll
+            for (int h = 0; h < 2; ++h) wf[b][h] = ld128(wb + ((int64_t)b * G + g) * kW8Tile + 16 * h);
+#pragma unroll
+        for (int t = 0; t < MT; ++t)
+#pragma unroll
+            for (int h = 0; h < 2; ++h) xf[t][h] = ld128(xp[t] + (int64_t)g * kGroup + 16 * h);
+#pragma unroll
+        for (int h = 0; h < 2; ++h)
+#pragma unroll
+            for (int b = 0; b < NB; ++b) {
+                const u32x4_t q = wf[b][h] ^ 0x80808080u;
+#pragma unroll
+                for (int t = 0; t < MT; ++t) acc[b][t] = mfma_i8_16x16x64(q, xf[t][h], acc[b][t]);
+            }
+    }
+#pragma unroll
+    for (int b = 0; b < NB; ++b)
+#pragma unroll
+        for (int t = 0; t < MT; ++t) red[(wave * NB * MT + b * MT + t) * 64 + lane] = acc[b][t];
+    __syncthreads();
+
+    for (int o = wave; o < NB * MT; o += W) {
+        i32x4_t sum = red[o * 64 + lane];
+        for (int w = 1; w < W; ++w) sum += red[(w * NB * MT + o) * 64 + lane];
+        const int b = o / MT, t = o % MT;
+        const int64_t r = row0 + 16 * t + j;
+        if (r < row_end) {
+            const Split rs(sx[src_row(r)]);
+            const int64_t n = n0 + 16 * b + 4 * c;
+            uint16_t h[4];
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                const float bv = bias ? h2f<DT>(bias[n + i]) : 0.0f;
+                h[i] = f2h<DT>(finish(sum[i], rs, Split(sw[(int64_t)e * N + n + i]), bv));
+            }
+            *reinterpret_cast<u32x2s_t *>(y + r * ldy + n) =
+                u32x2s_t{h[0] | (uint32_t)h[1] << 16, h[2] | (uint32_t)h[3] << 16};
+        }
+    }
+}
+
+// ---------------------------------------------------------------------------
+// Launchers
+// ---------------------------------------------------------------------------
+hipError_t launch_w8a8_quantize(const void *x, int64_t ldx, const int32_t *row_count, void *qx, float *sx, int64_t M,
+                                int64_t K, int dt, hipStream_t stream) {
+    if (M == 0) return hipSuccess;
+    const dim3 grid((unsigned)M);
+    if (dt == DT_BF16)
+        hipLaunchKernelGGL(w8a8_quantize_kernel<DT_BF16>, grid, dim3(256), 0, stream, (const uint16_t *)x, ldx, row_count,
+                           (uint8_t *)qx, sx, K);
+    else
+        hipLaunchKernelGGL(w8a8_quantize_kernel<DT_F16>, grid, dim3(256), 0, stream, (const uint16_t *)x, ldx, row_count,
+                           (uint8_t *)qx, sx, K);
+    return hipGetLastError();
+}
+
+template <int DT, int MT, int NB, bool GROUPED, int WMAX>
+static hipError_t split_launch(const W8A8Args &p, hipStream_t stream) {
+    const int64_t G = p.K / kGroup;
+    const int W = (int)(G < WMAX ? G : WMAX);
+    const int64_t ncb = p.N / (16 * NB);
+    const int64_t few = p.M < p.E ? p.M : p.E;                 // experts that can end in a partial tile
+    const int64_t mtiles = GROUPED ? p.M / (16 * MT) + few : (p.M + 16 * MT - 1) / (16 * MT);
+    if (mtiles * ncb > INT32_MAX) return hipErrorInvalidConfiguration;
+    hipLaunchKernelGGL((w8a8_split_kernel<DT, MT, NB, GROUPED, WMAX>), dim3((unsigned)(mtiles * ncb)), dim3(W * 64),
+                       (size_t)W * NB * MT * 1024, stream, p.qx, p.sx, p.offsets, p.sorted, p.topk, p.wp, p.sw, p.bias,
+                       p.y, p.ldy, p.M, p.X, p.K, p.N, p.E, (int)ncb);
+    return hipGetLastError();
+}
+
+template <int DT, bool GROUPED>
+static hipError_t w8a8_dispatch(const W8A8Args &p, hipStream_t stream) {
+    const int64_t rows = GROUPED ? p.M / p.E : p.M;
+    if (rows <= 16) return split_launch<DT, 1, 4, GROUPED, 16>(p, stream);
+    return split_launch<DT, 4, 4, GROUPED, 4>(p, stream);
+}
+
+hipError_t launch_w8a8(const W8A8Args &p, int dt, hipStream_t stream) {
+    if (p.M == 0) return hipSuccess;
+    if (dt == DT_BF16) return p.offsets ? w8a8_dispatch<DT_BF16, true>(p, stream) : w8a8_dispatch<DT_BF16, false>(p, stream);
+    return p.offsets ? w8a8_dispatch<DT_F16, true>(p, stream) : w8a8_dispatch<DT_F16, false>(p, stream);
+}
+
+}  // namespace w4

@@ -13,6 +13,8 @@
 // so lane l feeds weight column l % 16 and x row l % 16, both with rows
 // 128 g + 32 (l / 16) + 16 h .. + 15 of step h; result register r of lane l is
 // column 4 (l / 16) + r of x row l % 16: four neighbouring outputs per lane.
+#include <type_traits>
+
 #include "common.hpp"
 #include "launch.hpp"
 
@@ -121,6 +123,7 @@ w8a8_quantize_kernel(const uint16_t *__restrict__ x, int64_t ldx, const int32_t 
 struct Split {
     float m;
     int e;
+    Split() = default;
     __device__ __forceinline__ explicit Split(float s)
         : m(__builtin_amdgcn_frexp_mantf(s)), e(__builtin_amdgcn_frexp_expf(s)) {}
 };
@@ -251,6 +254,199 @@ w8a8_split_kernel(const uint8_t *__restrict__ qx, const float *__restrict__ sx, 
 }
 
 // ---------------------------------------------------------------------------
+// Tile kernel: BM x BN of y per workgroup, WM x WN waves, K in stages of 64.
+// ---------------------------------------------------------------------------
+constexpr int kXcd8 = 8;              // XCDs; workgroups go to them round-robin
+constexpr int kStageK = 64;           // K rows per stage
+constexpr int kStages = 4;            // stages in LDS
+
+// 16 bytes per lane from global memory (base + off) to LDS (lds_base + 16 lane), not
+// waited for here.  In assembly, since the compiler follows its own form of this
+// load with a wait for every outstanding load before any LDS read.
+__device__ __forceinline__ void dma16(const uint8_t *base, uint32_t off, uint32_t lds_base) {
+    asm volatile("s_mov_b32 m0, %2\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %0, %1" ::"v"(off), "s"(base), "s"(lds_base)
+                 : "memory");
+}
+
+// Every DMA but the newest N of this wave and every LDS read have landed; then
+// the workgroup's barrier.
+template <int N>
+__device__ __forceinline__ void wait_and_meet() {
+    asm volatile("s_waitcnt vmcnt(%0) lgkmcnt(0)\n\ts_barrier" ::"n"(N) : "memory");
+}
+
+template <int DT, int BM, int BN, int WM, int WN, bool GROUPED>
+__global__ void __launch_bounds__(WM * WN * 64)
+w8a8_tile_kernel(const uint8_t *__restrict__ qx, const float *__restrict__ sx, const int32_t *__restrict__ offsets,
+                 const int32_t *__restrict__ sorted, int topk, const uint8_t *__restrict__ wp,
+                 const float *__restrict__ sw, const uint16_t *__restrict__ bias, uint16_t *__restrict__ y, int64_t ldy,
+                 int64_t M, int64_t X, int64_t K, int64_t N, int E, int ncb, int per_xcd) {
+    constexpr int NW = WM * WN, TM = BM / WM, TN = BN / WN, RT = TM / 16, CT = TN / 16;
+    constexpr int ABYTES = BM * kStageK, BBYTES = BN * kStageK, SBYTES = ABYTES + BBYTES;
+    constexpr int AL = BM / 16 / NW, BL = BN / 16 / NW;      // DMA loads per wave and stage
+    static_assert(CT % 2 == 0 && BM % (16 * NW) == 0 && BN % (16 * NW) == 0, "whole loads and column pairs");
+    __shared__ __attribute__((aligned(1024))) uint8_t lds[kStages * SBYTES];
+
+    const int lane = lane_id();
+    const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    const int wm = wave / WN, wn = wave % WN;
+    const int S = (int)(K / kStageK);
+    // XCD x takes a contiguous range of the tiles
+    const int64_t id = (int64_t)(blockIdx.x % kXcd8) * per_xcd + blockIdx.x / kXcd8;
+    int64_t tile, n0;
+    int e = 0;
+    int64_t row0, row_end = M;
+    tile = id / ncb;
+    n0 = id % ncb * BN;
+    row0 = tile * BM;
+    if constexpr (GROUPED) {
+        if (!expert_tile(offsets, E, M, BM, tile, e, row0, row_end)) return;
+    } else {
+        if (row0 >= M) return;
+    }
+    auto src_row = [&](int64_t r) -> int64_t {
+        if (r >= row_end) r = row_end - 1;
+        if constexpr (GROUPED) {
+            if (sorted) {
+                const int64_t t = (int64_t)((uint32_t)sorted[r] / (uint32_t)topk);
+                return t < X ? t : X - 1;
+            }
+        }
+        return r;
+    };
+
+    // DMA sources.  x: a load fills 16 rows of 64 bytes, 16-byte chunk c of row r at chunk
+    // c ^ fx(r) of the row; W: a load fills one 1024-byte tile half, piece p at
+    // p ^ fw(p, tile).  Both permutations are their own inverses.
+    uint32_t aoffs[AL], boffs[BL];
+    const uint8_t *abase = qx, *bbase = wp + ((int64_t)e * (N / 16) + n0 / 16) * (K / kGroup) * kW8Tile;
+    if (!sorted) abase += row0 * K;          // gathered rows: X K < 2^32
+#pragma unroll
+    for (int i = 0; i < AL; ++i) {
+        const int r = lane >> 2, c = (lane & 3) ^ ((r >> 1) & 3) ^ (r >> 3);
+        const int64_t m = src_row(row0 + (wave + NW * i) * 16 + r);
+        aoffs[i] = (uint32_t)((sorted ? m : m - row0) * K) + 16 * c;
+    }
+#pragma unroll
+    for (int i = 0; i < BL; ++i) {
+        const int t = wave + NW * i, last = (int)((N - n0) / 16) - 1;
+        const int piece = lane ^ ((lane >> 4) & 1) ^ ((t & 1) << 3);
+        boffs[i] = (uint32_t)((t < last ? t : last) * (K * 16)) + 16 * piece;
+    }
+    const uint32_t lds0 = (uint32_t)(uintptr_t)(__attribute__((address_space(3))) uint8_t *)lds + wave * 1024;
+    auto fetch = [&](int s) {
+        const uint32_t base = lds0 + ((unsigned)s % kStages) * SBYTES;
+#pragma unroll
+        for (int i = 0; i < AL; ++i) dma16(abase, aoffs[i], base + NW * i * 1024);
+#pragma unroll
+        for (int i = 0; i < BL; ++i) dma16(bbase, boffs[i], base + ABYTES + NW * i * 1024);
+        abase += kStageK;
+        bbase += 1024;
+    };
+#pragma unroll
+    for (int s = 0; s < kStages; ++s)
+        if (s < S) fetch(s);
+
+    // LDS offsets of this lane's operands
+    const int i16 = lane & 15, q = lane >> 4;
+    const int aoff = (wm * TM + i16) * kStageK + 16 * (q ^ ((i16 >> 1) & 3) ^ (i16 >> 3));
+    // W operand row i of column block ct is column 32 (ct / 2) + 8 (i / 4) + 4 (ct % 2) + i % 4
+    // of the wave's tile: a lane then ends up with 8 neighbouring columns per pair of blocks
+    const int piece = ((q & 1) ^ ((i16 >> 2) & 1)) | (i16 & 3) << 1 | (i16 >> 3) << 3 | ((i16 >> 2) & 1) << 4 | (q >> 1) << 5;
+    const int boff = ABYTES + (wn * CT + (i16 >> 3)) * 1024 + 16 * piece;
+
+    i32x4_t acc[RT][CT];
+#pragma unroll
+    for (int rt = 0; rt < RT; ++rt)
+#pragma unroll
+        for (int ct = 0; ct < CT; ++ct) acc[rt][ct] = i32x4_t{0, 0, 0, 0};
+
+    u32x4_t xf[2][RT], wf[2][CT];
+    auto read = [&](int s, u32x4_t (&xd)[RT], u32x4_t (&wd)[CT]) {
+        const uint8_t *base = lds + ((unsigned)s % kStages) * SBYTES;
+#pragma unroll
+        for (int ct = 0; ct < CT; ++ct)
+            wd[ct] = *reinterpret_cast<const u32x4_t *>(base + (boff ^ ((ct & 1) * 128)) + (ct >> 1) * 2048);
+#pragma unroll
+        for (int rt = 0; rt < RT; ++rt) xd[rt] = *reinterpret_cast<const u32x4_t *>(base + aoff + rt * 16 * kStageK);
+    };
+    auto multiply = [&](const u32x4_t (&xd)[RT], const u32x4_t (&wd)[CT]) {
+#pragma unroll
+        for (int ct = 0; ct < CT; ++ct) {
+            const i32x4_t w = __builtin_bit_cast(i32x4_t, wd[ct] ^ 0x80808080u);
+#pragma unroll
+            for (int rt = 0; rt < RT; ++rt)
+                acc[rt][ct] = __builtin_amdgcn_mfma_i32_16x16x64_i8(w, __builtin_bit_cast(i32x4_t, xd[rt]), acc[rt][ct], 0, 0, 0);
+        }
+    };
+    constexpr int L = AL + BL;
+    // Stage 0 first; from then on the operands of stage s + 1 are read while stage s
+    // is multiplied: WAIT loads may be outstanding once stage s + 1 has landed (and stage s
+    // is in everybody's registers, so that its place can be filled again).
+    auto stage = [&](int s, auto wait, auto refill, u32x4_t (&xc)[RT], u32x4_t (&wc)[CT], u32x4_t (&xn)[RT],
+                     u32x4_t (&wnx)[CT]) {
+        constexpr int WAIT = decltype(wait)::value;
+        if constexpr (WAIT >= 0) {
+            wait_and_meet<WAIT>();
+            if constexpr (decltype(refill)::value) fetch(s + kStages);
+            read(s + 1, xn, wnx);
+        }
+        __builtin_amdgcn_sched_barrier(0);
+        multiply(xc, wc);
+        __builtin_amdgcn_sched_barrier(0);
+    };
+    using std::integral_constant;
+    using Yes = integral_constant<bool, true>;
+    using No = integral_constant<bool, false>;
+    if (S > 2) {
+        wait_and_meet<3 * L>();
+        read(0, xf[0], wf[0]);
+        int s = 0;
+        for (; s + kStages < S; s += 2) {
+            stage(s, integral_constant<int, 2 * L>{}, Yes{}, xf[0], wf[0], xf[1], wf[1]);
+            stage(s + 1, integral_constant<int, 2 * L>{}, Yes{}, xf[1], wf[1], xf[0], wf[0]);
+        }
+        stage(s, integral_constant<int, 2 * L>{}, No{}, xf[0], wf[0], xf[1], wf[1]);
+        stage(s + 1, integral_constant<int, L>{}, No{}, xf[1], wf[1], xf[0], wf[0]);
+    } else {
+        wait_and_meet<L>();
+        read(0, xf[0], wf[0]);
+    }
+    stage(S - 2, integral_constant<int, 0>{}, No{}, xf[0], wf[0], xf[1], wf[1]);
+    stage(S - 1, integral_constant<int, -1>{}, No{}, xf[1], wf[1], xf[0], wf[0]);
+
+    int64_t rows[RT];
+    Split rs[RT] = {};
+#pragma unroll
+    for (int rt = 0; rt < RT; ++rt) {
+        rows[rt] = row0 + wm * TM + rt * 16 + i16;
+        rs[rt] = Split(sx[src_row(rows[rt])]);
+    }
+#pragma unroll
+    for (int cc = 0; cc < CT / 2; ++cc) {
+        const int64_t n = n0 + wn * TN + 32 * cc + 8 * q;
+        if (n >= N) continue;
+        Split cs[8] = {};
+        float bv[8];
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+            cs[i] = Split(sw[(int64_t)e * N + n + i]);
+            bv[i] = bias ? h2f<DT>(bias[n + i]) : 0.0f;
+        }
+#pragma unroll
+        for (int rt = 0; rt < RT; ++rt) {
+            uint16_t h[8];
+#pragma unroll
+            for (int i = 0; i < 8; ++i) h[i] = f2h<DT>(finish(acc[rt][2 * cc + (i >> 2)][i & 3], rs[rt], cs[i], bv[i]));
+            if (rows[rt] < row_end)
+                *reinterpret_cast<u32x4_t *>(y + rows[rt] * ldy + n) =
+                    u32x4_t{h[0] | (uint32_t)h[1] << 16, h[2] | (uint32_t)h[3] << 16, h[4] | (uint32_t)h[5] << 16,
+                            h[6] | (uint32_t)h[7] << 16};
+        }
+    }
+}
+
+// ---------------------------------------------------------------------------
 // Launchers
 // ---------------------------------------------------------------------------
 hipError_t launch_w8a8_quantize(const void *x, int64_t ldx, const int32_t *row_count, void *qx, float *sx, int64_t M,
@@ -280,12 +476,27 @@ static hipError_t split_launch(const W8A8Args &p, hipStream_t stream) {
     return hipGetLastError();
 }
 
+template <int DT, int BM, int BN, int WM, int WN, bool GROUPED>
+static hipError_t tile8_launch(const W8A8Args &p, hipStream_t stream) {
+    const int64_t ncb = (p.N + BN - 1) / BN;
+    const int64_t few = p.M < p.E ? p.M : p.E;
+    const int64_t mtiles = GROUPED ? p.M / BM + few : (p.M + BM - 1) / BM;
+    const int64_t per_xcd = (mtiles * ncb + kXcd8 - 1) / kXcd8;
+    if (per_xcd * kXcd8 > INT32_MAX) return hipErrorInvalidConfiguration;
+    hipLaunchKernelGGL((w8a8_tile_kernel<DT, BM, BN, WM, WN, GROUPED>), dim3((unsigned)(per_xcd * kXcd8)),
+                       dim3(WM * WN * 64), 0, stream, p.qx, p.sx, p.offsets, p.sorted, p.topk, p.wp, p.sw, p.bias, p.y,
+                       p.ldy, p.M, p.X, p.K, p.N, p.E, (int)ncb, (int)per_xcd);
+    return hipGetLastError();
+}
+
 template <int DT, bool GROUPED>
 static hipError_t w8a8_dispatch(const W8A8Args &p, hipStream_t stream) {
     const int64_t rows = GROUPED ? p.M / p.E : p.M;
     if (rows <= 16) return split_launch<DT, 1, 4, GROUPED, 16>(p, stream);
-    return split_launch<DT, 4, 4, GROUPED, 4>(p, stream);
+    if (rows <= 64) return tile8_launch<DT, 64, 128, 2, 2, GROUPED>(p, stream);
+    return tile8_launch<DT, 256, 256, 2, 2, GROUPED>(p, stream);
 }
+
 
 hipError_t launch_w8a8(const W8A8Args &p, int dt, hipStream_t stream) {
     if (p.M == 0) return hipSuccess;

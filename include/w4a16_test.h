@@ -108,6 +108,13 @@ const char *w4a16_test_variant_name(int64_t M, int64_t K, int64_t N, int dt, int
  * queries follow.  Returns the number of shapes. */
 int w4a16_test_linear_plan(int shape, int slices);
 
+/*
+ * Select the kernel of the W8A8 products (dense and grouped) for subsequent
+ * calls: idx in [0, count), or -1 for the choice by size.  Not thread-safe; tests
+ * and tuning only.  Returns the number of configurations.
+ */
+int w4a16_test_w8a8_config(int idx);
+
 #ifdef __cplusplus
 }
 #endif

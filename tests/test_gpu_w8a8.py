@@ -289,3 +289,26 @@ def test_stream_and_graph():
         assert torch.equal(y, want[i])
         y.zero_()
         assert torch.equal(run_gemm(xs[2 - i], wp, swd, bd, N, BF16), want[2 - i])
+
+
+@pytest.fixture
+def config():
+    yield w4.w4a16_test_w8a8_config
+    w4.w4a16_test_w8a8_config(-1)
+
+
+@pytest.mark.parametrize("idx", range(w4.w4a16_test_w8a8_config(-1)))
+@pytest.mark.parametrize("M,K,N", [(1, 128, 64), (37, 256, 320), (150, 384, 192), (300, 1024, 576), (520, 640, 64)])
+def test_every_kernel(config, M, K, N, idx):
+    """Each kernel that a size may pick, on sizes that end inside its tiles and on short K."""
+    x, w, sw, b = problem(M, K, N, BF16, bias=True)
+    config(idx)
+    check_gemm(run_gemm(dev(x), packed(w), dev(sw), dev(b), N, BF16), x, w[0], sw[0], b)
+
+
+@pytest.mark.parametrize("idx", range(w4.w4a16_test_w8a8_config(-1)))
+@pytest.mark.parametrize("rows", [[1], [16, 1, 0, 33, 300], [1] * 70])
+def test_every_grouped_kernel(config, rows, idx):
+    config(idx)
+    test_grouped(rows, 640, 320, F16)
+    test_grouped_reads_tokens(37, 3, 70)

@@ -116,6 +116,7 @@ _SIGS = {
     "w4a16_test_mx_small_config": ([C.c_int], C.c_int),
     "w4a16_test_mx_tile_config": ([C.c_int], C.c_int),
     "w4a16_test_linear_plan": ([C.c_int, C.c_int], C.c_int),
+    "w4a16_test_w8a8_config": ([C.c_int], C.c_int),
     "w4a16_test_w8_config": ([C.c_int, C.c_int], C.c_int),
 }
 EXPORTED = tuple(_SIGS)
@@ -479,3 +480,7 @@ def w4a16_test_w8_config(small_idx: int, tile_idx: int) -> int:
 
 def w4a16_test_linear_plan(shape: int, slices: int) -> int:
     return lib().w4a16_test_linear_plan(int(shape), int(slices))
+
+
+def w4a16_test_w8a8_config(idx: int) -> int:
+    return lib().w4a16_test_w8a8_config(int(idx))

@@ -818,6 +818,11 @@ int w4a16_test_mx_small_config(int idx) {
     return w4::mx_small_config_count();
 }
 
+int w4a16_test_w8a8_config(int idx) {
+    w4::set_w8a8_config(idx);
+    return w4::w8a8_config_count();
+}
+
 int w4a16_test_w8_config(int small_idx, int tile_idx) {
     w4::set_w8_small_config(small_idx);
     w4::set_w8_tile_config(tile_idx);

@@ -229,6 +229,8 @@ struct W8A8Args {
     int E;
 };
 hipError_t launch_w8a8(const W8A8Args &p, int dt, hipStream_t stream);
+int w8a8_config_count();
+void set_w8a8_config(int idx);
 
 // MoE router: logits dtypes 0 fp16, 1 bf16, 2 fp32.
 size_t route_workspace_bytes(int64_t T, int64_t E);

@@ -13,6 +13,7 @@
 // so lane l feeds weight column l % 16 and x row l % 16, both with rows
 // 128 g + 32 (l / 16) + 16 h .. + 15 of step h; result register r of lane l is
 // column 4 (l / 16) + r of x row l % 16: four neighbouring outputs per lane.
+#include <atomic>
 #include <type_traits>
 
 #include "common.hpp"
@@ -259,6 +260,7 @@ w8a8_split_kernel(const uint8_t *__restrict__ qx, const float *__restrict__ sx, 
 constexpr int kXcd8 = 8;              // XCDs; workgroups go to them round-robin
 constexpr int kStageK = 64;           // K rows per stage
 constexpr int kStages = 4;            // stages in LDS
+constexpr unsigned kBand = 4;         // row tiles side by side on an XCD
 
 // 16 bytes per lane from global memory (base + off) to LDS (lds_base + 16 lane), not
 // waited for here.  In assembly, since the compiler follows its own form of this
@@ -275,12 +277,12 @@ __device__ __forceinline__ void wait_and_meet() {
     asm volatile("s_waitcnt vmcnt(%0) lgkmcnt(0)\n\ts_barrier" ::"n"(N) : "memory");
 }
 
-template <int DT, int BM, int BN, int WM, int WN, bool GROUPED>
+template <int DT, int BM, int BN, int WM, int WN, bool GROUPED, bool AHEAD>
 __global__ void __launch_bounds__(WM * WN * 64)
 w8a8_tile_kernel(const uint8_t *__restrict__ qx, const float *__restrict__ sx, const int32_t *__restrict__ offsets,
                  const int32_t *__restrict__ sorted, int topk, const uint8_t *__restrict__ wp,
                  const float *__restrict__ sw, const uint16_t *__restrict__ bias, uint16_t *__restrict__ y, int64_t ldy,
-                 int64_t M, int64_t X, int64_t K, int64_t N, int E, int ncb, int per_xcd) {
+                 int64_t M, int64_t X, int64_t K, int64_t N, int E, unsigned mtiles, unsigned ncb, unsigned per_xcd) {
     constexpr int NW = WM * WN, TM = BM / WM, TN = BN / WN, RT = TM / 16, CT = TN / 16;
     constexpr int ABYTES = BM * kStageK, BBYTES = BN * kStageK, SBYTES = ABYTES + BBYTES;
     constexpr int AL = BM / 16 / NW, BL = BN / 16 / NW;      // DMA loads per wave and stage
@@ -291,18 +293,18 @@ w8a8_tile_kernel(const uint8_t *__restrict__ qx, const float *__restrict__ sx, c
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const int wm = wave / WN, wn = wave % WN;
     const int S = (int)(K / kStageK);
-    // XCD x takes a contiguous range of the tiles
-    const int64_t id = (int64_t)(blockIdx.x % kXcd8) * per_xcd + blockIdx.x / kXcd8;
-    int64_t tile, n0;
+    // XCD x takes a contiguous range of the tiles, which run through bands of kBand row
+    // tiles column by column: the tiles at work on an XCD share x and W in its L2
+    const unsigned id = (blockIdx.x % kXcd8) * per_xcd + blockIdx.x / kXcd8, bsize = kBand * ncb;
+    const unsigned band = id / bsize, in = id % bsize;
+    if (band * kBand >= mtiles) return;
+    const unsigned high = mtiles - band * kBand < kBand ? mtiles - band * kBand : kBand;
+    if (in >= high * ncb) return;             // behind the last tile
+    const int64_t tile = band * kBand + in % high, n0 = (int64_t)(in / high) * BN;
     int e = 0;
-    int64_t row0, row_end = M;
-    tile = id / ncb;
-    n0 = id % ncb * BN;
-    row0 = tile * BM;
+    int64_t row0 = tile * BM, row_end = M;
     if constexpr (GROUPED) {
         if (!expert_tile(offsets, E, M, BM, tile, e, row0, row_end)) return;
-    } else {
-        if (row0 >= M) return;
     }
     auto src_row = [&](int64_t r) -> int64_t {
         if (r >= row_end) r = row_end - 1;
@@ -316,21 +318,24 @@ w8a8_tile_kernel(const uint8_t *__restrict__ qx, const float *__restrict__ sx, c
     };
 
     // DMA sources.  x: a load fills 16 rows of 64 bytes, 16-byte chunk c of row r at chunk
-    // c ^ fx(r) of the row; W: a load fills one 1024-byte tile half, piece p at
-    // p ^ fw(p, tile).  Both permutations are their own inverses.
+    // c ^ (-(r / 4) & 3) of its row; W: a load fills one 1024-byte half of a weight tile,
+    // piece p at p ^ 8 (tile & 1).  LDS serves a 128-bit read in four passes over the
+    // lanes' quads {0, 3, 5, 6}, {1, 2, 4, 7} and the same plus 8 (measured with pairs of
+    // quads on the same banks), 256 bytes each: with these orders the 16 lanes of a
+    // pass touch each bank once (4.06 clocks a read; orders for 8 neighbouring lanes 6.5 and 8.0).
     uint32_t aoffs[AL], boffs[BL];
     const uint8_t *abase = qx, *bbase = wp + ((int64_t)e * (N / 16) + n0 / 16) * (K / kGroup) * kW8Tile;
     if (!sorted) abase += row0 * K;          // gathered rows: X K < 2^32
 #pragma unroll
     for (int i = 0; i < AL; ++i) {
-        const int r = lane >> 2, c = (lane & 3) ^ ((r >> 1) & 3) ^ (r >> 3);
+        const int r = lane >> 2, c = (lane & 3) ^ (-(r >> 2) & 3);
         const int64_t m = src_row(row0 + (wave + NW * i) * 16 + r);
         aoffs[i] = (uint32_t)((sorted ? m : m - row0) * K) + 16 * c;
     }
 #pragma unroll
     for (int i = 0; i < BL; ++i) {
         const int t = wave + NW * i, last = (int)((N - n0) / 16) - 1;
-        const int piece = lane ^ ((lane >> 4) & 1) ^ ((t & 1) << 3);
+        const int piece = lane ^ ((t & 1) << 3);
         boffs[i] = (uint32_t)((t < last ? t : last) * (K * 16)) + 16 * piece;
     }
     const uint32_t lds0 = (uint32_t)(uintptr_t)(__attribute__((address_space(3))) uint8_t *)lds + wave * 1024;
@@ -344,15 +349,15 @@ w8a8_tile_kernel(const uint8_t *__restrict__ qx, const float *__restrict__ sx, c
         bbase += 1024;
     };
 #pragma unroll
-    for (int s = 0; s < kStages; ++s)
+    for (int s = 0; s < (AHEAD ? kStages : kStages - 1); ++s)
         if (s < S) fetch(s);
 
     // LDS offsets of this lane's operands
     const int i16 = lane & 15, q = lane >> 4;
-    const int aoff = (wm * TM + i16) * kStageK + 16 * (q ^ ((i16 >> 1) & 3) ^ (i16 >> 3));
+    const int aoff = (wm * TM + i16) * kStageK + 16 * (q ^ (-(i16 >> 2) & 3));
     // W operand row i of column block ct is column 32 (ct / 2) + 8 (i / 4) + 4 (ct % 2) + i % 4
     // of the wave's tile: a lane then ends up with 8 neighbouring columns per pair of blocks
-    const int piece = ((q & 1) ^ ((i16 >> 2) & 1)) | (i16 & 3) << 1 | (i16 >> 3) << 3 | ((i16 >> 2) & 1) << 4 | (q >> 1) << 5;
+    const int piece = (q & 1) | (i16 & 3) << 1 | (i16 >> 3) << 3 | ((i16 >> 2) & 1) << 4 | (q >> 1) << 5;
     const int boff = ABYTES + (wn * CT + (i16 >> 3)) * 1024 + 16 * piece;
 
     i32x4_t acc[RT][CT];
@@ -361,7 +366,7 @@ w8a8_tile_kernel(const uint8_t *__restrict__ qx, const float *__restrict__ sx, c
 #pragma unroll
         for (int ct = 0; ct < CT; ++ct) acc[rt][ct] = i32x4_t{0, 0, 0, 0};
 
-    u32x4_t xf[2][RT], wf[2][CT];
+    u32x4_t xf[AHEAD ? 2 : 1][RT], wf[AHEAD ? 2 : 1][CT];
     auto read = [&](int s, u32x4_t (&xd)[RT], u32x4_t (&wd)[CT]) {
         const uint8_t *base = lds + ((unsigned)s % kStages) * SBYTES;
 #pragma unroll
@@ -373,7 +378,7 @@ w8a8_tile_kernel(const uint8_t *__restrict__ qx, const float *__restrict__ sx, c
     auto multiply = [&](const u32x4_t (&xd)[RT], const u32x4_t (&wd)[CT]) {
 #pragma unroll
         for (int ct = 0; ct < CT; ++ct) {
-            const i32x4_t w = __builtin_bit_cast(i32x4_t, wd[ct] ^ 0x80808080u);
+            const i32x4_t w = __builtin_bit_cast(i32x4_t, !AHEAD && NW == 8 ? wd[ct] : wd[ct] ^ 0x80808080u);
 #pragma unroll
             for (int rt = 0; rt < RT; ++rt)
                 acc[rt][ct] = __builtin_amdgcn_mfma_i32_16x16x64_i8(w, __builtin_bit_cast(i32x4_t, xd[rt]), acc[rt][ct], 0, 0, 0);
@@ -398,22 +403,67 @@ w8a8_tile_kernel(const uint8_t *__restrict__ qx, const float *__restrict__ sx, c
     using std::integral_constant;
     using Yes = integral_constant<bool, true>;
     using No = integral_constant<bool, false>;
-    if (S > 2) {
-        wait_and_meet<3 * L>();
-        read(0, xf[0], wf[0]);
-        int s = 0;
-        for (; s + kStages < S; s += 2) {
-            stage(s, integral_constant<int, 2 * L>{}, Yes{}, xf[0], wf[0], xf[1], wf[1]);
-            stage(s + 1, integral_constant<int, 2 * L>{}, Yes{}, xf[1], wf[1], xf[0], wf[0]);
+    if constexpr (AHEAD) {
+        if (S > 2) {
+            wait_and_meet<3 * L>();
+            read(0, xf[0], wf[0]);
+            int s = 0;
+            for (; s + kStages < S; s += 2) {
+                stage(s, integral_constant<int, 2 * L>{}, Yes{}, xf[0], wf[0], xf[1], wf[1]);
+                stage(s + 1, integral_constant<int, 2 * L>{}, Yes{}, xf[1], wf[1], xf[0], wf[0]);
+            }
+            stage(s, integral_constant<int, 2 * L>{}, No{}, xf[0], wf[0], xf[1], wf[1]);
+            stage(s + 1, integral_constant<int, L>{}, No{}, xf[1], wf[1], xf[0], wf[0]);
+        } else {
+            wait_and_meet<L>();
+            read(0, xf[0], wf[0]);
         }
-        stage(s, integral_constant<int, 2 * L>{}, No{}, xf[0], wf[0], xf[1], wf[1]);
-        stage(s + 1, integral_constant<int, L>{}, No{}, xf[1], wf[1], xf[0], wf[0]);
+        stage(S - 2, integral_constant<int, 0>{}, No{}, xf[0], wf[0], xf[1], wf[1]);
+        stage(S - 1, integral_constant<int, -1>{}, No{}, xf[1], wf[1], xf[0], wf[0]);
+    } else if constexpr (NW == 8) {
+        // Two groups of waves, one of each on every SIMD, take turns: while one multiplies
+        // stage s, the other reads its operands.  A phase ends in a barrier; group 0
+        // reads stage s in phase 2 s and multiplies it in phase 2 s + 1, group 1 one phase
+        // later.  Stage s has landed by the end of phase 2 s - 1 (WAIT: later loads that
+        // may be outstanding); its place is filled again from phase 2 s + 2 on.
+        auto turn = [&](int s, auto wait, auto refill) {
+            constexpr int WAIT = decltype(wait)::value;
+            if constexpr (decltype(refill)::value) fetch(s + kStages - 1);
+            read(s, xf[0], wf[0]);
+#pragma unroll
+            for (int ct = 0; ct < CT; ++ct) {
+                wf[0][ct] ^= 0x80808080u;
+                asm volatile("" : "+v"(wf[0][ct]));
+            }
+            wait_and_meet<WAIT>();
+            __builtin_amdgcn_sched_barrier(0);
+            multiply(xf[0], wf[0]);
+            __builtin_amdgcn_sched_barrier(0);
+            wait_and_meet<63>();
+        };
+        if (S > 2) wait_and_meet<2 * L>();
+        else wait_and_meet<L>();
+        if (wave >= 4) wait_and_meet<63>();
+        int s = 0;
+        for (; s + kStages <= S; ++s) turn(s, integral_constant<int, 2 * L>{}, Yes{});
+        if (S > 2) turn(S - 3, integral_constant<int, L>{}, No{});
+        turn(S - 2, integral_constant<int, 0>{}, No{});
+        turn(S - 1, integral_constant<int, 0>{}, No{});
+        if (wave < 4) wait_and_meet<63>();
     } else {
-        wait_and_meet<L>();
-        read(0, xf[0], wf[0]);
+        // stage s has landed, and stage s - 1 is in everybody's registers: its place is filled again
+        auto plain = [&](int s, auto wait, auto refill) {
+            wait_and_meet<decltype(wait)::value>();
+            if constexpr (decltype(refill)::value) fetch(s + kStages - 1);
+            read(s, xf[0], wf[0]);
+            multiply(xf[0], wf[0]);
+        };
+        int s = 0;
+        for (; s + kStages <= S; ++s) plain(s, integral_constant<int, 2 * L>{}, Yes{});
+        if (S > 2) plain(S - 3, integral_constant<int, 2 * L>{}, No{});
+        plain(S - 2, integral_constant<int, L>{}, No{});
+        plain(S - 1, integral_constant<int, 0>{}, No{});
     }
-    stage(S - 2, integral_constant<int, 0>{}, No{}, xf[0], wf[0], xf[1], wf[1]);
-    stage(S - 1, integral_constant<int, -1>{}, No{}, xf[1], wf[1], xf[0], wf[0]);
 
     int64_t rows[RT];
     Split rs[RT] = {};
@@ -476,27 +526,41 @@ static hipError_t split_launch(const W8A8Args &p, hipStream_t stream) {
     return hipGetLastError();
 }
 
-template <int DT, int BM, int BN, int WM, int WN, bool GROUPED>
+template <int DT, int BM, int BN, int WM, int WN, bool GROUPED, bool AHEAD>
 static hipError_t tile8_launch(const W8A8Args &p, hipStream_t stream) {
     const int64_t ncb = (p.N + BN - 1) / BN;
     const int64_t few = p.M < p.E ? p.M : p.E;
     const int64_t mtiles = GROUPED ? p.M / BM + few : (p.M + BM - 1) / BM;
     const int64_t per_xcd = (mtiles * ncb + kXcd8 - 1) / kXcd8;
     if (per_xcd * kXcd8 > INT32_MAX) return hipErrorInvalidConfiguration;
-    hipLaunchKernelGGL((w8a8_tile_kernel<DT, BM, BN, WM, WN, GROUPED>), dim3((unsigned)(per_xcd * kXcd8)),
+    hipLaunchKernelGGL((w8a8_tile_kernel<DT, BM, BN, WM, WN, GROUPED, AHEAD>), dim3((unsigned)(per_xcd * kXcd8)),
                        dim3(WM * WN * 64), 0, stream, p.qx, p.sx, p.offsets, p.sorted, p.topk, p.wp, p.sw, p.bias, p.y,
-                       p.ldy, p.M, p.X, p.K, p.N, p.E, (int)ncb, (int)per_xcd);
+                       p.ldy, p.M, p.X, p.K, p.N, p.E, (unsigned)mtiles, (unsigned)ncb, (unsigned)per_xcd);
     return hipGetLastError();
 }
+
+// Test hook: the kernel of the next calls (-1: by size).
+static std::atomic<int> g_w8a8_cfg{-1};
+void set_w8a8_config(int idx) { g_w8a8_cfg.store(idx, std::memory_order_relaxed); }
 
 template <int DT, bool GROUPED>
 static hipError_t w8a8_dispatch(const W8A8Args &p, hipStream_t stream) {
     const int64_t rows = GROUPED ? p.M / p.E : p.M;
-    if (rows <= 16) return split_launch<DT, 1, 4, GROUPED, 16>(p, stream);
-    if (rows <= 64) return tile8_launch<DT, 64, 128, 2, 2, GROUPED>(p, stream);
-    return tile8_launch<DT, 256, 256, 2, 2, GROUPED>(p, stream);
+    int cfg = g_w8a8_cfg.load(std::memory_order_relaxed);
+    if (cfg < 0 || cfg >= w8a8_config_count()) cfg = rows <= 16 ? 0 : rows <= 64 ? 2 : 4;
+    switch (cfg) {
+        case 0: return split_launch<DT, 1, 4, GROUPED, 16>(p, stream);
+        case 1: return split_launch<DT, 4, 4, GROUPED, 4>(p, stream);
+        case 2: return tile8_launch<DT, 64, 128, 2, 2, GROUPED, true>(p, stream);
+        case 3: return tile8_launch<DT, 64, 128, 2, 2, GROUPED, false>(p, stream);
+        case 4: return tile8_launch<DT, 128, 128, 2, 2, GROUPED, false>(p, stream);
+        case 5: return tile8_launch<DT, 256, 256, 2, 4, GROUPED, false>(p, stream);
+        case 6: return tile8_launch<DT, 256, 128, 4, 2, GROUPED, true>(p, stream);
+        case 7: return tile8_launch<DT, 256, 128, 4, 2, GROUPED, false>(p, stream);
+        default: return tile8_launch<DT, 256, 256, 4, 2, GROUPED, false>(p, stream);
+    }
 }
-
+int w8a8_config_count() { return 9; }
 
 hipError_t launch_w8a8(const W8A8Args &p, int dt, hipStream_t stream) {
     if (p.M == 0) return hipSuccess;

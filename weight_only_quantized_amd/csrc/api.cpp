@@ -620,6 +620,22 @@ w4a16_status w8a8_gemm(const void *x, int64_t ldx, const void *w_packed, const f
     if (!aligned(x, 16) || !aligned(workspace, 16) || !aligned(w_packed, 16) || !aligned(y, 16) || !aligned(sw, 4) ||
         !aligned(bias, 2))
         return W4A16_ERR_ALIGN;
+    if (w4::w8a8_fused_ok(M, K)) {
+        if (current_device_ok() != 1) return W4A16_ERR_DEVICE;
+        w4::W8A8Args p{};
+        p.x = (const uint16_t *)x;
+        p.ldx = ldx;
+        p.X = p.M = M;
+        p.wp = (const uint8_t *)w_packed;
+        p.sw = sw;
+        p.bias = (const uint16_t *)bias;
+        p.y = (uint16_t *)y;
+        p.ldy = ldy;
+        p.K = K;
+        p.N = N;
+        p.E = 1;
+        return map_err(w4::launch_w8a8_fused(p, dt, (hipStream_t)stream));
+    }
     uint8_t *qx = (uint8_t *)workspace;
     float *sx = (float *)(qx + w8a8_sx_offset(M, K));
     st = w8a8_quantize(x, ldx, nullptr, qx, sx, M, K, dt, stream);

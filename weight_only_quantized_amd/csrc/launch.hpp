@@ -214,6 +214,8 @@ hipError_t launch_lin_zero_colsum(float *colsum, int64_t N, hipStream_t stream);
 hipError_t launch_w8a8_quantize(const void *x, int64_t ldx, const int32_t *row_count, void *qx, float *sx, int64_t M,
                                 int64_t K, int dt, hipStream_t stream);
 struct W8A8Args {
+    const uint16_t *x;          // fused quantization: x [M][K], row stride ldx (qx, sx unused)
+    int64_t ldx;
     const uint8_t *qx;          // codes [X][K] and scales [X] of the activations
     const float *sx;
     int64_t X;
@@ -229,6 +231,9 @@ struct W8A8Args {
     int E;
 };
 hipError_t launch_w8a8(const W8A8Args &p, int dt, hipStream_t stream);
+// The product of unquantized rows in one launch (p.x, p.ldx), where it exists.
+bool w8a8_fused_ok(int64_t M, int64_t K);
+hipError_t launch_w8a8_fused(const W8A8Args &p, int dt, hipStream_t stream);
 int w8a8_config_count();
 void set_w8a8_config(int idx);
 

@@ -165,69 +165,166 @@ __device__ __forceinline__ bool expert_tile(const int32_t *__restrict__ offsets,
 
 // ---------------------------------------------------------------------------
 // Split-K kernel: a workgroup owns 16 MT rows x 16 NB columns, its waves split
-// the 128-row groups of K and meet in LDS.
+// the 128-row groups of K and meet in LDS.  Each wave keeps the weights of D groups
+// in flight in registers.  FUSED: x comes in 16 bits, and the workgroup quantizes its
+// rows into LDS while the first weights are on their way.
 // ---------------------------------------------------------------------------
-template <int DT, int MT, int NB, bool GROUPED, int WMAX>
+constexpr int kFusedBytes = 64 * 1024;           // codes of a fused call's rows (row stride K + 16)
+
+// max over the wave's lanes
+__device__ __forceinline__ uint32_t wave_max(uint32_t v) {
+#pragma unroll
+    for (int off = 32; off > 0; off >>= 1) {
+        const uint32_t o = __shfl_xor(v, off);
+        v = o > v ? o : v;
+    }
+    return v;
+}
+
+template <int DT>
+__device__ __forceinline__ uint32_t top_of(const u32x4_t &v) {
+    uint32_t top = 0;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        const uint32_t w = v[i], a = mag_bits<DT>(w), b = mag_bits<DT>(w >> 16);
+        top = a > top ? a : top;
+        top = b > top ? b : top;
+    }
+    return top;
+}
+
+template <int DT>
+__device__ __forceinline__ u32x2s_t codes_of(const u32x4_t &v, const RowQuant &rq, float scale) {
+    uint32_t out[2] = {0, 0};
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+        const uint32_t w = v[i >> 1];
+        // codes of a row without a scale stay 0 (0 * inf would be NaN)
+        const int c = scale > 0.0f ? rq.code(h2f<DT>((uint16_t)(w >> (16 * (i & 1))))) : 0;
+        out[i >> 2] |= ((uint32_t)c & 0xFFu) << (8 * (i & 3));
+    }
+    return u32x2s_t{out[0], out[1]};
+}
+
+template <int DT, int MT, int NB, int D, int WMAX, bool GROUPED, bool FUSED>
 __global__ void __launch_bounds__(WMAX * 64)
-w8a8_split_kernel(const uint8_t *__restrict__ qx, const float *__restrict__ sx, const int32_t *__restrict__ offsets,
-                  const int32_t *__restrict__ sorted, int topk, const uint8_t *__restrict__ wp,
-                  const float *__restrict__ sw, const uint16_t *__restrict__ bias, uint16_t *__restrict__ y,
-                  int64_t ldy, int64_t M, int64_t X, int64_t K, int64_t N, int E, int ncb) {
-    extern __shared__ __attribute__((aligned(16))) uint8_t lds_raw[];
-    i32x4_t *red = reinterpret_cast<i32x4_t *>(lds_raw);      // [wave][MT * NB][64]
+w8a8_split_kernel(W8A8Args p, unsigned mtiles, unsigned ncb) {
+    static_assert(!GROUPED || !FUSED, "the grouped form reads quantized rows");
+    constexpr int RED = WMAX * NB * MT * 1024, LDS = FUSED && kFusedBytes > RED ? kFusedBytes : RED;
+    __shared__ __attribute__((aligned(16))) uint8_t lds[LDS];
+    __shared__ uint32_t tops[FUSED ? 16 * MT : 1];
+    i32x4_t *red = reinterpret_cast<i32x4_t *>(lds);          // [wave][MT * NB][64]
+    const int64_t K = p.K, N = p.N;
     const int G = (int)(K / kGroup), W = blockDim.x >> 6;
     const int lane = lane_id();
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const int j = lane & 15, c = lane >> 4;
-    const int64_t n0 = (int64_t)(blockIdx.x % (unsigned)ncb) * (16 * NB);
-    const int64_t tile = blockIdx.x / (unsigned)ncb;
+    const int64_t n0 = (int64_t)(blockIdx.x % ncb) * (16 * NB);
+    const int64_t tile = blockIdx.x / ncb;
     int e = 0;
-    int64_t row0 = tile * (16 * MT), row_end = M;
+    int64_t row0 = tile * (16 * MT), row_end = p.M;
     if constexpr (GROUPED) {
-        if (!expert_tile(offsets, E, M, 16 * MT, tile, e, row0, row_end)) return;
+        if (!expert_tile(p.offsets, p.E, p.M, 16 * MT, tile, e, row0, row_end)) return;
     }
     // x row of a tile's row; rows past the end take the last one and are not stored
     auto src_row = [&](int64_t r) -> int64_t {
         if (r >= row_end) r = row_end - 1;
         if constexpr (GROUPED) {
-            if (sorted) {
-                const int64_t t = (int64_t)((uint32_t)sorted[r] / (uint32_t)topk);
-                return t < X ? t : X - 1;
+            if (p.sorted) {
+                const int64_t t = (int64_t)((uint32_t)p.sorted[r] / (uint32_t)p.topk);
+                return t < p.X ? t : p.X - 1;
             }
         }
         return r;
     };
-    const uint8_t *xp[MT];
+    const int g0 = (int)((int64_t)G * wave / W), g1 = (int)((int64_t)G * (wave + 1) / W);
+    const uint8_t *wb = p.wp + ((int64_t)e * (N / 16) + n0 / 16) * G * kW8Tile + lane * 32;
+    u32x4_t wf[D][NB][2], xf[FUSED ? 1 : D][MT][2];
+    // groups past the wave's share re-read its last one
+    auto load_w = [&](int d, int g) {
+        g = g < g1 ? g : g1 - 1;
 #pragma unroll
-    for (int t = 0; t < MT; ++t) xp[t] = qx + src_row(row0 + 16 * t + j) * K + 32 * c;
-    const uint8_t *wb = wp + ((int64_t)e * (N / 16) + n0 / 16) * G * kW8Tile + lane * 32;
+        for (int b = 0; b < NB; ++b)
+#pragma unroll
+            for (int h = 0; h < 2; ++h) wf[d][b][h] = ld128(wb + ((int64_t)b * G + g) * kW8Tile + 16 * h);
+    };
+    const uint8_t *xp[MT];
+    auto load_x = [&](int d, int g) {
+        if constexpr (!FUSED) {
+            g = g < g1 ? g : g1 - 1;
+#pragma unroll
+            for (int t = 0; t < MT; ++t)
+#pragma unroll
+                for (int h = 0; h < 2; ++h) xf[d][t][h] = ld128(xp[t] + (int64_t)g * kGroup + 16 * h);
+        }
+    };
+#pragma unroll
+    for (int d = 0; d < D; ++d) load_w(d, g0 + d);
+
+    const int rows = (int)(row_end - row0 < 16 * MT ? row_end - row0 : 16 * MT);
+    const int stride = (int)K + 16;
+    if constexpr (FUSED) {
+        // pieces of 512 elements of a row, round robin over the waves
+        const int pieces = (int)((K + 511) / 512), total = pieces * rows;
+        for (int r = threadIdx.x; r < rows; r += W * 64) tops[r] = 0;
+        __syncthreads();
+        for (int i = wave; i < total; i += W) {
+            const int r = i / pieces, k = (i % pieces) * 512 + lane * 8;
+            uint32_t top = k < K ? top_of<DT>(ld128(p.x + (row0 + r) * p.ldx + k)) : 0;
+            top = wave_max(top);
+            if (lane == 0) atomicMax(&tops[r], top);
+        }
+        __syncthreads();
+        for (int i = wave; i < total; i += W) {
+            const int r = i / pieces, k = (i % pieces) * 512 + lane * 8;
+            const float scale = row_scale(mag_value<DT>(tops[r]));
+            if (k < K) {
+                const u32x2s_t q = codes_of<DT>(ld128(p.x + (row0 + r) * p.ldx + k), RowQuant(scale), scale);
+                *reinterpret_cast<u32x2s_t *>(lds + r * stride + k) = q;
+            }
+        }
+        __syncthreads();
+    } else {
+#pragma unroll
+        for (int t = 0; t < MT; ++t) xp[t] = p.qx + src_row(row0 + 16 * t + j) * K + 32 * c;
+#pragma unroll
+        for (int d = 0; d < D; ++d) load_x(d, g0 + d);
+    }
 
     i32x4_t acc[NB][MT];
 #pragma unroll
     for (int b = 0; b < NB; ++b)
 #pragma unroll
         for (int t = 0; t < MT; ++t) acc[b][t] = i32x4_t{0, 0, 0, 0};
-
-    const int g0 = (int)((int64_t)G * wave / W), g1 = (int)((int64_t)G * (wave + 1) / W);
-    u32x4_t wf[NB][2], xf[MT][2];
-    for (int g = g0; g < g1; ++g) {
+    for (int g = g0; g < g1; g += D) {
 #pragma unroll
-        for (int b = 0; b < NB; ++b)
+        for (int d = 0; d < D; ++d) {
+            if constexpr (FUSED) {
 #pragma unroll
-            for (int h = 0; h < 2; ++h) wf[b][h] = ld128(wb + ((int64_t)b * G + g) * kW8Tile + 16 * h);
+                for (int t = 0; t < MT; ++t) {
+                    const int r = 16 * t + j < rows ? 16 * t + j : rows - 1, gg = g + d < g1 ? g + d : g1 - 1;
 #pragma unroll
-        for (int t = 0; t < MT; ++t)
-#pragma unroll
-            for (int h = 0; h < 2; ++h) xf[t][h] = ld128(xp[t] + (int64_t)g * kGroup + 16 * h);
-#pragma unroll
-        for (int h = 0; h < 2; ++h)
-#pragma unroll
-            for (int b = 0; b < NB; ++b) {
-                const u32x4_t q = wf[b][h] ^ 0x80808080u;
-#pragma unroll
-                for (int t = 0; t < MT; ++t) acc[b][t] = mfma_i8_16x16x64(q, xf[t][h], acc[b][t]);
+                    for (int h = 0; h < 2; ++h)
+                        xf[0][t][h] = ld128(lds + r * stride + gg * kGroup + 32 * c + 16 * h);
+                }
             }
+            if (g + d < g1) {
+#pragma unroll
+                for (int h = 0; h < 2; ++h)
+#pragma unroll
+                    for (int b = 0; b < NB; ++b) {
+                        const u32x4_t q = wf[d][b][h] ^ 0x80808080u;
+#pragma unroll
+                        for (int t = 0; t < MT; ++t) acc[b][t] = mfma_i8_16x16x64(q, xf[FUSED ? 0 : d][t][h], acc[b][t]);
+                    }
+            }
+            if (g + D < g1) {
+                load_w(d, g + d + D);
+                load_x(d, g + d + D);
+            }
+        }
     }
+    if constexpr (FUSED) __syncthreads();            // the codes make room for the sums
 #pragma unroll
     for (int b = 0; b < NB; ++b)
 #pragma unroll
@@ -240,15 +337,15 @@ w8a8_split_kernel(const uint8_t *__restrict__ qx, const float *__restrict__ sx, 
         const int b = o / MT, t = o % MT;
         const int64_t r = row0 + 16 * t + j;
         if (r < row_end) {
-            const Split rs(sx[src_row(r)]);
+            const Split rs(FUSED ? row_scale(mag_value<DT>(tops[FUSED ? 16 * t + j : 0])) : p.sx[src_row(r)]);
             const int64_t n = n0 + 16 * b + 4 * c;
             uint16_t h[4];
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
-                const float bv = bias ? h2f<DT>(bias[n + i]) : 0.0f;
-                h[i] = f2h<DT>(finish(sum[i], rs, Split(sw[(int64_t)e * N + n + i]), bv));
+                const float bv = p.bias ? h2f<DT>(p.bias[n + i]) : 0.0f;
+                h[i] = f2h<DT>(finish(sum[i], rs, Split(p.sw[(int64_t)e * N + n + i]), bv));
             }
-            *reinterpret_cast<u32x2s_t *>(y + r * ldy + n) =
+            *reinterpret_cast<u32x2s_t *>(p.y + r * p.ldy + n) =
                 u32x2s_t{h[0] | (uint32_t)h[1] << 16, h[2] | (uint32_t)h[3] << 16};
         }
     }
@@ -512,17 +609,16 @@ hipError_t launch_w8a8_quantize(const void *x, int64_t ldx, const int32_t *row_c
     return hipGetLastError();
 }
 
-template <int DT, int MT, int NB, bool GROUPED, int WMAX>
+template <int DT, int MT, int NB, int D, int WMAX, bool GROUPED, bool FUSED>
 static hipError_t split_launch(const W8A8Args &p, hipStream_t stream) {
     const int64_t G = p.K / kGroup;
     const int W = (int)(G < WMAX ? G : WMAX);
     const int64_t ncb = p.N / (16 * NB);
     const int64_t few = p.M < p.E ? p.M : p.E;                 // experts that can end in a partial tile
     const int64_t mtiles = GROUPED ? p.M / (16 * MT) + few : (p.M + 16 * MT - 1) / (16 * MT);
-    if (mtiles * ncb > INT32_MAX) return hipErrorInvalidConfiguration;
-    hipLaunchKernelGGL((w8a8_split_kernel<DT, MT, NB, GROUPED, WMAX>), dim3((unsigned)(mtiles * ncb)), dim3(W * 64),
-                       (size_t)W * NB * MT * 1024, stream, p.qx, p.sx, p.offsets, p.sorted, p.topk, p.wp, p.sw, p.bias,
-                       p.y, p.ldy, p.M, p.X, p.K, p.N, p.E, (int)ncb);
+    if (p.N % (16 * NB) != 0 || mtiles * ncb > INT32_MAX) return hipErrorInvalidConfiguration;
+    hipLaunchKernelGGL((w8a8_split_kernel<DT, MT, NB, D, WMAX, GROUPED, FUSED>), dim3((unsigned)(mtiles * ncb)),
+                       dim3(W * 64), 0, stream, p, (unsigned)mtiles, (unsigned)ncb);
     return hipGetLastError();
 }
 
@@ -549,18 +645,50 @@ static hipError_t w8a8_dispatch(const W8A8Args &p, hipStream_t stream) {
     int cfg = g_w8a8_cfg.load(std::memory_order_relaxed);
     if (cfg < 0 || cfg >= w8a8_config_count()) cfg = rows <= 16 ? 0 : rows <= 64 ? 2 : 4;
     switch (cfg) {
-        case 0: return split_launch<DT, 1, 4, GROUPED, 16>(p, stream);
-        case 1: return split_launch<DT, 4, 4, GROUPED, 4>(p, stream);
+        case 0: return split_launch<DT, 1, 4, 2, 16, GROUPED, false>(p, stream);
+        case 1: return split_launch<DT, 4, 2, 2, 8, GROUPED, false>(p, stream);
         case 2: return tile8_launch<DT, 64, 128, 2, 2, GROUPED, true>(p, stream);
         case 3: return tile8_launch<DT, 64, 128, 2, 2, GROUPED, false>(p, stream);
         case 4: return tile8_launch<DT, 128, 128, 2, 2, GROUPED, false>(p, stream);
         case 5: return tile8_launch<DT, 256, 256, 2, 4, GROUPED, false>(p, stream);
         case 6: return tile8_launch<DT, 256, 128, 4, 2, GROUPED, true>(p, stream);
         case 7: return tile8_launch<DT, 256, 128, 4, 2, GROUPED, false>(p, stream);
-        default: return tile8_launch<DT, 256, 256, 4, 2, GROUPED, false>(p, stream);
+        case 8: return tile8_launch<DT, 256, 256, 4, 2, GROUPED, false>(p, stream);
+        case 9: return split_launch<DT, 1, 4, 1, 16, GROUPED, false>(p, stream);
+        case 10: return split_launch<DT, 1, 2, 2, 16, GROUPED, false>(p, stream);
+        case 11: return split_launch<DT, 1, 2, 4, 16, GROUPED, false>(p, stream);
+        case 12: return split_launch<DT, 1, 4, 2, 8, GROUPED, false>(p, stream);
+        case 13: return split_launch<DT, 1, 4, 4, 8, GROUPED, false>(p, stream);
+        case 14: return split_launch<DT, 1, 1, 4, 16, GROUPED, false>(p, stream);
+        case 15: return split_launch<DT, 2, 4, 2, 8, GROUPED, false>(p, stream);
+        case 16: return split_launch<DT, 2, 2, 2, 16, GROUPED, false>(p, stream);
+        case 17: return split_launch<DT, 2, 2, 4, 8, GROUPED, false>(p, stream);
+        case 18: return split_launch<DT, 4, 4, 1, 8, GROUPED, false>(p, stream);
+        case 19: return split_launch<DT, 4, 2, 1, 16, GROUPED, false>(p, stream);
+        case 20: return split_launch<DT, 8, 2, 1, 8, GROUPED, false>(p, stream);
+        default: return split_launch<DT, 4, 1, 2, 16, GROUPED, false>(p, stream);
     }
 }
-int w8a8_config_count() { return 9; }
+int w8a8_config_count() { return 22; }
+
+bool w8a8_fused_ok(int64_t M, int64_t K) { return M <= 16 && M * (K + 16) <= kFusedBytes; }
+
+template <int DT>
+static hipError_t w8a8_fused_dispatch(const W8A8Args &p, hipStream_t stream) {
+    switch (g_w8a8_cfg.load(std::memory_order_relaxed)) {
+        case 9: return split_launch<DT, 1, 4, 1, 16, false, true>(p, stream);
+        case 10: return split_launch<DT, 1, 2, 2, 16, false, true>(p, stream);
+        case 11: return split_launch<DT, 1, 2, 4, 16, false, true>(p, stream);
+        case 12: return split_launch<DT, 1, 4, 2, 8, false, true>(p, stream);
+        case 13: return split_launch<DT, 1, 4, 4, 8, false, true>(p, stream);
+        case 14: return split_launch<DT, 1, 1, 4, 16, false, true>(p, stream);
+        default: return split_launch<DT, 1, 4, 2, 16, false, true>(p, stream);
+    }
+}
+
+hipError_t launch_w8a8_fused(const W8A8Args &p, int dt, hipStream_t stream) {
+    return dt == DT_BF16 ? w8a8_fused_dispatch<DT_BF16>(p, stream) : w8a8_fused_dispatch<DT_F16>(p, stream);
+}
 
 hipError_t launch_w8a8(const W8A8Args &p, int dt, hipStream_t stream) {
     if (p.M == 0) return hipSuccess;

@@ -642,7 +642,7 @@ w4a16_status w8a8_grouped_gemm(const void *x, const int32_t *sorted_ids, int64_t
  *    W4A16_F16, W4A16_BF16 or W4A16_F32, aligned to its size.  1 <= E <= 1024,
  *    1 <= topk <= E, T * topk < 2^31.
  *  - token_mask: [T] bytes or NULL.  counts may be NULL, loss too; loss needs counts.
- *  - workspace (4-byte aligned): at least w4a16_moe_route_workspace_bytes(T, E); may be NULL
+ *  - workspace (16-byte aligned): at least w4a16_moe_route_workspace_bytes(T, E); may be NULL
  *    without counts or where that is 0.  Contents on entry are ignored; calls
  *    sharing it must be ordered on one stream.
  *  - No atomics on floating-point values: equal calls give equal bits.

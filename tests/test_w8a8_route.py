@@ -96,7 +96,7 @@ def test_router_refuses_the_rest():
     assert route(ids=None) == 1 and route(w=None) == 1 and route(loss=F + 2) == 4
     need = w4.w4a16_moe_route_workspace_bytes(4096, 64)
     assert need > 0 and route(T=4096, nb=need - 1) == 5 and route(T=4096, ws=None) == 5
-    assert route(T=4096, ws=F + 2) == 4
+    assert route(T=4096, ws=F + 8) == 4
     assert back(dz=None) == 1 and back(ids=None) == 1 and back(w=None) == 1
     assert back(dz=F + 2) == 4 and back(dw=F + 2) == 4 and back(dloss=F + 2) == 4 and back(lddl=63) == 2
     for T, E in ((0, 64), (-1, 64), (8, 0), (8, 1025), (1 << 31, 64)):

@@ -702,7 +702,7 @@ w4a16_status w4a16_moe_route(const void *logits, int64_t ld, const uint8_t *toke
         if (need > 0 && (!workspace || workspace_bytes < need)) return W4A16_ERR_WORKSPACE;
     }
     if (!aligned(logits, dt == W4A16_F32 ? 4 : 2) || !aligned(topk_ids, 4) || !aligned(topk_w, 4) ||
-        !aligned(counts, 4) || !aligned(loss, 4) || (counts && !aligned(workspace, 4)))
+        !aligned(counts, 4) || !aligned(loss, 4) || (counts && !aligned(workspace, 16)))
         return W4A16_ERR_ALIGN;
     if (current_device_ok() != 1) return W4A16_ERR_DEVICE;
     w4::RouteArgs p{};

@@ -12,7 +12,9 @@
 // The loss's part of h is E c_e / (C Tv) less a constant, which a softmax's
 // gradient ignores: E c_e - C is an integer, so no digits cancel.
 //
-// A group of LPT lanes owns a token; lane `sub` holds experts sub, sub + LPT, ...
+// A group of LPT lanes owns a token, EPL experts each, all of a token's work in
+// registers; 64 / LPT tokens share a wave.  Choosing takes topk rounds of "largest that is left",
+// each a maximum over EPL registers and log2 LPT lane exchanges.
 #include "common.hpp"
 #include "launch.hpp"
 
@@ -20,87 +22,218 @@ namespace w4 {
 
 enum { DT_F32 = 2 };
 
-template <int DT>
-__device__ __forceinline__ float load_logit(const void *p, int64_t i) {
-    if constexpr (DT == DT_F32) return static_cast<const float *>(p)[i];
-    else return h2f<DT>(static_cast<const uint16_t *>(p)[i]);
+// ---- lane exchanges ---------------------------------------------------------
+
+// The value of a lane that differs in bit OFF of its index, for reductions that have
+// already joined the lower bits: 4 and 8 mirror within 8 and 16 lanes, which then is the same.
+template <int OFF>
+__device__ __forceinline__ uint32_t other(uint32_t v) {
+    if constexpr (OFF >= 16) {
+        return __shfl_xor(v, OFF);
+    } else {
+        constexpr int ctrl = OFF == 1 ? 0xB1 : OFF == 2 ? 0x4E : OFF == 4 ? 0x141 : 0x140;
+        return (uint32_t)__builtin_amdgcn_update_dpp(0, (int)v, ctrl, 0xF, 0xF, true);
+    }
 }
+template <int LPT, int OFF = 1, typename T, typename F>
+__device__ __forceinline__ T group_reduce(T v, F join) {
+    static_assert(sizeof(T) == 4, "one register");
+    if constexpr (OFF < LPT) {
+        v = join(v, __builtin_bit_cast(T, other<OFF>(__builtin_bit_cast(uint32_t, v))));
+        return group_reduce<LPT, 2 * OFF>(v, join);
+    } else {
+        return v;
+    }
+}
+template <int LPT>
+__device__ __forceinline__ float group_sum(float v) {
+    return group_reduce<LPT>(v, [](float a, float b) { return a + b; });
+}
+template <int LPT>
+__device__ __forceinline__ float group_max(float v) {
+    return group_reduce<LPT>(v, [](float a, float b) { return fmaxf(a, b); });
+}
+template <int LPT>
+__device__ __forceinline__ uint32_t group_umax(uint32_t v) {
+    return group_reduce<LPT>(v, [](uint32_t a, uint32_t b) { return a > b ? a : b; });
+}
+
+// ---- logits -----------------------------------------------------------------
+
 template <int DT>
 __device__ __forceinline__ void store_logit(void *p, int64_t i, float v) {
     if constexpr (DT == DT_F32) static_cast<float *>(p)[i] = v;
     else static_cast<uint16_t *>(p)[i] = f2h<DT>(v);
 }
 
-template <int LPT>
-__device__ __forceinline__ float group_sum(float v) {
+// Where lane `sub` of a token holds experts: EPL neighbours (VEC: E is a multiple
+// of EPL and rows start on 16 bytes, so they come with wide loads), or every LPT-th.
+template <int LPT, int EPL, bool VEC>
+__device__ __forceinline__ int expert_of(int i, int sub) { return VEC ? sub * EPL + i : i * LPT + sub; }
+
+// A lane's logits as they are stored (16 or 32 bits); -inf behind the last expert.
+template <int DT, int LPT, int EPL, bool VEC>
+__device__ __forceinline__ void load_row(const void *logits, int64_t at, int E, int sub, uint32_t (&raw)[EPL]) {
+    constexpr uint32_t none = DT == DT_F32 ? 0xFF800000u : DT == DT_BF16 ? 0xFF80u : 0xFC00u;
+    if constexpr (VEC) {
+        constexpr int W = EPL * (DT == DT_F32 ? 4 : 2) / 4;               // registers
+        uint32_t buf[W];
+        if (sub * EPL < E) {
+            const uint8_t *src = static_cast<const uint8_t *>(logits) + (at + sub * EPL) * (DT == DT_F32 ? 4 : 2);
+            if constexpr (W % 4 == 0) {
 #pragma unroll
-    for (int off = LPT / 2; off > 0; off >>= 1) v += __shfl_xor(v, off);
-    return v;
+                for (int v = 0; v < W / 4; ++v) {
+                    const u32x4_t q = ld128(src + 16 * v);
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) buf[4 * v + i] = q[i];
+                }
+            } else {
+                const u32x2_t q = *reinterpret_cast<const u32x2_t *>(src);
+                buf[0] = q[0];
+                buf[1] = q[1];
+            }
+        } else {
+#pragma unroll
+            for (int i = 0; i < W; ++i) buf[i] = DT == DT_F32 ? none : none | none << 16;
+        }
+#pragma unroll
+        for (int i = 0; i < EPL; ++i)
+            raw[i] = DT == DT_F32 ? buf[DT == DT_F32 ? i : 0] : (buf[DT == DT_F32 ? 0 : i / 2] >> (16 * (i % 2))) & 0xFFFFu;
+    } else {
+#pragma unroll
+        for (int i = 0; i < EPL; ++i) {
+            const int e = i * LPT + sub;
+            if constexpr (DT == DT_F32) raw[i] = e < E ? static_cast<const uint32_t *>(logits)[at + e] : none;
+            else raw[i] = e < E ? static_cast<const uint16_t *>(logits)[at + e] : none;
+        }
+    }
 }
-template <int LPT>
-__device__ __forceinline__ float group_max(float v) {
-#pragma unroll
-    for (int off = LPT / 2; off > 0; off >>= 1) v = fmaxf(v, __shfl_xor(v, off));
-    return v;
+template <int DT>
+__device__ __forceinline__ float value_of(uint32_t raw) {
+    if constexpr (DT == DT_F32) return __uint_as_float(raw);
+    else return h2f<DT>((uint16_t)raw);
+}
+
+// Logits in an order that unsigned integers compare by; -0 counts as +0, -inf is 0, less
+// than every choice.  16-bit types carry the expert along (a lower one is larger), so one
+// maximum decides ties too.
+template <int DT>
+__device__ __forceinline__ uint32_t key_of(uint32_t raw, int e) {
+    if constexpr (DT == DT_F32) {
+        const uint32_t u = raw == 0x80000000u ? 0u : raw;
+        return raw == 0xFF800000u ? 0u : u ^ ((uint32_t)((int32_t)u >> 31) | 0x80000000u);
+    } else {
+        const uint32_t u = raw == 0x8000u ? 0u : raw;
+        const uint32_t o = u & 0x8000u ? u ^ 0xFFFFu : u | 0x8000u;
+        return raw == (DT == DT_BF16 ? 0xFF80u : 0xFC00u) ? 0u : o << 16 | (0xFFFFu - (uint32_t)e);
+    }
+}
+template <int DT>
+__device__ __forceinline__ float key_value(uint32_t key) {
+    if constexpr (DT == DT_F32) {
+        return __uint_as_float(key & 0x80000000u ? key ^ 0x80000000u : ~key);
+    } else {
+        const uint32_t o = key >> 16;
+        return h2f<DT>((uint16_t)(o & 0x8000u ? o ^ 0x8000u : o ^ 0xFFFFu));
+    }
 }
 
 // What a token's logits are good for: a distribution, nothing (every logit
 // -inf), or NaN (a NaN or +inf among them).
 enum { ROW_OK = 0, ROW_EMPTY = 1, ROW_NAN = 2 };
 
-// exp(z - max) in place of z, their sum, and the row's kind.
-template <int LPT, int EPL>
-__device__ __forceinline__ int row_softmax(float (&z)[EPL], float (&p)[EPL], float &top, float &sum) {
+// exp(z - max), their sum, and the row's kind.
+template <int DT, int LPT, int EPL>
+__device__ __forceinline__ int row_softmax(const uint32_t (&raw)[EPL], float (&p)[EPL], float &top, float &sum) {
     float m = -INFINITY;
     bool nan = false;
 #pragma unroll
     for (int i = 0; i < EPL; ++i) {
-        m = fmaxf(m, z[i]);
-        nan |= z[i] != z[i];
+        p[i] = value_of<DT>(raw[i]);
+        m = fmaxf(m, p[i]);
+        nan |= p[i] != p[i];
     }
     top = group_max<LPT>(m);
-    const bool any_nan = group_max<LPT>(nan ? 1.0f : 0.0f) > 0.0f;
+    const bool any_nan = group_umax<LPT>(nan ? 1u : 0u) != 0;
     const int kind = any_nan || top == INFINITY ? ROW_NAN : top == -INFINITY ? ROW_EMPTY : ROW_OK;
     float s = 0.0f;
 #pragma unroll
     for (int i = 0; i < EPL; ++i) {
-        p[i] = kind == ROW_OK ? expf(z[i] - top) : kind == ROW_NAN ? __builtin_nanf("") : 0.0f;
+        p[i] = kind == ROW_OK ? expf(p[i] - top) : kind == ROW_NAN ? __builtin_nanf("") : 0.0f;
         s += p[i];
     }
     sum = group_sum<LPT>(s);
     return kind;
 }
 
-constexpr int kRouteThreads = 256;
+// ---- forward ------------------------------------------------------------------
 
-template <int DT, int LPT, int EPL>
-__global__ void __launch_bounds__(kRouteThreads)
-route_kernel(RouteArgs p, float *__restrict__ part_p, int32_t *__restrict__ part_c) {
+constexpr int kRouteThreads = 256, kRouteWaves = kRouteThreads / 64;
+
+// loss = E x / (n tokens) from x = sum_e c_e P_e, n = sum_e c_e (0 without tokens)
+__device__ __forceinline__ float balance_loss(int E, double x, long long n, int tokens) {
+    const double tv = tokens > 0 ? tokens : 1, cc = n > 0 ? (double)n : 1.0;
+    return (float)(E * x / (cc * tv));
+}
+
+// Sums of x and n over a block of NW waves, valid in thread 0.
+template <int NW>
+__device__ __forceinline__ void block_sums(double &x, long long &n) {
+    __shared__ double xs[NW];
+    __shared__ long long ns[NW];
+#pragma unroll
+    for (int off = 32; off > 0; off >>= 1) {
+        x += __shfl_xor(x, off);
+        n += __shfl_xor(n, off);
+    }
+    if (lane_id() == 0) {
+        xs[threadIdx.x >> 6] = x;
+        ns[threadIdx.x >> 6] = n;
+    }
+    __syncthreads();
+    if (threadIdx.x == 0)
+        for (int w = 1; w < NW; ++w) {
+            x += xs[w];
+            n += ns[w];
+        }
+}
+
+// Workspace: the blocks' sums of probabilities [blocks][E] and counts [blocks][E + 1], and
+// the joining blocks' sums and ticket.
+struct RouteSpace {
+    float *p;
+    int32_t *c;
+    double *x;
+    long long *n;
+    uint32_t *ticket;
+};
+constexpr int kJoinExperts = 32, kJoinRows = 32, kMaxJoins = kMoeMaxExperts / kJoinExperts;
+
+// Counts are kept where COUNT; a single block finishes by itself.
+template <int DT, int LPT, int EPL, bool VEC, bool COUNT>
+__global__ void __launch_bounds__(kRouteThreads) route_kernel(RouteArgs p, RouteSpace ws) {
     constexpr int TPB = kRouteThreads / LPT;
-    __shared__ int cnt[kMoeMaxExperts + 1];
-    __shared__ float psum[kRouteThreads / 64][kMoeMaxExperts];
+    __shared__ int cnt[COUNT ? LPT * EPL + 1 : 1];
+    __shared__ float psum[COUNT ? kRouteWaves : 1][COUNT ? LPT * EPL : 1];
     const int E = p.E, tid = threadIdx.x, sub = tid % LPT;
-    if (part_c) {
+    float pacc[COUNT ? EPL : 1];
+    if constexpr (COUNT) {
         for (int e = tid; e <= E; e += kRouteThreads) cnt[e] = 0;
+#pragma unroll
+        for (int i = 0; i < EPL; ++i) pacc[i] = 0.0f;
+        if (blockIdx.x == 0 && tid == 0 && gridDim.x > 1) *ws.ticket = 0;
         __syncthreads();
     }
-    float pacc[EPL];
-#pragma unroll
-    for (int i = 0; i < EPL; ++i) pacc[i] = 0.0f;
-
     for (int64_t t = (int64_t)blockIdx.x * TPB + tid / LPT; t < p.T; t += (int64_t)gridDim.x * TPB) {
         int32_t *ids = p.ids + t * p.topk;
         float *w = p.w + t * p.topk;
         const bool live = !p.mask || p.mask[t] != 0;
-        float z[EPL], pe[EPL], top = 0.0f, sum = 1.0f;
+        uint32_t key[EPL];
+        float pe[EPL], top = 0.0f, sum = 1.0f;
         int kind = ROW_EMPTY;
         if (live) {
-#pragma unroll
-            for (int i = 0; i < EPL; ++i) {
-                const int e = i * LPT + sub;
-                z[i] = e < E ? load_logit<DT>(p.logits, t * p.ld + e) : -INFINITY;
-            }
-            kind = row_softmax<LPT, EPL>(z, pe, top, sum);
+            load_row<DT, LPT, EPL, VEC>(p.logits, t * p.ld, E, sub, key);
+            kind = row_softmax<DT, LPT, EPL>(key, pe, top, sum);
         }
         if (kind != ROW_OK) {
             const float fill = kind == ROW_NAN ? __builtin_nanf("") : 0.0f;
@@ -108,123 +241,177 @@ route_kernel(RouteArgs p, float *__restrict__ part_p, int32_t *__restrict__ part
                 ids[k] = -1;
                 w[k] = fill;
             }
-            if (kind == ROW_NAN && part_c) {
+            if constexpr (COUNT) {
+                if (kind == ROW_NAN) {
 #pragma unroll
-                for (int i = 0; i < EPL; ++i) pacc[i] = __builtin_nanf("");
-                if (sub == 0) atomicAdd(&cnt[E], 1);
+                    for (int i = 0; i < EPL; ++i) pacc[i] = __builtin_nanf("");
+                    if (sub == 0) atomicAdd(&cnt[E], 1);
+                }
             }
             continue;
         }
         const float inv = 1.0f / sum;
-        if (part_c) {
+        if constexpr (COUNT) {
 #pragma unroll
             for (int i = 0; i < EPL; ++i) pacc[i] += pe[i] * inv;
             if (sub == 0) atomicAdd(&cnt[E], 1);
         }
-        // the largest that is left, topk times
-        float chosen = 0.0f;
+#pragma unroll
+        for (int i = 0; i < EPL; ++i) key[i] = key_of<DT>(key[i], expert_of<LPT, EPL, VEC>(i, sub));
+        // the largest that is left, topk times; lane k % LPT keeps choice k
+        float chosen = 0.0f, mine = 0.0f;
         for (int k = 0; k < p.topk; ++k) {
-            float bv = -INFINITY;
-            int be = 1 << 30;
+            uint32_t m = key[0];
 #pragma unroll
-            for (int i = 0; i < EPL; ++i)
-                if (z[i] > bv) {
-                    bv = z[i];
-                    be = i * LPT + sub;
-                }
+            for (int i = 1; i < EPL; ++i) m = key[i] > m ? key[i] : m;
+            const uint32_t best = group_umax<LPT>(m);
+            int be = -1;
+            if constexpr (DT == DT_F32) {
+                uint32_t at = 0;                                 // the lowest expert at the best value, as 0xFFFF - e
 #pragma unroll
-            for (int off = LPT / 2; off > 0; off >>= 1) {
-                const float ov = __shfl_xor(bv, off);
-                const int oe = __shfl_xor(be, off);
-                if (ov > bv || (ov == bv && oe < be)) {
-                    bv = ov;
-                    be = oe;
+                for (int i = 0; i < EPL; ++i) {
+                    const uint32_t v = 0xFFFFu - (uint32_t)expert_of<LPT, EPL, VEC>(i, sub);
+                    at = key[i] == best && v > at ? v : at;
                 }
+                be = 0xFFFF - (int)group_umax<LPT>(at);
+#pragma unroll
+                for (int i = 0; i < EPL; ++i)
+                    if (expert_of<LPT, EPL, VEC>(i, sub) == be) key[i] = 0;
+            } else {
+                be = 0xFFFF - (int)(best & 0xFFFFu);
+#pragma unroll
+                for (int i = 0; i < EPL; ++i)
+                    if (key[i] == best) key[i] = 0;
             }
-            const bool none = bv == -INFINITY;
-#pragma unroll
-            for (int i = 0; i < EPL; ++i)
-                if (be == i * LPT + sub) z[i] = -INFINITY;
-            const float ex = none ? 0.0f : expf(bv - top);
+            const bool none = best == 0;
+            const float ex = none ? 0.0f : expf(key_value<DT>(best) - top);
             chosen += ex;
             if (sub == k % LPT) {
                 ids[k] = none ? -1 : be;
-                w[k] = p.renorm ? ex : ex * inv;
-                if (part_c && !none) atomicAdd(&cnt[be], 1);
+                mine = ex;
+                if (p.topk > LPT) w[k] = ex;
+                if constexpr (COUNT) {
+                    if (!none) atomicAdd(&cnt[be], 1);
+                }
             }
         }
-        if (p.renorm) {
-            for (int k = sub; k < p.topk; k += LPT) w[k] = w[k] / chosen;      // each lane its own values
+        const float scale = p.renorm ? 1.0f / chosen : inv;
+        if (p.topk > LPT) {
+            for (int k = sub; k < p.topk; k += LPT) w[k] *= scale;       // each lane its own values
+        } else if (sub < p.topk) {
+            w[sub] = mine * scale;
         }
     }
-    if (!part_c) return;
-    // sum over the token groups of a wave, then over the waves
+    if constexpr (COUNT) {
+        // sums over the token groups of a wave, then over the waves
 #pragma unroll
-    for (int i = 0; i < EPL; ++i) {
-        float v = pacc[i];
+        for (int i = 0; i < EPL; ++i) {
+            float v = pacc[i];
 #pragma unroll
-        for (int off = LPT; off < 64; off <<= 1) v += __shfl_xor(v, off);
-        const int e = i * LPT + sub;
-        if ((tid & 63) < LPT && e < E) psum[tid >> 6][e] = v;
-    }
-    __syncthreads();
-    for (int e = tid; e <= E; e += kRouteThreads) {
-        part_c[(int64_t)blockIdx.x * (E + 1) + e] = cnt[e];
-        if (e < E) {
+            for (int off = LPT; off < 64; off <<= 1) v += __shfl_xor(v, off);
+            const int e = expert_of<LPT, EPL, VEC>(i, sub);
+            if ((tid & 63) < LPT && e < E) psum[tid >> 6][e] = v;
+        }
+        __syncthreads();
+        double x = 0.0;
+        long long n = 0;
+        for (int e = tid; e <= E; e += kRouteThreads) {
+            const int c = cnt[e];
             float v = 0.0f;
+            if (e < E) {
 #pragma unroll
-            for (int w = 0; w < kRouteThreads / 64; ++w) v += psum[w][e];
-            part_p[(int64_t)blockIdx.x * E + e] = v;
+                for (int w = 0; w < kRouteWaves; ++w) v += psum[w][e];
+                x += (double)c * v;
+                n += c;
+            }
+            if (gridDim.x == 1) {
+                p.counts[e] = c;
+            } else {
+                ws.c[(int64_t)blockIdx.x * (E + 1) + e] = c;
+                if (e < E) ws.p[(int64_t)blockIdx.x * E + e] = v;
+            }
+        }
+        if (gridDim.x == 1 && p.loss) {
+            block_sums<kRouteWaves>(x, n);
+            if (tid == 0) *p.loss = balance_loss(E, x, n, cnt[E]);
         }
     }
 }
 
-// Counts and loss from the blocks' partial sums, in a fixed order.
-__global__ void __launch_bounds__(1024)
-route_join_kernel(const float *__restrict__ part_p, const int32_t *__restrict__ part_c, int blocks, int E,
-                  int32_t *__restrict__ counts, float *__restrict__ loss) {
-    const int e = threadIdx.x;
-    __shared__ double num[16];
-    __shared__ long long den[16];
-    __shared__ int tokens;
+// Counts and loss from the blocks' sums, in a fixed order: each workgroup sums kJoinExperts
+// experts (kJoinRows rows of the blocks side by side), the last one to finish adds up the
+// workgroups' shares of the loss.
+__global__ void __launch_bounds__(kJoinExperts * kJoinRows)
+route_join_kernel(RouteSpace ws, int blocks, int E, int32_t *__restrict__ counts, float *__restrict__ loss) {
+    __shared__ double ps[kJoinRows][kJoinExperts + 1];
+    __shared__ int cs[kJoinRows][kJoinExperts + 1];
+    __shared__ int toks[kJoinExperts * kJoinRows / 64];
+    __shared__ bool last;
+    const int col = threadIdx.x % kJoinExperts, row = threadIdx.x / kJoinExperts;
+    const int e = blockIdx.x * kJoinExperts + col;
     int c = 0;
-    double ps = 0.0;
-    for (int b = 0; b < blocks && e < E; ++b) {
-        c += part_c[(int64_t)b * (E + 1) + e];
-        ps += part_p[(int64_t)b * E + e];
+    double s = 0.0;
+    if (e < E) {
+        for (int b = row; b < blocks; b += kJoinRows) {
+            c += ws.c[(int64_t)b * (E + 1) + e];
+            s += ws.p[(int64_t)b * E + e];
+        }
     }
-    if (e < E) counts[e] = c;
-    if (e == 0) {
-        int tv = 0;
-        for (int b = 0; b < blocks; ++b) tv += part_c[(int64_t)b * (E + 1) + E];
-        counts[E] = tv;
-        tokens = tv;
-    }
-    double x = c * ps;
-    long long n = c;
+    ps[row][col] = s;
+    cs[row][col] = c;
+    int tv = 0;
+    if (blockIdx.x == 0) {
+        for (int b = threadIdx.x; b < blocks; b += kJoinExperts * kJoinRows) tv += ws.c[(int64_t)b * (E + 1) + E];
 #pragma unroll
-    for (int off = 32; off > 0; off >>= 1) {
-        x += __shfl_xor(x, off);
-        n += __shfl_xor(n, off);
-    }
-    if ((e & 63) == 0) {
-        num[e >> 6] = x;
-        den[e >> 6] = n;
+        for (int off = 32; off > 0; off >>= 1) tv += __shfl_xor(tv, off);
+        if (lane_id() == 0) toks[threadIdx.x >> 6] = tv;
     }
     __syncthreads();
-    if (e == 0 && loss) {
-        x = 0.0;
-        n = 0;
-        for (int w = 0; w < 16; ++w) {
-            x += num[w];
-            n += den[w];
+    if (threadIdx.x < 64) {
+        double x = 0.0;
+        long long n = 0;
+        if (threadIdx.x < kJoinExperts) {
+            for (int r = 1; r < kJoinRows; ++r) {
+                s += ps[r][col];
+                c += cs[r][col];
+            }
+            if (e < E) counts[e] = c;
+            x = (double)c * s;
+            n = c;
         }
-        const double tv = tokens > 0 ? tokens : 1, cc = n > 0 ? (double)n : 1.0;
-        *loss = (float)(E * x / (cc * tv));
+#pragma unroll
+        for (int off = 32; off > 0; off >>= 1) {
+            x += __shfl_xor(x, off);
+            n += __shfl_xor(n, off);
+        }
+        if (threadIdx.x == 0) {
+            if (blockIdx.x == 0) {
+                tv = 0;
+                for (int w = 0; w < kJoinExperts * kJoinRows / 64; ++w) tv += toks[w];
+                counts[E] = tv;
+            }
+            ws.x[blockIdx.x] = x;
+            ws.n[blockIdx.x] = n;
+            __threadfence();
+            last = atomicAdd(ws.ticket, 1u) == gridDim.x - 1;
+        }
+    }
+    __syncthreads();
+    if (last && threadIdx.x == 0 && loss) {
+        __threadfence();
+        double x = 0.0;
+        long long n = 0;
+        for (unsigned b = 0; b < gridDim.x; ++b) {
+            x += __hip_atomic_load(&ws.x[b], __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+            n += __hip_atomic_load(&ws.n[b], __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+        }
+        *loss = balance_loss(E, x, n, __hip_atomic_load(&counts[E], __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT));
     }
 }
 
-template <int DT, int LPT, int EPL>
+// ---- backward -----------------------------------------------------------------
+
+template <int DT, int LPT, int EPL, bool VEC>
 __global__ void __launch_bounds__(kRouteThreads) route_backward_kernel(RouteArgs p) {
     constexpr int TPB = kRouteThreads / LPT;
     const int E = p.E, tid = threadIdx.x, sub = tid % LPT;
@@ -241,61 +428,79 @@ __global__ void __launch_bounds__(kRouteThreads) route_backward_kernel(RouteArgs
         const float f = C > 0 && tv > 0 ? (float)((double)*p.dloss / ((double)C * tv)) : 0.0f;
 #pragma unroll
         for (int i = 0; i < EPL; ++i) {
-            const int e = i * LPT + sub;
+            const int e = expert_of<LPT, EPL, VEC>(i, sub);
             if (e < E) h0[i] = f * (float)((long long)E * p.counts[e] - C);
         }
     }
     for (int64_t t = (int64_t)blockIdx.x * TPB + tid / LPT; t < p.T; t += (int64_t)gridDim.x * TPB) {
         const bool live = !p.mask || p.mask[t] != 0;
-        float z[EPL], pe[EPL], sel[EPL], top = 0.0f, sum = 1.0f;
+        uint32_t raw[EPL];
+        float pe[EPL], out[EPL], top = 0.0f, sum = 1.0f;
         int kind = ROW_EMPTY;
         if (live) {
-#pragma unroll
-            for (int i = 0; i < EPL; ++i) {
-                const int e = i * LPT + sub;
-                z[i] = e < E ? load_logit<DT>(p.logits, t * p.ld + e) : -INFINITY;
-            }
-            kind = row_softmax<LPT, EPL>(z, pe, top, sum);
+            load_row<DT, LPT, EPL, VEC>(p.logits, t * p.ld, E, sub, raw);
+            kind = row_softmax<DT, LPT, EPL>(raw, pe, top, sum);
         }
         if (kind != ROW_OK) {
             const float fill = kind == ROW_NAN ? __builtin_nanf("") : 0.0f;
 #pragma unroll
+            for (int i = 0; i < EPL; ++i) out[i] = fill;
+        } else {
+            const float inv = 1.0f / sum;
+            float sel[EPL];
+#pragma unroll
+            for (int i = 0; i < EPL; ++i) sel[i] = 0.0f;
+            if (p.dw) {
+                const int32_t *ids = p.ids + t * p.topk;
+                const float *w = p.w + t * p.topk, *dw = p.dw + t * p.topk;
+                float mean = 0.0f;
+                if (p.renorm) {
+                    for (int k = sub; k < p.topk; k += LPT) mean += ids[k] >= 0 ? w[k] * dw[k] : 0.0f;
+                    mean = group_sum<LPT>(mean);
+                }
+                for (int k = 0; k < p.topk; ++k) {
+                    const int id = ids[k];
+                    const float v = p.renorm ? w[k] * (dw[k] - mean) : dw[k];
+#pragma unroll
+                    for (int i = 0; i < EPL; ++i) sel[i] += id == expert_of<LPT, EPL, VEC>(i, sub) ? v : 0.0f;
+                }
+            }
+            float dot = 0.0f;
+#pragma unroll
+            for (int i = 0; i < EPL; ++i) {
+                pe[i] *= inv;
+                out[i] = h0[i] + (p.renorm ? 0.0f : sel[i]);
+                dot += pe[i] * out[i];
+            }
+            dot = group_sum<LPT>(dot);
+#pragma unroll
+            for (int i = 0; i < EPL; ++i) out[i] = pe[i] * (out[i] - dot) + (p.renorm ? sel[i] : 0.0f);
+        }
+        if constexpr (VEC) {
+            constexpr int W = EPL * (DT == DT_F32 ? 4 : 2) / 4;
+            uint32_t buf[W];
+#pragma unroll
+            for (int i = 0; i < W; ++i) {
+                if constexpr (DT == DT_F32) buf[i] = __float_as_uint(out[i]);
+                else buf[i] = f2h<DT>(out[2 * i]) | (uint32_t)f2h<DT>(out[2 * i + 1]) << 16;
+            }
+            if (sub * EPL < E) {
+                uint8_t *dst = static_cast<uint8_t *>(p.dlogits) + (t * p.ldd + sub * EPL) * (DT == DT_F32 ? 4 : 2);
+                if constexpr (W % 4 == 0) {
+#pragma unroll
+                    for (int v = 0; v < W / 4; ++v)
+                        *reinterpret_cast<u32x4_t *>(dst + 16 * v) =
+                            u32x4_t{buf[4 * v], buf[4 * v + 1], buf[4 * v + 2], buf[4 * v + 3]};
+                } else {
+                    *reinterpret_cast<u32x2_t *>(dst) = u32x2_t{buf[0], buf[1]};
+                }
+            }
+        } else {
+#pragma unroll
             for (int i = 0; i < EPL; ++i) {
                 const int e = i * LPT + sub;
-                if (e < E) store_logit<DT>(p.dlogits, t * p.ldd + e, fill);
+                if (e < E) store_logit<DT>(p.dlogits, t * p.ldd + e, out[i]);
             }
-            continue;
-        }
-        const float inv = 1.0f / sum;
-#pragma unroll
-        for (int i = 0; i < EPL; ++i) sel[i] = 0.0f;
-        if (p.dw) {
-            const int32_t *ids = p.ids + t * p.topk;
-            const float *w = p.w + t * p.topk, *dw = p.dw + t * p.topk;
-            float mean = 0.0f;
-            if (p.renorm)
-                for (int k = 0; k < p.topk; ++k) mean += ids[k] >= 0 ? w[k] * dw[k] : 0.0f;
-            for (int k = 0; k < p.topk; ++k) {
-                const int id = ids[k];
-                const float v = p.renorm ? w[k] * (dw[k] - mean) : dw[k];
-#pragma unroll
-                for (int i = 0; i < EPL; ++i)
-                    if (id == i * LPT + sub) sel[i] += v;
-            }
-        }
-        float dot = 0.0f;
-#pragma unroll
-        for (int i = 0; i < EPL; ++i) {
-            pe[i] *= inv;
-            z[i] = h0[i] + (p.renorm ? 0.0f : sel[i]);
-            dot += pe[i] * z[i];
-        }
-        dot = group_sum<LPT>(dot);
-#pragma unroll
-        for (int i = 0; i < EPL; ++i) {
-            const int e = i * LPT + sub;
-            const float v = pe[i] * (z[i] - dot) + (p.renorm ? sel[i] : 0.0f);
-            if (e < E) store_logit<DT>(p.dlogits, t * p.ldd + e, v);
         }
     }
 }
@@ -303,60 +508,100 @@ __global__ void __launch_bounds__(kRouteThreads) route_backward_kernel(RouteArgs
 // ---------------------------------------------------------------------------
 // Launchers
 // ---------------------------------------------------------------------------
-static int64_t route_blocks(int64_t T, int) {
-    const int64_t b = (T + 3) / 4;
-    return b < 256 ? b : 256;
+
+// Lanes and experts per lane of a token.
+struct RouteShape { int lpt, epl; };
+static RouteShape route_shape(int64_t E) {
+    if (E <= 16) return {4, 4};
+    if (E <= 32) return {4, 8};
+    if (E <= 64) return {8, 8};
+    if (E <= 128) return {8, 16};
+    if (E <= 256) return {16, 16};
+    return E <= 512 ? RouteShape{32, 16} : RouteShape{64, 16};
 }
 
-size_t route_workspace_bytes(int64_t T, int64_t E) {
-    return (size_t)route_blocks(T, (int)E) * (size_t)(2 * E + 1) * 4;
+// Blocks of a counting call: one while it has at most two rounds of tokens (a second
+// launch costs as much as a round), at most 512 (their sums are read back).
+static int64_t route_blocks(int64_t T, int64_t E) {
+    const int64_t tpb = kRouteThreads / route_shape(E).lpt;
+    if (T <= 2 * tpb) return 1;
+    const int64_t b = (T + tpb - 1) / tpb;
+    return b < 512 ? b : 512;
 }
 
-template <int DT, int EPL>
+static size_t route_space(int64_t blocks, int64_t E, void *workspace, RouteSpace *out) {
+    if (blocks == 1) return 0;
+    uint8_t *at = (uint8_t *)workspace;
+    RouteSpace r;
+    r.x = (double *)at;
+    r.n = (long long *)(r.x + kMaxJoins);
+    r.ticket = (uint32_t *)(r.n + kMaxJoins);
+    r.p = (float *)(r.ticket + 2);
+    r.c = (int32_t *)(r.p + blocks * E);
+    if (out) *out = r;
+    return (size_t)((uint8_t *)(r.c + blocks * (E + 1)) - at);
+}
+
+size_t route_workspace_bytes(int64_t T, int64_t E) { return route_space(route_blocks(T, E), E, nullptr, nullptr); }
+
+// Wide loads: rows of whole lanes on 16 bytes.
+static bool route_vec(const void *p, int64_t ld, int E, int size) {
+    return E % route_shape(E).epl == 0 && ld * size % 16 == 0 && (uintptr_t)p % 16 == 0;
+}
+
+template <int DT, int LPT, int EPL>
 static hipError_t route_launch(const RouteArgs &p, void *workspace, hipStream_t stream) {
+    constexpr int TPB = kRouteThreads / LPT;
+    const bool vec = route_vec(p.logits, p.ld, p.E, DT == DT_F32 ? 4 : 2);
+    if (!p.counts) {
+        const int64_t b = (p.T + TPB - 1) / TPB;
+        auto kern = vec ? route_kernel<DT, LPT, EPL, true, false> : route_kernel<DT, LPT, EPL, false, false>;
+        hipLaunchKernelGGL(kern, dim3((unsigned)(b < 4096 ? b : 4096)), dim3(kRouteThreads), 0, stream, p, RouteSpace{});
+        return hipGetLastError();
+    }
     const int64_t nb = route_blocks(p.T, p.E);
-    float *pp = p.counts ? (float *)workspace : nullptr;
-    int32_t *pc = p.counts ? (int32_t *)workspace + nb * p.E : nullptr;
-    if (nb > 0)
-        hipLaunchKernelGGL((route_kernel<DT, 64, EPL>), dim3((unsigned)nb), dim3(kRouteThreads), 0, stream, p, pp, pc);
-    if (p.counts)
-        hipLaunchKernelGGL(route_join_kernel, dim3(1), dim3(1024), 0, stream, pp, pc, (int)nb, p.E, p.counts, p.loss);
+    RouteSpace ws{};
+    route_space(nb, p.E, workspace, &ws);
+    auto kern = vec ? route_kernel<DT, LPT, EPL, true, true> : route_kernel<DT, LPT, EPL, false, true>;
+    hipLaunchKernelGGL(kern, dim3((unsigned)nb), dim3(kRouteThreads), 0, stream, p, ws);
+    if (nb > 1)
+        hipLaunchKernelGGL(route_join_kernel, dim3((unsigned)((p.E + kJoinExperts - 1) / kJoinExperts)),
+                           dim3(kJoinExperts * kJoinRows), 0, stream, ws, (int)nb, p.E, p.counts, p.loss);
     return hipGetLastError();
 }
 
-template <int DT, int EPL>
-static hipError_t route_backward_launch(const RouteArgs &p, hipStream_t stream) {
-    const int64_t b = (p.T + 3) / 4;
-    hipLaunchKernelGGL((route_backward_kernel<DT, 64, EPL>), dim3((unsigned)(b < 4096 ? b : 4096)), dim3(kRouteThreads),
-                       0, stream, p);
+template <int DT, int LPT, int EPL>
+static hipError_t route_backward_launch(const RouteArgs &p, void *, hipStream_t stream) {
+    constexpr int TPB = kRouteThreads / LPT, size = DT == DT_F32 ? 4 : 2;
+    const bool vec = route_vec(p.logits, p.ld, p.E, size) && route_vec(p.dlogits, p.ldd, p.E, size);
+    const int64_t b = (p.T + TPB - 1) / TPB;
+    auto kern = vec ? route_backward_kernel<DT, LPT, EPL, true> : route_backward_kernel<DT, LPT, EPL, false>;
+    hipLaunchKernelGGL(kern, dim3((unsigned)(b < 2048 ? b : 2048)), dim3(kRouteThreads), 0, stream, p);
     return hipGetLastError();
 }
 
-#define W4_ROUTE_EPL(F, ...)                    \
-    (p.E <= 64    ? F<DT, 1>(__VA_ARGS__)       \
-     : p.E <= 128 ? F<DT, 2>(__VA_ARGS__)       \
-     : p.E <= 256 ? F<DT, 4>(__VA_ARGS__)       \
-     : p.E <= 512 ? F<DT, 8>(__VA_ARGS__)       \
-                  : F<DT, 16>(__VA_ARGS__))
-
-template <int DT>
-static hipError_t route_dt(const RouteArgs &p, void *workspace, hipStream_t stream) {
-    return W4_ROUTE_EPL(route_launch, p, workspace, stream);
-}
-template <int DT>
-static hipError_t route_backward_dt(const RouteArgs &p, hipStream_t stream) {
-    return W4_ROUTE_EPL(route_backward_launch, p, stream);
+template <int DT, bool BACKWARD>
+static hipError_t route_dispatch(const RouteArgs &p, void *workspace, hipStream_t stream) {
+    const RouteShape s = route_shape(p.E);
+#define W4_ROUTE(L, P)                                                                                 \
+    if (s.lpt == L && s.epl == P)                                                                      \
+        return BACKWARD ? route_backward_launch<DT, L, P>(p, workspace, stream) : route_launch<DT, L, P>(p, workspace, stream);
+    W4_ROUTE(4, 4) W4_ROUTE(4, 8) W4_ROUTE(8, 8) W4_ROUTE(8, 16) W4_ROUTE(16, 16) W4_ROUTE(32, 16) W4_ROUTE(64, 16)
+#undef W4_ROUTE
+    return hipErrorInvalidValue;
 }
 
 hipError_t launch_route(const RouteArgs &p, int dt, void *workspace, hipStream_t stream) {
-    if (dt == DT_F32) return route_dt<DT_F32>(p, workspace, stream);
-    return dt == DT_BF16 ? route_dt<DT_BF16>(p, workspace, stream) : route_dt<DT_F16>(p, workspace, stream);
+    if (dt == DT_F32) return route_dispatch<DT_F32, false>(p, workspace, stream);
+    return dt == DT_BF16 ? route_dispatch<DT_BF16, false>(p, workspace, stream)
+                         : route_dispatch<DT_F16, false>(p, workspace, stream);
 }
 
 hipError_t launch_route_backward(const RouteArgs &p, int dt, hipStream_t stream) {
     if (p.T == 0) return hipSuccess;
-    if (dt == DT_F32) return route_backward_dt<DT_F32>(p, stream);
-    return dt == DT_BF16 ? route_backward_dt<DT_BF16>(p, stream) : route_backward_dt<DT_F16>(p, stream);
+    if (dt == DT_F32) return route_dispatch<DT_F32, true>(p, nullptr, stream);
+    return dt == DT_BF16 ? route_dispatch<DT_BF16, true>(p, nullptr, stream)
+                         : route_dispatch<DT_F16, true>(p, nullptr, stream);
 }
 
 }  // namespace w4

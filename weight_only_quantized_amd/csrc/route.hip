@@ -168,34 +168,13 @@ __device__ __forceinline__ int row_softmax(const uint32_t (&raw)[EPL], float (&p
 
 // ---- forward ------------------------------------------------------------------
 
-constexpr int kRouteThreads = 256, kRouteWaves = kRouteThreads / 64;
+constexpr int kRouteThreads = 256;         // without counts, and backward
+constexpr int kCountThreads = 1024;        // with counts: few blocks, whose sums are read back
 
 // loss = E x / (n tokens) from x = sum_e c_e P_e, n = sum_e c_e (0 without tokens)
-__device__ __forceinline__ float balance_loss(int E, double x, long long n, int tokens) {
-    const double tv = tokens > 0 ? tokens : 1, cc = n > 0 ? (double)n : 1.0;
+__device__ __forceinline__ float balance_loss(int E, double x, int n, int tokens) {
+    const double tv = tokens > 0 ? tokens : 1, cc = n > 0 ? n : 1;
     return (float)(E * x / (cc * tv));
-}
-
-// Sums of x and n over a block of NW waves, valid in thread 0.
-template <int NW>
-__device__ __forceinline__ void block_sums(double &x, long long &n) {
-    __shared__ double xs[NW];
-    __shared__ long long ns[NW];
-#pragma unroll
-    for (int off = 32; off > 0; off >>= 1) {
-        x += __shfl_xor(x, off);
-        n += __shfl_xor(n, off);
-    }
-    if (lane_id() == 0) {
-        xs[threadIdx.x >> 6] = x;
-        ns[threadIdx.x >> 6] = n;
-    }
-    __syncthreads();
-    if (threadIdx.x == 0)
-        for (int w = 1; w < NW; ++w) {
-            x += xs[w];
-            n += ns[w];
-        }
 }
 
 // Workspace: the blocks' sums of probabilities [blocks][E] and counts [blocks][E + 1], and
@@ -204,21 +183,23 @@ struct RouteSpace {
     float *p;
     int32_t *c;
     double *x;
-    long long *n;
+    int32_t *n;
     uint32_t *ticket;
 };
 constexpr int kJoinExperts = 32, kJoinRows = 32, kMaxJoins = kMoeMaxExperts / kJoinExperts;
 
 // Counts are kept where COUNT; a single block finishes by itself.
 template <int DT, int LPT, int EPL, bool VEC, bool COUNT>
-__global__ void __launch_bounds__(kRouteThreads) route_kernel(RouteArgs p, RouteSpace ws) {
-    constexpr int TPB = kRouteThreads / LPT;
+__global__ void __launch_bounds__(COUNT ? kCountThreads : kRouteThreads) route_kernel(RouteArgs p, RouteSpace ws) {
+    constexpr int NT = COUNT ? kCountThreads : kRouteThreads, NW = NT / 64, TPB = NT / LPT;
     __shared__ int cnt[COUNT ? LPT * EPL + 1 : 1];
-    __shared__ float psum[COUNT ? kRouteWaves : 1][COUNT ? LPT * EPL : 1];
+    __shared__ float psum[COUNT ? NW : 1][COUNT ? LPT * EPL : 1];
+    __shared__ float xs[NW];
+    __shared__ int ns[NW];
     const int E = p.E, tid = threadIdx.x, sub = tid % LPT;
     float pacc[COUNT ? EPL : 1];
     if constexpr (COUNT) {
-        for (int e = tid; e <= E; e += kRouteThreads) cnt[e] = 0;
+        for (int e = tid; e <= E; e += NT) cnt[e] = 0;
 #pragma unroll
         for (int i = 0; i < EPL; ++i) pacc[i] = 0.0f;
         if (blockIdx.x == 0 && tid == 0 && gridDim.x > 1) *ws.ticket = 0;
@@ -313,15 +294,15 @@ __global__ void __launch_bounds__(kRouteThreads) route_kernel(RouteArgs p, Route
             if ((tid & 63) < LPT && e < E) psum[tid >> 6][e] = v;
         }
         __syncthreads();
-        double x = 0.0;
-        long long n = 0;
-        for (int e = tid; e <= E; e += kRouteThreads) {
+        float x = 0.0f;
+        int n = 0;
+        for (int e = tid; e <= E; e += NT) {
             const int c = cnt[e];
             float v = 0.0f;
             if (e < E) {
 #pragma unroll
-                for (int w = 0; w < kRouteWaves; ++w) v += psum[w][e];
-                x += (double)c * v;
+                for (int w = 0; w < NW; ++w) v += psum[w][e];
+                x += (float)c * v;
                 n += c;
             }
             if (gridDim.x == 1) {
@@ -332,8 +313,20 @@ __global__ void __launch_bounds__(kRouteThreads) route_kernel(RouteArgs p, Route
             }
         }
         if (gridDim.x == 1 && p.loss) {
-            block_sums<kRouteWaves>(x, n);
-            if (tid == 0) *p.loss = balance_loss(E, x, n, cnt[E]);
+            x = group_sum<64>(x);
+            n = group_reduce<64>(n, [](int u, int v) { return u + v; });
+            if (lane_id() == 0) {
+                xs[tid >> 6] = x;
+                ns[tid >> 6] = n;
+            }
+            __syncthreads();
+            if (tid == 0) {
+                for (int w = 1; w < NW; ++w) {
+                    x += xs[w];
+                    n += ns[w];
+                }
+                *p.loss = balance_loss(E, x, n, cnt[E]);
+            }
         }
     }
 }
@@ -351,11 +344,24 @@ route_join_kernel(RouteSpace ws, int blocks, int E, int32_t *__restrict__ counts
     const int e = blockIdx.x * kJoinExperts + col;
     int c = 0;
     double s = 0.0;
-    if (e < E) {
-        for (int b = row; b < blocks; b += kJoinRows) {
-            c += ws.c[(int64_t)b * (E + 1) + e];
-            s += ws.p[(int64_t)b * E + e];
+    const int ec = e < E ? e : E - 1;
+    // batches of loads that are all on their way before the first is used
+    constexpr int BATCH = 8;
+    for (int b0 = row; b0 < blocks; b0 += BATCH * kJoinRows) {
+        float pv[BATCH];
+        int cv[BATCH];
+#pragma unroll
+        for (int u = 0; u < BATCH; ++u) {
+            const int64_t b = b0 + u * kJoinRows < blocks ? b0 + u * kJoinRows : blocks - 1;
+            pv[u] = ws.p[b * E + ec];
+            cv[u] = ws.c[b * (E + 1) + ec];
         }
+#pragma unroll
+        for (int u = 0; u < BATCH; ++u)
+            if (e < E && b0 + u * kJoinRows < blocks) {
+                s += pv[u];
+                c += cv[u];
+            }
     }
     ps[row][col] = s;
     cs[row][col] = c;
@@ -369,7 +375,7 @@ route_join_kernel(RouteSpace ws, int blocks, int E, int32_t *__restrict__ counts
     __syncthreads();
     if (threadIdx.x < 64) {
         double x = 0.0;
-        long long n = 0;
+        int n = 0;
         if (threadIdx.x < kJoinExperts) {
             for (int r = 1; r < kJoinRows; ++r) {
                 s += ps[r][col];
@@ -400,7 +406,7 @@ route_join_kernel(RouteSpace ws, int blocks, int E, int32_t *__restrict__ counts
     if (last && threadIdx.x == 0 && loss) {
         __threadfence();
         double x = 0.0;
-        long long n = 0;
+        int n = 0;
         for (unsigned b = 0; b < gridDim.x; ++b) {
             x += __hip_atomic_load(&ws.x[b], __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
             n += __hip_atomic_load(&ws.n[b], __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
@@ -415,32 +421,43 @@ template <int DT, int LPT, int EPL, bool VEC>
 __global__ void __launch_bounds__(kRouteThreads) route_backward_kernel(RouteArgs p) {
     constexpr int TPB = kRouteThreads / LPT;
     const int E = p.E, tid = threadIdx.x, sub = tid % LPT;
-    // the loss's part of h
+    // the first row is on its way while the loss's part of h is formed
+    int64_t t = (int64_t)blockIdx.x * TPB + tid / LPT;
+    uint32_t raw[EPL];
+    if (t < p.T) load_row<DT, LPT, EPL, VEC>(p.logits, t * p.ld, E, sub, raw);
     float h0[EPL];
 #pragma unroll
     for (int i = 0; i < EPL; ++i) h0[i] = 0.0f;
     if (p.dloss) {
-        long long C = 0;
+        int C = 0;                                           // sum of the counts: below 2^31
         for (int e = tid & 63; e < E; e += 64) C += p.counts[e];
-#pragma unroll
-        for (int off = 32; off > 0; off >>= 1) C += __shfl_xor(C, off);
+        C = group_reduce<64>(C, [](int u, int v) { return u + v; });
         const int tv = p.counts[E];
-        const float f = C > 0 && tv > 0 ? (float)((double)*p.dloss / ((double)C * tv)) : 0.0f;
+        const float f = C > 0 && tv > 0 ? *p.dloss / ((float)C * (float)tv) : 0.0f;
 #pragma unroll
         for (int i = 0; i < EPL; ++i) {
             const int e = expert_of<LPT, EPL, VEC>(i, sub);
-            if (e < E) h0[i] = f * (float)((long long)E * p.counts[e] - C);
+            if (e < E) h0[i] = f * (float)__builtin_fma((double)E, (double)p.counts[e], -(double)C);
         }
     }
-    for (int64_t t = (int64_t)blockIdx.x * TPB + tid / LPT; t < p.T; t += (int64_t)gridDim.x * TPB) {
+    for (; t < p.T; t += (int64_t)gridDim.x * TPB) {
         const bool live = !p.mask || p.mask[t] != 0;
-        uint32_t raw[EPL];
+        // lane k keeps entry k (of LPT at a time)
+        int32_t id = -1;
+        float w = 0.0f, dw = 0.0f;
+        auto entries = [&](int k0) {
+            const int k = k0 + sub;
+            const bool held = p.dw && k < p.topk;
+            id = held ? p.ids[t * p.topk + k] : -1;
+            w = held ? p.w[t * p.topk + k] : 0.0f;
+            dw = held ? p.dw[t * p.topk + k] : 0.0f;
+        };
+        entries(0);
         float pe[EPL], out[EPL], top = 0.0f, sum = 1.0f;
         int kind = ROW_EMPTY;
-        if (live) {
-            load_row<DT, LPT, EPL, VEC>(p.logits, t * p.ld, E, sub, raw);
-            kind = row_softmax<DT, LPT, EPL>(raw, pe, top, sum);
-        }
+        if (live) kind = row_softmax<DT, LPT, EPL>(raw, pe, top, sum);
+        if (t + (int64_t)gridDim.x * TPB < p.T)
+            load_row<DT, LPT, EPL, VEC>(p.logits, (t + (int64_t)gridDim.x * TPB) * p.ld, E, sub, raw);
         if (kind != ROW_OK) {
             const float fill = kind == ROW_NAN ? __builtin_nanf("") : 0.0f;
 #pragma unroll
@@ -451,18 +468,24 @@ __global__ void __launch_bounds__(kRouteThreads) route_backward_kernel(RouteArgs
 #pragma unroll
             for (int i = 0; i < EPL; ++i) sel[i] = 0.0f;
             if (p.dw) {
-                const int32_t *ids = p.ids + t * p.topk;
-                const float *w = p.w + t * p.topk, *dw = p.dw + t * p.topk;
                 float mean = 0.0f;
                 if (p.renorm) {
-                    for (int k = sub; k < p.topk; k += LPT) mean += ids[k] >= 0 ? w[k] * dw[k] : 0.0f;
+                    mean = id >= 0 ? w * dw : 0.0f;
+                    for (int k = sub + LPT; k < p.topk; k += LPT)
+                        mean += p.ids[t * p.topk + k] >= 0 ? p.w[t * p.topk + k] * p.dw[t * p.topk + k] : 0.0f;
                     mean = group_sum<LPT>(mean);
                 }
-                for (int k = 0; k < p.topk; ++k) {
-                    const int id = ids[k];
-                    const float v = p.renorm ? w[k] * (dw[k] - mean) : dw[k];
+                for (int k0 = 0; k0 < p.topk; k0 += LPT) {
+                    if (k0 > 0) entries(k0);
+                    const float v = p.renorm ? w * (dw - mean) : dw;
+                    const int most = p.topk - k0 < LPT ? p.topk - k0 : LPT;
+                    for (int k = 0; k < most; ++k) {
+                        const int kid = __shfl(id, k, LPT);
+                        const float kv = __shfl(v, k, LPT);
 #pragma unroll
-                    for (int i = 0; i < EPL; ++i) sel[i] += id == expert_of<LPT, EPL, VEC>(i, sub) ? v : 0.0f;
+                        for (int i = 0; i < EPL; ++i)
+                            sel[i] += kid == expert_of<LPT, EPL, VEC>(i, sub) ? kv : 0.0f;
+                    }
                 }
             }
             float dot = 0.0f;
@@ -521,12 +544,12 @@ static RouteShape route_shape(int64_t E) {
 }
 
 // Blocks of a counting call: one while it has at most two rounds of tokens (a second
-// launch costs as much as a round), at most 512 (their sums are read back).
+// launch costs as much as a round), at most 256 (their sums are read back).
 static int64_t route_blocks(int64_t T, int64_t E) {
-    const int64_t tpb = kRouteThreads / route_shape(E).lpt;
+    const int64_t tpb = kCountThreads / route_shape(E).lpt;
     if (T <= 2 * tpb) return 1;
     const int64_t b = (T + tpb - 1) / tpb;
-    return b < 512 ? b : 512;
+    return b < 256 ? b : 256;
 }
 
 static size_t route_space(int64_t blocks, int64_t E, void *workspace, RouteSpace *out) {
@@ -534,9 +557,9 @@ static size_t route_space(int64_t blocks, int64_t E, void *workspace, RouteSpace
     uint8_t *at = (uint8_t *)workspace;
     RouteSpace r;
     r.x = (double *)at;
-    r.n = (long long *)(r.x + kMaxJoins);
+    r.n = (int32_t *)(r.x + kMaxJoins);
     r.ticket = (uint32_t *)(r.n + kMaxJoins);
-    r.p = (float *)(r.ticket + 2);
+    r.p = (float *)(r.ticket + 4);
     r.c = (int32_t *)(r.p + blocks * E);
     if (out) *out = r;
     return (size_t)((uint8_t *)(r.c + blocks * (E + 1)) - at);
@@ -551,9 +574,9 @@ static bool route_vec(const void *p, int64_t ld, int E, int size) {
 
 template <int DT, int LPT, int EPL>
 static hipError_t route_launch(const RouteArgs &p, void *workspace, hipStream_t stream) {
-    constexpr int TPB = kRouteThreads / LPT;
     const bool vec = route_vec(p.logits, p.ld, p.E, DT == DT_F32 ? 4 : 2);
     if (!p.counts) {
+        constexpr int TPB = kRouteThreads / LPT;
         const int64_t b = (p.T + TPB - 1) / TPB;
         auto kern = vec ? route_kernel<DT, LPT, EPL, true, false> : route_kernel<DT, LPT, EPL, false, false>;
         hipLaunchKernelGGL(kern, dim3((unsigned)(b < 4096 ? b : 4096)), dim3(kRouteThreads), 0, stream, p, RouteSpace{});
@@ -563,7 +586,7 @@ static hipError_t route_launch(const RouteArgs &p, void *workspace, hipStream_t 
     RouteSpace ws{};
     route_space(nb, p.E, workspace, &ws);
     auto kern = vec ? route_kernel<DT, LPT, EPL, true, true> : route_kernel<DT, LPT, EPL, false, true>;
-    hipLaunchKernelGGL(kern, dim3((unsigned)nb), dim3(kRouteThreads), 0, stream, p, ws);
+    hipLaunchKernelGGL(kern, dim3((unsigned)nb), dim3(kCountThreads), 0, stream, p, ws);
     if (nb > 1)
         hipLaunchKernelGGL(route_join_kernel, dim3((unsigned)((p.E + kJoinExperts - 1) / kJoinExperts)),
                            dim3(kJoinExperts * kJoinRows), 0, stream, ws, (int)nb, p.E, p.counts, p.loss);

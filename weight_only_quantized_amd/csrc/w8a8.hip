@@ -643,7 +643,7 @@ template <int DT, bool GROUPED>
 static hipError_t w8a8_dispatch(const W8A8Args &p, hipStream_t stream) {
     const int64_t rows = GROUPED ? p.M / p.E : p.M;
     int cfg = g_w8a8_cfg.load(std::memory_order_relaxed);
-    if (cfg < 0 || cfg >= w8a8_config_count()) cfg = rows <= 16 ? 0 : rows <= 64 ? 2 : 4;
+    if (cfg < 0 || cfg >= w8a8_config_count()) cfg = rows <= 16 ? 0 : rows <= 64 ? 2 : rows <= 512 ? 4 : 5;
     switch (cfg) {
         case 0: return split_launch<DT, 1, 4, 2, 16, GROUPED, false>(p, stream);
         case 1: return split_launch<DT, 4, 2, 2, 8, GROUPED, false>(p, stream);

@@ -142,6 +142,17 @@ __device__ __forceinline__ float key_value(uint32_t key) {
 // -inf), or NaN (a NaN or +inf among them).
 enum { ROW_OK = 0, ROW_EMPTY = 1, ROW_NAN = 2 };
 
+// exp(x) for x <= 0: exp2 of x log2(e), whose rounding (up to |x| half steps of the
+// result) is put back as a first-order term.  Results below 2^-126 may be 0.
+__device__ __forceinline__ float exp_neg(float x) {
+    constexpr float kLog2e = 0x1.715476p+0f, kLog2eLow = 0x1.4ae0c0p-26f, kLn2 = 0x1.62e430p-1f;
+    x = fmaxf(x, -150.0f);
+    const float h = x * kLog2e;
+    const float l = __builtin_fmaf(x, kLog2eLow, __builtin_fmaf(x, kLog2e, -h));
+    const float r = __builtin_amdgcn_exp2f(h);
+    return __builtin_fmaf(r, l * kLn2, r);
+}
+
 // exp(z - max), their sum, and the row's kind.
 template <int DT, int LPT, int EPL>
 __device__ __forceinline__ int row_softmax(const uint32_t (&raw)[EPL], float (&p)[EPL], float &top, float &sum) {
@@ -159,7 +170,7 @@ __device__ __forceinline__ int row_softmax(const uint32_t (&raw)[EPL], float (&p
     float s = 0.0f;
 #pragma unroll
     for (int i = 0; i < EPL; ++i) {
-        p[i] = kind == ROW_OK ? expf(p[i] - top) : kind == ROW_NAN ? __builtin_nanf("") : 0.0f;
+        p[i] = kind == ROW_OK ? exp_neg(p[i] - top) : kind == ROW_NAN ? __builtin_nanf("") : 0.0f;
         s += p[i];
     }
     sum = group_sum<LPT>(s);
@@ -239,8 +250,10 @@ __global__ void __launch_bounds__(COUNT ? kCountThreads : kRouteThreads) route_k
         }
 #pragma unroll
         for (int i = 0; i < EPL; ++i) key[i] = key_of<DT>(key[i], expert_of<LPT, EPL, VEC>(i, sub));
-        // the largest that is left, topk times; lane k % LPT keeps choice k
+        // the largest that is left, topk times; lane k % LPT keeps choice k until LPT of them
+        // are written together
         float chosen = 0.0f, mine = 0.0f;
+        int my_id = -1;
         for (int k = 0; k < p.topk; ++k) {
             uint32_t m = key[0];
 #pragma unroll
@@ -265,23 +278,30 @@ __global__ void __launch_bounds__(COUNT ? kCountThreads : kRouteThreads) route_k
                     if (key[i] == best) key[i] = 0;
             }
             const bool none = best == 0;
-            const float ex = none ? 0.0f : expf(key_value<DT>(best) - top);
+            const float ex = none ? 0.0f : exp_neg(key_value<DT>(best) - top);
             chosen += ex;
             if (sub == k % LPT) {
-                ids[k] = none ? -1 : be;
+                my_id = none ? -1 : be;
                 mine = ex;
-                if (p.topk > LPT) w[k] = ex;
+            }
+            if (k % LPT == LPT - 1 && k + 1 < p.topk) {
+                ids[k - (LPT - 1) + sub] = my_id;
+                w[k - (LPT - 1) + sub] = mine;
                 if constexpr (COUNT) {
-                    if (!none) atomicAdd(&cnt[be], 1);
+                    if (my_id >= 0) atomicAdd(&cnt[my_id], 1);
                 }
             }
         }
         const float scale = p.renorm ? 1.0f / chosen : inv;
-        if (p.topk > LPT) {
-            for (int k = sub; k < p.topk; k += LPT) w[k] *= scale;       // each lane its own values
-        } else if (sub < p.topk) {
-            w[sub] = mine * scale;
+        const int k0 = (p.topk - 1) / LPT * LPT;
+        if (k0 + sub < p.topk) {
+            ids[k0 + sub] = my_id;
+            w[k0 + sub] = mine * scale;
+            if constexpr (COUNT) {
+                if (my_id >= 0) atomicAdd(&cnt[my_id], 1);
+            }
         }
+        for (int k = sub; k < k0; k += LPT) w[k] *= scale;               // each lane its own values
     }
     if constexpr (COUNT) {
         // sums over the token groups of a wave, then over the waves
@@ -420,7 +440,10 @@ route_join_kernel(RouteSpace ws, int blocks, int E, int32_t *__restrict__ counts
 template <int DT, int LPT, int EPL, bool VEC>
 __global__ void __launch_bounds__(kRouteThreads) route_backward_kernel(RouteArgs p) {
     constexpr int TPB = kRouteThreads / LPT;
+    // a token's gradients through its chosen weights, one place per expert
+    __shared__ __attribute__((aligned(16))) float spread[TPB][LPT * EPL];
     const int E = p.E, tid = threadIdx.x, sub = tid % LPT;
+    float *const mine = spread[tid / LPT];
     // the first row is on its way while the loss's part of h is formed
     int64_t t = (int64_t)blockIdx.x * TPB + tid / LPT;
     uint32_t raw[EPL];
@@ -475,16 +498,46 @@ __global__ void __launch_bounds__(kRouteThreads) route_backward_kernel(RouteArgs
                         mean += p.ids[t * p.topk + k] >= 0 ? p.w[t * p.topk + k] * p.dw[t * p.topk + k] : 0.0f;
                     mean = group_sum<LPT>(mean);
                 }
-                for (int k0 = 0; k0 < p.topk; k0 += LPT) {
-                    if (k0 > 0) entries(k0);
-                    const float v = p.renorm ? w * (dw - mean) : dw;
-                    const int most = p.topk - k0 < LPT ? p.topk - k0 : LPT;
-                    for (int k = 0; k < most; ++k) {
-                        const int kid = __shfl(id, k, LPT);
-                        const float kv = __shfl(v, k, LPT);
+                // Through LDS: entry k's value to its expert's place (the lanes of a token are in
+                // one wave, whose LDS accesses complete in order), unless an expert comes twice
+                // (the entry that it finds in its place is another) or topk is past the lanes.
+                const float v = p.renorm ? w * (dw - mean) : dw;
+                const bool held = id >= 0 && id < E;
+                bool twice = p.topk > LPT;
+                if (!twice) {
 #pragma unroll
-                        for (int i = 0; i < EPL; ++i)
-                            sel[i] += kid == expert_of<LPT, EPL, VEC>(i, sub) ? kv : 0.0f;
+                    for (int i = 0; i < EPL; i += 4) *reinterpret_cast<volatile f32x4_t *>(mine + sub * EPL + i) = f32x4_t{};
+                    volatile float *const place = mine + (held ? id : 0);
+                    if (held) *place = (float)sub;
+                    const bool other_entry = held && *place != (float)sub;
+                    twice = group_umax<LPT>(other_entry ? 1u : 0u) != 0;
+                    if (held) *place = v;
+                    if constexpr (VEC) {
+#pragma unroll
+                        for (int i = 0; i < EPL; i += 4) {
+                            const f32x4_t q = *reinterpret_cast<volatile f32x4_t *>(mine + sub * EPL + i);
+#pragma unroll
+                            for (int u = 0; u < 4; ++u) sel[i + u] = q[u];
+                        }
+                    } else {
+#pragma unroll
+                        for (int i = 0; i < EPL; ++i) sel[i] = *static_cast<volatile float *>(mine + i * LPT + sub);
+                    }
+                }
+                if (twice) {
+#pragma unroll
+                    for (int i = 0; i < EPL; ++i) sel[i] = 0.0f;
+                    for (int k0 = 0; k0 < p.topk; k0 += LPT) {
+                        if (k0 > 0) entries(k0);
+                        const float kept = p.renorm ? w * (dw - mean) : dw;
+                        const int most = p.topk - k0 < LPT ? p.topk - k0 : LPT;
+                        for (int k = 0; k < most; ++k) {
+                            const int kid = __shfl(id, k, LPT);
+                            const float kv = __shfl(kept, k, LPT);
+#pragma unroll
+                            for (int i = 0; i < EPL; ++i)
+                                sel[i] += kid == expert_of<LPT, EPL, VEC>(i, sub) ? kv : 0.0f;
+                        }
                     }
                 }
             }

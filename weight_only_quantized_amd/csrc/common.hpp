@@ -207,4 +207,32 @@ __device__ __forceinline__ int wave_incl_scan(int v) {
     return v;
 }
 
+// The value of a lane that differs in bit OFF of its index, for reductions that have
+// already joined the lower bits: the DPP moves 4 and 8 mirror within 8 and 16 lanes, which
+// then is the same.
+template <int OFF>
+__device__ __forceinline__ uint32_t other_lane(uint32_t v) {
+    if constexpr (OFF >= 16) {
+        return __shfl_xor(v, OFF);
+    } else {
+        constexpr int ctrl = OFF == 1 ? 0xB1 : OFF == 2 ? 0x4E : OFF == 4 ? 0x141 : 0x140;
+        return (uint32_t)__builtin_amdgcn_update_dpp(0, (int)v, ctrl, 0xF, 0xF, true);
+    }
+}
+// Reduction over aligned groups of LANES lanes, in every lane of the group.
+template <int LANES, int OFF = 1, typename T, typename F>
+__device__ __forceinline__ T lane_reduce(T v, F join) {
+    static_assert(sizeof(T) == 4, "one register");
+    if constexpr (OFF < LANES) {
+        v = join(v, __builtin_bit_cast(T, other_lane<OFF>(__builtin_bit_cast(uint32_t, v))));
+        return lane_reduce<LANES, 2 * OFF>(v, join);
+    } else {
+        return v;
+    }
+}
+template <int LANES>
+__device__ __forceinline__ uint32_t lane_umax(uint32_t v) {
+    return lane_reduce<LANES>(v, [](uint32_t a, uint32_t b) { return a > b ? a : b; });
+}
+
 }  // namespace w4

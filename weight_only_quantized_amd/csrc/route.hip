@@ -22,40 +22,13 @@ namespace w4 {
 
 enum { DT_F32 = 2 };
 
-// ---- lane exchanges ---------------------------------------------------------
-
-// The value of a lane that differs in bit OFF of its index, for reductions that have
-// already joined the lower bits: 4 and 8 mirror within 8 and 16 lanes, which then is the same.
-template <int OFF>
-__device__ __forceinline__ uint32_t other(uint32_t v) {
-    if constexpr (OFF >= 16) {
-        return __shfl_xor(v, OFF);
-    } else {
-        constexpr int ctrl = OFF == 1 ? 0xB1 : OFF == 2 ? 0x4E : OFF == 4 ? 0x141 : 0x140;
-        return (uint32_t)__builtin_amdgcn_update_dpp(0, (int)v, ctrl, 0xF, 0xF, true);
-    }
-}
-template <int LPT, int OFF = 1, typename T, typename F>
-__device__ __forceinline__ T group_reduce(T v, F join) {
-    static_assert(sizeof(T) == 4, "one register");
-    if constexpr (OFF < LPT) {
-        v = join(v, __builtin_bit_cast(T, other<OFF>(__builtin_bit_cast(uint32_t, v))));
-        return group_reduce<LPT, 2 * OFF>(v, join);
-    } else {
-        return v;
-    }
-}
 template <int LPT>
 __device__ __forceinline__ float group_sum(float v) {
-    return group_reduce<LPT>(v, [](float a, float b) { return a + b; });
+    return lane_reduce<LPT>(v, [](float a, float b) { return a + b; });
 }
 template <int LPT>
 __device__ __forceinline__ float group_max(float v) {
-    return group_reduce<LPT>(v, [](float a, float b) { return fmaxf(a, b); });
-}
-template <int LPT>
-__device__ __forceinline__ uint32_t group_umax(uint32_t v) {
-    return group_reduce<LPT>(v, [](uint32_t a, uint32_t b) { return a > b ? a : b; });
+    return lane_reduce<LPT>(v, [](float a, float b) { return fmaxf(a, b); });
 }
 
 // ---- logits -----------------------------------------------------------------
@@ -165,7 +138,7 @@ __device__ __forceinline__ int row_softmax(const uint32_t (&raw)[EPL], float (&p
         nan |= p[i] != p[i];
     }
     top = group_max<LPT>(m);
-    const bool any_nan = group_umax<LPT>(nan ? 1u : 0u) != 0;
+    const bool any_nan = lane_umax<LPT>(nan ? 1u : 0u) != 0;
     const int kind = any_nan || top == INFINITY ? ROW_NAN : top == -INFINITY ? ROW_EMPTY : ROW_OK;
     float s = 0.0f;
 #pragma unroll
@@ -258,7 +231,7 @@ __global__ void __launch_bounds__(COUNT ? kCountThreads : kRouteThreads) route_k
             uint32_t m = key[0];
 #pragma unroll
             for (int i = 1; i < EPL; ++i) m = key[i] > m ? key[i] : m;
-            const uint32_t best = group_umax<LPT>(m);
+            const uint32_t best = lane_umax<LPT>(m);
             int be = -1;
             if constexpr (DT == DT_F32) {
                 uint32_t at = 0;                                 // the lowest expert at the best value, as 0xFFFF - e
@@ -267,7 +240,7 @@ __global__ void __launch_bounds__(COUNT ? kCountThreads : kRouteThreads) route_k
                     const uint32_t v = 0xFFFFu - (uint32_t)expert_of<LPT, EPL, VEC>(i, sub);
                     at = key[i] == best && v > at ? v : at;
                 }
-                be = 0xFFFF - (int)group_umax<LPT>(at);
+                be = 0xFFFF - (int)lane_umax<LPT>(at);
 #pragma unroll
                 for (int i = 0; i < EPL; ++i)
                     if (expert_of<LPT, EPL, VEC>(i, sub) == be) key[i] = 0;
@@ -334,7 +307,7 @@ __global__ void __launch_bounds__(COUNT ? kCountThreads : kRouteThreads) route_k
         }
         if (gridDim.x == 1 && p.loss) {
             x = group_sum<64>(x);
-            n = group_reduce<64>(n, [](int u, int v) { return u + v; });
+            n = lane_reduce<64>(n, [](int u, int v) { return u + v; });
             if (lane_id() == 0) {
                 xs[tid >> 6] = x;
                 ns[tid >> 6] = n;
@@ -454,7 +427,7 @@ __global__ void __launch_bounds__(kRouteThreads) route_backward_kernel(RouteArgs
     if (p.dloss) {
         int C = 0;                                           // sum of the counts: below 2^31
         for (int e = tid & 63; e < E; e += 64) C += p.counts[e];
-        C = group_reduce<64>(C, [](int u, int v) { return u + v; });
+        C = lane_reduce<64>(C, [](int u, int v) { return u + v; });
         const int tv = p.counts[E];
         const float f = C > 0 && tv > 0 ? *p.dloss / ((float)C * (float)tv) : 0.0f;
 #pragma unroll
@@ -510,7 +483,7 @@ __global__ void __launch_bounds__(kRouteThreads) route_backward_kernel(RouteArgs
                     volatile float *const place = mine + (held ? id : 0);
                     if (held) *place = (float)sub;
                     const bool other_entry = held && *place != (float)sub;
-                    twice = group_umax<LPT>(other_entry ? 1u : 0u) != 0;
+                    twice = lane_umax<LPT>(other_entry ? 1u : 0u) != 0;
                     if (held) *place = v;
                     if constexpr (VEC) {
 #pragma unroll

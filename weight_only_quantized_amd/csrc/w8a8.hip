@@ -28,91 +28,134 @@ typedef uint32_t u32x2s_t __attribute__((__vector_size__(2 * sizeof(uint32_t))))
 // Quantization of rows
 // ---------------------------------------------------------------------------
 
-// Scale of a row from its largest magnitude: NaN if the row holds a NaN or an
-// infinity (amax is then either, see row_amax).
-__device__ __forceinline__ float row_scale(float amax) {
+// Largest magnitude of 8 values as bits (magnitudes compare as integers, a NaN's
+// above infinity's), joined with what came before: two 16-bit maxima.
+typedef unsigned short u16x2_t __attribute__((ext_vector_type(2)));
+__device__ __forceinline__ void join_top(uint32_t &top, const u32x4_t &v) {
+    u16x2_t t = as<u16x2_t>(top);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) t = __builtin_elementwise_max(t, as<u16x2_t>(v[i] & 0x7FFF7FFFu));
+    top = __builtin_bit_cast(uint32_t, t);
+}
+__device__ __forceinline__ uint32_t larger_half(uint32_t top) {
+    const uint32_t a = top & 0xFFFFu, b = top >> 16;
+    return a > b ? a : b;
+}
+
+// Scale of a row from the bits of its largest magnitude; NaN if the row holds a NaN or an
+// infinity.
+template <int DT>
+__device__ __forceinline__ float row_scale(uint32_t top) {
+    const float amax = h2f<DT>((uint16_t)top);
     return amax < INFINITY ? amax / 127.0f : __builtin_nanf("");
 }
 
-// rne(x / s), exactly, for x of a 16-bit type, |x| <= 127 s (1 + 2^-23):
-// t = x (1 / s) is within 2^-15 of the quotient, so rint(t) is off by at most
-// one, and only where the quotient lies next to a border k + 1/2.  The
-// remainder x - q s is exact in fp32 (x and s / 2 are multiples of one unit that
-// |x - q s| <= s exceeds at most 2^24 times), so comparing it with s / 2 decides;
-// ties go to the even code.  Rows of tiny values are scaled by 2^64
-// (both x and s, exactly), which keeps s, 1 / s and s / 2 normal numbers.
+// rne(x / s) for x of a 16-bit type with |x| <= 127 s (1 + 2^-23), exactly.
+//
+// Nearly always: t = x (1 / s) is within 2^-17 of the quotient; adding 3 2^22 rounds it to
+// an integer q, held in the sum's low bits, and t - q, below 1/2 - 2^-16, says that
+// the quotient's nearest integer is the same.
+// Next to a border k + 1/2 (exact()): the remainder x - q s is exact in fp32 wherever it
+// is below s (x and s / 2 are multiples of one unit, at most 2^24 of which make s), so
+// comparing it with s / 2 decides; ties go to the even code.  Rows of tiny
+// values come here too and are scaled by 2^64 (both x and s, exactly), which keeps s, 1 / s and
+// s / 2 normal numbers.
 struct RowQuant {
-    float up, s, inv, half;       // multiplier of x, scaled s, its reciprocal, s / 2
-    __device__ __forceinline__ explicit RowQuant(float scale) {
-        up = scale < 0x1p-60f ? 0x1p64f : 1.0f;
-        s = scale * up;
-        const bool none = !(s > 0.0f);           // zero or NaN: every code is 0
-        inv = none ? 0.0f : 1.0f / s;
-        half = none ? INFINITY : 0.5f * s;
-        if (none) { s = 0.0f; up = 0.0f; }
+    float scale, inv, limit;
+    __device__ __forceinline__ explicit RowQuant(float s) : scale(s) {
+        const bool plain = s >= 0x1p-60f;                     // not zero, tiny or NaN
+        inv = plain ? 1.0f / s : 0.0f;
+        limit = plain ? 0.5f - 0x1p-16f : -1.0f;
     }
-    __device__ __forceinline__ int code(float x) const {
-        const float v = x * up;
-        float q = __builtin_rintf(v * inv);
+    __device__ __forceinline__ int exact(float x) const {
+        const float up = scale < 0x1p-60f ? 0x1p64f : 1.0f, s = scale * up;
+        if (!(s > 0.0f)) return 0;
+        const float half = 0.5f * s, v = x * up;
+        float q = __builtin_rintf(v * (1.0f / s));
         const float r = __builtin_fmaf(-q, s, v);
         const bool odd = ((int)q & 1) != 0;
         if (r > half || (r == half && odd)) q += 1.0f;
         if (r < -half || (r == -half && odd)) q -= 1.0f;
-        const int c = (int)q;
-        return c > 127 ? 127 : c < -127 ? -127 : c;
+        return q > 127.0f ? 127 : q < -127.0f ? -127 : (int)q;
     }
 };
 
-// max |x| where a NaN anywhere gives NaN: magnitudes compare as integers, NaN
-// patterns above infinity's.
+// Codes of 8 values.
 template <int DT>
-__device__ __forceinline__ uint32_t mag_bits(uint32_t h) { return h & 0x7FFFu; }
-template <int DT>
-__device__ __forceinline__ float mag_value(uint32_t m) { return h2f<DT>((uint16_t)m); }
-
-template <int DT>
-__global__ void __launch_bounds__(256)
-w8a8_quantize_kernel(const uint16_t *__restrict__ x, int64_t ldx, const int32_t *__restrict__ row_count,
-                     uint8_t *__restrict__ qx, float *__restrict__ sx, int64_t K) {
-    const int64_t m = blockIdx.x;
-    if (row_count && m >= *row_count) return;
-    const uint16_t *row = x + m * ldx;
-    uint32_t top = 0;
-    for (int64_t k = (int64_t)threadIdx.x * 8; k < K; k += 256 * 8) {
-        const u32x4_t v = ld128(row + k);
+__device__ __forceinline__ u32x2s_t codes_of(const u32x4_t &v, const RowQuant &rq) {
+    constexpr float kRound = 12582912.0f;                    // 3 2^22
+    uint32_t m[8];
+    float far = 0.0f;
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            const uint32_t w = v[i];
-            const uint32_t a = mag_bits<DT>(w), b = mag_bits<DT>(w >> 16);
-            top = a > top ? a : top;
-            top = b > top ? b : top;
-        }
+    for (int i = 0; i < 8; ++i) {
+        const uint32_t w = v[i >> 1];
+        const float x = h2f<DT>((uint16_t)(w >> (16 * (i & 1))));
+        const float sum = __builtin_fmaf(x, rq.inv, kRound);
+        far = fmaxf(far, __builtin_fabsf(__builtin_fmaf(x, rq.inv, kRound - sum)));
+        m[i] = __float_as_uint(sum);
     }
-    __shared__ uint32_t tops[4];
-#pragma unroll
-    for (int off = 32; off > 0; off >>= 1) {
-        const uint32_t o = __shfl_xor(top, off);
-        top = o > top ? o : top;
-    }
-    if (lane_id() == 0) tops[threadIdx.x >> 6] = top;
-    __syncthreads();
-#pragma unroll
-    for (int w = 0; w < 4; ++w) top = tops[w] > top ? tops[w] : top;
-    const float scale = row_scale(mag_value<DT>(top));
-    const RowQuant rq(scale);
-    for (int64_t k = (int64_t)threadIdx.x * 8; k < K; k += 256 * 8) {
-        const u32x4_t v = ld128(row + k);
-        uint32_t out[2] = {0, 0};
+    if (!(far <= rq.limit)) {
 #pragma unroll
         for (int i = 0; i < 8; ++i) {
             const uint32_t w = v[i >> 1];
-            // codes of a row without a scale stay 0 (0 * inf would be NaN)
-            const int c = scale > 0.0f ? rq.code(h2f<DT>((uint16_t)(w >> (16 * (i & 1))))) : 0;
-            out[i >> 2] |= ((uint32_t)c & 0xFFu) << (8 * (i & 3));
+            m[i] = (uint32_t)rq.exact(h2f<DT>((uint16_t)(w >> (16 * (i & 1)))));
         }
-        *reinterpret_cast<u32x2s_t *>(qx + m * K + k) = u32x2s_t{out[0], out[1]};
     }
-    if (threadIdx.x == 0) sx[m] = scale;
+    u32x2s_t out;
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+        const uint32_t a = __builtin_amdgcn_perm(m[4 * i + 1], m[4 * i], 0x0C0C0400u);
+        const uint32_t b = __builtin_amdgcn_perm(m[4 * i + 3], m[4 * i + 2], 0x0C0C0400u);
+        out[i] = a | b << 16;
+    }
+    return out;
+}
+
+// Quantization kernel: NW waves per row (workgroups of at least four waves), C pieces of 8
+// values per lane in registers between the maximum and the codes.  Bound by memory:
+// 3 bytes per element.
+template <int DT, int NW, int C>
+__global__ void __launch_bounds__(NW > 4 ? NW * 64 : 256)
+w8a8_quantize_kernel(const uint16_t *__restrict__ x, int64_t ldx, const int32_t *__restrict__ row_count,
+                     uint8_t *__restrict__ qx, float *__restrict__ sx, int64_t M, int64_t K) {
+    constexpr int RPB = NW >= 4 ? 1 : 4 / NW, NT = NW * 64;
+    __shared__ uint32_t tops[2][NW >= 4 ? NW : 1];
+    if (row_count) {
+        const int64_t n = *row_count;
+        M = n < M ? n : M;
+    }
+    const int wave = threadIdx.x >> 6, at = NW >= 4 ? threadIdx.x : lane_id();
+    int turn = 0;
+    for (int64_t m = (int64_t)blockIdx.x * RPB + (NW >= 4 ? 0 : wave); m < M; m += (int64_t)gridDim.x * RPB, turn ^= 1) {
+        const uint16_t *row = x + m * ldx;
+        uint32_t top = 0;
+        u32x4_t v[C];
+#pragma unroll
+        for (int i = 0; i < C; ++i) {
+            const int64_t k = ((int64_t)i * NT + at) * 8;
+            v[i] = k < K ? ld128(row + k) : u32x4_t{0, 0, 0, 0};
+        }
+#pragma unroll
+        for (int i = 0; i < C; ++i) join_top(top, v[i]);
+        for (int64_t k = ((int64_t)C * NT + at) * 8; k < K; k += NT * 8) join_top(top, ld128(row + k));
+        top = lane_umax<64>(larger_half(top));
+        if constexpr (NW >= 4) {
+            if (lane_id() == 0) tops[turn][wave] = top;
+            __syncthreads();
+#pragma unroll
+            for (int w = 0; w < NW; ++w) top = tops[turn][w] > top ? tops[turn][w] : top;
+        }
+        const float scale = row_scale<DT>(top);
+        const RowQuant rq(scale);
+#pragma unroll
+        for (int i = 0; i < C; ++i) {
+            const int64_t k = ((int64_t)i * NT + at) * 8;
+            if (k < K) *reinterpret_cast<u32x2s_t *>(qx + m * K + k) = codes_of<DT>(v[i], rq);
+        }
+        for (int64_t k = ((int64_t)C * NT + at) * 8; k < K; k += NT * 8)
+            *reinterpret_cast<u32x2s_t *>(qx + m * K + k) = codes_of<DT>(ld128(row + k), rq);
+        if (at == 0) sx[m] = scale;
+    }
 }
 
 // ---------------------------------------------------------------------------
@@ -170,41 +213,6 @@ __device__ __forceinline__ bool expert_tile(const int32_t *__restrict__ offsets,
 // rows into LDS while the first weights are on their way.
 // ---------------------------------------------------------------------------
 constexpr int kFusedBytes = 64 * 1024;           // codes of a fused call's rows (row stride K + 16)
-
-// max over the wave's lanes
-__device__ __forceinline__ uint32_t wave_max(uint32_t v) {
-#pragma unroll
-    for (int off = 32; off > 0; off >>= 1) {
-        const uint32_t o = __shfl_xor(v, off);
-        v = o > v ? o : v;
-    }
-    return v;
-}
-
-template <int DT>
-__device__ __forceinline__ uint32_t top_of(const u32x4_t &v) {
-    uint32_t top = 0;
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-        const uint32_t w = v[i], a = mag_bits<DT>(w), b = mag_bits<DT>(w >> 16);
-        top = a > top ? a : top;
-        top = b > top ? b : top;
-    }
-    return top;
-}
-
-template <int DT>
-__device__ __forceinline__ u32x2s_t codes_of(const u32x4_t &v, const RowQuant &rq, float scale) {
-    uint32_t out[2] = {0, 0};
-#pragma unroll
-    for (int i = 0; i < 8; ++i) {
-        const uint32_t w = v[i >> 1];
-        // codes of a row without a scale stay 0 (0 * inf would be NaN)
-        const int c = scale > 0.0f ? rq.code(h2f<DT>((uint16_t)(w >> (16 * (i & 1))))) : 0;
-        out[i >> 2] |= ((uint32_t)c & 0xFFu) << (8 * (i & 3));
-    }
-    return u32x2s_t{out[0], out[1]};
-}
 
 template <int DT, int MT, int NB, int D, int WMAX, bool GROUPED, bool FUSED>
 __global__ void __launch_bounds__(WMAX * 64)
@@ -268,20 +276,51 @@ w8a8_split_kernel(W8A8Args p, unsigned mtiles, unsigned ncb) {
         const int pieces = (int)((K + 511) / 512), total = pieces * rows;
         for (int r = threadIdx.x; r < rows; r += W * 64) tops[r] = 0;
         __syncthreads();
-        for (int i = wave; i < total; i += W) {
-            const int r = i / pieces, k = (i % pieces) * 512 + lane * 8;
-            uint32_t top = k < K ? top_of<DT>(ld128(p.x + (row0 + r) * p.ldx + k)) : 0;
-            top = wave_max(top);
+        // the first kHeld pieces of a wave stay in registers between maximum and codes
+        constexpr int kHeld = 4;
+        u32x4_t held[kHeld];
+        auto piece = [&](int i, int &r, int &k) {
+            r = i / pieces;
+            k = (i - r * pieces) * 512 + lane * 8;
+        };
+        auto fetch = [&](int r, int k) { return ld128(p.x + (row0 + r) * p.ldx + k); };
+        auto join = [&](int r, const u32x4_t &v) {
+            uint32_t top = 0;
+            join_top(top, v);
+            top = lane_umax<64>(larger_half(top));
             if (lane == 0) atomicMax(&tops[r], top);
+        };
+        auto store = [&](int r, int k, const u32x4_t &v) {
+            if (k < K) *reinterpret_cast<u32x2s_t *>(lds + r * stride + k) = codes_of<DT>(v, RowQuant(row_scale<DT>(tops[r])));
+        };
+#pragma unroll
+        for (int u = 0; u < kHeld; ++u) {
+            int r, k;
+            piece(wave + u * W, r, k);
+            held[u] = wave + u * W < total && k < K ? fetch(r, k) : u32x4_t{0, 0, 0, 0};
+        }
+#pragma unroll
+        for (int u = 0; u < kHeld; ++u) {
+            int r, k;
+            piece(wave + u * W, r, k);
+            if (wave + u * W < total) join(r, held[u]);
+        }
+        for (int i = wave + kHeld * W; i < total; i += W) {
+            int r, k;
+            piece(i, r, k);
+            join(r, k < K ? fetch(r, k) : u32x4_t{0, 0, 0, 0});
         }
         __syncthreads();
-        for (int i = wave; i < total; i += W) {
-            const int r = i / pieces, k = (i % pieces) * 512 + lane * 8;
-            const float scale = row_scale(mag_value<DT>(tops[r]));
-            if (k < K) {
-                const u32x2s_t q = codes_of<DT>(ld128(p.x + (row0 + r) * p.ldx + k), RowQuant(scale), scale);
-                *reinterpret_cast<u32x2s_t *>(lds + r * stride + k) = q;
-            }
+#pragma unroll
+        for (int u = 0; u < kHeld; ++u) {
+            int r, k;
+            piece(wave + u * W, r, k);
+            if (wave + u * W < total) store(r, k, held[u]);
+        }
+        for (int i = wave + kHeld * W; i < total; i += W) {
+            int r, k;
+            piece(i, r, k);
+            store(r, k, k < K ? fetch(r, k) : u32x4_t{0, 0, 0, 0});
         }
         __syncthreads();
     } else {
@@ -337,7 +376,7 @@ w8a8_split_kernel(W8A8Args p, unsigned mtiles, unsigned ncb) {
         const int b = o / MT, t = o % MT;
         const int64_t r = row0 + 16 * t + j;
         if (r < row_end) {
-            const Split rs(FUSED ? row_scale(mag_value<DT>(tops[FUSED ? 16 * t + j : 0])) : p.sx[src_row(r)]);
+            const Split rs(FUSED ? row_scale<DT>(tops[FUSED ? 16 * t + j : 0]) : p.sx[src_row(r)]);
             const int64_t n = n0 + 16 * b + 4 * c;
             uint16_t h[4];
 #pragma unroll
@@ -596,17 +635,32 @@ w8a8_tile_kernel(const uint8_t *__restrict__ qx, const float *__restrict__ sx, c
 // ---------------------------------------------------------------------------
 // Launchers
 // ---------------------------------------------------------------------------
+template <int DT, int NW, int C>
+static hipError_t quantize_launch(const void *x, int64_t ldx, const int32_t *row_count, void *qx, float *sx, int64_t M,
+                                  int64_t K, hipStream_t stream) {
+    constexpr int RPB = NW >= 4 ? 1 : 4 / NW;
+    const int64_t blocks = (M + RPB - 1) / RPB;
+    hipLaunchKernelGGL((w8a8_quantize_kernel<DT, NW, C>), dim3((unsigned)(blocks < 65536 ? blocks : 65536)),
+                       dim3(NW > 4 ? NW * 64 : 256), 0, stream, (const uint16_t *)x, ldx, row_count, (uint8_t *)qx, sx, M,
+                       K);
+    return hipGetLastError();
+}
+
+template <int DT>
+static hipError_t quantize_dispatch(const void *x, int64_t ldx, const int32_t *row_count, void *qx, float *sx, int64_t M,
+                                    int64_t K, hipStream_t stream) {
+    if (K <= 1024) return quantize_launch<DT, 1, 2>(x, ldx, row_count, qx, sx, M, K, stream);
+    if (K <= 2048) return quantize_launch<DT, 1, 4>(x, ldx, row_count, qx, sx, M, K, stream);
+    if (K <= 4096) return quantize_launch<DT, 4, 2>(x, ldx, row_count, qx, sx, M, K, stream);
+    if (K <= 8192) return quantize_launch<DT, 4, 4>(x, ldx, row_count, qx, sx, M, K, stream);
+    return quantize_launch<DT, 16, 2>(x, ldx, row_count, qx, sx, M, K, stream);
+}
+
 hipError_t launch_w8a8_quantize(const void *x, int64_t ldx, const int32_t *row_count, void *qx, float *sx, int64_t M,
                                 int64_t K, int dt, hipStream_t stream) {
     if (M == 0) return hipSuccess;
-    const dim3 grid((unsigned)M);
-    if (dt == DT_BF16)
-        hipLaunchKernelGGL(w8a8_quantize_kernel<DT_BF16>, grid, dim3(256), 0, stream, (const uint16_t *)x, ldx, row_count,
-                           (uint8_t *)qx, sx, K);
-    else
-        hipLaunchKernelGGL(w8a8_quantize_kernel<DT_F16>, grid, dim3(256), 0, stream, (const uint16_t *)x, ldx, row_count,
-                           (uint8_t *)qx, sx, K);
-    return hipGetLastError();
+    return dt == DT_BF16 ? quantize_dispatch<DT_BF16>(x, ldx, row_count, qx, sx, M, K, stream)
+                         : quantize_dispatch<DT_F16>(x, ldx, row_count, qx, sx, M, K, stream);
 }
 
 template <int DT, int MT, int NB, int D, int WMAX, bool GROUPED, bool FUSED>

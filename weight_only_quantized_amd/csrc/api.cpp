@@ -543,12 +543,35 @@ w4a16_status check_w8a8(int64_t M, int64_t K, int64_t N) {
     return rows_ok(M) ? W4A16_OK : W4A16_ERR_SHAPE;
 }
 
-// Workspace: the codes, then the scales.
+// Workspace: the codes, the scales, then room for the sums of K slices where a
+// product may be cut into them.
 size_t w8a8_sx_offset(int64_t M, int64_t K) { return ((size_t)M * (size_t)K + 255) & ~(size_t)255; }
+size_t w8a8_part_offset(int64_t M, int64_t K) { return (w8a8_sx_offset(M, K) + 4 * (size_t)M + 255) & ~(size_t)255; }
 
-size_t w8a8_bytes(int64_t M, int64_t K) {
+size_t w8a8_bytes(int64_t M, int64_t K, bool slices) {
     if (check_w8a8(M, K, 64) != W4A16_OK || M == 0) return 0;
+    if (slices && M <= w4::kW8A8SliceRows) return w8a8_part_offset(M, K) + w4::kW8A8PartBytes;
     return w8a8_sx_offset(M, K) + 4 * (size_t)M;
+}
+
+// Product of codes; part: room for the sums of slices, or NULL.
+w4a16_status w8a8_product(const void *qx, const float *sx, const void *w_packed, const float *sw, const void *bias,
+                          void *y, int64_t ldy, int64_t M, int64_t K, int64_t N, int dt, void *part, void *stream) {
+    w4::W8A8Args p{};
+    p.qx = (const uint8_t *)qx;
+    p.sx = sx;
+    p.X = p.M = M;
+    p.wp = (const uint8_t *)w_packed;
+    p.sw = sw;
+    p.bias = (const uint16_t *)bias;
+    p.y = (uint16_t *)y;
+    p.ldy = ldy;
+    p.K = K;
+    p.N = N;
+    p.E = 1;
+    p.part = (int32_t *)part;
+    p.slices = 1;
+    return map_err(w4::launch_w8a8(p, dt, (hipStream_t)stream));
 }
 
 w4a16_status check_router(int64_t T, int64_t E, int64_t topk, int dt) {
@@ -591,22 +614,10 @@ w4a16_status w8a8_gemm_prequant(const void *qx, const float *sx, const void *w_p
         !aligned(bias, 2))
         return W4A16_ERR_ALIGN;
     if (current_device_ok() != 1) return W4A16_ERR_DEVICE;
-    w4::W8A8Args p{};
-    p.qx = (const uint8_t *)qx;
-    p.sx = sx;
-    p.X = p.M = M;
-    p.wp = (const uint8_t *)w_packed;
-    p.sw = sw;
-    p.bias = (const uint16_t *)bias;
-    p.y = (uint16_t *)y;
-    p.ldy = ldy;
-    p.K = K;
-    p.N = N;
-    p.E = 1;
-    return map_err(w4::launch_w8a8(p, dt, (hipStream_t)stream));
+    return w8a8_product(qx, sx, w_packed, sw, bias, y, ldy, M, K, N, dt, nullptr, stream);
 }
 
-size_t w8a8_workspace_bytes(int64_t M, int64_t K) { return w8a8_bytes(M, K); }
+size_t w8a8_workspace_bytes(int64_t M, int64_t K) { return w8a8_bytes(M, K, true); }
 
 w4a16_status w8a8_gemm(const void *x, int64_t ldx, const void *w_packed, const float *sw, const void *bias, void *y,
                        int64_t ldy, int64_t M, int64_t K, int64_t N, int dt, void *workspace, size_t workspace_bytes,
@@ -616,12 +627,12 @@ w4a16_status w8a8_gemm(const void *x, int64_t ldx, const void *w_packed, const f
     if (st != W4A16_OK || (st = check_ld(&ldx, K)) != W4A16_OK || (st = check_ld(&ldy, N)) != W4A16_OK) return st;
     if (M == 0) return W4A16_OK;
     if (!x || !w_packed || !sw || !y) return W4A16_ERR_NULL;
-    if (!workspace || workspace_bytes < w8a8_bytes(M, K)) return W4A16_ERR_WORKSPACE;
+    if (!workspace || workspace_bytes < w8a8_bytes(M, K, true)) return W4A16_ERR_WORKSPACE;
     if (!aligned(x, 16) || !aligned(workspace, 16) || !aligned(w_packed, 16) || !aligned(y, 16) || !aligned(sw, 4) ||
         !aligned(bias, 2))
         return W4A16_ERR_ALIGN;
+    if (current_device_ok() != 1) return W4A16_ERR_DEVICE;
     if (w4::w8a8_fused_ok(M, K)) {
-        if (current_device_ok() != 1) return W4A16_ERR_DEVICE;
         w4::W8A8Args p{};
         p.x = (const uint16_t *)x;
         p.ldx = ldx;
@@ -638,12 +649,13 @@ w4a16_status w8a8_gemm(const void *x, int64_t ldx, const void *w_packed, const f
     }
     uint8_t *qx = (uint8_t *)workspace;
     float *sx = (float *)(qx + w8a8_sx_offset(M, K));
-    st = w8a8_quantize(x, ldx, nullptr, qx, sx, M, K, dt, stream);
+    st = map_err(w4::launch_w8a8_quantize(x, ldx, nullptr, qx, sx, M, K, dt, (hipStream_t)stream));
     if (st != W4A16_OK) return st;
-    return w8a8_gemm_prequant(qx, sx, w_packed, sw, bias, y, ldy, M, K, N, dt, stream);
+    return w8a8_product(qx, sx, w_packed, sw, bias, y, ldy, M, K, N, dt,
+                        M <= w4::kW8A8SliceRows ? qx + w8a8_part_offset(M, K) : nullptr, stream);
 }
 
-size_t w8a8_grouped_workspace_bytes(int64_t R, int64_t K) { return w8a8_bytes(R, K); }
+size_t w8a8_grouped_workspace_bytes(int64_t R, int64_t K) { return w8a8_bytes(R, K, false); }
 
 w4a16_status w8a8_grouped_gemm(const void *x, const int32_t *sorted_ids, int64_t topk, const int32_t *expert_offsets,
                                const void *w_packed, const float *sw, void *y, int64_t E, int64_t R, int64_t K,
@@ -655,7 +667,7 @@ w4a16_status w8a8_grouped_gemm(const void *x, const int32_t *sorted_ids, int64_t
     if (sorted_ids && (topk < 1 || topk > INT32_MAX || R % topk != 0)) return W4A16_ERR_SHAPE;
     if (R == 0) return W4A16_OK;
     if (!x || !expert_offsets || !w_packed || !sw || !y) return W4A16_ERR_NULL;
-    if (!workspace || workspace_bytes < w8a8_bytes(R, K)) return W4A16_ERR_WORKSPACE;
+    if (!workspace || workspace_bytes < w8a8_bytes(R, K, false)) return W4A16_ERR_WORKSPACE;
     if (!aligned(x, 16) || !aligned(workspace, 16) || !aligned(w_packed, 16) || !aligned(y, 16) || !aligned(sw, 4) ||
         !aligned(expert_offsets, 4) || !aligned(sorted_ids, 4))
         return W4A16_ERR_ALIGN;
@@ -676,6 +688,7 @@ w4a16_status w8a8_grouped_gemm(const void *x, const int32_t *sorted_ids, int64_t
     p.topk = sorted_ids ? (int)topk : 1;
     p.wp = (const uint8_t *)w_packed;
     p.sw = sw;
+    p.slices = 1;
     p.y = (uint16_t *)y;
     p.ldy = N;
     p.M = R;

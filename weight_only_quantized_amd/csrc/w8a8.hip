@@ -212,7 +212,8 @@ __device__ __forceinline__ bool expert_tile(const int32_t *__restrict__ offsets,
 // in flight in registers.  FUSED: x comes in 16 bits, and the workgroup quantizes its
 // rows into LDS while the first weights are on their way.
 // ---------------------------------------------------------------------------
-constexpr int kFusedBytes = 64 * 1024;           // codes of a fused call's rows (row stride K + 16)
+constexpr int kHeld = 2;                         // pieces of 512 elements that a wave of a fused call quantizes
+constexpr int kFusedBytes = 16 * (kHeld * 512 + 16);    // their codes, at most 16 rows of K + 16 bytes
 
 template <int DT, int MT, int NB, int D, int WMAX, bool GROUPED, bool FUSED>
 __global__ void __launch_bounds__(WMAX * 64)
@@ -266,64 +267,44 @@ w8a8_split_kernel(W8A8Args p, unsigned mtiles, unsigned ncb) {
                 for (int h = 0; h < 2; ++h) xf[d][t][h] = ld128(xp[t] + (int64_t)g * kGroup + 16 * h);
         }
     };
-#pragma unroll
-    for (int d = 0; d < D; ++d) load_w(d, g0 + d);
-
     const int rows = (int)(row_end - row0 < 16 * MT ? row_end - row0 : 16 * MT);
     const int stride = (int)K + 16;
     if constexpr (FUSED) {
-        // pieces of 512 elements of a row, round robin over the waves
+        // Pieces of 512 elements of a row, round robin over the waves, at most kHeld each.  They are
+        // requested before the weights: loads return in order.
         const int pieces = (int)((K + 511) / 512), total = pieces * rows;
+        u32x4_t held[kHeld];
+        int pr[kHeld], pk[kHeld];
+#pragma unroll
+        for (int u = 0; u < kHeld; ++u) {
+            const int i = wave + u * W;
+            pr[u] = i / pieces;
+            pk[u] = (i - pr[u] * pieces) * 512 + lane * 8;
+            if (i >= total || pk[u] >= K) pr[u] = -1;
+            held[u] = pr[u] >= 0 ? ld128(p.x + (row0 + pr[u]) * p.ldx + pk[u]) : u32x4_t{0, 0, 0, 0};
+        }
+#pragma unroll
+        for (int d = 0; d < D; ++d) load_w(d, g0 + d);
         for (int r = threadIdx.x; r < rows; r += W * 64) tops[r] = 0;
         __syncthreads();
-        // the first kHeld pieces of a wave stay in registers between maximum and codes
-        constexpr int kHeld = 4;
-        u32x4_t held[kHeld];
-        auto piece = [&](int i, int &r, int &k) {
-            r = i / pieces;
-            k = (i - r * pieces) * 512 + lane * 8;
-        };
-        auto fetch = [&](int r, int k) { return ld128(p.x + (row0 + r) * p.ldx + k); };
-        auto join = [&](int r, const u32x4_t &v) {
+#pragma unroll
+        for (int u = 0; u < kHeld; ++u) {
+            if (wave + u * W >= total) break;
             uint32_t top = 0;
-            join_top(top, v);
+            join_top(top, held[u]);
             top = lane_umax<64>(larger_half(top));
-            if (lane == 0) atomicMax(&tops[r], top);
-        };
-        auto store = [&](int r, int k, const u32x4_t &v) {
-            if (k < K) *reinterpret_cast<u32x2s_t *>(lds + r * stride + k) = codes_of<DT>(v, RowQuant(row_scale<DT>(tops[r])));
-        };
-#pragma unroll
-        for (int u = 0; u < kHeld; ++u) {
-            int r, k;
-            piece(wave + u * W, r, k);
-            held[u] = wave + u * W < total && k < K ? fetch(r, k) : u32x4_t{0, 0, 0, 0};
-        }
-#pragma unroll
-        for (int u = 0; u < kHeld; ++u) {
-            int r, k;
-            piece(wave + u * W, r, k);
-            if (wave + u * W < total) join(r, held[u]);
-        }
-        for (int i = wave + kHeld * W; i < total; i += W) {
-            int r, k;
-            piece(i, r, k);
-            join(r, k < K ? fetch(r, k) : u32x4_t{0, 0, 0, 0});
+            if (lane == 0) atomicMax(&tops[pr[u]], top);       // lane 0 of a piece is inside its row
         }
         __syncthreads();
 #pragma unroll
-        for (int u = 0; u < kHeld; ++u) {
-            int r, k;
-            piece(wave + u * W, r, k);
-            if (wave + u * W < total) store(r, k, held[u]);
-        }
-        for (int i = wave + kHeld * W; i < total; i += W) {
-            int r, k;
-            piece(i, r, k);
-            store(r, k, k < K ? fetch(r, k) : u32x4_t{0, 0, 0, 0});
-        }
+        for (int u = 0; u < kHeld; ++u)
+            if (pr[u] >= 0)
+                *reinterpret_cast<u32x2s_t *>(lds + pr[u] * stride + pk[u]) =
+                    codes_of<DT>(held[u], RowQuant(row_scale<DT>(tops[pr[u]])));
         __syncthreads();
     } else {
+#pragma unroll
+        for (int d = 0; d < D; ++d) load_w(d, g0 + d);
 #pragma unroll
         for (int t = 0; t < MT; ++t) xp[t] = p.qx + src_row(row0 + 16 * t + j) * K + 32 * c;
 #pragma unroll
@@ -413,12 +394,9 @@ __device__ __forceinline__ void wait_and_meet() {
     asm volatile("s_waitcnt vmcnt(%0) lgkmcnt(0)\n\ts_barrier" ::"n"(N) : "memory");
 }
 
-template <int DT, int BM, int BN, int WM, int WN, bool GROUPED, bool AHEAD>
+template <int DT, int BM, int BN, int WM, int WN, bool GROUPED>
 __global__ void __launch_bounds__(WM * WN * 64)
-w8a8_tile_kernel(const uint8_t *__restrict__ qx, const float *__restrict__ sx, const int32_t *__restrict__ offsets,
-                 const int32_t *__restrict__ sorted, int topk, const uint8_t *__restrict__ wp,
-                 const float *__restrict__ sw, const uint16_t *__restrict__ bias, uint16_t *__restrict__ y, int64_t ldy,
-                 int64_t M, int64_t X, int64_t K, int64_t N, int E, unsigned mtiles, unsigned ncb, unsigned per_xcd) {
+w8a8_tile_kernel(W8A8Args p, unsigned mtiles, unsigned ncb, unsigned per_xcd) {
     constexpr int NW = WM * WN, TM = BM / WM, TN = BN / WN, RT = TM / 16, CT = TN / 16;
     constexpr int ABYTES = BM * kStageK, BBYTES = BN * kStageK, SBYTES = ABYTES + BBYTES;
     constexpr int AL = BM / 16 / NW, BL = BN / 16 / NW;      // DMA loads per wave and stage
@@ -428,26 +406,31 @@ w8a8_tile_kernel(const uint8_t *__restrict__ qx, const float *__restrict__ sx, c
     const int lane = lane_id();
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const int wm = wave / WN, wn = wave % WN;
-    const int S = (int)(K / kStageK);
+    const int64_t K = p.K, N = p.N;
     // XCD x takes a contiguous range of the tiles, which run through bands of kBand row
-    // tiles column by column: the tiles at work on an XCD share x and W in its L2
-    const unsigned id = (blockIdx.x % kXcd8) * per_xcd + blockIdx.x / kXcd8, bsize = kBand * ncb;
+    // tiles column by column: the tiles at work on an XCD share x and W in its L2.  The slices of a
+    // tile follow each other on one XCD.
+    const unsigned slot = (blockIdx.x % kXcd8) * per_xcd + blockIdx.x / kXcd8;
+    const unsigned id = slot / p.slices, slice = slot % p.slices, bsize = kBand * ncb;
     const unsigned band = id / bsize, in = id % bsize;
     if (band * kBand >= mtiles) return;
     const unsigned high = mtiles - band * kBand < kBand ? mtiles - band * kBand : kBand;
     if (in >= high * ncb) return;             // behind the last tile
     const int64_t tile = band * kBand + in % high, n0 = (int64_t)(in / high) * BN;
     int e = 0;
-    int64_t row0 = tile * BM, row_end = M;
+    int64_t row0 = tile * BM, row_end = p.M;
     if constexpr (GROUPED) {
-        if (!expert_tile(offsets, E, M, BM, tile, e, row0, row_end)) return;
+        if (!expert_tile(p.offsets, p.E, p.M, BM, tile, e, row0, row_end)) return;
     }
+    // this slice's stages: at least two
+    const int all = (int)(K / kStageK);
+    const int first = (int)((int64_t)all * slice / p.slices), S = (int)((int64_t)all * (slice + 1) / p.slices) - first;
     auto src_row = [&](int64_t r) -> int64_t {
         if (r >= row_end) r = row_end - 1;
         if constexpr (GROUPED) {
-            if (sorted) {
-                const int64_t t = (int64_t)((uint32_t)sorted[r] / (uint32_t)topk);
-                return t < X ? t : X - 1;
+            if (p.sorted) {
+                const int64_t t = (int64_t)((uint32_t)p.sorted[r] / (uint32_t)p.topk);
+                return t < p.X ? t : p.X - 1;
             }
         }
         return r;
@@ -460,13 +443,15 @@ w8a8_tile_kernel(const uint8_t *__restrict__ qx, const float *__restrict__ sx, c
     // quads on the same banks), 256 bytes each: with these orders the 16 lanes of a
     // pass touch each bank once (4.06 clocks a read; orders for 8 neighbouring lanes 6.5 and 8.0).
     uint32_t aoffs[AL], boffs[BL];
-    const uint8_t *abase = qx, *bbase = wp + ((int64_t)e * (N / 16) + n0 / 16) * (K / kGroup) * kW8Tile;
-    if (!sorted) abase += row0 * K;          // gathered rows: X K < 2^32
+    const bool gather = GROUPED && p.sorted;
+    const uint8_t *abase = p.qx + (int64_t)first * kStageK;
+    const uint8_t *bbase = p.wp + ((int64_t)e * (N / 16) + n0 / 16) * (K / kGroup) * kW8Tile + (int64_t)first * 1024;
+    if (!gather) abase += row0 * K;          // gathered rows: X K < 2^32
 #pragma unroll
     for (int i = 0; i < AL; ++i) {
         const int r = lane >> 2, c = (lane & 3) ^ (-(r >> 2) & 3);
         const int64_t m = src_row(row0 + (wave + NW * i) * 16 + r);
-        aoffs[i] = (uint32_t)((sorted ? m : m - row0) * K) + 16 * c;
+        aoffs[i] = (uint32_t)((gather ? m : m - row0) * K) + 16 * c;
     }
 #pragma unroll
     for (int i = 0; i < BL; ++i) {
@@ -485,7 +470,7 @@ w8a8_tile_kernel(const uint8_t *__restrict__ qx, const float *__restrict__ sx, c
         bbase += 1024;
     };
 #pragma unroll
-    for (int s = 0; s < (AHEAD ? kStages : kStages - 1); ++s)
+    for (int s = 0; s < kStages - 1; ++s)
         if (s < S) fetch(s);
 
     // LDS offsets of this lane's operands
@@ -502,111 +487,95 @@ w8a8_tile_kernel(const uint8_t *__restrict__ qx, const float *__restrict__ sx, c
 #pragma unroll
         for (int ct = 0; ct < CT; ++ct) acc[rt][ct] = i32x4_t{0, 0, 0, 0};
 
-    u32x4_t xf[AHEAD ? 2 : 1][RT], wf[AHEAD ? 2 : 1][CT];
-    auto read = [&](int s, u32x4_t (&xd)[RT], u32x4_t (&wd)[CT]) {
+    u32x4_t xf[RT], wf[CT];
+    auto read = [&](int s) {
         const uint8_t *base = lds + ((unsigned)s % kStages) * SBYTES;
 #pragma unroll
         for (int ct = 0; ct < CT; ++ct)
-            wd[ct] = *reinterpret_cast<const u32x4_t *>(base + (boff ^ ((ct & 1) * 128)) + (ct >> 1) * 2048);
+            wf[ct] = *reinterpret_cast<const u32x4_t *>(base + (boff ^ ((ct & 1) * 128)) + (ct >> 1) * 2048);
 #pragma unroll
-        for (int rt = 0; rt < RT; ++rt) xd[rt] = *reinterpret_cast<const u32x4_t *>(base + aoff + rt * 16 * kStageK);
-    };
-    auto multiply = [&](const u32x4_t (&xd)[RT], const u32x4_t (&wd)[CT]) {
+        for (int rt = 0; rt < RT; ++rt) xf[rt] = *reinterpret_cast<const u32x4_t *>(base + aoff + rt * 16 * kStageK);
 #pragma unroll
         for (int ct = 0; ct < CT; ++ct) {
-            const i32x4_t w = __builtin_bit_cast(i32x4_t, !AHEAD && NW == 8 ? wd[ct] : wd[ct] ^ 0x80808080u);
+            wf[ct] ^= 0x80808080u;                     // u = q + 128 to two's complement q
+            asm volatile("" : "+v"(wf[ct]));
+        }
+    };
+    auto multiply = [&]() {
+        __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+        for (int ct = 0; ct < CT; ++ct)
 #pragma unroll
             for (int rt = 0; rt < RT; ++rt)
-                acc[rt][ct] = __builtin_amdgcn_mfma_i32_16x16x64_i8(w, __builtin_bit_cast(i32x4_t, xd[rt]), acc[rt][ct], 0, 0, 0);
-        }
+                acc[rt][ct] = __builtin_amdgcn_mfma_i32_16x16x64_i8(__builtin_bit_cast(i32x4_t, wf[ct]),
+                                                                    __builtin_bit_cast(i32x4_t, xf[rt]), acc[rt][ct], 0, 0, 0);
+        __builtin_amdgcn_sched_barrier(0);
     };
     constexpr int L = AL + BL;
-    // Stage 0 first; from then on the operands of stage s + 1 are read while stage s
-    // is multiplied: WAIT loads may be outstanding once stage s + 1 has landed (and stage s
-    // is in everybody's registers, so that its place can be filled again).
-    auto stage = [&](int s, auto wait, auto refill, u32x4_t (&xc)[RT], u32x4_t (&wc)[CT], u32x4_t (&xn)[RT],
-                     u32x4_t (&wnx)[CT]) {
-        constexpr int WAIT = decltype(wait)::value;
-        if constexpr (WAIT >= 0) {
-            wait_and_meet<WAIT>();
-            if constexpr (decltype(refill)::value) fetch(s + kStages);
-            read(s + 1, xn, wnx);
-        }
-        __builtin_amdgcn_sched_barrier(0);
-        multiply(xc, wc);
-        __builtin_amdgcn_sched_barrier(0);
-    };
     using std::integral_constant;
     using Yes = integral_constant<bool, true>;
     using No = integral_constant<bool, false>;
-    if constexpr (AHEAD) {
-        if (S > 2) {
-            wait_and_meet<3 * L>();
-            read(0, xf[0], wf[0]);
-            int s = 0;
-            for (; s + kStages < S; s += 2) {
-                stage(s, integral_constant<int, 2 * L>{}, Yes{}, xf[0], wf[0], xf[1], wf[1]);
-                stage(s + 1, integral_constant<int, 2 * L>{}, Yes{}, xf[1], wf[1], xf[0], wf[0]);
-            }
-            stage(s, integral_constant<int, 2 * L>{}, No{}, xf[0], wf[0], xf[1], wf[1]);
-            stage(s + 1, integral_constant<int, L>{}, No{}, xf[1], wf[1], xf[0], wf[0]);
-        } else {
-            wait_and_meet<L>();
-            read(0, xf[0], wf[0]);
-        }
-        stage(S - 2, integral_constant<int, 0>{}, No{}, xf[0], wf[0], xf[1], wf[1]);
-        stage(S - 1, integral_constant<int, -1>{}, No{}, xf[1], wf[1], xf[0], wf[0]);
-    } else if constexpr (NW == 8) {
-        // Two groups of waves, one of each on every SIMD, take turns: while one multiplies
-        // stage s, the other reads its operands.  A phase ends in a barrier; group 0
-        // reads stage s in phase 2 s and multiplies it in phase 2 s + 1, group 1 one phase
-        // later.  Stage s has landed by the end of phase 2 s - 1 (WAIT: later loads that
-        // may be outstanding); its place is filled again from phase 2 s + 2 on.
-        auto turn = [&](int s, auto wait, auto refill) {
-            constexpr int WAIT = decltype(wait)::value;
+    // One stage; WAIT later loads may be outstanding at its wait.
+    //
+    // Four waves: stage s has landed and stage s - 1 is in everybody's registers at the one
+    // barrier, and the place of stage s - 1 is filled again; a second workgroup on the compute
+    // unit fills the gaps.
+    //
+    // Eight waves: two groups, one wave of each on every SIMD, take turns: while one multiplies
+    // stage s, the other reads its operands.  A phase ends in a barrier; group 0
+    // reads stage s in phase 2 s and multiplies it in phase 2 s + 1, group 1 one phase
+    // later.  Stage s has landed by the end of phase 2 s - 1; its place is filled again
+    // from phase 2 s + 2 on.
+    auto turn = [&](int s, auto wait, auto refill) {
+        constexpr int WAIT = decltype(wait)::value;
+        if constexpr (NW == 8) {
             if constexpr (decltype(refill)::value) fetch(s + kStages - 1);
-            read(s, xf[0], wf[0]);
-#pragma unroll
-            for (int ct = 0; ct < CT; ++ct) {
-                wf[0][ct] ^= 0x80808080u;
-                asm volatile("" : "+v"(wf[0][ct]));
-            }
+            read(s);
             wait_and_meet<WAIT>();
-            __builtin_amdgcn_sched_barrier(0);
-            multiply(xf[0], wf[0]);
-            __builtin_amdgcn_sched_barrier(0);
+            multiply();
             wait_and_meet<63>();
-        };
+        } else {
+            wait_and_meet<WAIT>();
+            if constexpr (decltype(refill)::value) fetch(s + kStages - 1);
+            read(s);
+            multiply();
+        }
+    };
+    constexpr int EARLY = NW == 8 ? 1 : 0;      // eight waves wait for stage s + 1 in stage s
+    if constexpr (NW == 8) {
         if (S > 2) wait_and_meet<2 * L>();
         else wait_and_meet<L>();
         if (wave >= 4) wait_and_meet<63>();
-        int s = 0;
-        for (; s + kStages <= S; ++s) turn(s, integral_constant<int, 2 * L>{}, Yes{});
-        if (S > 2) turn(S - 3, integral_constant<int, L>{}, No{});
-        turn(S - 2, integral_constant<int, 0>{}, No{});
-        turn(S - 1, integral_constant<int, 0>{}, No{});
+    }
+    int s = 0;
+    for (; s + kStages <= S; ++s) turn(s, integral_constant<int, 2 * L>{}, Yes{});
+    if (S > 2) turn(S - 3, integral_constant<int, (2 - EARLY) * L>{}, No{});
+    turn(S - 2, integral_constant<int, (1 - EARLY) * L>{}, No{});
+    turn(S - 1, integral_constant<int, 0>{}, No{});
+    if constexpr (NW == 8) {
         if (wave < 4) wait_and_meet<63>();
-    } else {
-        // stage s has landed, and stage s - 1 is in everybody's registers: its place is filled again
-        auto plain = [&](int s, auto wait, auto refill) {
-            wait_and_meet<decltype(wait)::value>();
-            if constexpr (decltype(refill)::value) fetch(s + kStages - 1);
-            read(s, xf[0], wf[0]);
-            multiply(xf[0], wf[0]);
-        };
-        int s = 0;
-        for (; s + kStages <= S; ++s) plain(s, integral_constant<int, 2 * L>{}, Yes{});
-        if (S > 2) plain(S - 3, integral_constant<int, 2 * L>{}, No{});
-        plain(S - 2, integral_constant<int, L>{}, No{});
-        plain(S - 1, integral_constant<int, 0>{}, No{});
     }
 
+    if (p.slices > 1) {
+        // the slices' sums meet in w8a8_join_kernel
+        int *part = p.part + (int64_t)slice * p.M * N;
+#pragma unroll
+        for (int rt = 0; rt < RT; ++rt) {
+            const int64_t r = row0 + wm * TM + rt * 16 + i16;
+#pragma unroll
+            for (int ct = 0; ct < CT; ++ct) {
+                const int64_t n = n0 + wn * TN + 32 * (ct >> 1) + 8 * q + 4 * (ct & 1);
+                if (r < row_end && n < N) *reinterpret_cast<i32x4_t *>(part + r * N + n) = acc[rt][ct];
+            }
+        }
+        return;
+    }
     int64_t rows[RT];
     Split rs[RT] = {};
 #pragma unroll
     for (int rt = 0; rt < RT; ++rt) {
         rows[rt] = row0 + wm * TM + rt * 16 + i16;
-        rs[rt] = Split(sx[src_row(rows[rt])]);
+        rs[rt] = Split(p.sx[src_row(rows[rt])]);
     }
 #pragma unroll
     for (int cc = 0; cc < CT / 2; ++cc) {
@@ -616,8 +585,8 @@ w8a8_tile_kernel(const uint8_t *__restrict__ qx, const float *__restrict__ sx, c
         float bv[8];
 #pragma unroll
         for (int i = 0; i < 8; ++i) {
-            cs[i] = Split(sw[(int64_t)e * N + n + i]);
-            bv[i] = bias ? h2f<DT>(bias[n + i]) : 0.0f;
+            cs[i] = Split(p.sw[(int64_t)e * N + n + i]);
+            bv[i] = p.bias ? h2f<DT>(p.bias[n + i]) : 0.0f;
         }
 #pragma unroll
         for (int rt = 0; rt < RT; ++rt) {
@@ -625,10 +594,38 @@ w8a8_tile_kernel(const uint8_t *__restrict__ qx, const float *__restrict__ sx, c
 #pragma unroll
             for (int i = 0; i < 8; ++i) h[i] = f2h<DT>(finish(acc[rt][2 * cc + (i >> 2)][i & 3], rs[rt], cs[i], bv[i]));
             if (rows[rt] < row_end)
-                *reinterpret_cast<u32x4_t *>(y + rows[rt] * ldy + n) =
+                *reinterpret_cast<u32x4_t *>(p.y + rows[rt] * p.ldy + n) =
                     u32x4_t{h[0] | (uint32_t)h[1] << 16, h[2] | (uint32_t)h[3] << 16, h[4] | (uint32_t)h[5] << 16,
                             h[6] | (uint32_t)h[7] << 16};
         }
+    }
+}
+
+
+// y from the slices' sums; 4 columns per lane.
+template <int DT>
+__global__ void __launch_bounds__(256) w8a8_join_kernel(W8A8Args p) {
+    const int64_t quads = p.N / 4, total = p.M * quads;
+    for (int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x; i < total; i += (int64_t)gridDim.x * 256) {
+        const int64_t r = i / quads, n = (i % quads) * 4;
+        const int *part = p.part + r * p.N + n;
+        i32x4_t sum = {0, 0, 0, 0}, next[4];
+        for (int s0 = 0; s0 < p.slices; s0 += 4) {
+#pragma unroll
+            for (int u = 0; u < 4; ++u)
+                next[u] = *reinterpret_cast<const i32x4_t *>(part + (int64_t)(s0 + u < p.slices ? s0 + u : 0) * p.M * p.N);
+#pragma unroll
+            for (int u = 0; u < 4; ++u)
+                if (s0 + u < p.slices) sum += next[u];
+        }
+        const Split rs(p.sx[r]);
+        uint16_t h[4];
+#pragma unroll
+        for (int u = 0; u < 4; ++u) {
+            const float bv = p.bias ? h2f<DT>(p.bias[n + u]) : 0.0f;
+            h[u] = f2h<DT>(finish(sum[u], rs, Split(p.sw[n + u]), bv));
+        }
+        *reinterpret_cast<u32x2s_t *>(p.y + r * p.ldy + n) = u32x2s_t{h[0] | (uint32_t)h[1] << 16, h[2] | (uint32_t)h[3] << 16};
     }
 }
 
@@ -676,67 +673,73 @@ static hipError_t split_launch(const W8A8Args &p, hipStream_t stream) {
     return hipGetLastError();
 }
 
-template <int DT, int BM, int BN, int WM, int WN, bool GROUPED, bool AHEAD>
+template <int DT, int BM, int BN, int WM, int WN, bool GROUPED>
 static hipError_t tile8_launch(const W8A8Args &p, hipStream_t stream) {
     const int64_t ncb = (p.N + BN - 1) / BN;
     const int64_t few = p.M < p.E ? p.M : p.E;
     const int64_t mtiles = GROUPED ? p.M / BM + few : (p.M + BM - 1) / BM;
-    const int64_t per_xcd = (mtiles * ncb + kXcd8 - 1) / kXcd8;
-    if (per_xcd * kXcd8 > INT32_MAX) return hipErrorInvalidConfiguration;
-    hipLaunchKernelGGL((w8a8_tile_kernel<DT, BM, BN, WM, WN, GROUPED, AHEAD>), dim3((unsigned)(per_xcd * kXcd8)),
-                       dim3(WM * WN * 64), 0, stream, p.qx, p.sx, p.offsets, p.sorted, p.topk, p.wp, p.sw, p.bias, p.y,
-                       p.ldy, p.M, p.X, p.K, p.N, p.E, (unsigned)mtiles, (unsigned)ncb, (unsigned)per_xcd);
+    const int64_t per_xcd = (mtiles * ncb * p.slices + kXcd8 - 1) / kXcd8;
+    if (per_xcd * kXcd8 > INT32_MAX || p.slices < 1 || p.K / kStageK / p.slices < 2) return hipErrorInvalidConfiguration;
+    if (p.slices > 1 && (GROUPED || !p.part || p.slices * p.M * p.N * 4 > kW8A8PartBytes)) return hipErrorInvalidConfiguration;
+    hipLaunchKernelGGL((w8a8_tile_kernel<DT, BM, BN, WM, WN, GROUPED>), dim3((unsigned)(per_xcd * kXcd8)),
+                       dim3(WM * WN * 64), 0, stream, p, (unsigned)mtiles, (unsigned)ncb, (unsigned)per_xcd);
+    const hipError_t err = hipGetLastError();
+    if (err != hipSuccess || p.slices == 1) return err;
+    const int64_t blocks = (p.M * (p.N / 4) + 255) / 256;
+    hipLaunchKernelGGL(w8a8_join_kernel<DT>, dim3((unsigned)(blocks < 4096 ? blocks : 4096)), dim3(256), 0, stream, p);
     return hipGetLastError();
 }
+
+// Column blocks of 16 per workgroup of the split-K kernel: as many as leave about a
+// workgroup per compute unit.
+static int split_columns(int64_t N) { return N >= 64 * 192 ? 4 : N >= 32 * 192 ? 2 : 1; }
 
 // Test hook: the kernel of the next calls (-1: by size).
 static std::atomic<int> g_w8a8_cfg{-1};
 void set_w8a8_config(int idx) { g_w8a8_cfg.store(idx, std::memory_order_relaxed); }
 
 template <int DT, bool GROUPED>
-static hipError_t w8a8_dispatch(const W8A8Args &p, hipStream_t stream) {
-    const int64_t rows = GROUPED ? p.M / p.E : p.M;
+static hipError_t w8a8_dispatch(const W8A8Args &args, hipStream_t stream) {
+    const int64_t rows = GROUPED ? args.M / args.E : args.M;
     int cfg = g_w8a8_cfg.load(std::memory_order_relaxed);
-    if (cfg < 0 || cfg >= w8a8_config_count()) cfg = rows <= 16 ? 0 : rows <= 64 ? 2 : rows <= 512 ? 4 : 5;
-    switch (cfg) {
-        case 0: return split_launch<DT, 1, 4, 2, 16, GROUPED, false>(p, stream);
-        case 1: return split_launch<DT, 4, 2, 2, 8, GROUPED, false>(p, stream);
-        case 2: return tile8_launch<DT, 64, 128, 2, 2, GROUPED, true>(p, stream);
-        case 3: return tile8_launch<DT, 64, 128, 2, 2, GROUPED, false>(p, stream);
-        case 4: return tile8_launch<DT, 128, 128, 2, 2, GROUPED, false>(p, stream);
-        case 5: return tile8_launch<DT, 256, 256, 2, 4, GROUPED, false>(p, stream);
-        case 6: return tile8_launch<DT, 256, 128, 4, 2, GROUPED, true>(p, stream);
-        case 7: return tile8_launch<DT, 256, 128, 4, 2, GROUPED, false>(p, stream);
-        case 8: return tile8_launch<DT, 256, 256, 4, 2, GROUPED, false>(p, stream);
-        case 9: return split_launch<DT, 1, 4, 1, 16, GROUPED, false>(p, stream);
-        case 10: return split_launch<DT, 1, 2, 2, 16, GROUPED, false>(p, stream);
-        case 11: return split_launch<DT, 1, 2, 4, 16, GROUPED, false>(p, stream);
-        case 12: return split_launch<DT, 1, 4, 2, 8, GROUPED, false>(p, stream);
-        case 13: return split_launch<DT, 1, 4, 4, 8, GROUPED, false>(p, stream);
-        case 14: return split_launch<DT, 1, 1, 4, 16, GROUPED, false>(p, stream);
-        case 15: return split_launch<DT, 2, 4, 2, 8, GROUPED, false>(p, stream);
-        case 16: return split_launch<DT, 2, 2, 2, 16, GROUPED, false>(p, stream);
-        case 17: return split_launch<DT, 2, 2, 4, 8, GROUPED, false>(p, stream);
-        case 18: return split_launch<DT, 4, 4, 1, 8, GROUPED, false>(p, stream);
-        case 19: return split_launch<DT, 4, 2, 1, 16, GROUPED, false>(p, stream);
-        case 20: return split_launch<DT, 8, 2, 1, 8, GROUPED, false>(p, stream);
-        default: return split_launch<DT, 4, 1, 2, 16, GROUPED, false>(p, stream);
+    if (cfg < 0 || cfg % 100 >= w8a8_config_count()) cfg = rows <= 16 ? 0 : rows <= 32 ? 1 : rows <= 64 ? 7 : rows <= 512 ? 8 : 13;
+    W8A8Args p = args;
+    p.slices = cfg >= 100 && p.part ? cfg / 100 : 1;
+    switch (cfg % 100) {
+        case 0:
+            switch (split_columns(p.N)) {
+                case 4: return split_launch<DT, 1, 4, 2, 16, GROUPED, false>(p, stream);
+                case 2: return split_launch<DT, 1, 2, 2, 16, GROUPED, false>(p, stream);
+                default: return split_launch<DT, 1, 1, 4, 16, GROUPED, false>(p, stream);
+            }
+        case 1: return split_launch<DT, 2, 4, 2, 8, GROUPED, false>(p, stream);
+        case 2: return split_launch<DT, 2, 2, 2, 8, GROUPED, false>(p, stream);
+        case 3: return split_launch<DT, 2, 1, 4, 16, GROUPED, false>(p, stream);
+        case 4: return split_launch<DT, 4, 4, 1, 8, GROUPED, false>(p, stream);
+        case 5: return split_launch<DT, 4, 2, 2, 8, GROUPED, false>(p, stream);
+        case 6: return tile8_launch<DT, 64, 64, 2, 2, GROUPED>(p, stream);
+        case 7: return tile8_launch<DT, 64, 128, 2, 2, GROUPED>(p, stream);
+        case 8: return tile8_launch<DT, 128, 128, 2, 2, GROUPED>(p, stream);
+        case 9: return tile8_launch<DT, 128, 256, 2, 4, GROUPED>(p, stream);
+        case 10: return tile8_launch<DT, 256, 128, 4, 2, GROUPED>(p, stream);
+        case 11: return tile8_launch<DT, 128, 128, 2, 4, GROUPED>(p, stream);
+        case 12: return tile8_launch<DT, 64, 256, 1, 4, GROUPED>(p, stream);
+        default: return tile8_launch<DT, 256, 256, 2, 4, GROUPED>(p, stream);
     }
 }
-int w8a8_config_count() { return 22; }
+int w8a8_config_count() { return 14; }
 
-bool w8a8_fused_ok(int64_t M, int64_t K) { return M <= 16 && M * (K + 16) <= kFusedBytes; }
+bool w8a8_fused_ok(int64_t M, int64_t K) {
+    const int64_t W = K / kGroup < 16 ? K / kGroup : 16;
+    return M <= 16 && M * ((K + 511) / 512) <= kHeld * W;
+}
 
 template <int DT>
 static hipError_t w8a8_fused_dispatch(const W8A8Args &p, hipStream_t stream) {
-    switch (g_w8a8_cfg.load(std::memory_order_relaxed)) {
-        case 9: return split_launch<DT, 1, 4, 1, 16, false, true>(p, stream);
-        case 10: return split_launch<DT, 1, 2, 2, 16, false, true>(p, stream);
-        case 11: return split_launch<DT, 1, 2, 4, 16, false, true>(p, stream);
-        case 12: return split_launch<DT, 1, 4, 2, 8, false, true>(p, stream);
-        case 13: return split_launch<DT, 1, 4, 4, 8, false, true>(p, stream);
-        case 14: return split_launch<DT, 1, 1, 4, 16, false, true>(p, stream);
-        default: return split_launch<DT, 1, 4, 2, 16, false, true>(p, stream);
+    switch (split_columns(p.N)) {
+        case 4: return split_launch<DT, 1, 4, 2, 16, false, true>(p, stream);
+        case 2: return split_launch<DT, 1, 2, 2, 16, false, true>(p, stream);
+        default: return split_launch<DT, 1, 1, 4, 16, false, true>(p, stream);
     }
 }
 

@@ -110,8 +110,9 @@ int w4a16_test_linear_plan(int shape, int slices);
 
 /*
  * Select the kernel of the W8A8 products (dense and grouped) for subsequent
- * calls: idx in [0, count), or -1 for the choice by size.  Not thread-safe; tests
- * and tuning only.  Returns the number of configurations.
+ * calls: idx in [0, count), plus 100 n for n slices of K where the kernel takes and the
+ * workspace holds them, or -1 for the choice by size.  Not thread-safe; tests
+ * and tuning only.  Returns the number of kernels.
  */
 int w4a16_test_w8a8_config(int idx);
 

@@ -297,10 +297,11 @@ def config():
     w4.w4a16_test_w8a8_config(-1)
 
 
-@pytest.mark.parametrize("idx", range(w4.w4a16_test_w8a8_config(-1)))
-@pytest.mark.parametrize("M,K,N", [(1, 128, 64), (37, 256, 320), (150, 384, 192), (300, 1024, 576), (520, 640, 64)])
+@pytest.mark.parametrize("idx", [n * 100 + i for i in range(w4.w4a16_test_w8a8_config(-1)) for n in (0, 2, 3, 8)])
+@pytest.mark.parametrize("M,K,N", [(1, 128, 64), (37, 256, 320), (150, 384, 192), (300, 1024, 576), (520, 2688, 64)])
 def test_every_kernel(config, M, K, N, idx):
-    """Each kernel that a size may pick, on sizes that end inside its tiles and on short K."""
+    """Each kernel that a size may pick, whole and in slices, on sizes that end inside its tiles
+    and on short K."""
     x, w, sw, b = problem(M, K, N, BF16, bias=True)
     config(idx)
     check_gemm(run_gemm(dev(x), packed(w), dev(sw), dev(b), N, BF16), x, w[0], sw[0], b)

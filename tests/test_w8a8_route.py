@@ -49,7 +49,7 @@ def test_refuses_weights_and_results(f, kw, status):
     (pre, dict(ldy=260), 4),
     (gemm, dict(M=-1), 2), (gemm, dict(x=None), 1), (gemm, dict(x=F + 8), 4), (gemm, dict(ldx=8), 2),
     (gemm, dict(ldx=260), 4), (gemm, dict(ldy=8), 2), (gemm, dict(ldy=257), 4), (gemm, dict(ws=None), 5),
-    (gemm, dict(nb=1024 + 15), 5), (gemm, dict(ws=F + 8), 4), (gemm, dict(bias=F + 1), 4),
+    (gemm, dict(nb=1024 + 255 + (32 << 20)), 5), (gemm, dict(ws=F + 8), 4), (gemm, dict(bias=F + 1), 4),
     (grouped, dict(R=-1), 2), (grouped, dict(E=0), 2), (grouped, dict(E=(1 << 20) + 1), 2), (grouped, dict(x=None), 1),
     (grouped, dict(off=None), 1), (grouped, dict(off=F + 2), 4), (grouped, dict(srt=F + 2), 4),
     (grouped, dict(srt=F, topk=0), 2), (grouped, dict(srt=F, topk=3), 2), (grouped, dict(srt=F, topk=1 << 33), 2),
@@ -62,8 +62,13 @@ def test_refuses(f, kw, status):
 def test_workspace_sizes():
     for q in (w4.w8a8_workspace_bytes, w4.w8a8_grouped_workspace_bytes):
         assert q(0, 256) == 0 and q(-1, 256) == 0 and q(4, 100) == 0 and q(4, 1 << 17) == 0
-        pass
         assert q(1 << 20, 14336) == (1 << 20) * (14336 + 4)
+    assert w4.w8a8_grouped_workspace_bytes(4, 256) == 1024 + 16
+    assert w4.w8a8_grouped_workspace_bytes(3, 128) == 512 + 12
+    # up to 1024 rows: 32 MiB for the sums of K slices, behind the scales
+    assert w4.w8a8_workspace_bytes(4, 256) == 1024 + 256 + (32 << 20)
+    assert w4.w8a8_workspace_bytes(1024, 256) == 1024 * 256 + 4096 + (32 << 20)
+    assert w4.w8a8_workspace_bytes(1025, 256) == 1025 * 256 + 4100
 
 
 def test_no_rows_is_a_no_op():

@@ -235,7 +235,7 @@ struct W8A8Args {
 // Products of up to kW8A8SliceRows rows may be cut into K slices, whose sums take
 // at most kW8A8PartBytes.
 constexpr int64_t kW8A8SliceRows = 1024;
-constexpr int64_t kW8A8PartBytes = int64_t(256) << 20;
+constexpr int64_t kW8A8PartBytes = int64_t(32) << 20;
 hipError_t launch_w8a8(const W8A8Args &p, int dt, hipStream_t stream);
 // The product of unquantized rows in one launch (p.x, p.ldx), where it exists.
 bool w8a8_fused_ok(int64_t M, int64_t K);

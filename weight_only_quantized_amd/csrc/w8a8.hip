@@ -372,11 +372,12 @@ w8a8_split_kernel(W8A8Args p, unsigned mtiles, unsigned ncb) {
 }
 
 // ---------------------------------------------------------------------------
-// Tile kernel: BM x BN of y per workgroup, WM x WN waves, K in stages of 64.
+// Tile kernel: BM x BN of y per workgroup, WM x WN waves, K in stages of 64 HALVES, NBUF
+// stages in LDS.  Two halves: whole cache lines of x rows, where with stages of 64 every
+// line comes twice (64 x 128 tiles, 4096 x 4096 x 14336: 517 -> 326 us); one half: more
+// stages in flight, spread evenly (256 x 256 tiles, 8192^3: 410 us against 422).
 // ---------------------------------------------------------------------------
 constexpr int kXcd8 = 8;              // XCDs; workgroups go to them round-robin
-constexpr int kStageK = 64;           // K rows per stage
-constexpr int kStages = 4;            // stages in LDS
 constexpr unsigned kBand = 4;         // row tiles side by side on an XCD
 
 // 16 bytes per lane from global memory (base + off) to LDS (lds_base + 16 lane), not
@@ -394,14 +395,16 @@ __device__ __forceinline__ void wait_and_meet() {
     asm volatile("s_waitcnt vmcnt(%0) lgkmcnt(0)\n\ts_barrier" ::"n"(N) : "memory");
 }
 
-template <int DT, int BM, int BN, int WM, int WN, bool GROUPED>
+template <int DT, int BM, int BN, int WM, int WN, int HALVES, int NBUF, bool GROUPED>
 __global__ void __launch_bounds__(WM * WN * 64)
 w8a8_tile_kernel(W8A8Args p, unsigned mtiles, unsigned ncb, unsigned per_xcd) {
     constexpr int NW = WM * WN, TM = BM / WM, TN = BN / WN, RT = TM / 16, CT = TN / 16;
-    constexpr int ABYTES = BM * kStageK, BBYTES = BN * kStageK, SBYTES = ABYTES + BBYTES;
-    constexpr int AL = BM / 16 / NW, BL = BN / 16 / NW;      // DMA loads per wave and stage
-    static_assert(CT % 2 == 0 && BM % (16 * NW) == 0 && BN % (16 * NW) == 0, "whole loads and column pairs");
-    __shared__ __attribute__((aligned(1024))) uint8_t lds[kStages * SBYTES];
+    constexpr int SK = 64 * HALVES, ABYTES = BM * SK, SBYTES = ABYTES + BN * SK;
+    constexpr int RPL = 16 / HALVES;                                    // x rows per DMA load
+    constexpr int AL = BM / RPL / NW, BL = BN / RPL / NW, L = AL + BL;  // loads per wave and stage
+    static_assert(HALVES == 1 || HALVES == 2, "stages of 64 or 128");
+    static_assert(CT % 2 == 0 && BM % (RPL * NW) == 0 && BN % (RPL * NW) == 0, "whole loads and column pairs");
+    __shared__ __attribute__((aligned(1024))) uint8_t lds[NBUF * SBYTES];
 
     const int lane = lane_id();
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
@@ -422,9 +425,9 @@ w8a8_tile_kernel(W8A8Args p, unsigned mtiles, unsigned ncb, unsigned per_xcd) {
     if constexpr (GROUPED) {
         if (!expert_tile(p.offsets, p.E, p.M, BM, tile, e, row0, row_end)) return;
     }
-    // this slice's stages: at least two
-    const int all = (int)(K / kStageK);
-    const int first = (int)((int64_t)all * slice / p.slices), S = (int)((int64_t)all * (slice + 1) / p.slices) - first;
+    // this slice's 128-row groups: at least one
+    const int all = (int)(K / kGroup), first = (int)((int64_t)all * slice / p.slices);
+    const int S = ((int)((int64_t)all * (slice + 1) / p.slices) - first) * (2 / HALVES);
     auto src_row = [&](int64_t r) -> int64_t {
         if (r >= row_end) r = row_end - 1;
         if constexpr (GROUPED) {
@@ -436,50 +439,55 @@ w8a8_tile_kernel(W8A8Args p, unsigned mtiles, unsigned ncb, unsigned per_xcd) {
         return r;
     };
 
-    // DMA sources.  x: a load fills 16 rows of 64 bytes, 16-byte chunk c of row r at chunk
-    // c ^ (-(r / 4) & 3) of its row; W: a load fills one 1024-byte half of a weight tile,
-    // piece p at p ^ 8 (tile & 1).  LDS serves a 128-bit read in four passes over the
-    // lanes' quads {0, 3, 5, 6}, {1, 2, 4, 7} and the same plus 8 (measured with pairs of
-    // quads on the same banks), 256 bytes each: with these orders the 16 lanes of a
-    // pass touch each bank once (4.06 clocks a read; orders for 8 neighbouring lanes 6.5 and 8.0).
+    // DMA sources.  x: a load fills 16 rows of 64 bytes or 8 of 128, 16-byte chunk c of row r at
+    // chunk c ^ fx(r) of its row, fx(r) = (-(r / 4) & 3) + 4 (r / 2 % 2) of the row's last four bits
+    // (rows of 64 bytes: the first term); W: a load fills one 1024-byte half of a weight tile, piece p
+    // at p ^ 8 (tile & 1).  LDS serves a
+    // 128-bit read in four passes over the lanes' quads {0, 3, 5, 6}, {1, 2, 4, 7} and the
+    // same plus 8 (measured with pairs of quads on the same banks), 256 bytes each: with these
+    // orders the 16 lanes of a pass touch each bank once (4.06 clocks a read; orders for 8
+    // neighbouring lanes 6.5 and 8.0).
+    auto fx = [](int r) { return (-(r >> 2) & 3) | (HALVES == 2 ? ((r >> 1) & 1) << 2 : 0); };
     uint32_t aoffs[AL], boffs[BL];
     const bool gather = GROUPED && p.sorted;
-    const uint8_t *abase = p.qx + (int64_t)first * kStageK;
-    const uint8_t *bbase = p.wp + ((int64_t)e * (N / 16) + n0 / 16) * (K / kGroup) * kW8Tile + (int64_t)first * 1024;
+    const uint8_t *abase = p.qx + (int64_t)first * kGroup;
+    const uint8_t *bbase = p.wp + (((int64_t)e * (N / 16) + n0 / 16) * (K / kGroup) + first) * kW8Tile;
     if (!gather) abase += row0 * K;          // gathered rows: X K < 2^32
 #pragma unroll
     for (int i = 0; i < AL; ++i) {
-        const int r = lane >> 2, c = (lane & 3) ^ (-(r >> 2) & 3);
-        const int64_t m = src_row(row0 + (wave + NW * i) * 16 + r);
+        const int r = (wave + NW * i) * RPL + lane / (4 * HALVES), c = (lane % (4 * HALVES)) ^ fx(r & 15);
+        const int64_t m = src_row(row0 + r);
         aoffs[i] = (uint32_t)((gather ? m : m - row0) * K) + 16 * c;
     }
 #pragma unroll
     for (int i = 0; i < BL; ++i) {
-        const int t = wave + NW * i, last = (int)((N - n0) / 16) - 1;
+        const int t = (wave + NW * i) / HALVES, half = (wave + NW * i) % HALVES, last = (int)((N - n0) / 16) - 1;
         const int piece = lane ^ ((t & 1) << 3);
-        boffs[i] = (uint32_t)((t < last ? t : last) * (K * 16)) + 16 * piece;
+        boffs[i] = (uint32_t)((t < last ? t : last) * (K * 16)) + 1024 * half + 16 * piece;
     }
     const uint32_t lds0 = (uint32_t)(uintptr_t)(__attribute__((address_space(3))) uint8_t *)lds + wave * 1024;
-    auto fetch = [&](int s) {
-        const uint32_t base = lds0 + ((unsigned)s % kStages) * SBYTES;
+    uint32_t place = 0;                      // of the next stage to fetch
+    auto fetch = [&]() {
+        const uint32_t base = lds0 + place;
 #pragma unroll
         for (int i = 0; i < AL; ++i) dma16(abase, aoffs[i], base + NW * i * 1024);
 #pragma unroll
         for (int i = 0; i < BL; ++i) dma16(bbase, boffs[i], base + ABYTES + NW * i * 1024);
-        abase += kStageK;
-        bbase += 1024;
+        abase += SK;
+        bbase += 1024 * HALVES;
+        place = place + SBYTES == NBUF * SBYTES ? 0 : place + SBYTES;
     };
 #pragma unroll
-    for (int s = 0; s < kStages - 1; ++s)
-        if (s < S) fetch(s);
+    for (int s = 0; s < NBUF - 1; ++s)
+        if (s < S) fetch();
 
-    // LDS offsets of this lane's operands
+    // LDS offsets of this lane's operands in the first half of a stage
     const int i16 = lane & 15, q = lane >> 4;
-    const int aoff = (wm * TM + i16) * kStageK + 16 * (q ^ (-(i16 >> 2) & 3));
+    const int aoff = (wm * TM + i16) * SK + 16 * (q ^ fx(i16));
     // W operand row i of column block ct is column 32 (ct / 2) + 8 (i / 4) + 4 (ct % 2) + i % 4
     // of the wave's tile: a lane then ends up with 8 neighbouring columns per pair of blocks
     const int piece = (q & 1) | (i16 & 3) << 1 | (i16 >> 3) << 3 | ((i16 >> 2) & 1) << 4 | (q >> 1) << 5;
-    const int boff = ABYTES + (wn * CT + (i16 >> 3)) * 1024 + 16 * piece;
+    const int boff = ABYTES + (wn * CT + (i16 >> 3)) * 1024 * HALVES + 16 * piece;
 
     i32x4_t acc[RT][CT];
 #pragma unroll
@@ -488,13 +496,15 @@ w8a8_tile_kernel(W8A8Args p, unsigned mtiles, unsigned ncb, unsigned per_xcd) {
         for (int ct = 0; ct < CT; ++ct) acc[rt][ct] = i32x4_t{0, 0, 0, 0};
 
     u32x4_t xf[RT], wf[CT];
-    auto read = [&](int s) {
-        const uint8_t *base = lds + ((unsigned)s % kStages) * SBYTES;
+    uint32_t at = 0;                         // place of the stage that is multiplied
+    auto read = [&](int half) {
+        const uint8_t *base = lds + at;
 #pragma unroll
         for (int ct = 0; ct < CT; ++ct)
-            wf[ct] = *reinterpret_cast<const u32x4_t *>(base + (boff ^ ((ct & 1) * 128)) + (ct >> 1) * 2048);
+            wf[ct] = *reinterpret_cast<const u32x4_t *>(base + (boff ^ ((ct & 1) * 128)) + (ct >> 1) * 2048 * HALVES + half * 1024);
 #pragma unroll
-        for (int rt = 0; rt < RT; ++rt) xf[rt] = *reinterpret_cast<const u32x4_t *>(base + aoff + rt * 16 * kStageK);
+        for (int rt = 0; rt < RT; ++rt)
+            xf[rt] = *reinterpret_cast<const u32x4_t *>(base + (aoff ^ (half * 64)) + rt * 16 * SK);
 #pragma unroll
         for (int ct = 0; ct < CT; ++ct) {
             wf[ct] ^= 0x80808080u;                     // u = q + 128 to two's complement q
@@ -511,7 +521,6 @@ w8a8_tile_kernel(W8A8Args p, unsigned mtiles, unsigned ncb, unsigned per_xcd) {
                                                                     __builtin_bit_cast(i32x4_t, xf[rt]), acc[rt][ct], 0, 0, 0);
         __builtin_amdgcn_sched_barrier(0);
     };
-    constexpr int L = AL + BL;
     using std::integral_constant;
     using Yes = integral_constant<bool, true>;
     using No = integral_constant<bool, false>;
@@ -522,36 +531,44 @@ w8a8_tile_kernel(W8A8Args p, unsigned mtiles, unsigned ncb, unsigned per_xcd) {
     // unit fills the gaps.
     //
     // Eight waves: two groups, one wave of each on every SIMD, take turns: while one multiplies
-    // stage s, the other reads its operands.  A phase ends in a barrier; group 0
-    // reads stage s in phase 2 s and multiplies it in phase 2 s + 1, group 1 one phase
-    // later.  Stage s has landed by the end of phase 2 s - 1; its place is filled again
-    // from phase 2 s + 2 on.
-    auto turn = [&](int s, auto wait, auto refill) {
+    // a half stage, the other reads its operands.  A phase ends in a barrier; group 0 reads half
+    // h of stage s in phase 2 (HALVES s + h) and multiplies it in the next, group 1 one phase
+    // later.  The place of stage s - 1 is free when group 0 begins stage s (group 1 has read its last
+    // half in the phase before) and is filled again from there on.  Every wave waits for its
+    // loads of stage s + 1 at the end of its last reads of stage s, which is a barrier before group 0
+    // reads stage s + 1.
+    auto stage = [&](auto wait, auto refill) {
         constexpr int WAIT = decltype(wait)::value;
         if constexpr (NW == 8) {
-            if constexpr (decltype(refill)::value) fetch(s + kStages - 1);
-            read(s);
-            wait_and_meet<WAIT>();
-            multiply();
-            wait_and_meet<63>();
+            if constexpr (decltype(refill)::value) fetch();
+#pragma unroll
+            for (int h = 0; h < HALVES; ++h) {
+                read(h);
+                if (h == HALVES - 1) wait_and_meet<WAIT>();
+                else wait_and_meet<63>();
+                multiply();
+                wait_and_meet<63>();
+            }
         } else {
             wait_and_meet<WAIT>();
-            if constexpr (decltype(refill)::value) fetch(s + kStages - 1);
-            read(s);
-            multiply();
+            if constexpr (decltype(refill)::value) fetch();
+#pragma unroll
+            for (int h = 0; h < HALVES; ++h) {
+                read(h);
+                multiply();
+            }
         }
+        at = at + SBYTES == NBUF * SBYTES ? 0 : at + SBYTES;
     };
-    constexpr int EARLY = NW == 8 ? 1 : 0;      // eight waves wait for stage s + 1 in stage s
+    using Rest = integral_constant<int, (NBUF - 2) * L>;
     if constexpr (NW == 8) {
-        if (S > 2) wait_and_meet<2 * L>();
-        else wait_and_meet<L>();
+        if (S >= NBUF - 1) wait_and_meet<(NBUF - 2) * L>();
+        else wait_and_meet<0>();
         if (wave >= 4) wait_and_meet<63>();
     }
     int s = 0;
-    for (; s + kStages <= S; ++s) turn(s, integral_constant<int, 2 * L>{}, Yes{});
-    if (S > 2) turn(S - 3, integral_constant<int, (2 - EARLY) * L>{}, No{});
-    turn(S - 2, integral_constant<int, (1 - EARLY) * L>{}, No{});
-    turn(S - 1, integral_constant<int, 0>{}, No{});
+    for (; s + NBUF <= S; ++s) stage(Rest{}, Yes{});
+    for (; s < S; ++s) stage(integral_constant<int, 0>{}, No{});
     if constexpr (NW == 8) {
         if (wave < 4) wait_and_meet<63>();
     }
@@ -675,15 +692,15 @@ static hipError_t split_launch(const W8A8Args &p, hipStream_t stream) {
 
 static bool slices_fit(const W8A8Args &p, int slices);
 
-template <int DT, int BM, int BN, int WM, int WN, bool GROUPED>
+template <int DT, int BM, int BN, int WM, int WN, int HALVES, int NBUF, bool GROUPED>
 static hipError_t tile8_launch(const W8A8Args &p, hipStream_t stream) {
     const int64_t ncb = (p.N + BN - 1) / BN;
     const int64_t few = p.M < p.E ? p.M : p.E;
     const int64_t mtiles = GROUPED ? p.M / BM + few : (p.M + BM - 1) / BM;
     const int64_t per_xcd = (mtiles * ncb * p.slices + kXcd8 - 1) / kXcd8;
-    if (per_xcd * kXcd8 > INT32_MAX || p.slices < 1 || p.K / kStageK / p.slices < 2) return hipErrorInvalidConfiguration;
+    if (per_xcd * kXcd8 > INT32_MAX || p.slices < 1 || p.K / kGroup < p.slices) return hipErrorInvalidConfiguration;
     if (p.slices > 1 && (GROUPED || !slices_fit(p, p.slices))) return hipErrorInvalidConfiguration;
-    hipLaunchKernelGGL((w8a8_tile_kernel<DT, BM, BN, WM, WN, GROUPED>), dim3((unsigned)(per_xcd * kXcd8)),
+    hipLaunchKernelGGL((w8a8_tile_kernel<DT, BM, BN, WM, WN, HALVES, NBUF, GROUPED>), dim3((unsigned)(per_xcd * kXcd8)),
                        dim3(WM * WN * 64), 0, stream, p, (unsigned)mtiles, (unsigned)ncb, (unsigned)per_xcd);
     const hipError_t err = hipGetLastError();
     if (err != hipSuccess || p.slices == 1) return err;
@@ -694,7 +711,9 @@ static hipError_t tile8_launch(const W8A8Args &p, hipStream_t stream) {
 
 // Column blocks of 16 per workgroup of the split-K kernel: as many as leave about a
 // workgroup per compute unit.
-static int split_columns(int64_t N) { return N >= 64 * 192 ? 4 : N >= 32 * 192 ? 2 : 1; }
+static int split_columns(int64_t N, int64_t mtiles) {
+    return N * mtiles >= 64 * 192 ? 4 : N * mtiles >= 32 * 192 ? 2 : 1;
+}
 
 // The kernels, by number.  0: split-K, 16 rows; 1, 2: split-K, 32 rows; 3 ..: tiles.
 struct W8A8Kernel {
@@ -715,7 +734,7 @@ int w8a8_config_count() { return kKernelCount; }
 // the best of the measured ones.
 static double kernel_us(const W8A8Kernel &k, int64_t mtiles, int64_t M, int64_t K, int64_t N, int slices) {
     const int64_t wg = mtiles * ((N + k.bn - 1) / k.bn) * slices, G = K / kGroup;
-    const double steps = k.waves ? (double)((G + k.waves - 1) / k.waves) : (double)K / kStageK / slices;
+    const double steps = k.waves ? (double)((G + k.waves - 1) / k.waves) : (double)K / 64 / slices;
     const int64_t full = wg / (256 * k.resident), left = (wg - full * 256 * k.resident + 255) / 256;
     double us = 4 + steps * full * (k.step + k.more * (k.resident - 1)) + (double)(full + (left > 0));
     if (left > 0) us += steps * (k.step + k.more * (double)(left - 1));
@@ -727,7 +746,7 @@ static std::atomic<int> g_w8a8_cfg{-1};
 void set_w8a8_config(int idx) { g_w8a8_cfg.store(idx, std::memory_order_relaxed); }
 
 static bool slices_fit(const W8A8Args &p, int slices) {
-    return p.part && p.K / kStageK / slices >= 4 && (double)slices * (double)p.M * (double)p.N * 4 <= (double)kW8A8PartBytes;
+    return p.part && p.K / kGroup / slices >= 2 && (double)slices * (double)p.M * (double)p.N * 4 <= (double)kW8A8PartBytes;
 }
 
 // Gathered rows of the tile kernels are addressed with 32 bits.
@@ -749,7 +768,7 @@ static void pick_kernel(const W8A8Args &p, int &kernel, int &slices) {
     double best = 1e30;
     for (int i = 0; i < kKernelCount; ++i) {
         const W8A8Kernel &k = kKernels[i];
-        if (i == 0 && split_columns(p.N) != 1) continue;
+        if (i == 0 && split_columns(p.N, 1) != 1) continue;
         if (k.waves == 0 && !tile_ok(p)) continue;
         const int64_t few = p.M < p.E ? p.M : p.E;
         const int64_t mtiles = p.offsets ? (p.M + (int64_t)k.bm * few / 2) / k.bm : (p.M + k.bm - 1) / k.bm;
@@ -772,18 +791,18 @@ static hipError_t w8a8_dispatch(const W8A8Args &args, hipStream_t stream) {
     pick_kernel(p, kernel, p.slices);
     switch (kernel) {
         case 0:
-            switch (split_columns(p.N)) {
+            switch (split_columns(p.N, GROUPED ? (p.M < p.E ? p.M : p.E) : 1)) {
                 case 4: return split_launch<DT, 1, 4, 2, 16, GROUPED, false>(p, stream);
                 case 2: return split_launch<DT, 1, 2, 2, 16, GROUPED, false>(p, stream);
                 default: return split_launch<DT, 1, 1, 4, 16, GROUPED, false>(p, stream);
             }
         case 1: return split_launch<DT, 2, 4, 2, 8, GROUPED, false>(p, stream);
         case 2: return split_launch<DT, 2, 2, 2, 8, GROUPED, false>(p, stream);
-        case 3: return tile8_launch<DT, 64, 64, 2, 2, GROUPED>(p, stream);
-        case 4: return tile8_launch<DT, 64, 128, 2, 2, GROUPED>(p, stream);
-        case 5: return tile8_launch<DT, 128, 128, 2, 4, GROUPED>(p, stream);
-        case 6: return tile8_launch<DT, 128, 256, 2, 4, GROUPED>(p, stream);
-        default: return tile8_launch<DT, 256, 256, 2, 4, GROUPED>(p, stream);
+        case 3: return tile8_launch<DT, 64, 64, 2, 2, 2, 3, GROUPED>(p, stream);
+        case 4: return tile8_launch<DT, 64, 128, 2, 2, 2, 2, GROUPED>(p, stream);
+        case 5: return tile8_launch<DT, 128, 128, 2, 4, 2, 2, GROUPED>(p, stream);
+        case 6: return tile8_launch<DT, 128, 256, 2, 4, 2, 3, GROUPED>(p, stream);
+        default: return tile8_launch<DT, 256, 256, 2, 4, 1, 4, GROUPED>(p, stream);
     }
 }
 
@@ -794,7 +813,7 @@ bool w8a8_fused_ok(int64_t M, int64_t K) {
 
 template <int DT>
 static hipError_t w8a8_fused_dispatch(const W8A8Args &p, hipStream_t stream) {
-    switch (split_columns(p.N)) {
+    switch (split_columns(p.N, 1)) {
         case 4: return split_launch<DT, 1, 4, 2, 16, false, true>(p, stream);
         case 2: return split_launch<DT, 1, 2, 2, 16, false, true>(p, stream);
         default: return split_launch<DT, 1, 1, 4, 16, false, true>(p, stream);

@@ -14,6 +14,7 @@
 // 128 g + 32 (l / 16) + 16 h .. + 15 of step h; result register r of lane l is
 // column 4 (l / 16) + r of x row l % 16: four neighbouring outputs per lane.
 #include <atomic>
+#include <cmath>
 #include <type_traits>
 
 #include "common.hpp"
@@ -720,25 +721,27 @@ struct W8A8Kernel {
     int bm, bn;
     int resident;              // workgroups on a compute unit
     int waves;                 // split-K: waves that share K (tiles: 0)
-    double step, more;         // us per step (a 128-row group per wave, or a stage), per further resident workgroup
+    double step, more, round;  // us per step (a 128-row group per wave, or 64 of K), per further resident
+                               // workgroup, per round of resident workgroups
 };
-static constexpr W8A8Kernel kKernels[] = {{16, 16, 2, 16, 0.85, 1.30}, {32, 64, 2, 8, 1.75, 2.09}, {32, 32, 2, 8, 1.27, 1.15},
-                                          {64, 64, 5, 0, 0.228, 0.118}, {64, 128, 3, 0, 0.307, 0.171},
-                                          {128, 128, 2, 0, 0.352, 0.302}, {128, 256, 1, 0, 0.49, 0}, {256, 256, 1, 0, 0.68, 0}};
+static constexpr W8A8Kernel kKernels[] = {{16, 16, 2, 16, 0.70, 4.3, 2.7},  {32, 64, 2, 8, 2.2, 1.36, 0.4},
+                                          {32, 32, 2, 8, 1.16, 7.1, 0.2},   {64, 64, 3, 0, 0.153, 0.089, 0.1},
+                                          {64, 128, 3, 0, 0.282, 0.099, 0.7}, {128, 256, 1, 0, 0.399, 0, 1.4},
+                                          {256, 256, 1, 0, 0.529, 0, 1.0}};
 constexpr int kKernelCount = sizeof(kKernels) / sizeof(kKernels[0]);
 int w8a8_config_count() { return kKernelCount; }
 
 // Estimated time in us of a kernel whose tiles cover `mtiles` row tiles of M rows, K
-// cut into `slices`.  The constants of kKernels and of this formula are a fit to 1500 measured
-// products (20 to 4096 rows, K and N from 512 to 14336); the choice by it is on average 3% slower than
-// the best of the measured ones.
+// cut into `slices`.  The constants of kKernels and of this formula are fitted to 1800 measured
+// products (20 to 4096 rows, K from 512 to 14336, N from 1024 to 14336) such that the choice by it is
+// near the best: 0.2% slower on average, 8% at most.
 static double kernel_us(const W8A8Kernel &k, int64_t mtiles, int64_t M, int64_t K, int64_t N, int slices) {
     const int64_t wg = mtiles * ((N + k.bn - 1) / k.bn) * slices, G = K / kGroup;
-    const double steps = k.waves ? (double)((G + k.waves - 1) / k.waves) : (double)K / 64 / slices;
+    const double steps = k.waves ? (G >= k.waves ? (double)G / k.waves : 1.0) : (double)K / 64 / slices;
     const int64_t full = wg / (256 * k.resident), left = (wg - full * 256 * k.resident + 255) / 256;
-    double us = 4 + steps * full * (k.step + k.more * (k.resident - 1)) + (double)(full + (left > 0));
+    double us = 4 + steps * full * (k.step + k.more * (k.resident - 1)) + k.round * (double)(full + (left > 0));
     if (left > 0) us += steps * (k.step + k.more * (double)(left - 1));
-    return slices > 1 ? us + 2.6 + 1.7e-6 * (double)(slices * M * N) : us;
+    return slices > 1 ? us + 2.8 + 1.84e-6 * (double)(slices * M * N) : us;
 }
 
 // Test hook: the kernel of the next calls, plus 100 times its slices (-1: by size).
@@ -761,17 +764,22 @@ static void pick_kernel(const W8A8Args &p, int &kernel, int &slices) {
         if (kernel >= 3 && forced >= 200 && slices_fit(p, forced / 100)) slices = forced / 100;
         return;
     }
-    // grouped: every expert ends in a partial tile, half empty on average
-    const int64_t rows = p.offsets ? p.M / p.E : p.M;
+    // grouped: the experts' row counts are on the device.  With counts spread as skewed routing spreads
+    // them (exponentially around their mean), an expert has 1 / (1 - exp(-bm / mean)) row tiles.
+    const double held = (double)(p.M < p.E ? p.M : p.E), mean = p.offsets ? (double)p.M / held : 0;
+    if (p.offsets ? p.M <= 3 * (int64_t)p.E : p.M <= 16) {
+        // grouped, M / E = 0.5, 1, 2 (64 experts, 2048 x 2816): 28.7, 46.3, 60.5 us against 33, 59, 65 us with
+        // 64 x 128 tiles; M / E = 4: 70.8 against 68.6 us
+        kernel = p.offsets ? 2 : 0;
+        return;
+    }
     kernel = 0;
-    if (rows <= 16) return;
     double best = 1e30;
     for (int i = 0; i < kKernelCount; ++i) {
         const W8A8Kernel &k = kKernels[i];
         if (i == 0 && split_columns(p.N, 1) != 1) continue;
         if (k.waves == 0 && !tile_ok(p)) continue;
-        const int64_t few = p.M < p.E ? p.M : p.E;
-        const int64_t mtiles = p.offsets ? (p.M + (int64_t)k.bm * few / 2) / k.bm : (p.M + k.bm - 1) / k.bm;
+        const int64_t mtiles = p.offsets ? (int64_t)std::ceil(held / (1 - std::exp(-k.bm / mean))) : (p.M + k.bm - 1) / k.bm;
         for (int n = 1; n <= 8; n *= 2) {
             if (n > 1 && (k.waves != 0 || !slices_fit(p, n))) break;
             const double us = kernel_us(k, mtiles, p.M, p.K, p.N, n);
@@ -800,8 +808,7 @@ static hipError_t w8a8_dispatch(const W8A8Args &args, hipStream_t stream) {
         case 2: return split_launch<DT, 2, 2, 2, 8, GROUPED, false>(p, stream);
         case 3: return tile8_launch<DT, 64, 64, 2, 2, 2, 3, GROUPED>(p, stream);
         case 4: return tile8_launch<DT, 64, 128, 2, 2, 2, 2, GROUPED>(p, stream);
-        case 5: return tile8_launch<DT, 128, 128, 2, 4, 2, 2, GROUPED>(p, stream);
-        case 6: return tile8_launch<DT, 128, 256, 2, 4, 2, 3, GROUPED>(p, stream);
+        case 5: return tile8_launch<DT, 128, 256, 2, 4, 2, 3, GROUPED>(p, stream);
         default: return tile8_launch<DT, 256, 256, 2, 4, 1, 4, GROUPED>(p, stream);
     }
 }

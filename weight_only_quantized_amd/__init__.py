@@ -141,22 +141,32 @@ def lib():
 
 
 def _ptr(t):
-    if t is None:
-        return None
-    if isinstance(t, int):
+    if t is None or type(t) is int:
         return t
-    return t.data_ptr()
+    return t if isinstance(t, int) else t.data_ptr()
+
+
+def _current_stream_calls():
+    """torch's calls for the current device and its current stream's address (the
+    latter without building a Stream object: 0.4 instead of 2.8 us, against 4.2 us for a whole
+    launch), looked up once."""
+    import torch
+    raw = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+    if raw is None:
+        return lambda device: torch.cuda.current_stream(device).cuda_stream, torch.cuda.current_device
+    return raw, torch.cuda.current_device
+
+
+_stream_calls = None
 
 
 def _stream(stream):
+    global _stream_calls
     if stream is None:
-        import torch
-        raw = getattr(torch._C, "_cuda_getCurrentRawStream", None)
-        if raw is None:
-            return torch.cuda.current_stream().cuda_stream
-        # the same address without building a Stream object (0.4 instead of 2.8 us,
-        # against 4.2 us for a whole launch)
-        return raw(torch.cuda.current_device())
+        if _stream_calls is None:
+            _stream_calls = _current_stream_calls()
+        raw, device = _stream_calls
+        return raw(device())
     if isinstance(stream, int):
         return stream
     return stream.cuda_stream

@@ -126,27 +126,29 @@ __device__ __forceinline__ float exp_neg(float x) {
     return __builtin_fmaf(r, l * kLn2, r);
 }
 
-// exp(z - max), their sum, and the row's kind.
+// exp(z - max) (finite whatever the row holds), one over their sum, and the row's kind.  The
+// reciprocal of a row without a distribution is 0 or NaN, which spreads to all its probabilities.
 template <int DT, int LPT, int EPL>
-__device__ __forceinline__ int row_softmax(const uint32_t (&raw)[EPL], float (&p)[EPL], float &top, float &sum) {
+__device__ __forceinline__ int row_softmax(const uint32_t (&raw)[EPL], float (&p)[EPL], float &top, float &inv) {
     float m = -INFINITY;
-    bool nan = false;
+    uint32_t nan = 0;
 #pragma unroll
     for (int i = 0; i < EPL; ++i) {
         p[i] = value_of<DT>(raw[i]);
         m = fmaxf(m, p[i]);
-        nan |= p[i] != p[i];
+        nan |= p[i] != p[i] ? 1u : 0u;
     }
     top = group_max<LPT>(m);
-    const bool any_nan = lane_umax<LPT>(nan ? 1u : 0u) != 0;
-    const int kind = any_nan || top == INFINITY ? ROW_NAN : top == -INFINITY ? ROW_EMPTY : ROW_OK;
+    nan = lane_umax<LPT>(nan);
+    const int kind = nan != 0 || top == INFINITY ? ROW_NAN : top == -INFINITY ? ROW_EMPTY : ROW_OK;
     float s = 0.0f;
 #pragma unroll
     for (int i = 0; i < EPL; ++i) {
-        p[i] = kind == ROW_OK ? exp_neg(p[i] - top) : kind == ROW_NAN ? __builtin_nanf("") : 0.0f;
+        p[i] = exp_neg(p[i] - top);
         s += p[i];
     }
-    sum = group_sum<LPT>(s);
+    s = group_sum<LPT>(s);
+    inv = kind == ROW_OK ? 1.0f / s : kind == ROW_NAN ? __builtin_nanf("") : 0.0f;
     return kind;
 }
 
@@ -161,7 +163,7 @@ __device__ __forceinline__ float balance_loss(int E, double x, int n, int tokens
     return (float)(E * x / (cc * tv));
 }
 
-// Workspace: the blocks' sums of probabilities [blocks][E] and counts [blocks][E + 1], and
+// Workspace: the blocks' sums of probabilities [E][blocks] and counts [E + 1][blocks], and
 // the joining blocks' sums and ticket.
 struct RouteSpace {
     float *p;
@@ -170,7 +172,8 @@ struct RouteSpace {
     int32_t *n;
     uint32_t *ticket;
 };
-constexpr int kJoinExperts = 32, kJoinRows = 32, kMaxJoins = kMoeMaxExperts / kJoinExperts;
+constexpr int kMaxBlocks = 256;            // of a counting call
+constexpr int kJoinWaves = 8, kMaxJoins = kMoeMaxExperts / kJoinWaves + 1;
 
 // Counts are kept where COUNT; a single block finishes by itself.
 template <int DT, int LPT, int EPL, bool VEC, bool COUNT>
@@ -194,11 +197,16 @@ __global__ void __launch_bounds__(COUNT ? kCountThreads : kRouteThreads) route_k
         float *w = p.w + t * p.topk;
         const bool live = !p.mask || p.mask[t] != 0;
         uint32_t key[EPL];
-        float pe[EPL], top = 0.0f, sum = 1.0f;
+        float pe[EPL], top = 0.0f, inv = 0.0f;
         int kind = ROW_EMPTY;
         if (live) {
             load_row<DT, LPT, EPL, VEC>(p.logits, t * p.ld, E, sub, key);
-            kind = row_softmax<DT, LPT, EPL>(key, pe, top, sum);
+            kind = row_softmax<DT, LPT, EPL>(key, pe, top, inv);
+            if constexpr (COUNT) {
+#pragma unroll
+                for (int i = 0; i < EPL; ++i) pacc[i] = __builtin_fmaf(pe[i], inv, pacc[i]);
+                if (sub == 0 && kind != ROW_EMPTY) atomicAdd(&cnt[E], 1);
+            }
         }
         if (kind != ROW_OK) {
             const float fill = kind == ROW_NAN ? __builtin_nanf("") : 0.0f;
@@ -206,74 +214,58 @@ __global__ void __launch_bounds__(COUNT ? kCountThreads : kRouteThreads) route_k
                 ids[k] = -1;
                 w[k] = fill;
             }
-            if constexpr (COUNT) {
-                if (kind == ROW_NAN) {
-#pragma unroll
-                    for (int i = 0; i < EPL; ++i) pacc[i] = __builtin_nanf("");
-                    if (sub == 0) atomicAdd(&cnt[E], 1);
-                }
-            }
             continue;
-        }
-        const float inv = 1.0f / sum;
-        if constexpr (COUNT) {
-#pragma unroll
-            for (int i = 0; i < EPL; ++i) pacc[i] += pe[i] * inv;
-            if (sub == 0) atomicAdd(&cnt[E], 1);
         }
 #pragma unroll
         for (int i = 0; i < EPL; ++i) key[i] = key_of<DT>(key[i], expert_of<LPT, EPL, VEC>(i, sub));
-        // the largest that is left, topk times; lane k % LPT keeps choice k until LPT of them
-        // are written together
-        float chosen = 0.0f, mine = 0.0f;
+        // the largest that is left, topk times; lane k % LPT keeps choice k (its key, 0 if there
+        // is none) until LPT of them are written together
+        float chosen = 0.0f;
+        uint32_t mine = 0;
         int my_id = -1;
+        auto flush = [&](int k0, int n) {
+            const float ex = mine ? exp_neg(key_value<DT>(mine) - top) : 0.0f;
+            if (sub < n) {
+                ids[k0 + sub] = my_id;
+                w[k0 + sub] = ex;
+                if constexpr (COUNT) {
+                    if (my_id >= 0) atomicAdd(&cnt[my_id], 1);
+                }
+            }
+            chosen += sub < n ? ex : 0.0f;
+            return ex;
+        };
         for (int k = 0; k < p.topk; ++k) {
             uint32_t m = key[0];
 #pragma unroll
             for (int i = 1; i < EPL; ++i) m = key[i] > m ? key[i] : m;
             const uint32_t best = lane_umax<LPT>(m);
-            int be = -1;
+            int be;
             if constexpr (DT == DT_F32) {
                 uint32_t at = 0;                                 // the lowest expert at the best value, as 0xFFFF - e
 #pragma unroll
                 for (int i = 0; i < EPL; ++i) {
                     const uint32_t v = 0xFFFFu - (uint32_t)expert_of<LPT, EPL, VEC>(i, sub);
-                    at = key[i] == best && v > at ? v : at;
+                    const uint32_t c = key[i] == best ? v : 0u;
+                    at = c > at ? c : at;
                 }
                 be = 0xFFFF - (int)lane_umax<LPT>(at);
 #pragma unroll
-                for (int i = 0; i < EPL; ++i)
-                    if (expert_of<LPT, EPL, VEC>(i, sub) == be) key[i] = 0;
+                for (int i = 0; i < EPL; ++i) key[i] = expert_of<LPT, EPL, VEC>(i, sub) == be ? 0u : key[i];
             } else {
                 be = 0xFFFF - (int)(best & 0xFFFFu);
 #pragma unroll
-                for (int i = 0; i < EPL; ++i)
-                    if (key[i] == best) key[i] = 0;
+                for (int i = 0; i < EPL; ++i) key[i] = key[i] == best ? 0u : key[i];
             }
-            const bool none = best == 0;
-            const float ex = none ? 0.0f : exp_neg(key_value<DT>(best) - top);
-            chosen += ex;
-            if (sub == k % LPT) {
-                my_id = none ? -1 : be;
-                mine = ex;
-            }
-            if (k % LPT == LPT - 1 && k + 1 < p.topk) {
-                ids[k - (LPT - 1) + sub] = my_id;
-                w[k - (LPT - 1) + sub] = mine;
-                if constexpr (COUNT) {
-                    if (my_id >= 0) atomicAdd(&cnt[my_id], 1);
-                }
-            }
+            const bool here = sub == k % LPT;
+            mine = here ? best : mine;
+            my_id = here ? (best == 0 ? -1 : be) : my_id;
+            if (k % LPT == LPT - 1 && k + 1 < p.topk) flush(k - (LPT - 1), LPT);
         }
-        const float scale = p.renorm ? 1.0f / chosen : inv;
         const int k0 = (p.topk - 1) / LPT * LPT;
-        if (k0 + sub < p.topk) {
-            ids[k0 + sub] = my_id;
-            w[k0 + sub] = mine * scale;
-            if constexpr (COUNT) {
-                if (my_id >= 0) atomicAdd(&cnt[my_id], 1);
-            }
-        }
+        const float ex = flush(k0, p.topk - k0);
+        const float scale = p.renorm ? 1.0f / group_sum<LPT>(chosen) : inv;
+        if (k0 + sub < p.topk) w[k0 + sub] = ex * scale;
         for (int k = sub; k < k0; k += LPT) w[k] *= scale;               // each lane its own values
     }
     if constexpr (COUNT) {
@@ -301,8 +293,8 @@ __global__ void __launch_bounds__(COUNT ? kCountThreads : kRouteThreads) route_k
             if (gridDim.x == 1) {
                 p.counts[e] = c;
             } else {
-                ws.c[(int64_t)blockIdx.x * (E + 1) + e] = c;
-                if (e < E) ws.p[(int64_t)blockIdx.x * E + e] = v;
+                ws.c[(int64_t)e * gridDim.x + blockIdx.x] = c;
+                if (e < E) ws.p[(int64_t)e * gridDim.x + blockIdx.x] = v;
             }
         }
         if (gridDim.x == 1 && p.loss) {
@@ -324,87 +316,67 @@ __global__ void __launch_bounds__(COUNT ? kCountThreads : kRouteThreads) route_k
     }
 }
 
-// Counts and loss from the blocks' sums, in a fixed order: each workgroup sums kJoinExperts
-// experts (kJoinRows rows of the blocks side by side), the last one to finish adds up the
-// workgroups' shares of the loss.
-__global__ void __launch_bounds__(kJoinExperts * kJoinRows)
+// Counts and loss from the blocks' sums, in a fixed order: a wave per expert (and one for the
+// tokens), the last workgroup to finish adds up the workgroups' shares of the loss.
+__global__ void __launch_bounds__(kJoinWaves * 64)
 route_join_kernel(RouteSpace ws, int blocks, int E, int32_t *__restrict__ counts, float *__restrict__ loss) {
-    __shared__ double ps[kJoinRows][kJoinExperts + 1];
-    __shared__ int cs[kJoinRows][kJoinExperts + 1];
-    __shared__ int toks[kJoinExperts * kJoinRows / 64];
+    __shared__ double xs[kJoinWaves];
+    __shared__ int ns[kJoinWaves];
     __shared__ bool last;
-    const int col = threadIdx.x % kJoinExperts, row = threadIdx.x / kJoinExperts;
-    const int e = blockIdx.x * kJoinExperts + col;
+    const int lane = lane_id(), wave = threadIdx.x >> 6;
+    const int e = blockIdx.x * kJoinWaves + wave;          // E: the tokens
     int c = 0;
-    double s = 0.0;
-    const int ec = e < E ? e : E - 1;
-    // batches of loads that are all on their way before the first is used
-    constexpr int BATCH = 8;
-    for (int b0 = row; b0 < blocks; b0 += BATCH * kJoinRows) {
-        float pv[BATCH];
-        int cv[BATCH];
+    float s = 0.0f;
+    if (e <= E) {
+        int cv[kMaxBlocks / 64];
+        float pv[kMaxBlocks / 64];
 #pragma unroll
-        for (int u = 0; u < BATCH; ++u) {
-            const int64_t b = b0 + u * kJoinRows < blocks ? b0 + u * kJoinRows : blocks - 1;
-            pv[u] = ws.p[b * E + ec];
-            cv[u] = ws.c[b * (E + 1) + ec];
+        for (int u = 0; u < kMaxBlocks / 64; ++u) {
+            const int b = lane + 64 * u;
+            cv[u] = b < blocks ? ws.c[(int64_t)e * blocks + b] : 0;
+            pv[u] = b < blocks && e < E ? ws.p[(int64_t)e * blocks + b] : 0.0f;
         }
 #pragma unroll
-        for (int u = 0; u < BATCH; ++u)
-            if (e < E && b0 + u * kJoinRows < blocks) {
-                s += pv[u];
-                c += cv[u];
-            }
+        for (int u = 0; u < kMaxBlocks / 64; ++u) {
+            c += cv[u];
+            s += pv[u];
+        }
+        c = lane_reduce<64>(c, [](int a, int b) { return a + b; });
+        s = group_sum<64>(s);
+        if (lane == 0) counts[e] = c;
     }
-    ps[row][col] = s;
-    cs[row][col] = c;
-    int tv = 0;
-    if (blockIdx.x == 0) {
-        for (int b = threadIdx.x; b < blocks; b += kJoinExperts * kJoinRows) tv += ws.c[(int64_t)b * (E + 1) + E];
-#pragma unroll
-        for (int off = 32; off > 0; off >>= 1) tv += __shfl_xor(tv, off);
-        if (lane_id() == 0) toks[threadIdx.x >> 6] = tv;
+    if (!loss) return;
+    if (lane == 0) {
+        xs[wave] = e < E ? (double)c * s : 0.0;
+        ns[wave] = e < E ? c : 0;
     }
     __syncthreads();
-    if (threadIdx.x < 64) {
+    if (threadIdx.x == 0) {
         double x = 0.0;
         int n = 0;
-        if (threadIdx.x < kJoinExperts) {
-            for (int r = 1; r < kJoinRows; ++r) {
-                s += ps[r][col];
-                c += cs[r][col];
-            }
-            if (e < E) counts[e] = c;
-            x = (double)c * s;
-            n = c;
+        for (int w = 0; w < kJoinWaves; ++w) {
+            x += xs[w];
+            n += ns[w];
         }
-#pragma unroll
-        for (int off = 32; off > 0; off >>= 1) {
-            x += __shfl_xor(x, off);
-            n += __shfl_xor(n, off);
-        }
-        if (threadIdx.x == 0) {
-            if (blockIdx.x == 0) {
-                tv = 0;
-                for (int w = 0; w < kJoinExperts * kJoinRows / 64; ++w) tv += toks[w];
-                counts[E] = tv;
-            }
-            ws.x[blockIdx.x] = x;
-            ws.n[blockIdx.x] = n;
-            __threadfence();
-            last = atomicAdd(ws.ticket, 1u) == gridDim.x - 1;
-        }
+        ws.x[blockIdx.x] = x;
+        ws.n[blockIdx.x] = n;
+        __threadfence();
+        last = atomicAdd(ws.ticket, 1u) == gridDim.x - 1;
     }
     __syncthreads();
-    if (last && threadIdx.x == 0 && loss) {
+    if (last && wave == 0) {
         __threadfence();
         double x = 0.0;
         int n = 0;
-        for (unsigned b = 0; b < gridDim.x; ++b) {
+        for (unsigned b = lane; b < gridDim.x; b += 64) {
             x += __hip_atomic_load(&ws.x[b], __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
             n += __hip_atomic_load(&ws.n[b], __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
         }
-        *loss = balance_loss(E, x, n, __hip_atomic_load(&counts[E], __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT));
+#pragma unroll
+        for (int off = 32; off > 0; off >>= 1) x += __shfl_xor(x, off);
+        n = lane_reduce<64>(n, [](int a, int b) { return a + b; });
+        if (lane == 0)
+            *loss = balance_loss(E, x, n, __hip_atomic_load(&counts[E], __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT));
     }
 }
 
@@ -432,8 +404,8 @@ __global__ void __launch_bounds__(kRouteThreads) route_backward_kernel(RouteArgs
         const float f = C > 0 && tv > 0 ? *p.dloss / ((float)C * (float)tv) : 0.0f;
 #pragma unroll
         for (int i = 0; i < EPL; ++i) {
-            const int e = expert_of<LPT, EPL, VEC>(i, sub);
-            if (e < E) h0[i] = f * (float)__builtin_fma((double)E, (double)p.counts[e], -(double)C);
+            const int e = expert_of<LPT, EPL, VEC>(i, sub), c = p.counts[e < E ? e : E - 1];
+            h0[i] = f * (float)__builtin_fma((double)E, (double)c, -(double)C);
         }
     }
     for (; t < p.T; t += (int64_t)gridDim.x * TPB) {
@@ -449,9 +421,9 @@ __global__ void __launch_bounds__(kRouteThreads) route_backward_kernel(RouteArgs
             dw = held ? p.dw[t * p.topk + k] : 0.0f;
         };
         entries(0);
-        float pe[EPL], out[EPL], top = 0.0f, sum = 1.0f;
+        float pe[EPL], out[EPL], top = 0.0f, inv = 0.0f;
         int kind = ROW_EMPTY;
-        if (live) kind = row_softmax<DT, LPT, EPL>(raw, pe, top, sum);
+        if (live) kind = row_softmax<DT, LPT, EPL>(raw, pe, top, inv);
         if (t + (int64_t)gridDim.x * TPB < p.T)
             load_row<DT, LPT, EPL, VEC>(p.logits, (t + (int64_t)gridDim.x * TPB) * p.ld, E, sub, raw);
         if (kind != ROW_OK) {
@@ -459,7 +431,6 @@ __global__ void __launch_bounds__(kRouteThreads) route_backward_kernel(RouteArgs
 #pragma unroll
             for (int i = 0; i < EPL; ++i) out[i] = fill;
         } else {
-            const float inv = 1.0f / sum;
             float sel[EPL];
 #pragma unroll
             for (int i = 0; i < EPL; ++i) sel[i] = 0.0f;
@@ -570,12 +541,12 @@ static RouteShape route_shape(int64_t E) {
 }
 
 // Blocks of a counting call: one while it has at most two rounds of tokens (a second
-// launch costs as much as a round), at most 256 (their sums are read back).
+// launch costs as much as a round).
 static int64_t route_blocks(int64_t T, int64_t E) {
     const int64_t tpb = kCountThreads / route_shape(E).lpt;
     if (T <= 2 * tpb) return 1;
     const int64_t b = (T + tpb - 1) / tpb;
-    return b < 256 ? b : 256;
+    return b < kMaxBlocks ? b : kMaxBlocks;
 }
 
 static size_t route_space(int64_t blocks, int64_t E, void *workspace, RouteSpace *out) {
@@ -614,8 +585,8 @@ static hipError_t route_launch(const RouteArgs &p, void *workspace, hipStream_t 
     auto kern = vec ? route_kernel<DT, LPT, EPL, true, true> : route_kernel<DT, LPT, EPL, false, true>;
     hipLaunchKernelGGL(kern, dim3((unsigned)nb), dim3(kCountThreads), 0, stream, p, ws);
     if (nb > 1)
-        hipLaunchKernelGGL(route_join_kernel, dim3((unsigned)((p.E + kJoinExperts - 1) / kJoinExperts)),
-                           dim3(kJoinExperts * kJoinRows), 0, stream, ws, (int)nb, p.E, p.counts, p.loss);
+        hipLaunchKernelGGL(route_join_kernel, dim3((unsigned)(p.E / kJoinWaves + 1)), dim3(kJoinWaves * 64), 0, stream,
+                           ws, (int)nb, p.E, p.counts, p.loss);
     return hipGetLastError();
 }
 

@@ -518,8 +518,7 @@ w8a8_tile_kernel(W8A8Args p, unsigned mtiles, unsigned ncb, unsigned per_xcd) {
         for (int ct = 0; ct < CT; ++ct)
 #pragma unroll
             for (int rt = 0; rt < RT; ++rt)
-                acc[rt][ct] = __builtin_amdgcn_mfma_i32_16x16x64_i8(__builtin_bit_cast(i32x4_t, wf[ct]),
-                                                                    __builtin_bit_cast(i32x4_t, xf[rt]), acc[rt][ct], 0, 0, 0);
+                acc[rt][ct] = __builtin_amdgcn_mfma_i32_16x16x64_i8((i32x4_t)wf[ct], (i32x4_t)xf[rt], acc[rt][ct], 0, 0, 0);
         __builtin_amdgcn_sched_barrier(0);
     };
     using std::integral_constant;

@@ -663,6 +663,16 @@ static hipError_t quantize_launch(const void *x, int64_t ldx, const int32_t *row
 template <int DT>
 static hipError_t quantize_dispatch(const void *x, int64_t ldx, const int32_t *row_count, void *qx, float *sx, int64_t M,
                                     int64_t K, hipStream_t stream) {
+    // Small matrices: one piece per lane, for a short chain of loads and conversions (77 rows of 8192:
+    // 3.9 us against 5.9); large ones: more per lane, fewer maxima across waves (4096 rows of
+    // 4096: 13.3 us against 15.6; 1024 rows: 5.6 against 5.8).
+    if (M * K <= int64_t(3) << 20) {
+        if (K <= 512) return quantize_launch<DT, 1, 1>(x, ldx, row_count, qx, sx, M, K, stream);
+        if (K <= 2048) return quantize_launch<DT, 4, 1>(x, ldx, row_count, qx, sx, M, K, stream);
+        if (K <= 4096) return quantize_launch<DT, 8, 1>(x, ldx, row_count, qx, sx, M, K, stream);
+        if (K <= 8192) return quantize_launch<DT, 16, 1>(x, ldx, row_count, qx, sx, M, K, stream);
+        return quantize_launch<DT, 16, 2>(x, ldx, row_count, qx, sx, M, K, stream);
+    }
     if (K <= 1024) return quantize_launch<DT, 1, 2>(x, ldx, row_count, qx, sx, M, K, stream);
     if (K <= 2048) return quantize_launch<DT, 1, 4>(x, ldx, row_count, qx, sx, M, K, stream);
     if (K <= 4096) return quantize_launch<DT, 4, 2>(x, ldx, row_count, qx, sx, M, K, stream);

@@ -734,7 +734,7 @@ struct W8A8Kernel {
                                // workgroup, per round of resident workgroups
 };
 static constexpr W8A8Kernel kKernels[] = {{16, 16, 2, 16, 0.70, 4.3, 2.7},  {32, 64, 2, 8, 2.2, 1.36, 0.4},
-                                          {32, 32, 2, 8, 1.16, 7.1, 0.2},   {64, 64, 3, 0, 0.153, 0.089, 0.1},
+                                          {32, 32, 2, 16, 2.2, 7.1, 0.2},   {64, 64, 3, 0, 0.153, 0.089, 0.1},
                                           {64, 128, 3, 0, 0.282, 0.099, 0.7}, {128, 256, 1, 0, 0.399, 0, 1.4},
                                           {256, 256, 1, 0, 0.529, 0, 1.0}};
 constexpr int kKernelCount = sizeof(kKernels) / sizeof(kKernels[0]);
@@ -776,13 +776,10 @@ static void pick_kernel(const W8A8Args &p, int &kernel, int &slices) {
     // grouped: the experts' row counts are on the device.  With counts spread as skewed routing spreads
     // them (exponentially around their mean), an expert has 1 / (1 - exp(-bm / mean)) row tiles.
     const double held = (double)(p.M < p.E ? p.M : p.E), mean = p.offsets ? (double)p.M / held : 0;
-    if (p.offsets ? p.M <= 3 * (int64_t)p.E : p.M <= 16) {
-        // grouped, M / E = 0.5, 1, 2 (64 experts, 2048 x 2816): 28.7, 46.3, 60.5 us against 33, 59, 65 us with
-        // 64 x 128 tiles; M / E = 4: 70.8 against 68.6 us
-        kernel = p.offsets ? 2 : 0;
-        return;
-    }
+    // At most 8 rows per expert on average: 16-row tiles (64 experts, 1408 x 2048, M / E = 0.5, 2, 4, 8: 15.5,
+    // 27.5, 35.4, 42.4 us against 19, 34, 40, 46 us with the best others; M / E = 16: 51.5 against 49.9 us).
     kernel = 0;
+    if (p.offsets ? p.M <= 8 * (int64_t)p.E : p.M <= 16) return;
     double best = 1e30;
     for (int i = 0; i < kKernelCount; ++i) {
         const W8A8Kernel &k = kKernels[i];
@@ -808,13 +805,15 @@ static hipError_t w8a8_dispatch(const W8A8Args &args, hipStream_t stream) {
     pick_kernel(p, kernel, p.slices);
     switch (kernel) {
         case 0:
+            // grouped: one group of weights in flight leaves room for two workgroups on a compute unit
+            // (M / E = 0.5 as above: 15.5 us against 18.6)
             switch (split_columns(p.N, GROUPED ? (p.M < p.E ? p.M : p.E) : 1)) {
-                case 4: return split_launch<DT, 1, 4, 2, 16, GROUPED, false>(p, stream);
+                case 4: return split_launch<DT, 1, 4, GROUPED ? 1 : 2, 16, GROUPED, false>(p, stream);
                 case 2: return split_launch<DT, 1, 2, 2, 16, GROUPED, false>(p, stream);
                 default: return split_launch<DT, 1, 1, 4, 16, GROUPED, false>(p, stream);
             }
         case 1: return split_launch<DT, 2, 4, 2, 8, GROUPED, false>(p, stream);
-        case 2: return split_launch<DT, 2, 2, 2, 8, GROUPED, false>(p, stream);
+        case 2: return split_launch<DT, 2, 2, 1, 16, GROUPED, false>(p, stream);
         case 3: return tile8_launch<DT, 64, 64, 2, 2, 2, 3, GROUPED>(p, stream);
         case 4: return tile8_launch<DT, 64, 128, 2, 2, 2, 2, GROUPED>(p, stream);
         case 5: return tile8_launch<DT, 128, 256, 2, 4, 2, 3, GROUPED>(p, stream);

@@ -87,18 +87,34 @@ __device__ __forceinline__ float value_of(uint32_t raw) {
     else return h2f<DT>((uint16_t)raw);
 }
 
-// Logits in an order that unsigned integers compare by; -0 counts as +0, -inf is 0, less
-// than every choice.  16-bit types carry the expert along (a lower one is larger), so one
-// maximum decides ties too.
+// Logits in an order that unsigned integers compare by; -0 counts as +0, and keys up to kNoKey
+// (-inf's, and 0 for an expert already chosen) are no choice.  16-bit types carry the expert
+// along (a lower one is larger), so one maximum decides ties too.
 template <int DT>
-__device__ __forceinline__ uint32_t key_of(uint32_t raw, int e) {
+constexpr uint32_t kNoKey = DT == DT_F32 ? 0x007FFFFFu : DT == DT_BF16 ? 0x007FFFFFu : 0x03FFFFFFu;
+
+template <int DT, int LPT, int EPL, bool VEC>
+__device__ __forceinline__ void make_keys(uint32_t (&key)[EPL], int sub) {
     if constexpr (DT == DT_F32) {
-        const uint32_t u = raw == 0x80000000u ? 0u : raw;
-        return raw == 0xFF800000u ? 0u : u ^ ((uint32_t)((int32_t)u >> 31) | 0x80000000u);
+#pragma unroll
+        for (int i = 0; i < EPL; ++i) {
+            const uint32_t u = key[i] == 0x80000000u ? 0u : key[i];
+            key[i] = u ^ ((uint32_t)((int32_t)u >> 31) | 0x80000000u);
+        }
     } else {
-        const uint32_t u = raw == 0x8000u ? 0u : raw;
-        const uint32_t o = u & 0x8000u ? u ^ 0xFFFFu : u | 0x8000u;
-        return raw == (DT == DT_BF16 ? 0xFF80u : 0xFC00u) ? 0u : o << 16 | (0xFFFFu - (uint32_t)e);
+        typedef unsigned short u16x2 __attribute__((ext_vector_type(2)));
+        typedef short i16x2 __attribute__((ext_vector_type(2)));
+#pragma unroll
+        for (int i = 0; i < EPL; i += 2) {
+            const uint32_t w = key[i] | key[i + 1] << 16;
+            const uint32_t neg = __builtin_bit_cast(uint32_t, as<i16x2>(w) >> 15);          // all ones in negative halves
+            const uint32_t o = w ^ (neg | 0x80008000u);
+            // -0 came to 0x7FFF, +0 to 0x8000
+            const u16x2 up = u16x2{1, 1} - __builtin_elementwise_min(as<u16x2>(o ^ 0x7FFF7FFFu), u16x2{1, 1});
+            const uint32_t k = __builtin_bit_cast(uint32_t, as<u16x2>(o) + up);
+            key[i] = k << 16 | (0xFFFFu - (uint32_t)expert_of<LPT, EPL, VEC>(i, sub));
+            key[i + 1] = (k & 0xFFFF0000u) | (0xFFFFu - (uint32_t)expert_of<LPT, EPL, VEC>(i + 1, sub));
+        }
     }
 }
 template <int DT>
@@ -115,41 +131,44 @@ __device__ __forceinline__ float key_value(uint32_t key) {
 // -inf), or NaN (a NaN or +inf among them).
 enum { ROW_OK = 0, ROW_EMPTY = 1, ROW_NAN = 2 };
 
-// exp(x) for x <= 0: exp2 of x log2(e), whose rounding (up to |x| half steps of the
-// result) is put back as a first-order term.  Results below 2^-126 may be 0.
-__device__ __forceinline__ float exp_neg(float x) {
-    constexpr float kLog2e = 0x1.715476p+0f, kLog2eLow = 0x1.4ae0c0p-26f, kLn2 = 0x1.62e430p-1f;
-    x = fmaxf(x, -150.0f);
-    const float h = x * kLog2e;
-    const float l = __builtin_fmaf(x, kLog2eLow, __builtin_fmaf(x, kLog2e, -h));
-    const float r = __builtin_amdgcn_exp2f(h);
-    return __builtin_fmaf(r, l * kLn2, r);
-}
+// exp(z - max) as exp2 of the difference times log2(e): the difference and the product round
+// once each and log2(e) is off by a quarter of a half step, so the result is off by
+// 2.25 |z - max| half steps and exp2's one step.  -inf gives 0, a NaN or +inf in the row NaN.  Results below 2^-126
+// may be 0.
+constexpr float kLog2e = 0x1.715476p+0f;
+__device__ __forceinline__ float exp_from(float z, float top) { return __builtin_amdgcn_exp2f((z - top) * kLog2e); }
 
-// exp(z - max) (finite whatever the row holds), one over their sum, and the row's kind.  The
-// reciprocal of a row without a distribution is 0 or NaN, which spreads to all its probabilities.
+// A row's exponentials, one over their sum, and its kind.  The reciprocal of a row
+// without a distribution is 0 or NaN (the exponentials of a row of nothing but -inf are set to 0).
 template <int DT, int LPT, int EPL>
 __device__ __forceinline__ int row_softmax(const uint32_t (&raw)[EPL], float (&p)[EPL], float &top, float &inv) {
     float m = -INFINITY;
-    uint32_t nan = 0;
 #pragma unroll
     for (int i = 0; i < EPL; ++i) {
         p[i] = value_of<DT>(raw[i]);
-        m = fmaxf(m, p[i]);
-        nan |= p[i] != p[i] ? 1u : 0u;
+        m = fmaxf(m, p[i]);                       // a NaN does not count here
     }
     top = group_max<LPT>(m);
-    nan = lane_umax<LPT>(nan);
-    const int kind = nan != 0 || top == INFINITY ? ROW_NAN : top == -INFINITY ? ROW_EMPTY : ROW_OK;
+    if (top == -INFINITY) {                       // nothing but -inf, or NaN among it
+        uint32_t nan = 0;
+#pragma unroll
+        for (int i = 0; i < EPL; ++i) {
+            nan |= p[i] != p[i] ? 1u : 0u;
+            p[i] = 0.0f;
+        }
+        const bool any = lane_umax<LPT>(nan) != 0;
+        inv = any ? __builtin_nanf("") : 0.0f;
+        return any ? ROW_NAN : ROW_EMPTY;
+    }
     float s = 0.0f;
 #pragma unroll
     for (int i = 0; i < EPL; ++i) {
-        p[i] = exp_neg(p[i] - top);
+        p[i] = exp_from(p[i], top);
         s += p[i];
     }
     s = group_sum<LPT>(s);
-    inv = kind == ROW_OK ? 1.0f / s : kind == ROW_NAN ? __builtin_nanf("") : 0.0f;
-    return kind;
+    inv = 1.0f / s;
+    return s == s ? ROW_OK : ROW_NAN;
 }
 
 // ---- forward ------------------------------------------------------------------
@@ -216,15 +235,14 @@ __global__ void __launch_bounds__(COUNT ? kCountThreads : kRouteThreads) route_k
             }
             continue;
         }
-#pragma unroll
-        for (int i = 0; i < EPL; ++i) key[i] = key_of<DT>(key[i], expert_of<LPT, EPL, VEC>(i, sub));
-        // the largest that is left, topk times; lane k % LPT keeps choice k (its key, 0 if there
-        // is none) until LPT of them are written together
+        make_keys<DT, LPT, EPL, VEC>(key, sub);
+        // the largest that is left, topk times; lane k % LPT keeps choice k until LPT of them
+        // are written together
         float chosen = 0.0f;
         uint32_t mine = 0;
         int my_id = -1;
         auto flush = [&](int k0, int n) {
-            const float ex = mine ? exp_neg(key_value<DT>(mine) - top) : 0.0f;
+            const float ex = my_id >= 0 ? exp_from(key_value<DT>(mine), top) : 0.0f;
             if (sub < n) {
                 ids[k0 + sub] = my_id;
                 w[k0 + sub] = ex;
@@ -259,7 +277,7 @@ __global__ void __launch_bounds__(COUNT ? kCountThreads : kRouteThreads) route_k
             }
             const bool here = sub == k % LPT;
             mine = here ? best : mine;
-            my_id = here ? (best == 0 ? -1 : be) : my_id;
+            my_id = here ? (best <= kNoKey<DT> ? -1 : be) : my_id;
             if (k % LPT == LPT - 1 && k + 1 < p.topk) flush(k - (LPT - 1), LPT);
         }
         const int k0 = (p.topk - 1) / LPT * LPT;

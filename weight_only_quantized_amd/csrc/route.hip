@@ -15,6 +15,8 @@
 // A group of LPT lanes owns a token, EPL experts each, all of a token's work in
 // registers; 64 / LPT tokens share a wave.  Choosing takes topk rounds of "largest that is left",
 // each a maximum over EPL registers and log2 LPT lane exchanges.
+#include <type_traits>
+
 #include "common.hpp"
 #include "launch.hpp"
 
@@ -117,6 +119,25 @@ __device__ __forceinline__ void make_keys(uint32_t (&key)[EPL], int sub) {
         }
     }
 }
+// Falling order of N keys in registers (odd-even merge sort, 63 exchanges of 16 keys).
+template <int N>
+__device__ __forceinline__ void sort_keys(uint32_t (&key)[N]) {
+#pragma unroll
+    for (int p = 1; p < N; p *= 2)
+#pragma unroll
+        for (int k = p; k >= 1; k /= 2)
+#pragma unroll
+            for (int j = k % p; j + k < N; j += 2 * k)
+#pragma unroll
+                for (int i = 0; i < k; ++i) {
+                    if (i + j + k < N && (i + j) / (2 * p) == (i + j + k) / (2 * p)) {
+                        const uint32_t a = key[i + j], b = key[i + j + k];
+                        key[i + j] = a > b ? a : b;
+                        key[i + j + k] = a > b ? b : a;
+                    }
+                }
+}
+
 template <int DT>
 __device__ __forceinline__ float key_value(uint32_t key) {
     if constexpr (DT == DT_F32) {
@@ -253,13 +274,18 @@ __global__ void __launch_bounds__(COUNT ? kCountThreads : kRouteThreads) route_k
             chosen += sub < n ? ex : 0.0f;
             return ex;
         };
-        for (int k = 0; k < p.topk; ++k) {
-            uint32_t m = key[0];
+        auto keep = [&](int k, uint32_t best, int be) {
+            const bool here = sub == k % LPT;
+            mine = here ? best : mine;
+            my_id = here ? (best <= kNoKey<DT> ? -1 : be) : my_id;
+            if (k % LPT == LPT - 1 && k + 1 < p.topk) flush(k - (LPT - 1), LPT);
+        };
+        if constexpr (DT == DT_F32) {
+            for (int k = 0; k < p.topk; ++k) {
+                uint32_t m = key[0];
 #pragma unroll
-            for (int i = 1; i < EPL; ++i) m = key[i] > m ? key[i] : m;
-            const uint32_t best = lane_umax<LPT>(m);
-            int be;
-            if constexpr (DT == DT_F32) {
+                for (int i = 1; i < EPL; ++i) m = key[i] > m ? key[i] : m;
+                const uint32_t best = lane_umax<LPT>(m);
                 uint32_t at = 0;                                 // the lowest expert at the best value, as 0xFFFF - e
 #pragma unroll
                 for (int i = 0; i < EPL; ++i) {
@@ -267,18 +293,30 @@ __global__ void __launch_bounds__(COUNT ? kCountThreads : kRouteThreads) route_k
                     const uint32_t c = key[i] == best ? v : 0u;
                     at = c > at ? c : at;
                 }
-                be = 0xFFFF - (int)lane_umax<LPT>(at);
+                const int be = 0xFFFF - (int)lane_umax<LPT>(at);
 #pragma unroll
                 for (int i = 0; i < EPL; ++i) key[i] = expert_of<LPT, EPL, VEC>(i, sub) == be ? 0u : key[i];
-            } else {
-                be = 0xFFFF - (int)(best & 0xFFFFu);
-#pragma unroll
-                for (int i = 0; i < EPL; ++i) key[i] = key[i] == best ? 0u : key[i];
+                keep(k, best, be);
             }
-            const bool here = sub == k % LPT;
-            mine = here ? best : mine;
-            my_id = here ? (best <= kNoKey<DT> ? -1 : be) : my_id;
-            if (k % LPT == LPT - 1 && k + 1 < p.topk) flush(k - (LPT - 1), LPT);
+        } else {
+            // Unequal keys: each lane sorts its own once, a round compares the lanes' first ones and
+            // its winner moves up.  Per wave 126 instructions and 25 a round, against 80 a round with a
+            // maximum over all keys and a pass that takes the winner out (16384 tokens, 256 experts:
+            // SORTUS).
+            sort_keys(key);
+            auto rounds = [&](auto depth) {
+                constexpr int DEPTH = decltype(depth)::value;    // at most so many of a lane's keys are chosen
+                for (int k = 0; k < p.topk; ++k) {
+                    const uint32_t best = lane_umax<LPT>(key[0]);
+                    const bool won = key[0] == best;
+#pragma unroll
+                    for (int i = 0; i + 1 < DEPTH; ++i) key[i] = won ? key[i + 1] : key[i];
+                    key[DEPTH - 1] = won ? 0u : key[DEPTH - 1];
+                    keep(k, best, 0xFFFF - (int)(best & 0xFFFFu));
+                }
+            };
+            if (EPL > 8 && p.topk <= 8) rounds(std::integral_constant<int, 8 < EPL ? 8 : EPL>{});
+            else rounds(std::integral_constant<int, EPL>{});
         }
         const int k0 = (p.topk - 1) / LPT * LPT;
         const float ex = flush(k0, p.topk - k0);
@@ -411,12 +449,31 @@ __global__ void __launch_bounds__(kRouteThreads) route_backward_kernel(RouteArgs
     int64_t t = (int64_t)blockIdx.x * TPB + tid / LPT;
     uint32_t raw[EPL];
     if (t < p.T) load_row<DT, LPT, EPL, VEC>(p.logits, t * p.ld, E, sub, raw);
+    // lane k of a token keeps entry k (of LPT at a time)
+    int32_t id = -1;
+    float w = 0.0f, dw = 0.0f;
+    auto entries = [&](int64_t tok, int k0) {
+        const int k = k0 + sub;
+        const bool held = p.dw && tok < p.T && k < p.topk;
+        id = held ? p.ids[tok * p.topk + k] : -1;
+        w = held ? p.w[tok * p.topk + k] : 0.0f;
+        dw = held ? p.dw[tok * p.topk + k] : 0.0f;
+    };
+    entries(t, 0);
     float h0[EPL];
 #pragma unroll
     for (int i = 0; i < EPL; ++i) h0[i] = 0.0f;
     if (p.dloss) {
         int C = 0;                                           // sum of the counts: below 2^31
-        for (int e = tid & 63; e < E; e += 64) C += p.counts[e];
+        constexpr int CL = (LPT * EPL + 63) / 64;
+        int cv[CL];
+#pragma unroll
+        for (int i = 0; i < CL; ++i) {
+            const int e = (tid & 63) + 64 * i;
+            cv[i] = p.counts[e < E ? e : E];
+        }
+#pragma unroll
+        for (int i = 0; i < CL; ++i) C += (tid & 63) + 64 * i < E ? cv[i] : 0;
         C = lane_reduce<64>(C, [](int u, int v) { return u + v; });
         const int tv = p.counts[E];
         const float f = C > 0 && tv > 0 ? *p.dloss / ((float)C * (float)tv) : 0.0f;
@@ -428,17 +485,6 @@ __global__ void __launch_bounds__(kRouteThreads) route_backward_kernel(RouteArgs
     }
     for (; t < p.T; t += (int64_t)gridDim.x * TPB) {
         const bool live = !p.mask || p.mask[t] != 0;
-        // lane k keeps entry k (of LPT at a time)
-        int32_t id = -1;
-        float w = 0.0f, dw = 0.0f;
-        auto entries = [&](int k0) {
-            const int k = k0 + sub;
-            const bool held = p.dw && k < p.topk;
-            id = held ? p.ids[t * p.topk + k] : -1;
-            w = held ? p.w[t * p.topk + k] : 0.0f;
-            dw = held ? p.dw[t * p.topk + k] : 0.0f;
-        };
-        entries(0);
         float pe[EPL], out[EPL], top = 0.0f, inv = 0.0f;
         int kind = ROW_EMPTY;
         if (live) kind = row_softmax<DT, LPT, EPL>(raw, pe, top, inv);
@@ -490,7 +536,7 @@ __global__ void __launch_bounds__(kRouteThreads) route_backward_kernel(RouteArgs
 #pragma unroll
                     for (int i = 0; i < EPL; ++i) sel[i] = 0.0f;
                     for (int k0 = 0; k0 < p.topk; k0 += LPT) {
-                        if (k0 > 0) entries(k0);
+                        if (k0 > 0) entries(t, k0);
                         const float kept = p.renorm ? w * (dw - mean) : dw;
                         const int most = p.topk - k0 < LPT ? p.topk - k0 : LPT;
                         for (int k = 0; k < most; ++k) {
@@ -514,6 +560,7 @@ __global__ void __launch_bounds__(kRouteThreads) route_backward_kernel(RouteArgs
 #pragma unroll
             for (int i = 0; i < EPL; ++i) out[i] = pe[i] * (out[i] - dot) + (p.renorm ? sel[i] : 0.0f);
         }
+        entries(t + (int64_t)gridDim.x * TPB, 0);
         if constexpr (VEC) {
             constexpr int W = EPL * (DT == DT_F32 ? 4 : 2) / 4;
             uint32_t buf[W];

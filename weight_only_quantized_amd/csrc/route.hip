@@ -203,7 +203,7 @@ __device__ __forceinline__ float balance_loss(int E, double x, int n, int tokens
     return (float)(E * x / (cc * tv));
 }
 
-// Workspace: the blocks' sums of probabilities [E][blocks] and counts [E + 1][blocks], and
+// Workspace: the blocks' sums of probabilities [blocks][E] and counts [blocks][E + 1], and
 // the joining blocks' sums and ticket.
 struct RouteSpace {
     float *p;
@@ -213,7 +213,39 @@ struct RouteSpace {
     uint32_t *ticket;
 };
 constexpr int kMaxBlocks = 256;            // of a counting call
-constexpr int kJoinWaves = 8, kMaxJoins = kMoeMaxExperts / kJoinWaves + 1;
+constexpr int kJoinRows = 16, kMaxJoins = kMoeMaxExperts / 64 + 1;
+
+// Sums of v over the 64 / LPT token groups of a wave.  Within a row of 16 lanes by rotation; across
+// rows by exchanging halves of two registers, which adds up both in one register: a lane is left with the
+// first EPL / 4 (LPT 32: EPL / 2) sums from the index that is returned on.
+template <int LPT, int EPL>
+__device__ __forceinline__ int join_groups(float (&v)[EPL]) {
+    if constexpr (LPT == 64) return 0;
+    if constexpr (LPT <= 8) {
+#pragma unroll
+        for (int i = 0; i < EPL; ++i) {
+            auto turn = [&](auto ctrl) {
+                const int o = __builtin_amdgcn_update_dpp(0, __float_as_int(v[i]), decltype(ctrl)::value, 0xF, 0xF, true);
+                v[i] += __int_as_float(o);
+            };
+            if constexpr (LPT == 4) turn(std::integral_constant<int, 0x124>{});       // row_ror:4
+            turn(std::integral_constant<int, 0x128>{});                               // row_ror:8
+        }
+    }
+    const int row = lane_id() >> 4;
+#pragma unroll
+    for (int i = 0; i < EPL / 2; ++i) {
+        const auto s = __builtin_amdgcn_permlane32_swap(__float_as_uint(v[i]), __float_as_uint(v[i + EPL / 2]), false, false);
+        v[i] = __uint_as_float(s[0]) + __uint_as_float(s[1]);
+    }
+    if constexpr (LPT == 32) return (row >> 1) * (EPL / 2);
+#pragma unroll
+    for (int i = 0; i < EPL / 4; ++i) {
+        const auto s = __builtin_amdgcn_permlane16_swap(__float_as_uint(v[i]), __float_as_uint(v[i + EPL / 4]), false, false);
+        v[i] = __uint_as_float(s[0]) + __uint_as_float(s[1]);
+    }
+    return (row >> 1) * (EPL / 2) + (row & 1) * (EPL / 4);
+}
 
 // Counts are kept where COUNT; a single block finishes by itself.
 template <int DT, int LPT, int EPL, bool VEC, bool COUNT>
@@ -326,13 +358,12 @@ __global__ void __launch_bounds__(COUNT ? kCountThreads : kRouteThreads) route_k
     }
     if constexpr (COUNT) {
         // sums over the token groups of a wave, then over the waves
+        const int left = join_groups<LPT, EPL>(pacc);
+        constexpr int KEPT = LPT <= 16 ? EPL / 4 : LPT == 32 ? EPL / 2 : EPL;
 #pragma unroll
-        for (int i = 0; i < EPL; ++i) {
-            float v = pacc[i];
-#pragma unroll
-            for (int off = LPT; off < 64; off <<= 1) v += __shfl_xor(v, off);
-            const int e = expert_of<LPT, EPL, VEC>(i, sub);
-            if ((tid & 63) < LPT && e < E) psum[tid >> 6][e] = v;
+        for (int i = 0; i < KEPT; ++i) {
+            const int e = expert_of<LPT, EPL, VEC>(i + left, sub);
+            if ((tid & 15) < LPT && e < E) psum[tid >> 6][e] = pacc[i];
         }
         __syncthreads();
         float x = 0.0f;
@@ -349,8 +380,8 @@ __global__ void __launch_bounds__(COUNT ? kCountThreads : kRouteThreads) route_k
             if (gridDim.x == 1) {
                 p.counts[e] = c;
             } else {
-                ws.c[(int64_t)e * gridDim.x + blockIdx.x] = c;
-                if (e < E) ws.p[(int64_t)e * gridDim.x + blockIdx.x] = v;
+                ws.c[(int64_t)blockIdx.x * (E + 1) + e] = c;
+                if (e < E) ws.p[(int64_t)blockIdx.x * E + e] = v;
             }
         }
         if (gridDim.x == 1 && p.loss) {
@@ -372,67 +403,64 @@ __global__ void __launch_bounds__(COUNT ? kCountThreads : kRouteThreads) route_k
     }
 }
 
-// Counts and loss from the blocks' sums, in a fixed order: a wave per expert (and one for the
-// tokens), the last workgroup to finish adds up the workgroups' shares of the loss.
-__global__ void __launch_bounds__(kJoinWaves * 64)
+// Counts and loss from the blocks' sums, in a fixed order: a workgroup sums 64 experts
+// (index E: the tokens), kJoinRows waves taking every kJoinRows-th block; the last one to finish adds up the
+// workgroups' shares of the loss.
+__global__ void __launch_bounds__(kJoinRows * 64)
 route_join_kernel(RouteSpace ws, int blocks, int E, int32_t *__restrict__ counts, float *__restrict__ loss) {
-    __shared__ double xs[kJoinWaves];
-    __shared__ int ns[kJoinWaves];
-    __shared__ bool last;
-    const int lane = lane_id(), wave = threadIdx.x >> 6;
-    const int e = blockIdx.x * kJoinWaves + wave;          // E: the tokens
-    int c = 0;
+    constexpr int BATCH = kMaxBlocks / kJoinRows;
+    __shared__ float ps[kJoinRows][64];
+    __shared__ int cs[kJoinRows][64];
+    const int lane = lane_id(), row = threadIdx.x >> 6;
+    const int e = blockIdx.x * 64 + lane, ec = e < E ? e : E;
+    float pv[BATCH];
+    int cv[BATCH];
+    // all loads are on their way before the first is used
+#pragma unroll
+    for (int u = 0; u < BATCH; ++u) {
+        const int64_t b = row + u * kJoinRows < blocks ? row + u * kJoinRows : blocks - 1;
+        cv[u] = ws.c[b * (E + 1) + ec];
+        pv[u] = ws.p[b * E + (e < E ? e : E - 1)];
+    }
     float s = 0.0f;
-    if (e <= E) {
-        int cv[kMaxBlocks / 64];
-        float pv[kMaxBlocks / 64];
+    int c = 0;
 #pragma unroll
-        for (int u = 0; u < kMaxBlocks / 64; ++u) {
-            const int b = lane + 64 * u;
-            cv[u] = b < blocks ? ws.c[(int64_t)e * blocks + b] : 0;
-            pv[u] = b < blocks && e < E ? ws.p[(int64_t)e * blocks + b] : 0.0f;
-        }
-#pragma unroll
-        for (int u = 0; u < kMaxBlocks / 64; ++u) {
-            c += cv[u];
+    for (int u = 0; u < BATCH; ++u)
+        if (row + u * kJoinRows < blocks) {
             s += pv[u];
+            c += cv[u];
         }
-        c = lane_reduce<64>(c, [](int a, int b) { return a + b; });
-        s = group_sum<64>(s);
-        if (lane == 0) counts[e] = c;
-    }
-    if (!loss) return;
-    if (lane == 0) {
-        xs[wave] = e < E ? (double)c * s : 0.0;
-        ns[wave] = e < E ? c : 0;
-    }
+    ps[row][lane] = s;
+    cs[row][lane] = c;
     __syncthreads();
-    if (threadIdx.x == 0) {
-        double x = 0.0;
-        int n = 0;
-        for (int w = 0; w < kJoinWaves; ++w) {
-            x += xs[w];
-            n += ns[w];
-        }
+    if (row != 0) return;
+#pragma unroll
+    for (int r = 1; r < kJoinRows; ++r) {
+        s += ps[r][lane];
+        c += cs[r][lane];
+    }
+    if (e <= E) counts[e] = c;
+    if (!loss) return;
+    double x = e < E ? (double)c * s : 0.0;
+    const int n = lane_reduce<64>(e < E ? c : 0, [](int a, int b) { return a + b; });
+#pragma unroll
+    for (int off = 32; off > 0; off >>= 1) x += __shfl_xor(x, off);
+    int last = 0;
+    if (lane == 0) {
         ws.x[blockIdx.x] = x;
         ws.n[blockIdx.x] = n;
         __threadfence();
         last = atomicAdd(ws.ticket, 1u) == gridDim.x - 1;
     }
-    __syncthreads();
-    if (last && wave == 0) {
+    if (__builtin_amdgcn_readfirstlane(last) && lane == 0) {
         __threadfence();
-        double x = 0.0;
-        int n = 0;
-        for (unsigned b = lane; b < gridDim.x; b += 64) {
+        x = 0.0;
+        int all = 0;
+        for (unsigned b = 0; b < gridDim.x; ++b) {
             x += __hip_atomic_load(&ws.x[b], __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
-            n += __hip_atomic_load(&ws.n[b], __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+            all += __hip_atomic_load(&ws.n[b], __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
         }
-#pragma unroll
-        for (int off = 32; off > 0; off >>= 1) x += __shfl_xor(x, off);
-        n = lane_reduce<64>(n, [](int a, int b) { return a + b; });
-        if (lane == 0)
-            *loss = balance_loss(E, x, n, __hip_atomic_load(&counts[E], __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT));
+        *loss = balance_loss(E, x, all, __hip_atomic_load(&counts[E], __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT));
     }
 }
 
@@ -444,6 +472,7 @@ __global__ void __launch_bounds__(kRouteThreads) route_backward_kernel(RouteArgs
     // a token's gradients through its chosen weights, one place per expert
     __shared__ __attribute__((aligned(16))) float spread[TPB][LPT * EPL];
     const int E = p.E, tid = threadIdx.x, sub = tid % LPT;
+    __shared__ __attribute__((aligned(16))) float hs[LPT * EPL];
     float *const mine = spread[tid / LPT];
     // the first row is on its way while the loss's part of h is formed
     int64_t t = (int64_t)blockIdx.x * TPB + tid / LPT;
@@ -477,11 +506,11 @@ __global__ void __launch_bounds__(kRouteThreads) route_backward_kernel(RouteArgs
         C = lane_reduce<64>(C, [](int u, int v) { return u + v; });
         const int tv = p.counts[E];
         const float f = C > 0 && tv > 0 ? *p.dloss / ((float)C * (float)tv) : 0.0f;
+        for (int e = tid; e < LPT * EPL; e += kRouteThreads)
+            hs[e] = e < E ? f * (float)__builtin_fma((double)E, (double)p.counts[e], -(double)C) : 0.0f;
+        __syncthreads();
 #pragma unroll
-        for (int i = 0; i < EPL; ++i) {
-            const int e = expert_of<LPT, EPL, VEC>(i, sub), c = p.counts[e < E ? e : E - 1];
-            h0[i] = f * (float)__builtin_fma((double)E, (double)c, -(double)C);
-        }
+        for (int i = 0; i < EPL; ++i) h0[i] = hs[expert_of<LPT, EPL, VEC>(i, sub)];
     }
     for (; t < p.T; t += (int64_t)gridDim.x * TPB) {
         const bool live = !p.mask || p.mask[t] != 0;
@@ -650,7 +679,7 @@ static hipError_t route_launch(const RouteArgs &p, void *workspace, hipStream_t 
     auto kern = vec ? route_kernel<DT, LPT, EPL, true, true> : route_kernel<DT, LPT, EPL, false, true>;
     hipLaunchKernelGGL(kern, dim3((unsigned)nb), dim3(kCountThreads), 0, stream, p, ws);
     if (nb > 1)
-        hipLaunchKernelGGL(route_join_kernel, dim3((unsigned)(p.E / kJoinWaves + 1)), dim3(kJoinWaves * 64), 0, stream,
+        hipLaunchKernelGGL(route_join_kernel, dim3((unsigned)(p.E / 64 + 1)), dim3(kJoinRows * 64), 0, stream,
                            ws, (int)nb, p.E, p.counts, p.loss);
     return hipGetLastError();
 }

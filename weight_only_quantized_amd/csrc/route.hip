@@ -210,10 +210,12 @@ struct RouteSpace {
     int32_t *c;
     double *x;
     int32_t *n;
+    int32_t *tokens;
     uint32_t *ticket;
 };
 constexpr int kMaxBlocks = 256;            // of a counting call
 constexpr int kJoinRows = 16, kMaxJoins = kMoeMaxExperts / 64 + 1;
+static_assert(kMaxJoins <= 64, "one wave adds up the joining workgroups");
 
 // Sums of v over the 64 / LPT token groups of a wave.  Within a row of 16 lanes by rotation; across
 // rows by exchanging halves of two registers, which adds up both in one register: a lane is left with the
@@ -445,23 +447,32 @@ route_join_kernel(RouteSpace ws, int blocks, int E, int32_t *__restrict__ counts
     const int n = lane_reduce<64>(e < E ? c : 0, [](int a, int b) { return a + b; });
 #pragma unroll
     for (int off = 32; off > 0; off >>= 1) x += __shfl_xor(x, off);
-    int last = 0;
+    const bool owner = e == E;                    // one lane of the last workgroup has the tokens
+    if (gridDim.x == 1) {
+        const int tokens = __builtin_amdgcn_readlane(c, E & 63);
+        if (lane == 0) *loss = balance_loss(E, x, n, tokens);
+        return;
+    }
+    // What crosses workgroups is stored and loaded at device scope, past the XCDs' caches, so that
+    // waiting for the stores orders them before the ticket without writing a cache back.
+    if (owner) __hip_atomic_store(ws.tokens, c, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
     if (lane == 0) {
-        ws.x[blockIdx.x] = x;
-        ws.n[blockIdx.x] = n;
-        __threadfence();
-        last = atomicAdd(ws.ticket, 1u) == gridDim.x - 1;
+        __hip_atomic_store(&ws.x[blockIdx.x], x, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+        __hip_atomic_store(&ws.n[blockIdx.x], n, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
     }
-    if (__builtin_amdgcn_readfirstlane(last) && lane == 0) {
-        __threadfence();
-        x = 0.0;
-        int all = 0;
-        for (unsigned b = 0; b < gridDim.x; ++b) {
-            x += __hip_atomic_load(&ws.x[b], __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
-            all += __hip_atomic_load(&ws.n[b], __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
-        }
-        *loss = balance_loss(E, x, all, __hip_atomic_load(&counts[E], __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT));
-    }
+    asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
+    unsigned order = 0;
+    if (lane == 0) order = __hip_atomic_fetch_add(ws.ticket, 1u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+    if (__builtin_amdgcn_readfirstlane(order) != gridDim.x - 1) return;
+    asm volatile("" ::: "memory");
+    const bool in = lane < (int)gridDim.x;
+    x = in ? __hip_atomic_load(&ws.x[lane], __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT) : 0.0;
+    const int part = in ? __hip_atomic_load(&ws.n[lane], __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT) : 0;
+    const int tokens = __hip_atomic_load(ws.tokens, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+#pragma unroll
+    for (int off = 32; off > 0; off >>= 1) x += __shfl_xor(x, off);
+    const int all = lane_reduce<64>(part, [](int a, int b) { return a + b; });
+    if (lane == 0) *loss = balance_loss(E, x, all, tokens);
 }
 
 // ---- backward -----------------------------------------------------------------
@@ -649,7 +660,8 @@ static size_t route_space(int64_t blocks, int64_t E, void *workspace, RouteSpace
     RouteSpace r;
     r.x = (double *)at;
     r.n = (int32_t *)(r.x + kMaxJoins);
-    r.ticket = (uint32_t *)(r.n + kMaxJoins);
+    r.tokens = r.n + kMaxJoins;
+    r.ticket = (uint32_t *)(r.tokens + 1);
     r.p = (float *)(r.ticket + 4);
     r.c = (int32_t *)(r.p + blocks * E);
     if (out) *out = r;

@@ -592,12 +592,16 @@ w4a16_status w8a8_gemm_prequant(const void *qx, const float *sx, const void *w_p
                                 const void *bias, void *y, int64_t ldy, int64_t M, int64_t K, int64_t N, int dt,
                                 void *stream);
 
-/* Scratch of w8a8_gemm: the codes and scales of M rows.  0 for sizes that the call rejects. */
+/* Scratch of w8a8_gemm: the codes and scales of M rows, and for M <= 1024 another 32 MiB
+ * for the sums of K slices.  0 for sizes that the call rejects. */
 size_t w8a8_workspace_bytes(int64_t M, int64_t K);
 
 /* y [M][N] from x [M][K] (dtype dt): w8a8_quantize into the workspace, then the
- * product.  Contents of the workspace on entry are ignored, on return unspecified;
- * calls sharing it must be ordered on one stream. */
+ * product; up to about 16384 elements of x (4 rows of 4096) in one kernel that quantizes x while the
+ * first weights are on their way.  Up to 16 rows run a kernel whose waves split K, more
+ * rows that one or tiles, cut into slices of K whose sums meet in the workspace where the tiles are
+ * few.  Contents of the workspace on entry are ignored, on return unspecified; calls
+ * sharing it must be ordered on one stream.  ldx, ldy: row strides of x and y. */
 w4a16_status w8a8_gemm(const void *x, int64_t ldx, const void *w_packed, const float *sw, const void *bias, void *y,
                        int64_t ldy, int64_t M, int64_t K, int64_t N, int dt, void *workspace, size_t workspace_bytes,
                        void *stream);

@@ -99,11 +99,14 @@ def spread(z):
 
 
 def prob_bound(z):
-    """Relative error of a softmax weight: the difference z - max is rounded once
-    (|difference| half steps in the exponent), exp is within one step, the sum of up to 1024
-    exponentials goes through at most 16 + 6 additions, then a reciprocal, a product and,
-    renormalized, a sum of the chosen ones and a division."""
-    return U32 * (2 * spread(z).amax() + 2 + 2 + 22 + 3 + 12)
+    """Relative error of a softmax weight, in half steps of fp32.  The difference d = max - z and
+    its product with log2(e) round once each, and log2(e) = 1.44269504 in fp32 is off by 1.93e-8, less than
+    a quarter of a half step: |d| (1 + 1 + 1/4) in the exponent; exp2 is within one step (2).
+    The sum over the row carries the mean of these errors by weight: the mean of d under the
+    softmax is at most its entropy, ln 1024 < 7.  That sum goes through at most 16 + 6 additions,
+    then a reciprocal, a product and, renormalized, a sum of the chosen ones and a division."""
+    far = spread(z).amax()
+    return U32 * (2.25 * (far + min(float(far), 7.0)) + 2 + 2 + 22 + 3 + 12)
 
 
 def route_backward(z, ids, w, counts, dw, dloss, renorm, mask=None):

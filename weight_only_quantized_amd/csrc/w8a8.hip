@@ -7,6 +7,11 @@
 // The integer sum is exact (|q W| <= 2^14 and K < 2^17: below 2^31), so every
 // kernel and every split of K gives the same bits.
 //
+// Bounds.  Few rows: the weights' bytes (one row of 4096 x 14336 with its quantization 12.5 us,
+// 4.7 TB/s; a large copy reaches 4.93).  Many rows: the matrix core (8192^3 410 us, 2.67 POP/s,
+// the matrix core busy in 75% of the clocks at the 1.7 GHz that its power leaves; zeros for data
+// take 360 us).  In between: what 64-row tiles draw from L2 into LDS, about 12 TB/s.
+//
 // Weights: the 2048-byte tiles of w8.hip (16 columns x 128 rows, stored as
 // q + 128; slot 16 c + j holds rows 32 c .. + 31 of column j).  Matrix-core
 // mapping (v_mfma_i32_16x16x64_i8): W is the first operand and x the second,
@@ -114,7 +119,8 @@ __device__ __forceinline__ u32x2s_t codes_of(const u32x4_t &v, const RowQuant &r
 
 // Quantization kernel: NW waves per row (workgroups of at least four waves), C pieces of 8
 // values per lane in registers between the maximum and the codes.  Bound by memory:
-// 3 bytes per element.
+// 3 bytes per element (4096 x 4096: 13 us, 3.9 TB/s); small calls by a load, the maximum across
+// waves and the conversions in turn (77 x 8192: 4 us).
 template <int DT, int NW, int C>
 __global__ void __launch_bounds__(NW > 4 ? NW * 64 : 256)
 w8a8_quantize_kernel(const uint16_t *__restrict__ x, int64_t ldx, const int32_t *__restrict__ row_count,
@@ -210,7 +216,8 @@ __device__ __forceinline__ bool expert_tile(const int32_t *__restrict__ offsets,
 // ---------------------------------------------------------------------------
 // Split-K kernel: a workgroup owns 16 MT rows x 16 NB columns, its waves split
 // the 128-row groups of K and meet in LDS.  Each wave keeps the weights of D groups
-// in flight in registers.  FUSED: x comes in 16 bits, and the workgroup quantizes its
+// in flight in registers; W goes from memory into operands without LDS, since each byte is used by one
+// wave only.  FUSED: x comes in 16 bits, and the workgroup quantizes its
 // rows into LDS while the first weights are on their way.
 // ---------------------------------------------------------------------------
 constexpr int kHeld = 2;                         // pieces of 512 elements that a wave of a fused call quantizes
@@ -694,7 +701,7 @@ static hipError_t split_launch(const W8A8Args &p, hipStream_t stream) {
     const int64_t ncb = p.N / (16 * NB);
     const int64_t few = p.M < p.E ? p.M : p.E;                 // experts that can end in a partial tile
     const int64_t mtiles = GROUPED ? p.M / (16 * MT) + few : (p.M + 16 * MT - 1) / (16 * MT);
-    if (p.N % (16 * NB) != 0 || mtiles * ncb > INT32_MAX) return hipErrorInvalidConfiguration;
+    if (p.N % (16 * NB) != 0 || mtiles * ncb * W * 64 > UINT32_MAX) return hipErrorInvalidConfiguration;
     hipLaunchKernelGGL((w8a8_split_kernel<DT, MT, NB, D, WMAX, GROUPED, FUSED>), dim3((unsigned)(mtiles * ncb)),
                        dim3(W * 64), 0, stream, p, (unsigned)mtiles, (unsigned)ncb);
     return hipGetLastError();
@@ -708,7 +715,7 @@ static hipError_t tile8_launch(const W8A8Args &p, hipStream_t stream) {
     const int64_t few = p.M < p.E ? p.M : p.E;
     const int64_t mtiles = GROUPED ? p.M / BM + few : (p.M + BM - 1) / BM;
     const int64_t per_xcd = (mtiles * ncb * p.slices + kXcd8 - 1) / kXcd8;
-    if (per_xcd * kXcd8 > INT32_MAX || p.slices < 1 || p.K / kGroup < p.slices) return hipErrorInvalidConfiguration;
+    if (per_xcd * kXcd8 * WM * WN * 64 > UINT32_MAX || p.slices < 1 || p.K / kGroup < p.slices) return hipErrorInvalidConfiguration;
     if (p.slices > 1 && (GROUPED || !slices_fit(p, p.slices))) return hipErrorInvalidConfiguration;
     hipLaunchKernelGGL((w8a8_tile_kernel<DT, BM, BN, WM, WN, HALVES, NBUF, GROUPED>), dim3((unsigned)(per_xcd * kXcd8)),
                        dim3(WM * WN * 64), 0, stream, p, (unsigned)mtiles, (unsigned)ncb, (unsigned)per_xcd);

@@ -403,8 +403,10 @@ __device__ __forceinline__ void wait_and_meet() {
     asm volatile("s_waitcnt vmcnt(%0) lgkmcnt(0)\n\ts_barrier" ::"n"(N) : "memory");
 }
 
+// (Registers for as many workgroups per compute unit as LDS holds: 64 x 128 tiles three, which
+// take 106 us instead of 118 for 512 tokens top-8 of 64 experts, 2048 x 2816.)
 template <int DT, int BM, int BN, int WM, int WN, int HALVES, int NBUF, bool GROUPED>
-__global__ void __launch_bounds__(WM * WN * 64)
+__global__ void __launch_bounds__(WM * WN * 64, WM * WN == 8 ? 2 : (160 << 10) / (NBUF * (BM + BN) * 64 * HALVES))
 w8a8_tile_kernel(W8A8Args p, unsigned mtiles, unsigned ncb, unsigned per_xcd) {
     constexpr int NW = WM * WN, TM = BM / WM, TN = BN / WN, RT = TM / 16, CT = TN / 16;
     constexpr int SK = 64 * HALVES, ABYTES = BM * SK, SBYTES = ABYTES + BN * SK;
@@ -486,7 +488,7 @@ w8a8_tile_kernel(W8A8Args p, unsigned mtiles, unsigned ncb, unsigned per_xcd) {
         place = place + SBYTES == NBUF * SBYTES ? 0 : place + SBYTES;
     };
 #pragma unroll
-    for (int s = 0; s < NBUF - 1; ++s)
+    for (int s = 0; s < (NW == 8 ? NBUF - 1 : NBUF); ++s)
         if (s < S) fetch();
 
     // LDS offsets of this lane's operands in the first half of a stage
@@ -503,81 +505,117 @@ w8a8_tile_kernel(W8A8Args p, unsigned mtiles, unsigned ncb, unsigned per_xcd) {
 #pragma unroll
         for (int ct = 0; ct < CT; ++ct) acc[rt][ct] = i32x4_t{0, 0, 0, 0};
 
-    u32x4_t xf[RT], wf[CT];
-    uint32_t at = 0;                         // place of the stage that is multiplied
-    auto read = [&](int half) {
+    constexpr int SETS = NW == 8 ? 1 : 2 * HALVES;      // operands of half stages in registers
+    u32x4_t xf[SETS][RT], wf[SETS][CT];
+    uint32_t at = 0;                         // place of the next stage to read
+    auto read = [&](auto set, int half) {
+        constexpr int U = decltype(set)::value;
         const uint8_t *base = lds + at;
 #pragma unroll
         for (int ct = 0; ct < CT; ++ct)
-            wf[ct] = *reinterpret_cast<const u32x4_t *>(base + (boff ^ ((ct & 1) * 128)) + (ct >> 1) * 2048 * HALVES + half * 1024);
+            wf[U][ct] = *reinterpret_cast<const u32x4_t *>(base + (boff ^ ((ct & 1) * 128)) + (ct >> 1) * 2048 * HALVES + half * 1024);
 #pragma unroll
         for (int rt = 0; rt < RT; ++rt)
-            xf[rt] = *reinterpret_cast<const u32x4_t *>(base + (aoff ^ (half * 64)) + rt * 16 * SK);
+            xf[U][rt] = *reinterpret_cast<const u32x4_t *>(base + (aoff ^ (half * 64)) + rt * 16 * SK);
+    };
+    auto passed = [&]() { at = at + SBYTES == NBUF * SBYTES ? 0 : at + SBYTES; };
+    auto to_signed = [&](auto set) {
+        constexpr int U = decltype(set)::value;
 #pragma unroll
         for (int ct = 0; ct < CT; ++ct) {
-            wf[ct] ^= 0x80808080u;                     // u = q + 128 to two's complement q
-            asm volatile("" : "+v"(wf[ct]));
+            wf[U][ct] ^= 0x80808080u;                  // u = q + 128 to two's complement q
+            asm volatile("" : "+v"(wf[U][ct]));
         }
     };
-    auto multiply = [&]() {
+    auto multiply = [&](auto set) {
+        constexpr int U = decltype(set)::value;
         __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
         for (int ct = 0; ct < CT; ++ct)
 #pragma unroll
             for (int rt = 0; rt < RT; ++rt)
-                acc[rt][ct] = __builtin_amdgcn_mfma_i32_16x16x64_i8((i32x4_t)wf[ct], (i32x4_t)xf[rt], acc[rt][ct], 0, 0, 0);
+                acc[rt][ct] = __builtin_amdgcn_mfma_i32_16x16x64_i8((i32x4_t)wf[U][ct], (i32x4_t)xf[U][rt], acc[rt][ct], 0, 0, 0);
         __builtin_amdgcn_sched_barrier(0);
     };
     using std::integral_constant;
-    using Yes = integral_constant<bool, true>;
-    using No = integral_constant<bool, false>;
-    // One stage; WAIT later loads may be outstanding at its wait.
-    //
-    // Four waves: stage s has landed and stage s - 1 is in everybody's registers at the one
-    // barrier, and the place of stage s - 1 is filled again; a second workgroup on the compute
-    // unit fills the gaps.
-    //
-    // Eight waves: two groups, one wave of each on every SIMD, take turns: while one multiplies
-    // a half stage, the other reads its operands.  A phase ends in a barrier; group 0 reads half
-    // h of stage s in phase 2 (HALVES s + h) and multiplies it in the next, group 1 one phase
-    // later.  The place of stage s - 1 is free when group 0 begins stage s (group 1 has read its last
-    // half in the phase before) and is filled again from there on.  Every wave waits for its
-    // loads of stage s + 1 at the end of its last reads of stage s, which is a barrier before group 0
-    // reads stage s + 1.
-    auto stage = [&](auto wait, auto refill) {
-        constexpr int WAIT = decltype(wait)::value;
-        if constexpr (NW == 8) {
+    using Zero = integral_constant<int, 0>;
+    if constexpr (NW == 8) {
+        // Two groups of waves, one wave of each on every SIMD, take turns: while one multiplies
+        // a half stage, the other reads its operands.  A phase ends in a barrier; group 0 reads half
+        // h of stage s in phase 2 (HALVES s + h) and multiplies it in the next, group 1 one phase
+        // later.  The place of stage s - 1 is free when group 0 begins stage s (group 1 has read its last
+        // half in the phase before) and is filled again from there on.  Every wave waits for its
+        // loads of stage s + 1 (WAIT later loads may be outstanding) at the end of its last reads of
+        // stage s, which is a barrier before group 0 reads stage s + 1.
+        auto stage = [&](auto wait, auto refill) {
+            constexpr int WAIT = decltype(wait)::value;
             if constexpr (decltype(refill)::value) fetch();
 #pragma unroll
             for (int h = 0; h < HALVES; ++h) {
-                read(h);
+                read(Zero{}, h);
+                to_signed(Zero{});
                 if (h == HALVES - 1) wait_and_meet<WAIT>();
                 else wait_and_meet<63>();
-                multiply();
+                multiply(Zero{});
                 wait_and_meet<63>();
             }
-        } else {
-            wait_and_meet<WAIT>();
-            if constexpr (decltype(refill)::value) fetch();
-#pragma unroll
-            for (int h = 0; h < HALVES; ++h) {
-                read(h);
-                multiply();
-            }
-        }
-        at = at + SBYTES == NBUF * SBYTES ? 0 : at + SBYTES;
-    };
-    using Rest = integral_constant<int, (NBUF - 2) * L>;
-    if constexpr (NW == 8) {
+            passed();
+        };
         if (S >= NBUF - 1) wait_and_meet<(NBUF - 2) * L>();
         else wait_and_meet<0>();
         if (wave >= 4) wait_and_meet<63>();
-    }
-    int s = 0;
-    for (; s + NBUF <= S; ++s) stage(Rest{}, Yes{});
-    for (; s < S; ++s) stage(integral_constant<int, 0>{}, No{});
-    if constexpr (NW == 8) {
+        int s = 0;
+        for (; s + NBUF <= S; ++s) stage(integral_constant<int, (NBUF - 2) * L>{}, integral_constant<bool, true>{});
+        for (; s < S; ++s) stage(Zero{}, integral_constant<bool, false>{});
         if (wave < 4) wait_and_meet<63>();
+    } else {
+        // The operands of stage s + 1 are on their way into registers while stage s is multiplied.
+        // Behind the barrier stage s + 1 has landed and everybody has read stage s, whose place is
+        // filled again.
+        auto read_stage = [&](auto set) {
+            constexpr int U = decltype(set)::value * HALVES;
+            read(integral_constant<int, U>{}, 0);
+            if constexpr (HALVES == 2) read(integral_constant<int, U + HALVES - 1>{}, 1);
+            passed();
+        };
+        auto multiply_stage = [&](auto set) {
+            constexpr int U = decltype(set)::value * HALVES;
+            to_signed(integral_constant<int, U>{});
+            multiply(integral_constant<int, U>{});
+            if constexpr (HALVES == 2) {
+                to_signed(integral_constant<int, U + HALVES - 1>{});
+                multiply(integral_constant<int, U + HALVES - 1>{});
+            }
+        };
+        auto step = [&](auto set) {
+            wait_and_meet<(NBUF - 2) * L>();
+            fetch();
+            read_stage(integral_constant<int, 1 - decltype(set)::value>{});
+            __builtin_amdgcn_sched_barrier(0);
+            multiply_stage(set);
+        };
+        auto last_step = [&](auto set, int s) {
+            if (s + 1 < S) {
+                wait_and_meet<0>();
+                if (s + NBUF < S) fetch();
+                read_stage(integral_constant<int, 1 - decltype(set)::value>{});
+                __builtin_amdgcn_sched_barrier(0);
+            }
+            multiply_stage(set);
+        };
+        using One = integral_constant<int, 1>;
+        if (S >= NBUF) wait_and_meet<(NBUF - 1) * L>();
+        else wait_and_meet<0>();
+        read_stage(Zero{});
+        int s = 0;
+        for (; s + 1 + NBUF < S; s += 2) {
+            step(Zero{});
+            step(One{});
+        }
+        for (; s < S; s += 2) {
+            last_step(Zero{}, s);
+            if (s + 1 < S) last_step(One{}, s + 1);
+        }
     }
 
     if (p.slices > 1) {
@@ -732,32 +770,34 @@ static int split_columns(int64_t N, int64_t mtiles) {
     return N * mtiles >= 64 * 192 ? 4 : N * mtiles >= 32 * 192 ? 2 : 1;
 }
 
-// The kernels, by number.  0: split-K, 16 rows; 1, 2: split-K, 32 rows; 3 ..: tiles.
+// The kernels, by number.  0: split-K, 16 rows; 1, 2: split-K, 32 rows; 3 ..: tiles.  7 has kernel 3's tiles
+// and more stages in flight, for a workgroup alone on its compute unit (77 x 8192 x 8192: 22.8 us against 26.4);
+// three that share one are as fast with three stages each (1024 x 4096 x 4096: 35.0 us against 36.0).
 struct W8A8Kernel {
     int bm, bn;
     int resident;              // workgroups on a compute unit
     int waves;                 // split-K: waves that share K (tiles: 0)
-    double step, more, round;  // us per step (a 128-row group per wave, or 64 of K), per further resident
-                               // workgroup, per round of resident workgroups
+    double base, step, more, round;  // us: a launch, per step (a 128-row group per wave, or 64 of K), per further
+                                     // resident workgroup, per round of resident workgroups
 };
-static constexpr W8A8Kernel kKernels[] = {{16, 16, 2, 16, 0.70, 4.3, 2.7},  {32, 64, 2, 8, 2.2, 1.36, 0.4},
-                                          {32, 32, 2, 16, 2.2, 7.1, 0.2},   {64, 64, 3, 0, 0.153, 0.089, 0.1},
-                                          {64, 128, 3, 0, 0.282, 0.099, 0.7}, {128, 256, 1, 0, 0.399, 0, 1.4},
-                                          {256, 256, 1, 0, 0.529, 0, 1.0}};
+static constexpr W8A8Kernel kKernels[] = {{16, 16, 2, 16, 0.27, 1.22, 1.09, 3.25},  {32, 64, 2, 8, 2.46, 1.74, 2.11, 0.54},
+                                          {32, 32, 2, 16, 1.72, 2.12, 2.64, 0},     {64, 64, 3, 0, 3.53, 0.144, 0.091, 0.055},
+                                          {64, 128, 3, 0, 3.06, 0.309, 0.098, 0.29}, {128, 256, 1, 0, 3.15, 0.411, 0, 1.71},
+                                          {256, 256, 1, 0, 3.25, 0.525, 0, 3.51},   {64, 64, 2, 0, 4.28, 0.129, 0.101, 0}};
 constexpr int kKernelCount = sizeof(kKernels) / sizeof(kKernels[0]);
 int w8a8_config_count() { return kKernelCount; }
 
 // Estimated time in us of a kernel whose tiles cover `mtiles` row tiles of M rows, K
-// cut into `slices`.  The constants of kKernels and of this formula are fitted to 1800 measured
-// products (20 to 4096 rows, K from 512 to 14336, N from 1024 to 14336) such that the choice by it is
-// near the best: 0.2% slower on average, 8% at most.
+// cut into `slices`.  The constants of kKernels and of this formula are fitted to 5700 measured
+// products (338 sizes of 17 to 4096 rows, K from 256 to 14336, N from 512 to 14336) such that the choice by
+// it is near the best: 1.0% slower on average, 14% at most.
 static double kernel_us(const W8A8Kernel &k, int64_t mtiles, int64_t M, int64_t K, int64_t N, int slices) {
     const int64_t wg = mtiles * ((N + k.bn - 1) / k.bn) * slices, G = K / kGroup;
     const double steps = k.waves ? (G >= k.waves ? (double)G / k.waves : 1.0) : (double)K / 64 / slices;
     const int64_t full = wg / (256 * k.resident), left = (wg - full * 256 * k.resident + 255) / 256;
-    double us = 4 + steps * full * (k.step + k.more * (k.resident - 1)) + k.round * (double)(full + (left > 0));
+    double us = k.base + steps * full * (k.step + k.more * (k.resident - 1)) + k.round * (double)(full + (left > 0));
     if (left > 0) us += steps * (k.step + k.more * (double)(left - 1));
-    return slices > 1 ? us + 2.8 + 1.84e-6 * (double)(slices * M * N) : us;
+    return slices > 1 ? us + 2.22 + 2.38e-6 * (double)(slices * M * N) : us;
 }
 
 // Test hook: the kernel of the next calls, plus 100 times its slices (-1: by size).
@@ -824,7 +864,8 @@ static hipError_t w8a8_dispatch(const W8A8Args &args, hipStream_t stream) {
         case 3: return tile8_launch<DT, 64, 64, 2, 2, 2, 3, GROUPED>(p, stream);
         case 4: return tile8_launch<DT, 64, 128, 2, 2, 2, 2, GROUPED>(p, stream);
         case 5: return tile8_launch<DT, 128, 256, 2, 4, 2, 3, GROUPED>(p, stream);
-        default: return tile8_launch<DT, 256, 256, 2, 4, 1, 4, GROUPED>(p, stream);
+        case 6: return tile8_launch<DT, 256, 256, 2, 4, 1, 4, GROUPED>(p, stream);
+        default: return tile8_launch<DT, 64, 64, 2, 2, 2, 5, GROUPED>(p, stream);
     }
 }
 

@@ -10,7 +10,7 @@
 // Bounds.  Few rows: the weights' bytes (one row of 4096 x 14336 with its quantization 12.5 us,
 // 4.7 TB/s; a large copy reaches 4.93).  Many rows: the matrix core (8192^3 410 us, 2.67 POP/s,
 // the matrix core busy in 75% of the clocks at the 1.7 GHz that its power leaves; zeros for data
-// take 360 us).  In between: what 64-row tiles draw from L2 into LDS, about 12 TB/s.
+// take 360 us).  In between: what 64-row tiles draw from L2 into LDS, about 15 TB/s.
 //
 // Weights: the 2048-byte tiles of w8.hip (16 columns x 128 rows, stored as
 // q + 128; slot 16 c + j holds rows 32 c .. + 31 of column j).  Matrix-core

@@ -390,11 +390,16 @@ constexpr unsigned kBand = 4;         // row tiles side by side on an XCD
 
 // 16 bytes per lane from global memory (base + off) to LDS (lds_base + 16 lane), not
 // waited for here.  In assembly, since the compiler follows its own form of this
-// load with a wait for every outstanding load before any LDS read.
+// load with a wait for every outstanding load before any LDS read.  It names M0, which the compiler
+// writes for loads and indexed registers of its own (and warns that it then does not keep M0's old
+// value, which is meant).
+#pragma clang diagnostic push
+#pragma clang diagnostic ignored "-Winline-asm"
 __device__ __forceinline__ void dma16(const uint8_t *base, uint32_t off, uint32_t lds_base) {
     asm volatile("s_mov_b32 m0, %2\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %0, %1" ::"v"(off), "s"(base), "s"(lds_base)
-                 : "memory");
+                 : "memory", "m0");
 }
+#pragma clang diagnostic pop
 
 // Every DMA but the newest N of this wave and every LDS read have landed; then
 // the workgroup's barrier.

@@ -32,3 +32,17 @@ def test_assembly_that_writes_m0_says_so():
                 seen += 1
                 assert block.rstrip().endswith('"m0")') or '"m0",' in block.rsplit(":", 1)[1], (name, block)
     assert seen >= 1
+
+
+def test_matrix_core_calls_keep_their_operands():
+    """Every call of a matrix-core builtin stands in a function that uses the result and both
+    operands once more behind it, so that no allocation can place the result over an operand."""
+    seen = 0
+    for name, text in SOURCES.items():
+        for m in re.finditer(r"__builtin_amdgcn_mfma_\w+\(", text):
+            seen += 1
+            rest = text[m.start():]
+            body = rest[:rest.find("\n}\n")]
+            assert re.search(r'keep_live\(r, a, b\);|asm\("" : "\+v"\(r\) : "v"\(a\), "v"\(b\)\);', body), (
+                name, text.count("\n", 0, m.start()) + 1)
+    assert seen >= 8

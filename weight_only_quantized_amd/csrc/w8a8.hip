@@ -408,6 +408,14 @@ __device__ __forceinline__ void wait_and_meet() {
     asm volatile("s_waitcnt vmcnt(%0) lgkmcnt(0)\n\ts_barrier" ::"n"(N) : "memory");
 }
 
+// Matrix-core step whose sources stay live past it (the destination must not share their
+// registers), without ordering it against memory operations.
+__device__ __forceinline__ i32x4_t mfma_step(const u32x4_t &a, const u32x4_t &b, const i32x4_t &c) {
+    i32x4_t r = __builtin_amdgcn_mfma_i32_16x16x64_i8(__builtin_bit_cast(i32x4_t, a), __builtin_bit_cast(i32x4_t, b), c, 0, 0, 0);
+    asm("" : "+v"(r) : "v"(a), "v"(b));
+    return r;
+}
+
 // (Registers for as many workgroups per compute unit as LDS holds: 64 x 128 tiles three, which
 // take 106 us instead of 118 for 512 tokens top-8 of 64 experts, 2048 x 2816.)
 template <int DT, int BM, int BN, int WM, int WN, int HALVES, int NBUF, bool GROUPED>
@@ -539,7 +547,7 @@ w8a8_tile_kernel(W8A8Args p, unsigned mtiles, unsigned ncb, unsigned per_xcd) {
         for (int ct = 0; ct < CT; ++ct)
 #pragma unroll
             for (int rt = 0; rt < RT; ++rt)
-                acc[rt][ct] = __builtin_amdgcn_mfma_i32_16x16x64_i8((i32x4_t)wf[U][ct], (i32x4_t)xf[U][rt], acc[rt][ct], 0, 0, 0);
+                acc[rt][ct] = mfma_step(wf[U][ct], xf[U][rt], acc[rt][ct]);
         __builtin_amdgcn_sched_barrier(0);
     };
     using std::integral_constant;

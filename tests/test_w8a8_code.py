@@ -3,7 +3,9 @@ compile to, have to keep whatever a build's register allocation looks like."""
 import os
 import re
 
-from test_codegen import CSRC
+import pytest
+
+from test_codegen import CSRC, HIPCC, _all_asm
 
 SOURCES = {f: open(os.path.join(CSRC, f)).read() for f in sorted(os.listdir(CSRC)) if f.endswith((".hip", ".hpp"))}
 
@@ -46,3 +48,29 @@ def test_matrix_core_calls_keep_their_operands():
             assert re.search(r'keep_live\(r, a, b\);|asm\("" : "\+v"\(r\) : "v"\(a\), "v"\(b\)\);', body), (
                 name, text.count("\n", 0, m.start()) + 1)
     assert seen >= 8
+
+
+def kernels(source):
+    """(name, lines of assembly) of a source's kernels."""
+    srcs, asms = _all_asm()
+    text = dict(zip([os.path.basename(s) for s in srcs], asms))[source]
+    for m in re.finditer(r"^(_Z\w+):.*?^\s*s_endpgm.*?^\.Lfunc_end\d+:", text, re.M | re.S):
+        lines = [line.split(";")[0].strip() for line in m.group(0).splitlines()]
+        yield m.group(1), [line for line in lines if line and not line.startswith(".")]
+
+
+needs_hipcc = pytest.mark.skipif(not os.path.exists(HIPCC), reason="hipcc not available")
+
+
+@needs_hipcc
+def test_joined_shares_are_released_and_acquired():
+    """The workgroups' shares of the balance loss are written before the ticket that hands them over
+    and read behind it by the memory model's own means: a release (the cache written back) in front of
+    the ticket, an acquire (the cache invalidated) behind it."""
+    code = [lines for name, lines in kernels("route.hip") if "route_join_kernel" in name]
+    assert len(code) == 1
+    at = [i for i, line in enumerate(code[0]) if line.startswith("global_atomic_add")]
+    assert len(at) == 1
+    before, behind = code[0][:at[0]], code[0][at[0]:]
+    assert any(line.startswith("buffer_wbl2") and "sc1" in line for line in before)
+    assert any(line.startswith("buffer_inv") and "sc1" in line for line in behind)

@@ -450,28 +450,28 @@ route_join_kernel(RouteSpace ws, int blocks, int E, int32_t *__restrict__ counts
     const int n = lane_reduce<64>(e < E ? c : 0, [](int a, int b) { return a + b; });
 #pragma unroll
     for (int off = 32; off > 0; off >>= 1) x += __shfl_xor(x, off);
-    const bool owner = e == E;                    // one lane of the last workgroup has the tokens
+    // expert index E, the tokens, is in the last workgroup
+    int tokens = __builtin_amdgcn_readlane(c, E & 63);
     if (gridDim.x == 1) {
-        const int tokens = __builtin_amdgcn_readlane(c, E & 63);
         if (lane == 0) *loss = balance_loss(E, x, n, tokens);
         return;
     }
-    // What crosses workgroups is stored and loaded at device scope, past the XCDs' caches, so that
-    // waiting for the stores orders them before the ticket without writing a cache back.
-    if (owner) __hip_atomic_store(ws.tokens, c, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
-    if (lane == 0) {
-        __hip_atomic_store(&ws.x[blockIdx.x], x, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
-        __hip_atomic_store(&ws.n[blockIdx.x], n, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
-    }
-    asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
+    // One lane writes the workgroup's shares and takes a ticket, which releases them; whoever draws the last
+    // one has acquired all (the caches' write-back included, the whole call takes 13.1 us for 16384 x 256, against 13.0
+    // with stores past the caches and no order but the hardware's).
     unsigned order = 0;
-    if (lane == 0) order = __hip_atomic_fetch_add(ws.ticket, 1u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+    if (lane == 0) {
+        ws.x[blockIdx.x] = x;
+        ws.n[blockIdx.x] = n;
+        if (blockIdx.x == gridDim.x - 1) *ws.tokens = tokens;
+        order = __hip_atomic_fetch_add(ws.ticket, 1u, __ATOMIC_ACQ_REL, __HIP_MEMORY_SCOPE_AGENT);
+    }
     if (__builtin_amdgcn_readfirstlane(order) != gridDim.x - 1) return;
-    asm volatile("" ::: "memory");
+    __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "agent");           // for the other lanes
     const bool in = lane < (int)gridDim.x;
-    x = in ? __hip_atomic_load(&ws.x[lane], __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT) : 0.0;
-    const int part = in ? __hip_atomic_load(&ws.n[lane], __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT) : 0;
-    const int tokens = __hip_atomic_load(ws.tokens, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+    x = in ? ws.x[lane] : 0.0;
+    const int part = in ? ws.n[lane] : 0;
+    tokens = *ws.tokens;
 #pragma unroll
     for (int off = 32; off > 0; off >>= 1) x += __shfl_xor(x, off);
     const int all = lane_reduce<64>(part, [](int a, int b) { return a + b; });

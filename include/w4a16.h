@@ -614,7 +614,8 @@ size_t w8a8_grouped_workspace_bytes(int64_t R, int64_t K);
  * products with expert e's weights.
  *   sorted_ids  NULL: row r multiplies row r of x [R][K].  Else the int32 array that
  *               w4a16_moe_align writes for R = T * topk entries: row r multiplies row
- *               sorted_ids[r] / topk of x [T][K], and every token is quantized once
+ *               sorted_ids[r] / topk of x [T][K]; every token is quantized once (where T K
+ *               reaches 2^32, once per row of y that it enters)
  *   topk        entries per token, R % topk == 0; ignored without sorted_ids
  *   expert_offsets  DEVICE int32[E+1], non-decreasing, offsets[0] = 0, offsets[E] <= R
  *               (read on the device only); rows behind offsets[E] are left as they were

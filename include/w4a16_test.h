@@ -116,6 +116,10 @@ int w4a16_test_linear_plan(int shape, int slices);
  */
 int w4a16_test_w8a8_config(int idx);
 
+/* Kernel of a W8A8 product by its size, plus 100 times its slices of K (E = 0: dense, with the
+ * workspace's room); -1 if no kernel's launch takes the size.  Host only. */
+int w4a16_test_w8a8_plan(int64_t M, int64_t K, int64_t N, int64_t E);
+
 #ifdef __cplusplus
 }
 #endif

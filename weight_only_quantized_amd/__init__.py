@@ -117,6 +117,7 @@ _SIGS = {
     "w4a16_test_mx_tile_config": ([C.c_int], C.c_int),
     "w4a16_test_linear_plan": ([C.c_int, C.c_int], C.c_int),
     "w4a16_test_w8a8_config": ([C.c_int], C.c_int),
+    "w4a16_test_w8a8_plan": ([_i64, _i64, _i64, _i64], C.c_int),
     "w4a16_test_w8_config": ([C.c_int, C.c_int], C.c_int),
 }
 EXPORTED = tuple(_SIGS)
@@ -494,3 +495,7 @@ def w4a16_test_linear_plan(shape: int, slices: int) -> int:
 
 def w4a16_test_w8a8_config(idx: int) -> int:
     return lib().w4a16_test_w8a8_config(int(idx))
+
+
+def w4a16_test_w8a8_plan(M: int, K: int, N: int, E: int) -> int:
+    return lib().w4a16_test_w8a8_plan(M, K, N, E)

@@ -675,17 +675,20 @@ w4a16_status w8a8_grouped_gemm(const void *x, const int32_t *sorted_ids, int64_t
     const int64_t X = sorted_ids ? R / topk : R;
     uint8_t *qx = (uint8_t *)workspace;
     float *sx = (float *)(qx + w8a8_sx_offset(R, K));
-    // without a gather only the rows in front of offsets[E] exist
-    st = map_err(w4::launch_w8a8_quantize(x, K, sorted_ids ? nullptr : expert_offsets + E, qx, sx, X, K, dt,
-                                          (hipStream_t)stream));
+    // each token's codes once, where 32 bits address them (the same codes in the experts' order cost topk times the
+    // quantization, some percent of such a product); without a gather only the rows in front of offsets[E] exist
+    const bool by_token = sorted_ids && X * K <= w4::kW8A8GatherBytes;
+    st = map_err(by_token ? w4::launch_w8a8_quantize(x, K, nullptr, qx, sx, X, K, dt, (hipStream_t)stream)
+                          : w4::launch_w8a8_quantize_routed(x, K, expert_offsets + E, sorted_ids, (int)topk, X, qx, sx, R, K,
+                                                            dt, (hipStream_t)stream));
     if (st != W4A16_OK) return st;
     w4::W8A8Args p{};
     p.qx = qx;
     p.sx = sx;
-    p.X = X;
+    p.X = by_token ? X : R;
     p.offsets = expert_offsets;
-    p.sorted = sorted_ids;
-    p.topk = sorted_ids ? (int)topk : 1;
+    p.sorted = by_token ? sorted_ids : nullptr;
+    p.topk = by_token ? (int)topk : 1;
     p.wp = (const uint8_t *)w_packed;
     p.sw = sw;
     p.slices = 1;
@@ -850,6 +853,11 @@ int w4a16_test_mx_small_config(int idx) {
 int w4a16_test_w8a8_config(int idx) {
     w4::set_w8a8_config(idx);
     return w4::w8a8_config_count();
+}
+
+int w4a16_test_w8a8_plan(int64_t M, int64_t K, int64_t N, int64_t E) {
+    if (check_w8a8(M, K, N) != W4A16_OK || M == 0 || E < 0 || E > (int64_t(1) << 20)) return -1;
+    return w4::w8a8_plan(M, K, N, (int)E);
 }
 
 int w4a16_test_w8_config(int small_idx, int tile_idx) {

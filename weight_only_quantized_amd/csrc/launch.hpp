@@ -213,6 +213,10 @@ hipError_t launch_lin_zero_colsum(float *colsum, int64_t N, hipStream_t stream);
 // W8A8: activations quantized per row, products of 8-bit integers.
 hipError_t launch_w8a8_quantize(const void *x, int64_t ldx, const int32_t *row_count, void *qx, float *sx, int64_t M,
                                 int64_t K, int dt, hipStream_t stream);
+// The same with row m taken from x row sorted[m] / topk of X.
+hipError_t launch_w8a8_quantize_routed(const void *x, int64_t ldx, const int32_t *row_count, const int32_t *sorted,
+                                       int topk, int64_t X, void *qx, float *sx, int64_t M, int64_t K, int dt,
+                                       hipStream_t stream);
 struct W8A8Args {
     const uint16_t *x;          // fused quantization: x [M][K], row stride ldx (qx, sx unused)
     int64_t ldx;
@@ -236,7 +240,12 @@ struct W8A8Args {
 // at most kW8A8PartBytes.
 constexpr int64_t kW8A8SliceRows = 1024;
 constexpr int64_t kW8A8PartBytes = int64_t(32) << 20;
+// Codes that the products read by token: rows are addressed with 32 bits.  Past that
+// they are quantized into the experts' order.
+constexpr int64_t kW8A8GatherBytes = (int64_t(1) << 32) - 128;
 hipError_t launch_w8a8(const W8A8Args &p, int dt, hipStream_t stream);
+// Kernel (plus 100 times the slices of K) of a product by its size, E = 0: dense; -1: no grid fits.
+int w8a8_plan(int64_t M, int64_t K, int64_t N, int E);
 // The product of unquantized rows in one launch (p.x, p.ldx), where it exists.
 bool w8a8_fused_ok(int64_t M, int64_t K);
 hipError_t launch_w8a8_fused(const W8A8Args &p, int dt, hipStream_t stream);

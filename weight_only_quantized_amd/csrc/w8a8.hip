@@ -121,10 +121,12 @@ __device__ __forceinline__ u32x2s_t codes_of(const u32x4_t &v, const RowQuant &r
 // values per lane in registers between the maximum and the codes.  Bound by memory:
 // 3 bytes per element (4096 x 4096: 13 us, 3.9 TB/s); small calls by a load, the maximum across
 // waves and the conversions in turn (77 x 8192: 4 us).
-template <int DT, int NW, int C>
+// GATHER: row m is that of x row sorted[m] / topk (ids past the X rows take the last one).
+template <int DT, int NW, int C, bool GATHER>
 __global__ void __launch_bounds__(NW > 4 ? NW * 64 : 256)
 w8a8_quantize_kernel(const uint16_t *__restrict__ x, int64_t ldx, const int32_t *__restrict__ row_count,
-                     uint8_t *__restrict__ qx, float *__restrict__ sx, int64_t M, int64_t K) {
+                     const int32_t *__restrict__ sorted, int topk, int64_t X, uint8_t *__restrict__ qx,
+                     float *__restrict__ sx, int64_t M, int64_t K) {
     constexpr int RPB = NW >= 4 ? 1 : 4 / NW, NT = NW * 64;
     __shared__ uint32_t tops[2][NW >= 4 ? NW : 1];
     if (row_count) {
@@ -134,7 +136,12 @@ w8a8_quantize_kernel(const uint16_t *__restrict__ x, int64_t ldx, const int32_t 
     const int wave = threadIdx.x >> 6, at = NW >= 4 ? threadIdx.x : lane_id();
     int turn = 0;
     for (int64_t m = (int64_t)blockIdx.x * RPB + (NW >= 4 ? 0 : wave); m < M; m += (int64_t)gridDim.x * RPB, turn ^= 1) {
-        const uint16_t *row = x + m * ldx;
+        int64_t src = m;
+        if constexpr (GATHER) {
+            src = (int64_t)((uint32_t)sorted[m] / (uint32_t)topk);
+            src = src < X ? src : X - 1;
+        }
+        const uint16_t *row = x + src * ldx;
         uint32_t top = 0;
         u32x4_t v[C];
 #pragma unroll
@@ -475,7 +482,7 @@ w8a8_tile_kernel(W8A8Args p, unsigned mtiles, unsigned ncb, unsigned per_xcd) {
     const bool gather = GROUPED && p.sorted;
     const uint8_t *abase = p.qx + (int64_t)first * kGroup;
     const uint8_t *bbase = p.wp + (((int64_t)e * (N / 16) + n0 / 16) * (K / kGroup) + first) * kW8Tile;
-    if (!gather) abase += row0 * K;          // gathered rows: X K < 2^32
+    if (!gather) abase += row0 * K;          // gathered rows: X K <= kW8A8GatherBytes
 #pragma unroll
     for (int i = 0; i < AL; ++i) {
         const int r = (wave + NW * i) * RPL + lane / (4 * HALVES), c = (lane % (4 * HALVES)) ^ fx(r & 15);
@@ -707,42 +714,63 @@ __global__ void __launch_bounds__(256) w8a8_join_kernel(W8A8Args p) {
 // ---------------------------------------------------------------------------
 // Launchers
 // ---------------------------------------------------------------------------
-template <int DT, int NW, int C>
-static hipError_t quantize_launch(const void *x, int64_t ldx, const int32_t *row_count, void *qx, float *sx, int64_t M,
-                                  int64_t K, hipStream_t stream) {
+struct QuantizeArgs {
+    const uint16_t *x;
+    int64_t ldx;
+    const int32_t *row_count, *sorted;
+    int topk;
+    int64_t X;
+    uint8_t *qx;
+    float *sx;
+    int64_t M, K;
+};
+
+template <int DT, int NW, int C, bool GATHER = false>
+static hipError_t quantize_launch(const QuantizeArgs &a, hipStream_t stream) {
     constexpr int RPB = NW >= 4 ? 1 : 4 / NW;
-    const int64_t blocks = (M + RPB - 1) / RPB;
-    hipLaunchKernelGGL((w8a8_quantize_kernel<DT, NW, C>), dim3((unsigned)(blocks < 65536 ? blocks : 65536)),
-                       dim3(NW > 4 ? NW * 64 : 256), 0, stream, (const uint16_t *)x, ldx, row_count, (uint8_t *)qx, sx, M,
-                       K);
+    const int64_t blocks = (a.M + RPB - 1) / RPB;
+    hipLaunchKernelGGL((w8a8_quantize_kernel<DT, NW, C, GATHER>), dim3((unsigned)(blocks < 65536 ? blocks : 65536)),
+                       dim3(NW > 4 ? NW * 64 : 256), 0, stream, a.x, a.ldx, a.row_count, a.sorted, a.topk, a.X, a.qx, a.sx,
+                       a.M, a.K);
     return hipGetLastError();
 }
 
+template <int DT, bool GATHER>
+static hipError_t quantize_large(const QuantizeArgs &a, hipStream_t stream) {
+    if (a.K <= 1024) return quantize_launch<DT, 1, 2, GATHER>(a, stream);
+    if (a.K <= 2048) return quantize_launch<DT, 1, 4, GATHER>(a, stream);
+    if (a.K <= 4096) return quantize_launch<DT, 4, 2, GATHER>(a, stream);
+    if (a.K <= 8192) return quantize_launch<DT, 4, 4, GATHER>(a, stream);
+    return quantize_launch<DT, 16, 2, GATHER>(a, stream);
+}
+
 template <int DT>
-static hipError_t quantize_dispatch(const void *x, int64_t ldx, const int32_t *row_count, void *qx, float *sx, int64_t M,
-                                    int64_t K, hipStream_t stream) {
+static hipError_t quantize_dispatch(const QuantizeArgs &a, hipStream_t stream) {
+    if (a.sorted) return quantize_large<DT, true>(a, stream);
     // Small matrices: one piece per lane, for a short chain of loads and conversions (77 rows of 8192:
     // 3.9 us against 5.9); large ones: more per lane, fewer maxima across waves (4096 rows of
     // 4096: 13.3 us against 15.6; 1024 rows: 5.6 against 5.8).
-    if (M * K <= int64_t(3) << 20) {
-        if (K <= 512) return quantize_launch<DT, 1, 1>(x, ldx, row_count, qx, sx, M, K, stream);
-        if (K <= 2048) return quantize_launch<DT, 4, 1>(x, ldx, row_count, qx, sx, M, K, stream);
-        if (K <= 4096) return quantize_launch<DT, 8, 1>(x, ldx, row_count, qx, sx, M, K, stream);
-        if (K <= 8192) return quantize_launch<DT, 16, 1>(x, ldx, row_count, qx, sx, M, K, stream);
-        return quantize_launch<DT, 16, 2>(x, ldx, row_count, qx, sx, M, K, stream);
+    if (a.M * a.K <= int64_t(3) << 20) {
+        if (a.K <= 512) return quantize_launch<DT, 1, 1>(a, stream);
+        if (a.K <= 2048) return quantize_launch<DT, 4, 1>(a, stream);
+        if (a.K <= 4096) return quantize_launch<DT, 8, 1>(a, stream);
+        if (a.K <= 8192) return quantize_launch<DT, 16, 1>(a, stream);
+        return quantize_launch<DT, 16, 2>(a, stream);
     }
-    if (K <= 1024) return quantize_launch<DT, 1, 2>(x, ldx, row_count, qx, sx, M, K, stream);
-    if (K <= 2048) return quantize_launch<DT, 1, 4>(x, ldx, row_count, qx, sx, M, K, stream);
-    if (K <= 4096) return quantize_launch<DT, 4, 2>(x, ldx, row_count, qx, sx, M, K, stream);
-    if (K <= 8192) return quantize_launch<DT, 4, 4>(x, ldx, row_count, qx, sx, M, K, stream);
-    return quantize_launch<DT, 16, 2>(x, ldx, row_count, qx, sx, M, K, stream);
+    return quantize_large<DT, false>(a, stream);
 }
 
 hipError_t launch_w8a8_quantize(const void *x, int64_t ldx, const int32_t *row_count, void *qx, float *sx, int64_t M,
                                 int64_t K, int dt, hipStream_t stream) {
+    return launch_w8a8_quantize_routed(x, ldx, row_count, nullptr, 1, M, qx, sx, M, K, dt, stream);
+}
+
+hipError_t launch_w8a8_quantize_routed(const void *x, int64_t ldx, const int32_t *row_count, const int32_t *sorted,
+                                       int topk, int64_t X, void *qx, float *sx, int64_t M, int64_t K, int dt,
+                                       hipStream_t stream) {
     if (M == 0) return hipSuccess;
-    return dt == DT_BF16 ? quantize_dispatch<DT_BF16>(x, ldx, row_count, qx, sx, M, K, stream)
-                         : quantize_dispatch<DT_F16>(x, ldx, row_count, qx, sx, M, K, stream);
+    const QuantizeArgs a{(const uint16_t *)x, ldx, row_count, sorted, topk, X, (uint8_t *)qx, sx, M, K};
+    return dt == DT_BF16 ? quantize_dispatch<DT_BF16>(a, stream) : quantize_dispatch<DT_F16>(a, stream);
 }
 
 template <int DT, int MT, int NB, int D, int WMAX, bool GROUPED, bool FUSED>
@@ -768,6 +796,7 @@ static hipError_t tile8_launch(const W8A8Args &p, hipStream_t stream) {
     const int64_t per_xcd = (mtiles * ncb * p.slices + kXcd8 - 1) / kXcd8;
     if (per_xcd * kXcd8 * WM * WN * 64 > UINT32_MAX || p.slices < 1 || p.K / kGroup < p.slices) return hipErrorInvalidConfiguration;
     if (p.slices > 1 && (GROUPED || !slices_fit(p, p.slices))) return hipErrorInvalidConfiguration;
+    if (p.sorted && p.X * p.K > kW8A8GatherBytes) return hipErrorInvalidConfiguration;
     hipLaunchKernelGGL((w8a8_tile_kernel<DT, BM, BN, WM, WN, HALVES, NBUF, GROUPED>), dim3((unsigned)(per_xcd * kXcd8)),
                        dim3(WM * WN * 64), 0, stream, p, (unsigned)mtiles, (unsigned)ncb, (unsigned)per_xcd);
     const hipError_t err = hipGetLastError();
@@ -821,15 +850,22 @@ static bool slices_fit(const W8A8Args &p, int slices) {
     return p.part && p.K / kGroup / slices >= 2 && (double)slices * (double)p.M * (double)p.N * 4 <= (double)kW8A8PartBytes;
 }
 
-// Gathered rows of the tile kernels are addressed with 32 bits.
-static bool tile_ok(const W8A8Args &p) { return !p.sorted || p.X * p.K < (int64_t(1) << 32); }
+// A launch has at most 2^32 - 1 threads.
+static bool grid_fits(const W8A8Args &p, int kernel, int slices) {
+    const W8A8Kernel &k = kKernels[kernel];
+    const int64_t few = p.M < p.E ? p.M : p.E, G = p.K / kGroup;
+    const int64_t mtiles = p.offsets ? p.M / k.bm + few : (p.M + k.bm - 1) / k.bm;
+    const int64_t bn = kernel == 0 ? 16 * split_columns(p.N, p.offsets ? few : 1) : k.bn;
+    const int64_t wgs = mtiles * ((p.N + bn - 1) / bn) * slices + kXcd8;
+    const int64_t threads = k.waves ? 64 * (G < k.waves ? G : k.waves) : k.bm <= 64 ? 256 : 512;
+    return wgs <= UINT32_MAX / threads;
+}
 
 static void pick_kernel(const W8A8Args &p, int &kernel, int &slices) {
     const int forced = g_w8a8_cfg.load(std::memory_order_relaxed);
     slices = 1;
     if (forced >= 0 && forced % 100 < kKernelCount) {
         kernel = forced % 100;
-        if (kernel >= 3 && !tile_ok(p)) kernel = 1;
         if (kernel >= 3 && forced >= 200 && slices_fit(p, forced / 100)) slices = forced / 100;
         return;
     }
@@ -839,15 +875,14 @@ static void pick_kernel(const W8A8Args &p, int &kernel, int &slices) {
     // At most 8 rows per expert on average: 16-row tiles (64 experts, 1408 x 2048, M / E = 0.5, 2, 4, 8: 15.5,
     // 27.5, 35.4, 42.4 us against 19, 34, 40, 46 us with the best others; M / E = 16: 51.5 against 49.9 us).
     kernel = 0;
-    if (p.offsets ? p.M <= 8 * (int64_t)p.E : p.M <= 16) return;
+    if ((p.offsets ? p.M <= 8 * (int64_t)p.E : p.M <= 16) && grid_fits(p, 0, 1)) return;
     double best = 1e30;
     for (int i = 0; i < kKernelCount; ++i) {
         const W8A8Kernel &k = kKernels[i];
         if (i == 0 && split_columns(p.N, 1) != 1) continue;
-        if (k.waves == 0 && !tile_ok(p)) continue;
         const int64_t mtiles = p.offsets ? (int64_t)std::ceil(held / (1 - std::exp(-k.bm / mean))) : (p.M + k.bm - 1) / k.bm;
         for (int n = 1; n <= 8; n *= 2) {
-            if (n > 1 && (k.waves != 0 || !slices_fit(p, n))) break;
+            if ((n > 1 && (k.waves != 0 || !slices_fit(p, n))) || !grid_fits(p, i, n)) break;
             const double us = kernel_us(k, mtiles, p.M, p.K, p.N, n);
             if (us < best) {
                 best = us;
@@ -856,6 +891,21 @@ static void pick_kernel(const W8A8Args &p, int &kernel, int &slices) {
             }
         }
     }
+}
+
+int w8a8_plan(int64_t M, int64_t K, int64_t N, int E) {
+    static const int32_t offsets = 0;
+    static int32_t room = 0;
+    W8A8Args p{};
+    p.M = p.X = M;
+    p.K = K;
+    p.N = N;
+    p.E = E > 0 ? E : 1;
+    p.offsets = E > 0 ? &offsets : nullptr;
+    p.part = E == 0 && M <= kW8A8SliceRows ? &room : nullptr;
+    int kernel = 0, slices = 1;
+    pick_kernel(p, kernel, slices);
+    return grid_fits(p, kernel, slices) ? kernel + 100 * slices : -1;
 }
 
 template <int DT, bool GROUPED>

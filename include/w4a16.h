@@ -593,8 +593,13 @@ w4a16_status w8a8_gemm_prequant(const void *qx, const float *sx, const void *w_p
                                 void *stream);
 
 /* Scratch of w8a8_gemm: the codes and scales of M rows, and for M <= 1024 another 32 MiB
- * for the sums of K slices.  0 for sizes that the call rejects. */
+ * for the sums of K slices (so 1024 rows need more than 1025).  0 for sizes that the
+ * call rejects. */
 size_t w8a8_workspace_bytes(int64_t M, int64_t K);
+
+/* Scratch that serves w8a8_gemm with any number of rows up to M, and any K up to
+ * this one: the largest of their w8a8_workspace_bytes.  For programs that keep one workspace. */
+size_t w8a8_max_workspace_bytes(int64_t M, int64_t K);
 
 /* y [M][N] from x [M][K] (dtype dt): w8a8_quantize into the workspace, then the
  * product; up to about 16384 elements of x (4 rows of 4096) in one kernel that quantizes x while the

@@ -33,3 +33,16 @@ def test_two_entries_per_token_past_32_bits():
     for e in range(E):
         for a, b in ((o[e], o[e] + 3), (o[e + 1] - 20, o[e + 1])):
             check_gemm(y[a:b], x[srt[a:b].long() // topk].cpu(), w[e], sw[e], None)
+
+
+def test_one_workspace_for_all_row_counts():
+    """A workspace for up to 1100 rows serves every call, whose results are those of a workspace of its own."""
+    K, N, dt = 2048, 192, BF16
+    x, w, sw, b = problem(1100, K, N, dt, bias=True)
+    xd, wp, swd, bd = dev(x), packed(w), dev(sw), dev(b)
+    nb = w4.w8a8_max_workspace_bytes(1100, K)
+    ws = workspace(nb)
+    for M in (1100, 1, 16, 70, 300, 1024, 1025):
+        y = torch.full((M, N), 9.0, dtype=x.dtype, device=DEV)
+        w4.w8a8_gemm(xd, wp, swd, y, M, K, N, bias=bd, dt=dt, workspace=ws, workspace_bytes=nb)
+        check_gemm(y, x[:M], w[0], sw[0], b)

@@ -32,3 +32,27 @@ def test_every_size_has_a_kernel():
             assert plan >= 100, (M, K, N, E)
             seen.add(plan % 100)
     assert len(seen) >= 6
+
+
+ROWS = (1, 2, 4, 16, 17, 77, 512, 1023, 1024, 1025, 1026, 2048, 4096, 1 << 17, 1 << 20)
+
+
+@pytest.mark.parametrize("K", [128, 4096, 14336, 130944])
+def test_one_workspace_serves_every_row_count(K):
+    """The size for all calls of up to so many rows grows with the rows and covers each of them."""
+    last = 0
+    for M in ROWS:
+        room = w4.w8a8_max_workspace_bytes(M, K)
+        assert room >= last and all(room >= w4.w8a8_workspace_bytes(m, K) for m in ROWS if m <= M)
+        assert any(room == w4.w8a8_workspace_bytes(m, K) for m in ROWS if m <= M)
+        last = room
+    for M, k in ((0, K), (-1, K), (1 << 31, K), (4, 100), (4, 1 << 17)):
+        assert w4.w8a8_max_workspace_bytes(M, k) == 0
+
+
+def test_calls_take_the_common_workspace():
+    """What a call finds after the workspace's size is right: a bias off its alignment."""
+    F, K, N = 1 << 40, 4096, 64
+    room = w4.w8a8_max_workspace_bytes(4096, K)
+    for M in (1, 16, 512, 1024, 1025, 4096):
+        assert w4.lib().w8a8_gemm(F, 0, F, F, F + 1, F, 0, M, K, N, 1, F, room, None) == 4

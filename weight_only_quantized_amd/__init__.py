@@ -96,6 +96,7 @@ _SIGS = {
     "w8a8_quantize": ([_p, _i64, _p, _p, _p, _i64, _i64, C.c_int, _p], C.c_int),
     "w8a8_gemm_prequant": ([_p, _p, _p, _p, _p, _p, _i64, _i64, _i64, _i64, C.c_int, _p], C.c_int),
     "w8a8_workspace_bytes": ([_i64, _i64], C.c_size_t),
+    "w8a8_max_workspace_bytes": ([_i64, _i64], C.c_size_t),
     "w8a8_gemm": ([_p, _i64, _p, _p, _p, _p, _i64, _i64, _i64, _i64, C.c_int, _p, C.c_size_t, _p], C.c_int),
     "w8a8_grouped_workspace_bytes": ([_i64, _i64], C.c_size_t),
     "w8a8_grouped_gemm": ([_p, _p, _i64, _p, _p, _p, _p, _i64, _i64, _i64, _i64, C.c_int, _p, C.c_size_t, _p], C.c_int),
@@ -389,6 +390,10 @@ def w8a8_gemm_prequant(qx, sx, w_packed, sw, y, M, K, N, bias=None, dt=W4A16_BF1
 
 def w8a8_workspace_bytes(M: int, K: int) -> int:
     return lib().w8a8_workspace_bytes(M, K)
+
+
+def w8a8_max_workspace_bytes(M: int, K: int) -> int:
+    return lib().w8a8_max_workspace_bytes(M, K)
 
 
 def w8a8_gemm(x, w_packed, sw, y, M, K, N, bias=None, dt=W4A16_BF16, ldx=0, ldy=0, workspace=None,

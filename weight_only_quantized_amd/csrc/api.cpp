@@ -619,6 +619,12 @@ w4a16_status w8a8_gemm_prequant(const void *qx, const float *sx, const void *w_p
 
 size_t w8a8_workspace_bytes(int64_t M, int64_t K) { return w8a8_bytes(M, K, true); }
 
+size_t w8a8_max_workspace_bytes(int64_t M, int64_t K) {
+    // both grow with M, below and above the limit of slices
+    const size_t all = w8a8_bytes(M, K, true), sliced = w8a8_bytes(M < w4::kW8A8SliceRows ? M : w4::kW8A8SliceRows, K, true);
+    return all == 0 || all > sliced ? all : sliced;
+}
+
 w4a16_status w8a8_gemm(const void *x, int64_t ldx, const void *w_packed, const float *sw, const void *bias, void *y,
                        int64_t ldy, int64_t M, int64_t K, int64_t N, int dt, void *workspace, size_t workspace_bytes,
                        void *stream) {

@@ -74,3 +74,22 @@ def test_joined_shares_are_released_and_acquired():
     before, behind = code[0][:at[0]], code[0][at[0]:]
     assert any(line.startswith("buffer_wbl2") and "sc1" in line for line in before)
     assert any(line.startswith("buffer_inv") and "sc1" in line for line in behind)
+
+
+@needs_hipcc
+@pytest.mark.parametrize("source", ["route.hip", "w8a8.hip"])
+def test_shared_memory_is_accessed_as_such(source):
+    """No access through generic addresses: one waits for every outstanding load of its wave and
+    says nothing about the order of shared memory."""
+    for name, lines in kernels(source):
+        bad = [line for line in lines if line.startswith("flat_")]
+        assert not bad, (name, len(bad), bad[:3])
+
+
+@needs_hipcc
+@pytest.mark.parametrize("source", ["route.hip", "w8a8.hip"])
+def test_nothing_is_spilled(source):
+    srcs, asms = _all_asm()
+    text = dict(zip([os.path.basename(s) for s in srcs], asms))[source]
+    sizes = re.findall(r"\.amdhsa_private_segment_fixed_size (\d+)", text)
+    assert len(sizes) > 10 and set(sizes) == {"0"}

@@ -489,6 +489,11 @@ __global__ void __launch_bounds__(kRouteThreads, LPT == 64 && !VEC ? 2 : 4) rout
     const int E = p.E, tid = threadIdx.x, sub = tid % LPT;
     __shared__ __attribute__((aligned(16))) float hs[LPT * EPL];
     float *const mine = spread[tid / LPT];
+    // What the lanes of a wave wrote to LDS in front of it is there for all of them behind it.
+    auto meet = []() {
+        __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+        __builtin_amdgcn_wave_barrier();
+    };
     // the first row is on its way while the loss's part of h is formed
     int64_t t = (int64_t)blockIdx.x * TPB + tid / LPT;
     uint32_t raw[EPL];
@@ -550,32 +555,36 @@ __global__ void __launch_bounds__(kRouteThreads, LPT == 64 && !VEC ? 2 : 4) rout
                         mean += p.ids[t * p.topk + k] >= 0 ? p.w[t * p.topk + k] * p.dw[t * p.topk + k] : 0.0f;
                     mean = group_sum<LPT>(mean);
                 }
-                // Through LDS: entry k's value to its expert's place (the lanes of a token are in
-                // one wave, whose LDS accesses complete in order), unless an expert comes twice
-                // (the entry that it finds in its place is another) or topk is past the lanes.
+                // Through LDS: entry k's value to its expert's place (the lanes of a token are in one wave,
+                // whose steps meet() orders), unless an expert comes twice (the entry that it finds in its
+                // place is another) or topk is past the lanes.
                 const float v = p.renorm ? w * (dw - mean) : dw;
                 const bool held = id >= 0 && id < E;
                 bool twice = p.topk > LPT;
                 if (!twice) {
 #pragma unroll
-                    for (int i = 0; i < EPL; i += 4) *reinterpret_cast<volatile f32x4_t *>(mine + sub * EPL + i) = f32x4_t{};
-                    volatile float *const place = mine + (held ? id : 0);
+                    for (int i = 0; i < EPL; i += 4) *reinterpret_cast<f32x4_t *>(mine + sub * EPL + i) = f32x4_t{};
+                    meet();
+                    float *const place = mine + (held ? id : 0);
                     if (held) *place = (float)sub;
+                    meet();
                     const bool other_entry = held && *place != (float)sub;
                     twice = lane_umax<LPT>(other_entry ? 1u : 0u) != 0;
+                    meet();
                     if (held) *place = v;
+                    meet();
                     if constexpr (VEC) {
 #pragma unroll
                         for (int i = 0; i < EPL; i += 4) {
-                            const f32x4_t q =
-                                *reinterpret_cast<volatile f32x4_t *>(mine + expert_of<DT, LPT, EPL, VEC>(i, sub));
+                            const f32x4_t q = *reinterpret_cast<const f32x4_t *>(mine + expert_of<DT, LPT, EPL, VEC>(i, sub));
 #pragma unroll
                             for (int u = 0; u < 4; ++u) sel[i + u] = q[u];
                         }
                     } else {
 #pragma unroll
-                        for (int i = 0; i < EPL; ++i) sel[i] = *static_cast<volatile float *>(mine + i * LPT + sub);
+                        for (int i = 0; i < EPL; ++i) sel[i] = mine[i * LPT + sub];
                     }
+                    meet();
                 }
                 if (twice) {
 #pragma unroll

@@ -480,9 +480,10 @@ route_join_kernel(RouteSpace ws, int blocks, int E, int32_t *__restrict__ counts
 
 // ---- backward -----------------------------------------------------------------
 
+// (Four waves per SIMD hold the 1024 workgroups of 16384 tokens of 256 experts at once.  All forms fit its 128 registers
+// without spilling; left alone, one would take more: 142 for wide fp32 rows of 513 to 1024 experts.)
 template <int DT, int LPT, int EPL, bool VEC>
-// (four waves per SIMD: 16384 tokens of 256 experts then have all their workgroups resident, 6.9 us against 8.2)
-__global__ void __launch_bounds__(kRouteThreads, LPT == 64 && !VEC ? 2 : 4) route_backward_kernel(RouteArgs p) {
+__global__ void __launch_bounds__(kRouteThreads, 4) route_backward_kernel(RouteArgs p) {
     constexpr int TPB = kRouteThreads / LPT;
     // a token's gradients through its chosen weights, one place per expert
     __shared__ __attribute__((aligned(16))) float spread[TPB][LPT * EPL];

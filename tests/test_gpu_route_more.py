@@ -50,3 +50,40 @@ def test_choices_whose_distance_leaves_fp32():
     ri, rw, rc, _ = ref.route(z, 8, True)
     assert torch.equal(ids.cpu(), ri) and torch.equal(cnt.cpu(), rc)
     assert bool(((w.cpu().double() - rw).abs() <= 2.0 ** -22 * rw).all())
+
+
+@pytest.mark.parametrize("dt", [F16, BF16, F32])
+@pytest.mark.parametrize("E,pad,lpad", [(16, 8, 16), (64, 8, 16), (120, 40, 8), (256, 8, 24), (512, 16, 8), (1000, 24, 8)])
+def test_wide_rows_inside_wider_buffers(E, pad, lpad, dt):
+    """Rows of whole 16-byte pieces with gaps between them: the gaps are neither read (NaN) nor written."""
+    T, topk = 70, 6
+    z = logits_of(T, E, dt, seed=4)
+    wide = torch.full((T, E + pad), float("nan"), dtype=z.dtype)
+    wide[:, :E] = z
+    g = torch.Generator().manual_seed(E)
+    dw, dloss = torch.randn((T, topk), generator=g).to(DEV), torch.tensor([0.6], device=DEV)
+    for renorm in (False, True):
+        ids, w, cnt, loss = run(wide.to(DEV), topk, renorm, dt, ld=E + pad, E=E)
+        check(z, (ids, w, cnt, loss), topk, renorm)
+        for ld, lddl in ((E + pad, E + lpad), (0, E + lpad), (E + pad, 0)):
+            dz = run_bwd((wide if ld else z).to(DEV), ids, w, cnt, dw, dloss, topk, renorm, dt, ld=ld, lddl=lddl, E=E)
+            check_bwd(z, dz[:, :E], ids, w, cnt, dw, dloss, renorm)
+            assert bool((dz[:, E:] == 9.0).all())
+
+
+@pytest.mark.parametrize("dt", [F16, BF16, F32])
+@pytest.mark.parametrize("T,E,topk", [(3000, 40, 20), (500, 8, 8), (90, 600, 40)])
+def test_backward_of_more_choices_than_lanes(T, E, topk, dt):
+    """Several tokens per wave and loops over the tokens, some of them padding."""
+    z = logits_of(T, E, dt, seed=6)
+    mask = (torch.rand(T, generator=torch.Generator().manual_seed(E)) > 0.2).to(torch.uint8)
+    dw = torch.randn((T, topk), generator=torch.Generator().manual_seed(T)).to(DEV)
+    for renorm in (False, True):
+        ids, w, cnt, _ = run(z.to(DEV), topk, renorm, dt, mask=mask.to(DEV))
+        dz = run_bwd(z.to(DEV), ids, w, cnt, dw, None, topk, renorm, dt, mask=mask.to(DEV))
+        # (the other file's bound counts 16 chosen ones: topk - 16 additions more)
+        want, size = ref.route_backward(z, ids.cpu(), w.cpu(), cnt.cpu(), dw.cpu(), None, renorm, mask)
+        td = z.dtype
+        bound = (ref.prob_bound(z) + (48 + topk) * ref.U32) * size * (1 + ref.half_step(td)) + ref.half_step(td) * want.abs()
+        bound = bound + torch.finfo(td).smallest_normal * torch.finfo(td).eps
+        assert bool(((dz.cpu().double() - want).abs() <= bound).all())

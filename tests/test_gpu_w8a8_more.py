@@ -46,3 +46,75 @@ def test_one_workspace_for_all_row_counts():
         y = torch.full((M, N), 9.0, dtype=x.dtype, device=DEV)
         w4.w8a8_gemm(xd, wp, swd, y, M, K, N, bias=bd, dt=dt, workspace=ws, workspace_bytes=nb)
         check_gemm(y, x[:M], w[0], sw[0], b)
+
+
+@pytest.fixture
+def config():
+    yield w4.w4a16_test_w8a8_config
+    w4.w4a16_test_w8a8_config(-1)
+
+
+@pytest.mark.parametrize("dt", [F16, BF16])
+@pytest.mark.parametrize("kernel", [3, 4, 5, 6, 7])
+@pytest.mark.parametrize("M,slices", [(33, 4), (300, 2), (700, 8)])
+def test_slices_between_gaps(config, M, slices, kernel, dt):
+    """Products cut into slices of K whose rows of x and y lie in wider buffers: what lies between stays."""
+    K, N = 2048, 192
+    x, w, sw, b = problem(M, K, N, dt, seed=7, bias=True)
+    wide = torch.full((M, K + 24), float("nan"), dtype=x.dtype)
+    wide[:, :K] = x
+    config(kernel + 100 * slices)
+    assert w4.w4a16_test_w8a8_plan(M, K, N, 0) == kernel + 100 * slices
+    y = torch.full((M, N + 40), 9.0, dtype=x.dtype, device=DEV)
+    nb = w4.w8a8_workspace_bytes(M, K)
+    w4.w8a8_gemm(dev(wide), packed(w), dev(sw), y, M, K, N, bias=dev(b), dt=dt, ldx=K + 24, ldy=N + 40,
+                 workspace=workspace(nb), workspace_bytes=nb)
+    check_gemm(y[:, :N], x, w[0], sw[0], b)
+    assert bool((y[:, N:] == 9.0).all())
+
+
+@pytest.mark.parametrize("gather", [False, True])
+@pytest.mark.parametrize("T,topk,E", [(6, 4, 16), (150, 2, 6)])
+def test_grouped_call_in_a_graph(T, topk, E, gather):
+    """Captured, then replayed on other tokens and another routing, with eager work between the replays."""
+    K, N, R, dt = 256, 192, T * topk, BF16
+    _, w, sw, _ = problem(1, K, N, dt, E=E)
+    wp, swd, nb = packed(w), dev(sw), w4.w8a8_grouped_workspace_bytes(R, K)
+    g = torch.Generator().manual_seed(T)
+
+    def routing():
+        ids = torch.stack([torch.randperm(E, generator=g)[:topk] for _ in range(T)])
+        ids[torch.rand((T, topk), generator=g) < 0.1] = -1
+        off, srt, row_of = (torch.zeros(n, dtype=torch.int32, device=DEV) for n in (E + 1, R, R))
+        w4.w4a16_moe_align(ids.to(torch.int32).to(DEV), T, topk, E, off, srt, row_of)
+        return torch.randn((T if gather else R, K), generator=g).to(torch.bfloat16).to(DEV), off, srt
+
+    def call(x, off, srt, y, ws):
+        w4.w8a8_grouped_gemm(x, off, wp, swd, y, E, R, K, N, sorted_ids=srt if gather else None, topk=topk, dt=dt,
+                             workspace=ws, workspace_bytes=nb)
+    inputs = [routing() for _ in range(3)]
+    want = []
+    for v in inputs:
+        want.append(torch.full((R, N), 9.0, dtype=torch.bfloat16, device=DEV))
+        call(*v, want[-1], workspace(nb))
+        for e in range(E):
+            a, b = int(v[1][e]), int(v[1][e + 1])
+            rows = v[0][v[2][a:b].long() // topk] if gather else v[0][a:b]
+            if b > a:
+                check_gemm(want[-1][a:b], rows.cpu(), w[e], sw[e], None)
+    static, y, ws = [t.clone() for t in inputs[0]], torch.zeros_like(want[0]), workspace(nb)
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        call(*static, y, ws)
+    torch.cuda.synchronize()
+    for i in (0, 1, 2, 1, 0):
+        for s, t in zip(static, inputs[i]):
+            s.copy_(t)
+        y.fill_(9.0)
+        graph.replay()
+        torch.cuda.synchronize()
+        assert torch.equal(y, want[i])
+        other = torch.full_like(y, 9.0)
+        call(*inputs[2 - i], other, workspace(nb))
+        assert torch.equal(other, want[2 - i])

@@ -721,7 +721,7 @@ static hipError_t route_launch(const RouteArgs &p, void *workspace, hipStream_t 
 }
 
 template <int DT, int LPT, int EPL>
-static hipError_t route_backward_launch(const RouteArgs &p, void *, hipStream_t stream) {
+static hipError_t route_backward_launch(const RouteArgs &p, hipStream_t stream) {
     constexpr int TPB = kRouteThreads / LPT, size = DT == DT_F32 ? 4 : 2;
     const bool vec = route_vec(p.logits, p.ld, p.E, size) && route_vec(p.dlogits, p.ldd, p.E, size);
     const int64_t b = (p.T + TPB - 1) / TPB;
@@ -735,7 +735,7 @@ static hipError_t route_dispatch(const RouteArgs &p, void *workspace, hipStream_
     const RouteShape s = route_shape(p.E);
 #define W4_ROUTE(L, P)                                                                                 \
     if (s.lpt == L && s.epl == P)                                                                      \
-        return BACKWARD ? route_backward_launch<DT, L, P>(p, workspace, stream) : route_launch<DT, L, P>(p, workspace, stream);
+        return BACKWARD ? route_backward_launch<DT, L, P>(p, stream) : route_launch<DT, L, P>(p, workspace, stream);
     W4_ROUTE(4, 4) W4_ROUTE(4, 8) W4_ROUTE(8, 8) W4_ROUTE(8, 16) W4_ROUTE(16, 16) W4_ROUTE(32, 16) W4_ROUTE(64, 16)
 #undef W4_ROUTE
     return hipErrorInvalidValue;

@@ -28,7 +28,6 @@
 namespace w4 {
 
 constexpr int kW8Tile = 2048;
-typedef uint32_t u32x2s_t __attribute__((__vector_size__(2 * sizeof(uint32_t))));
 
 // ---------------------------------------------------------------------------
 // Quantization of rows
@@ -88,7 +87,7 @@ struct RowQuant {
 
 // Codes of 8 values.
 template <int DT>
-__device__ __forceinline__ u32x2s_t codes_of(const u32x4_t &v, const RowQuant &rq) {
+__device__ __forceinline__ u32x2_t codes_of(const u32x4_t &v, const RowQuant &rq) {
     constexpr float kRound = 12582912.0f;                    // 3 2^22
     uint32_t m[8];
     float far = 0.0f;
@@ -107,7 +106,7 @@ __device__ __forceinline__ u32x2s_t codes_of(const u32x4_t &v, const RowQuant &r
             m[i] = (uint32_t)rq.exact(h2f<DT>((uint16_t)(w >> (16 * (i & 1)))));
         }
     }
-    u32x2s_t out;
+    u32x2_t out;
 #pragma unroll
     for (int i = 0; i < 2; ++i) {
         const uint32_t a = __builtin_amdgcn_perm(m[4 * i + 1], m[4 * i], 0x0C0C0400u);
@@ -164,10 +163,10 @@ w8a8_quantize_kernel(const uint16_t *__restrict__ x, int64_t ldx, const int32_t 
 #pragma unroll
         for (int i = 0; i < C; ++i) {
             const int64_t k = ((int64_t)i * NT + at) * 8;
-            if (k < K) *reinterpret_cast<u32x2s_t *>(qx + m * K + k) = codes_of<DT>(v[i], rq);
+            if (k < K) *reinterpret_cast<u32x2_t *>(qx + m * K + k) = codes_of<DT>(v[i], rq);
         }
         for (int64_t k = ((int64_t)C * NT + at) * 8; k < K; k += NT * 8)
-            *reinterpret_cast<u32x2s_t *>(qx + m * K + k) = codes_of<DT>(ld128(row + k), rq);
+            *reinterpret_cast<u32x2_t *>(qx + m * K + k) = codes_of<DT>(ld128(row + k), rq);
         if (at == 0) sx[m] = scale;
     }
 }
@@ -232,7 +231,7 @@ constexpr int kFusedBytes = 16 * (kHeld * 512 + 16);    // their codes, at most 
 
 template <int DT, int MT, int NB, int D, int WMAX, bool GROUPED, bool FUSED>
 __global__ void __launch_bounds__(WMAX * 64)
-w8a8_split_kernel(W8A8Args p, unsigned mtiles, unsigned ncb) {
+w8a8_split_kernel(W8A8Args p, unsigned ncb) {
     static_assert(!GROUPED || !FUSED, "the grouped form reads quantized rows");
     constexpr int RED = WMAX * NB * MT * 1024, LDS = FUSED && kFusedBytes > RED ? kFusedBytes : RED;
     __shared__ __attribute__((aligned(16))) uint8_t lds[LDS];
@@ -314,7 +313,7 @@ w8a8_split_kernel(W8A8Args p, unsigned mtiles, unsigned ncb) {
 #pragma unroll
         for (int u = 0; u < kHeld; ++u)
             if (pr[u] >= 0)
-                *reinterpret_cast<u32x2s_t *>(lds + pr[u] * stride + pk[u]) =
+                *reinterpret_cast<u32x2_t *>(lds + pr[u] * stride + pk[u]) =
                     codes_of<DT>(held[u], RowQuant(row_scale<DT>(tops[pr[u]])));
         __syncthreads();
     } else {
@@ -380,8 +379,8 @@ w8a8_split_kernel(W8A8Args p, unsigned mtiles, unsigned ncb) {
                 const float bv = p.bias ? h2f<DT>(p.bias[n + i]) : 0.0f;
                 h[i] = f2h<DT>(finish(sum[i], rs, Split(p.sw[(int64_t)e * N + n + i]), bv));
             }
-            *reinterpret_cast<u32x2s_t *>(p.y + r * p.ldy + n) =
-                u32x2s_t{h[0] | (uint32_t)h[1] << 16, h[2] | (uint32_t)h[3] << 16};
+            *reinterpret_cast<u32x2_t *>(p.y + r * p.ldy + n) =
+                u32x2_t{h[0] | (uint32_t)h[1] << 16, h[2] | (uint32_t)h[3] << 16};
         }
     }
 }
@@ -683,7 +682,6 @@ w8a8_tile_kernel(W8A8Args p, unsigned mtiles, unsigned ncb, unsigned per_xcd) {
     }
 }
 
-
 // y from the slices' sums; 4 columns per lane.
 template <int DT>
 __global__ void __launch_bounds__(256) w8a8_join_kernel(W8A8Args p) {
@@ -707,7 +705,7 @@ __global__ void __launch_bounds__(256) w8a8_join_kernel(W8A8Args p) {
             const float bv = p.bias ? h2f<DT>(p.bias[n + u]) : 0.0f;
             h[u] = f2h<DT>(finish(sum[u], rs, Split(p.sw[n + u]), bv));
         }
-        *reinterpret_cast<u32x2s_t *>(p.y + r * p.ldy + n) = u32x2s_t{h[0] | (uint32_t)h[1] << 16, h[2] | (uint32_t)h[3] << 16};
+        *reinterpret_cast<u32x2_t *>(p.y + r * p.ldy + n) = u32x2_t{h[0] | (uint32_t)h[1] << 16, h[2] | (uint32_t)h[3] << 16};
     }
 }
 
@@ -782,7 +780,7 @@ static hipError_t split_launch(const W8A8Args &p, hipStream_t stream) {
     const int64_t mtiles = GROUPED ? p.M / (16 * MT) + few : (p.M + 16 * MT - 1) / (16 * MT);
     if (p.N % (16 * NB) != 0 || mtiles * ncb * W * 64 > UINT32_MAX) return hipErrorInvalidConfiguration;
     hipLaunchKernelGGL((w8a8_split_kernel<DT, MT, NB, D, WMAX, GROUPED, FUSED>), dim3((unsigned)(mtiles * ncb)),
-                       dim3(W * 64), 0, stream, p, (unsigned)mtiles, (unsigned)ncb);
+                       dim3(W * 64), 0, stream, p, (unsigned)ncb);
     return hipGetLastError();
 }
 

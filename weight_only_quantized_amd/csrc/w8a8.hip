@@ -10,7 +10,9 @@
 // Bounds.  Few rows: the weights' bytes (one row of 4096 x 14336 with its quantization 12.5 us,
 // 4.7 TB/s; a large copy reaches 4.93).  Many rows: the matrix core (8192^3 410 us, 2.67 POP/s,
 // the matrix core busy in 75% of the clocks at the 1.7 GHz that its power leaves; zeros for data
-// take 360 us).  In between: what 64-row tiles draw from L2 into LDS, about 15 TB/s.
+// take 360 us).  In between, 40 to 3000 rows, 2 to 5 times the larger of the two: what 64-row tiles draw from L2
+// into LDS, about 15 TB/s (351 x 4096 x 8192: 768 workgroups, 403 MB, 26 us); 128 x 256 tiles draw a third of it, with
+// too few workgroups for the card.
 //
 // Weights: the 2048-byte tiles of w8.hip (16 columns x 128 rows, stored as
 // q + 128; slot 16 c + j holds rows 32 c .. + 31 of column j).  Matrix-core
@@ -830,7 +832,8 @@ int w8a8_config_count() { return kKernelCount; }
 // Estimated time in us of a kernel whose tiles cover `mtiles` row tiles of M rows, K
 // cut into `slices`.  The constants of kKernels and of this formula are fitted to 5700 measured
 // products (338 sizes of 17 to 4096 rows, K from 256 to 14336, N from 512 to 14336) such that the choice by
-// it is near the best: 1.0% slower on average, 14% at most.
+// it is near the best of these kernels: there 1.0% slower on average, 14% at most; on 90 other sizes of the same
+// ranges 1.2% on average, more than 5% for 8 of them, 22% at most (284 x 2560 x 3584).
 static double kernel_us(const W8A8Kernel &k, int64_t mtiles, int64_t M, int64_t K, int64_t N, int slices) {
     const int64_t wg = mtiles * ((N + k.bn - 1) / k.bn) * slices, G = K / kGroup;
     const double steps = k.waves ? (G >= k.waves ? (double)G / k.waves : 1.0) : (double)K / 64 / slices;
@@ -871,7 +874,11 @@ static void pick_kernel(const W8A8Args &p, int &kernel, int &slices) {
     // them (exponentially around their mean), an expert has 1 / (1 - exp(-bm / mean)) row tiles.
     const double held = (double)(p.M < p.E ? p.M : p.E), mean = p.offsets ? (double)p.M / held : 0;
     // At most 8 rows per expert on average: 16-row tiles (64 experts, 1408 x 2048, M / E = 0.5, 2, 4, 8: 15.5,
-    // 27.5, 35.4, 42.4 us against 19, 34, 40, 46 us with the best others; M / E = 16: 51.5 against 49.9 us).
+    // 27.5, 35.4, 42.4 us against 19, 34, 40, 46 us with the best others; M / E = 16: 51.5 against 49.9 us; 16 experts of
+    // 4096 x 1024 and 2048 x 4096, M / E = 8: 18.9 and 30.9 us, the best; but 128 experts of 768 x 2048, M / E = 8: 56 against
+    // 51 us, and 8 experts of 4096 x 14336, M / E = 4: 91 against 82 us).  Dense products of up to 16 rows: near the best where
+    // the weights are most of the time (16 x 4096 x 14336), slower on small ones (20 sizes of 2 to 16 rows: 13% on average, at
+    // most 57%, 15 x 1280 x 5184 11.9 against 7.6 us).
     kernel = 0;
     if ((p.offsets ? p.M <= 8 * (int64_t)p.E : p.M <= 16) && grid_fits(p, 0, 1)) return;
     double best = 1e30;
